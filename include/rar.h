@@ -368,6 +368,115 @@ rar_status rar_bucket_allreduce_arena(rar_buckets_t b, int N, rar_chunking chunk
                                       void *const arenas[], void *const ready_events[], void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Producers of the gradients: the embedding, the linear layer and 8-bit   */
+/* activation checkpoints.  These make the tensors whose gradients the     */
+/* calls above reduce: a Transformer's embedding table and its projections */
+/* W (in x out) with biases.                                               */
+/*                                                                         */
+/* Matrices are row-major with a leading dimension in elements (ld >= the  */
+/* row length, at most 2^22; K, N, D at most 2^20; T at most 2^24).        */
+/* Matrices in the operator's type need element alignment only; rows of    */
+/* whole 16-byte groups at 16-byte aligned addresses are read directly,    */
+/* others are copied into the workspace first.  Outputs must not overlap   */
+/* inputs or each other, unless a call says so (RAR_EINVAL); two views of  */
+/* one leading dimension with disjoint columns do not overlap.  Device     */
+/* buffers belong to the current device.                                   */
+/*                                                                         */
+/* Workspaces are the caller's: `ws` is device memory, 16-byte aligned, of */
+/* at least the bytes the matching query gives (RAR_EINVAL otherwise); it  */
+/* holds nothing between calls and need not be cleared.  Calls that may    */
+/* overlap in time (other streams, other graphs) need workspaces of their  */
+/* own.  Nothing is allocated, so every call can be captured.              */
+/*                                                                         */
+/* Numerics: bf16 operands are widened exactly; products, sums and         */
+/* activations are binary32; each output is rounded once, to nearest even. */
+/* Results depend on the inputs and the sizes only, not on timing: no      */
+/* floating-point atomics.  NaN and infinity propagate.                    */
+/* ---------------------------------------------------------------------- */
+
+typedef struct rar_linear_s *rar_linear_t;
+
+typedef enum {
+    RAR_ACT_NONE = 0,
+    RAR_ACT_RELU = 1, /* max(z, 0); derivative 0 at 0 */
+    RAR_ACT_GELU = 2  /* z * Phi(z), Phi the normal distribution function (the erf form) */
+} rar_act;
+
+/* Values of a row that share one scale in an 8-bit checkpoint. */
+#define RAR_CKPT_GROUP 32
+
+/* Embedding lookup: out[t] = scale * table[ids[t]] for t < T.  table is V x D
+ * (contiguous), ids T int64, out T x D with leading dimension ldo.  An id
+ * outside 0..V-1 (padding) gives a row of zeros.  T == 0 is a no-op. */
+rar_status rar_embed_lookup(int64_t V, int64_t D, rar_dtype dtype, const void *table, int64_t T,
+                            const int64_t *ids, float scale, void *out, int64_t ldo, void *stream);
+
+/* Workspace of rar_embed_grad. */
+rar_status rar_embed_grad_workspace(int64_t V, int64_t D, int64_t T, int64_t *bytes);
+
+/* Gradient of the lookup: grad[v] = scale * (sum of dy[t] over the t with
+ * ids[t] == v), for every v < V: rows that no token names become zero.  With
+ * accumulate != 0 the sum is added to grad instead, and rows that no token
+ * names are not touched.  dy is T x D with leading dimension lddy, grad V x D
+ * contiguous.  Ids outside 0..V-1 are skipped.  Terms are added in an order
+ * that the ids alone determine. */
+rar_status rar_embed_grad(int64_t V, int64_t D, rar_dtype dtype, int64_t T, const int64_t *ids, const void *dy,
+                          int64_t lddy, float scale, int accumulate, void *grad, void *ws, int64_t ws_bytes,
+                          void *stream);
+
+/* A linear layer of K inputs and N outputs: host memory only, immutable, any
+ * number of threads and streams. */
+rar_status rar_linear_plan(int64_t K, int64_t N, rar_dtype dtype, rar_act act, rar_linear_t *out);
+
+rar_status rar_linear_destroy(rar_linear_t plan);
+
+/* Workspaces of a forward and of a backward call on T rows.  Either output
+ * may be NULL. */
+rar_status rar_linear_workspace(rar_linear_t plan, int64_t T, int64_t *forward_bytes, int64_t *backward_bytes);
+
+/* z = x W + bias, y = act(z) + residual.  x is T x K, w K x N contiguous, bias
+ * N or NULL, residual T x N or NULL (it may be y itself), y T x N.  pre (or
+ * NULL) receives z for the backward pass: in the layer's type with leading
+ * dimension ldp, or, with pre_scales, as an 8-bit checkpoint (the one
+ * rar_ckpt_store makes of z rounded to the layer's type; ldp is ignored).  The
+ * activation is taken of the unrounded z.  T == 0 is a no-op. */
+rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const void *x, int64_t ldx, const void *w,
+                              const void *bias, const void *residual, int64_t ldr, void *y, int64_t ldy, void *pre,
+                              int64_t ldp, uint8_t *pre_scales, void *ws, int64_t ws_bytes, void *stream);
+
+/* With dz = dy * act'(z):  dx = dz W^T,  dw = x^T dz,  db = column sums of dz.
+ * dx (T x K), dw (K x N contiguous) and db (N) may each be NULL.  With
+ * accumulate != 0 dw and db are added to (dx is not).  x and w are the
+ * forward call's; x may be NULL without dw, w without dx.  pre is z as the
+ * forward call wrote it; it is ignored, and may be NULL, for RAR_ACT_NONE.
+ * With x_scales, x holds the codes of an 8-bit checkpoint of x (ldx ignored),
+ * with pre_scales pre holds those of z.  dz is rounded to the layer's type
+ * for the two products; db sums it unrounded.  The residual's gradient is dy. */
+rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                               const uint8_t *x_scales, const void *w, const void *pre, int64_t ldp,
+                               const uint8_t *pre_scales, void *dx, int64_t lddx, void *dw, void *db, int accumulate,
+                               void *ws, int64_t ws_bytes, void *stream);
+
+/* An 8-bit checkpoint of a T x D matrix: e4m3 codes, T rows of *pitch bytes (D
+ * rounded up to whole groups of RAR_CKPT_GROUP; the codes behind D are zero),
+ * and one scale byte a group, T rows of *groups bytes. */
+rar_status rar_ckpt_size(int64_t D, int64_t *pitch, int64_t *groups);
+
+/* For every group of a row: e is the smallest exponent >= -126 with max|x| <=
+ * 448 * 2^e over the group's finite values, the scale byte e + 127, and each
+ * code x / 2^e rounded to the nearest e4m3 value (ties to even).  NaN and
+ * infinities become NaN.  x is T x D with leading dimension ldx; codes must be
+ * 16-byte aligned (RAR_EALIGN). */
+rar_status rar_ckpt_store(int64_t T, int64_t D, rar_dtype dtype, const void *x, int64_t ldx, uint8_t *codes,
+                          uint8_t *scales, void *stream);
+
+/* y = act(code * 2^(scale - 127)), T x D with leading dimension ldy: the stored
+ * activation again, or the activation function of a stored z.  (A stored value
+ * may have rounded up to 2^128: it loads as infinity.) */
+rar_status rar_ckpt_load(int64_t T, int64_t D, rar_dtype dtype, const uint8_t *codes, const uint8_t *scales,
+                         rar_act act, void *y, int64_t ldy, void *stream);
+
+/* ---------------------------------------------------------------------- */
 
 /* Static description of a status code; never NULL. */
 const char *rar_strerror(rar_status s);
@@ -375,7 +484,8 @@ const char *rar_strerror(rar_status s);
 /* Library version as major*10000 + minor*100 + patch (0.2.0 = 200 adds
  * rar_rank_stride, 0.3.0 = 300 rar_rank_stride_tune, 0.4.0 = 400
  * rar_allreduce_ring_noalloc, 0.5.0 = 500 rar_rank_stride_tune_stats,
- * 0.6.0 = 600 rar_rank_stride_candidate and the wider stride search). */
+ * 0.6.0 = 600 rar_rank_stride_candidate and the wider stride search,
+ * 0.7.0 = 700 rar_embed_*, rar_linear_* and rar_ckpt_*). */
 int rar_version(void);
 
 #ifdef __cplusplus

@@ -15,6 +15,7 @@ _i64 = ctypes.c_int64
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _ip = ctypes.POINTER(ctypes.c_int)
 _int = ctypes.c_int
+_f = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/rar.h
 SIGNATURES = {
@@ -43,6 +44,19 @@ SIGNATURES = {
     "rar_bucket_unpack": (_int, [_vp, _int, _int, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp]),
     "rar_bucket_allreduce_mean": (_int, [_vp, _int, _int, _int, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp]),
     "rar_bucket_allreduce_arena": (_int, [_vp, _int, _int, _int, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp]),
+    "rar_embed_lookup": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _f, _vp, _i64, _vp]),
+    "rar_embed_grad_workspace": (_int, [_i64, _i64, _i64, _i64p]),
+    "rar_embed_grad": (_int, [_i64, _i64, _int, _i64, _vp, _vp, _i64, _f, _int, _vp, _vp, _i64, _vp]),
+    "rar_linear_plan": (_int, [_i64, _i64, _int, _int, ctypes.POINTER(_vp)]),
+    "rar_linear_destroy": (_int, [_vp]),
+    "rar_linear_workspace": (_int, [_vp, _i64, _i64p, _i64p]),
+    "rar_linear_forward": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                                  _vp]),
+    "rar_linear_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                   _int, _vp, _i64, _vp]),
+    "rar_ckpt_size": (_int, [_i64, _i64p, _i64p]),
+    "rar_ckpt_store": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _vp, _vp]),
+    "rar_ckpt_load": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _i64, _vp]),
     "rar_strerror": (ctypes.c_char_p, [_int]),
     "rar_version": (_int, []),
 }

@@ -9,6 +9,13 @@ unchecked.  ``stream`` may be a torch stream, an
 integer hipStream_t, or None for torch's current stream on the current
 device (the default stream when torch has no GPU).
 
+The operators on matrices (rar_embed_*, rar_linear_*, rar_ckpt_*) take 2-D
+tensors whose rows are contiguous; the distance between rows is the leading
+dimension.  An integer address stands for a contiguous matrix.  Their tensors
+must be on the current device.  ``ws`` is a uint8 tensor of at least the
+queried bytes, or None: then one is allocated for the call, and returned to
+torch's allocator in the order of the call's stream.
+
 Status codes other than RAR_OK raise RarError carrying the code.
 """
 from __future__ import annotations
@@ -26,6 +33,8 @@ OK, EINVAL, EMISMATCH, EALIGN, ENOMEM, EHIP, ETOOLARGE = 0, -1, -2, -3, -4, -5, 
 MAX_RANKS = 64
 MAX_STRIDE_CANDIDATES = 64
 STATIC_WS_ELEMS = 1 << 24
+ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
+CKPT_GROUP = 32
 
 
 class RarError(RuntimeError):
@@ -385,3 +394,206 @@ def rar_bucket_allreduce_arena(b: Buckets, arenas: Sequence, ready_events=None, 
             ev[i] = None if e is None else (e if isinstance(e, int) else int(e.cuda_event)) or None
     _check(lib().rar_bucket_allreduce_arena(b.handle, len(arenas), int(chunking), int(algo), _ptr_array(arenas),
                                             ev, _stream(stream)), "rar_bucket_allreduce_arena")
+
+
+# ---------------------------------------------------------------------------
+# Producers of the gradients: embedding, linear layer, 8-bit checkpoints
+# ---------------------------------------------------------------------------
+
+def _device_of(x, what: str) -> None:
+    import torch
+    if not x.is_cuda:
+        if x.numel():
+            raise ValueError(f"{what}: tensor must be on the GPU")
+    elif x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensor is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _matrix(x, what: str, tdtype, rows: int, cols: int):
+    """(address, leading dimension) of a rows x cols matrix argument."""
+    if x is None:
+        return 0, cols
+    if isinstance(x, int):
+        return x, cols
+    if not hasattr(x, "data_ptr"):
+        raise TypeError(f"{what}: not a device buffer: {type(x)!r}")
+    if x.dtype != tdtype:
+        raise ValueError(f"{what}: dtype {x.dtype}, expected {tdtype}")
+    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+        raise ValueError(f"{what}: shape {tuple(x.shape)}, expected ({rows}, {cols})")
+    if rows == 0:
+        return 0, cols
+    ld, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    if rows == 1:
+        ld = cols  # the stride of a single row says nothing
+    elif ld < cols:
+        raise ValueError(f"{what}: rows overlap (stride {ld} for {cols} columns)")
+    _device_of(x, what)
+    return x.data_ptr(), ld
+
+
+def _dense(x, what: str, tdtype, numel: int) -> int:
+    """Address of a contiguous argument of exactly numel elements."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    if not hasattr(x, "data_ptr"):
+        raise TypeError(f"{what}: not a device buffer: {type(x)!r}")
+    if x.dtype != tdtype:
+        raise ValueError(f"{what}: dtype {x.dtype}, expected {tdtype}")
+    if x.numel() != numel:
+        raise ValueError(f"{what}: {x.numel()} elements, expected {numel}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: tensor must be contiguous")
+    _device_of(x, what)
+    return x.data_ptr()
+
+
+def _workspace(ws, nbytes: int, stream):
+    """(address, bytes, owner) of the call's workspace."""
+    if ws is not None:
+        if not hasattr(ws, "element_size"):
+            raise TypeError("ws must be a tensor (its size is checked)")
+        return _dense(ws, "ws", ws.dtype, ws.numel()), ws.numel() * ws.element_size(), ws
+    if nbytes == 0:
+        return 0, 0, None
+    import torch
+    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream else stream
+        if hasattr(s, "cuda_stream") and s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+            # the allocator may hand the memory out again only once this stream has used it, and this
+            # stream may use it only once its last user on the current stream is done
+            s.wait_stream(torch.cuda.current_stream())
+            t.record_stream(s)
+    return t.data_ptr(), nbytes, t
+
+
+def rar_embed_lookup(V: int, D: int, dtype: int, table, T: int, ids, out, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[ids[t]]; rows of ids outside 0..V-1 are zero."""
+    import torch
+    td = _torch_dtype(dtype)
+    ptr, ldo = _matrix(out, "out", td, T, D)
+    _check(lib().rar_embed_lookup(V, D, dtype, _dense(table, "table", td, V * D), T,
+                                  _dense(ids, "ids", torch.int64, T), scale, ptr, ldo, _stream(stream)),
+           "rar_embed_lookup")
+
+
+def rar_embed_grad_workspace(V: int, D: int, T: int) -> int:
+    out = ctypes.c_int64()
+    _check(lib().rar_embed_grad_workspace(V, D, T, ctypes.byref(out)), "rar_embed_grad_workspace")
+    return out.value
+
+
+def rar_embed_grad(V: int, D: int, dtype: int, T: int, ids, dy, grad, scale: float = 1.0, accumulate: bool = False,
+                   ws=None, stream=None) -> None:
+    """grad[v] (+)= scale * the sum of dy[t] over the t with ids[t] == v."""
+    import torch
+    td = _torch_dtype(dtype)
+    dptr, lddy = _matrix(dy, "dy", td, T, D)
+    gptr, iptr = _dense(grad, "grad", td, V * D), _dense(ids, "ids", torch.int64, T)
+    wptr, wbytes, _own = _workspace(ws, 0 if ws is not None else rar_embed_grad_workspace(V, D, T), stream)
+    _check(lib().rar_embed_grad(V, D, dtype, T, iptr, dptr, lddy, scale, int(bool(accumulate)), gptr, wptr, wbytes,
+                                _stream(stream)), "rar_embed_grad")
+
+
+class Linear:
+    """Owner of a rar_linear_t; destroyed with the object or by rar_linear_destroy."""
+
+    def __init__(self, handle: int, K: int, N: int, dtype: int, act: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.K, self.N, self.dtype, self.act = K, N, dtype, act
+        self._bytes = {}
+
+    def __del__(self):
+        try:
+            rar_linear_destroy(self)
+        except Exception:
+            pass
+
+
+def rar_linear_plan(K: int, N: int, dtype: int = F32, act: int = ACT_NONE) -> Linear:
+    out = ctypes.c_void_p()
+    _check(lib().rar_linear_plan(int(K), int(N), int(dtype), int(act), ctypes.byref(out)), "rar_linear_plan")
+    return Linear(out.value, int(K), int(N), int(dtype), int(act))
+
+
+def rar_linear_destroy(plan: Linear) -> None:
+    if plan.handle:
+        h, plan.handle = plan.handle, ctypes.c_void_p()
+        _check(lib().rar_linear_destroy(h), "rar_linear_destroy")
+
+
+def rar_linear_workspace(plan: Linear, T: int):
+    """(forward bytes, backward bytes) for T rows."""
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().rar_linear_workspace(plan.handle, int(T), ctypes.byref(f), ctypes.byref(b)), "rar_linear_workspace")
+    return f.value, b.value
+
+
+def _kept(x, scales, what: str, td, T: int, cols: int):
+    """(address, leading dimension, scales' address) of a matrix or its 8-bit checkpoint."""
+    if scales is None:
+        return (*_matrix(x, what, td, T, cols), 0)
+    import torch
+    groups = -(-cols // CKPT_GROUP)
+    return (_dense(x, what, torch.uint8, T * groups * CKPT_GROUP), cols,
+            _dense(scales, f"{what}_scales", torch.uint8, T * groups))
+
+
+def rar_linear_forward(plan: Linear, T: int, x, w, bias, residual, y, pre=None, pre_scales=None, ws=None,
+                       stream=None) -> None:
+    """z = x w + bias, y = act(z) + residual; bias and residual may be None.
+    pre receives z, as an 8-bit checkpoint when pre_scales is given."""
+    td, K, N = _torch_dtype(plan.dtype), plan.K, plan.N
+    xp, ldx = _matrix(x, "x", td, T, K)
+    wp, bp = _dense(w, "w", td, K * N), _dense(bias, "bias", td, N)
+    rp, ldr = _matrix(residual, "residual", td, T, N)
+    yp, ldy = _matrix(y, "y", td, T, N)
+    pp, ldp, sp = _kept(pre, pre_scales, "pre", td, T, N)
+    wsp, wsb, _own = _workspace(ws, 0 if ws is not None else rar_linear_workspace(plan, T)[0], stream)
+    _check(lib().rar_linear_forward(plan.handle, T, xp, ldx, wp, bp, rp, ldr, yp, ldy, pp, ldp, sp, wsp, wsb,
+                                    _stream(stream)), "rar_linear_forward")
+
+
+def rar_linear_backward(plan: Linear, T: int, dy, x, w, pre, dx, dw, db, x_scales=None, pre_scales=None,
+                        accumulate: bool = False, ws=None, stream=None) -> None:
+    """dz = dy act'(z); dx = dz w^T, dw (+)= x^T dz, db (+)= column sums of dz.
+    dx, dw and db may each be None; x and pre may be 8-bit checkpoints."""
+    td, K, N = _torch_dtype(plan.dtype), plan.K, plan.N
+    dyp, lddy = _matrix(dy, "dy", td, T, N)
+    xp, ldx, xs = _kept(x, x_scales, "x", td, T, K)
+    wp = _dense(w, "w", td, K * N)
+    pp, ldp, ps = _kept(pre, pre_scales, "pre", td, T, N) if plan.act != ACT_NONE else (0, N, 0)
+    dxp, lddx = _matrix(dx, "dx", td, T, K)
+    dwp, dbp = _dense(dw, "dw", td, K * N), _dense(db, "db", td, N)
+    wsp, wsb, _own = _workspace(ws, 0 if ws is not None else rar_linear_workspace(plan, T)[1], stream)
+    _check(lib().rar_linear_backward(plan.handle, T, dyp, lddy, xp, ldx, xs, wp, pp, ldp, ps, dxp, lddx, dwp, dbp,
+                                     int(bool(accumulate)), wsp, wsb, _stream(stream)), "rar_linear_backward")
+
+
+def rar_ckpt_size(D: int):
+    """(bytes of a row of codes, bytes of a row of scales) of an 8-bit checkpoint of D columns."""
+    p, g = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().rar_ckpt_size(int(D), ctypes.byref(p), ctypes.byref(g)), "rar_ckpt_size")
+    return p.value, g.value
+
+
+def rar_ckpt_store(T: int, D: int, dtype: int, x, codes, scales, stream=None) -> None:
+    """codes (T x pitch) and scales (T x groups), both uint8, receive the 8-bit checkpoint of x (T x D)."""
+    xp, ldx, cp, sp = *_matrix(x, "x", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
+    _check(lib().rar_ckpt_store(T, D, dtype, xp, ldx, cp, sp, _stream(stream)), "rar_ckpt_store")
+
+
+def rar_ckpt_load(T: int, D: int, dtype: int, codes, scales, y, act: int = ACT_NONE, stream=None) -> None:
+    """y (T x D) = act(what the checkpoint holds)."""
+    yp, ldy, cp, sp = *_matrix(y, "y", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
+    _check(lib().rar_ckpt_load(T, D, dtype, cp, sp, act, yp, ldy, _stream(stream)), "rar_ckpt_load")
+
+
+def _ckpt(codes, scales, T: int, D: int):
+    import torch
+    groups = -(-D // CKPT_GROUP)
+    return (_dense(codes, "codes", torch.uint8, T * groups * CKPT_GROUP),
+            _dense(scales, "scales", torch.uint8, T * groups))

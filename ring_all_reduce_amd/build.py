@@ -20,7 +20,8 @@ PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "librar.so"
-SOURCES = [CSRC / "rar_host.cpp", CSRC / "rar_kernels.hip"]
+SOURCES = [CSRC / "rar_host.cpp", CSRC / "rar_kernels.hip",
+           CSRC / "ops_host.cpp", CSRC / "linear.hip", CSRC / "embed.hip", CSRC / "ckpt.hip"]
 # reference stream kernels for the benchmark's ceiling rows (not the path)
 REF_LIB = PKG / "libstream_ref.so"
 REF_SOURCES = [CSRC / "stream_ref.hip"]

@@ -1,0 +1,726 @@
+// linear.hip -- CDNA4 (gfx950) kernels of the linear layer: the matrix products
+// of its forward and backward pass on the matrix cores, with the layer's
+// epilogues, and the streaming passes around them.
+//
+//   forward   z = x W + b, y = act(z) + r       A = x  (k contiguous), B = W  (k slow)
+//   grad x    dx = dz W^T                       A = dz (k contiguous), B = W  (k contiguous)
+//   grad W    dW = x^T dz                       A = x  (k slow),       B = dz (k slow)
+//
+// Every product is D[m][n] = sum_k A(m,k) B(n,k).  The matrix instruction's first
+// operand takes B and the second A, so a lane ends with four consecutive n of
+// one row m and stores them together.
+#include "act.h"
+#include "ops_internal.h"
+
+#pragma clang fp contract(off)
+
+#define RAR_LDS __attribute__((address_space(3)))
+
+namespace rar {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kGemmThreads = 256;
+constexpr int kRowBytes = 128;             // bytes of reduction per step of a contiguous operand
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// ---------------------------------------------------------------------------
+// Staging: memory -> LDS, 16 bytes a lane, without passing through registers
+// ---------------------------------------------------------------------------
+//
+// One step stages kRowBytes / ES reduction indices of R rows of an operand.
+//   contiguous: LDS row r holds its 128 bytes of k; the 16-byte chunk c lies at
+//               slot c ^ (r & 7), so 16 lanes that read one chunk of 16 rows
+//               touch every bank once.
+//   slow:       LDS row k holds R elements; bf16 units of 16 elements are
+//               permuted by f(k), binary32 by one bit of k, so that the four
+//               k rows of a transposing read (or the two of a binary32 read)
+//               lie in different banks.
+// The destination of such a load is linear in the lane, so the permutation is
+// applied to the address that each lane reads.
+//
+// The buffer descriptor's range ends with the operand's last element: rows
+// behind it read as zero, whatever lies there.  Where a contiguous operand's
+// reduction ends inside a step, the chunks behind the end are sent out of
+// range too, since what follows them is the next row.  The descriptor moves
+// along the reduction in 64 bits; offsets inside a tile stay under 2^31.
+template <int ES>
+__device__ __forceinline__ int slow_perm(int k)
+{
+    return ES == 2 ? ((k & 3) | (((k >> 3) & 3) << 2)) : ((k >> 2) & 1);
+}
+
+template <int ES, int R, bool CONTIG>
+struct Stage {
+    static constexpr int kLoads = R * kRowBytes / (kGemmThreads * 16);
+    static constexpr int kStep = kRowBytes / ES;  // reduction indices of one step
+    uint32_t voff[kLoads];
+    const char *base;
+    int64_t left;     // bytes from base to the end of the operand
+    int64_t advance;  // bytes per step
+
+    // Row lengths in whole 16-byte groups: the range is checked by the dword,
+    // and the host packs rows that end inside one with zeros.
+    static __device__ __forceinline__ int64_t whole(int64_t n) { return (n + 16 / ES - 1) / (16 / ES) * (16 / ES); }
+
+    // rows [r0, ...) of `rows`, reduction indices [k0, ...) of `kred`
+    __device__ __forceinline__ void init(const void *p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t kred)
+    {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        if (CONTIG) {
+            base = (const char *)p + (r0 * ld + k0) * ES;
+            left = ((rows - 1 - r0) * ld + whole(kred - k0)) * ES;
+            advance = kRowBytes;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int r = (j * 4 + wave) * 8 + (lane >> 3);
+                voff[j] = (uint32_t)(r * ld * ES) + (((lane & 7) ^ (r & 7)) << 4);
+            }
+        } else {
+            constexpr int RB = R * ES;
+            base = (const char *)p + (k0 * ld + r0) * ES;
+            left = ((kred - 1 - k0) * ld + whole(rows - r0)) * ES;
+            advance = kStep * ld * ES;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int at = (j * 4 + wave) * 1024 + lane * 16;
+                const int k = at / RB, slot = (at % RB) / 16;
+                int src;
+                if (ES == 2)
+                    src = (((slot >> 1) ^ (slow_perm<2>(k) & (R / 16 - 1))) << 1) | (slot & 1);
+                else
+                    src = slot ^ (slow_perm<4>(k) << 3);
+                voff[j] = (uint32_t)(k * ld * ES) + src * 16;
+            }
+        }
+    }
+
+    // chunks of a contiguous operand behind the last `kleft` reduction indices
+    __device__ __forceinline__ void cut(int64_t kleft)
+    {
+        if (!CONTIG)
+            return;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int r = (j * 4 + wave) * 8 + (lane >> 3);
+            const int chunk = (lane & 7) ^ (r & 7);
+            if (chunk * (16 / ES) >= kleft)
+                voff[j] = kOutOfRange;
+        }
+    }
+
+    __device__ __forceinline__ void load(RAR_LDS char *__restrict__ lds)
+    {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int64_t n = left < 0 ? 0 : (left > 0x7fffffff ? 0x7fffffff : left);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * 4 + wave) * 1024), 16, voff[j], 0,
+                                                     0, 0);
+        base += advance;
+        left -= advance;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Fragments
+// ---------------------------------------------------------------------------
+
+// bf16, v_mfma_f32_16x16x32: lane l holds row l % 16 and the eight reduction
+// indices (l / 16) * 8 .. +7 of a step's half `sub`.  A slow operand is read
+// with the transposing LDS read: each 16 lanes read four k rows of 16 columns
+// and receive their own column's four values.
+template <int R, bool CONTIG, int NF>
+struct Frag16 {
+    uint32_t off[CONTIG ? 1 : NF];
+
+    __device__ __forceinline__ void init(int w0)
+    {
+        const int lane = threadIdx.x & 63;
+        if (CONTIG) {
+            off[0] = (w0 + (lane & 15)) * kRowBytes + (((lane >> 4) ^ (lane & 7)) << 4);
+        } else {
+            const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
+            const int f = slow_perm<2>(k) & (R / 16 - 1);
+#pragma unroll
+            for (int i = 0; i < (CONTIG ? 1 : NF); ++i)
+                off[i] = k * (R * 2) + (((w0 / 16 + i) ^ f) << 5) + (lane & 3) * 8;
+        }
+    }
+
+    __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int sub, int i) const
+    {
+        if (CONTIG)
+            return *(const RAR_LDS bf16x8 *)(lds + (off[0] ^ (sub << 6)) + i * 16 * kRowBytes);
+        const RAR_LDS char *p = lds + off[CONTIG ? 0 : i] + sub * 32 * (R * 2);
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)p);
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)(p + 4 * (R * 2)));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// binary32, v_mfma_f32_32x32x2: lane l holds row l % 32; in a group of eight
+// reduction indices the lower half-wave holds the first four, one per
+// instruction.
+template <int R, bool CONTIG>
+struct Frag32 {
+    uint32_t off;
+
+    __device__ __forceinline__ void init(int w0)
+    {
+        const int lane = threadIdx.x & 63;
+        const int row = w0 + (lane & 31), half = lane >> 5;
+        if (CONTIG)
+            off = row * kRowBytes + ((half ^ (row & 7)) << 4);
+        else
+            off = half * 4 * (R * 4) + ((row * 4) ^ (half << 7));
+    }
+
+    __device__ __forceinline__ f32x4 read(const RAR_LDS char *__restrict__ lds, int c, int i) const
+    {
+        if (CONTIG)
+            return *(const RAR_LDS f32x4 *)(lds + (off ^ (c << 5)) + i * 32 * kRowBytes);
+        // 32 columns are 128 bytes: an odd block of them flips the permuted bit
+        const RAR_LDS char *p = lds + (off ^ (i << 7)) + c * 8 * (R * 4);
+        return f32x4{*(const RAR_LDS float *)p, *(const RAR_LDS float *)(p + R * 4),
+                     *(const RAR_LDS float *)(p + 2 * R * 4), *(const RAR_LDS float *)(p + 3 * R * 4)};
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Epilogue: eight consecutive n of row m
+// ---------------------------------------------------------------------------
+
+// A group of 32 consecutive n lies in four neighbouring lanes.  Every lane of
+// the wave calls this; rows and columns outside the matrix take part in the
+// group's exchange only.
+template <class T>
+__device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t n, float (&v)[8])
+{
+    const bool vec = p.vec;
+    const int cnt = m >= p.M || n >= p.N ? 0 : (p.N - n < 8 ? (int)(p.N - n) : 8);
+    T *const out = (T *)p.out + m * p.ldo + n;
+    float t[8];
+    if (p.mode == kModeForward) {
+        if (p.bias) {
+            load8((const T *)p.bias + n, cnt, vec, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += t[i];
+        }
+        if (p.pre_scales) {
+            // the checkpoint of z, as rar_ckpt_store makes it of z in the layer's type
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                t[i] = i < cnt ? to_f32(from_f32<T>(v[i])) : 0.0f;
+                top = ckpt_top(top, t[i]);
+            }
+            top = max(top, (uint32_t)__shfl_xor(top, 1));
+            top = max(top, (uint32_t)__shfl_xor(top, 2));
+            const int e = ckpt_exponent(top);
+            const int64_t groups = (p.N + kCkptGroup - 1) / kCkptGroup;
+            const int64_t g = n / kCkptGroup;
+            if (m < p.M && g < groups) {
+                *reinterpret_cast<u32x2 *>((uint8_t *)p.pre + m * groups * kCkptGroup + n) =
+                    u32x2{ckpt_codes4(f32x4{t[0], t[1], t[2], t[3]}, e), ckpt_codes4(f32x4{t[4], t[5], t[6], t[7]}, e)};
+                if (n % kCkptGroup == 0)
+                    p.pre_scales[m * groups + g] = (uint8_t)e;
+            }
+        } else if (p.pre) {
+            store8((T *)p.pre + m * p.ldp + n, cnt, vec, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = act_value(p.act, v[i]);
+        if (p.res) {
+            load8((const T *)p.res + m * p.ldr + n, cnt, vec, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += t[i];
+        }
+    } else if (p.accumulate) {
+        load8(out, cnt, vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += t[i];
+    }
+    store8(out, cnt, vec, v);
+}
+
+// A wave's 32 rows of W columns pass through LDS, so that a lane finishes eight
+// consecutive columns of one row and a row's lanes access whole lines.  The
+// 16-byte chunk c of row r lies at slot c ^ (r & 15): a column of rows spreads
+// over the banks.
+template <int W>
+__device__ __forceinline__ RAR_LDS f32x4 *tile_slot(RAR_LDS char *tile, int r, int c)
+{
+    return (RAR_LDS f32x4 *)(tile + r * (W * 4) + ((c ^ (r & 15)) << 4));
+}
+
+template <class T, int W>
+__device__ __forceinline__ void finish_rows(const GemmParams &p, int split, RAR_LDS char *tile, int64_t m0, int64_t n0)
+{
+    constexpr int kLanes = W / 8, kRows = 64 / kLanes;
+    const int lane = threadIdx.x & 63, q = lane % kLanes;
+    const int64_t n = n0 + q * 8;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+    for (int r = lane / kLanes; r < 32; r += kRows) {
+        const f32x4 lo = *tile_slot<W>(tile, r, 2 * q), hi = *tile_slot<W>(tile, r, 2 * q + 1);
+        const int64_t m = m0 + r;
+        if (p.mode == kModePartial) {
+            if (m < p.M && n < p.pitch) {  // pitch is whole groups; columns behind N hold anything
+                float *o = p.part + ((int64_t)split * p.M + m) * p.pitch + n;
+                store4(o, lo);
+                store4(o + 4, hi);
+            }
+            continue;
+        }
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        epilogue<T>(p, m, n, v);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+// Workgroups go to the eight XCDs in turn; each XCD gets one run of tiles, in
+// bands of four tile rows, so that its L2 holds the operands they share.
+__device__ __forceinline__ void tile_of(const GemmParams &p, int64_t &tm, int64_t &tn, int &split)
+{
+    const int64_t tiles = p.tiles_m * p.tiles_n, total = tiles * p.splits;
+    int64_t id = blockIdx.x;
+    const int64_t per = total / 8;
+    if (id < per * 8)
+        id = (id % 8) * per + id / 8;
+    split = (int)(id / tiles);
+    id -= split * tiles;
+    const int64_t band = 4 * p.tiles_n;
+    const int64_t first = id / band * 4;
+    const int64_t rows = p.tiles_m - first < 4 ? p.tiles_m - first : 4;
+    const int64_t in = id % band;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+__device__ __forceinline__ void wait_loads_and_meet()
+{
+    // own loads into LDS have arrived and own LDS reads are done; then everyone's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Rows I0 .. I1 - 1 of a wave's fragments, one step of 32 reduction indices.
+template <int FM, int FN, int I0, int I1>
+__device__ __forceinline__ void products(f32x4 (&acc)[FM][FN], const bf16x8 (&a)[FM], const bf16x8 (&b)[FN])
+{
+#pragma unroll
+    for (int i = I0; i < I1; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// bf16 product
+// ---------------------------------------------------------------------------
+//
+// Four waves as 2 x 2 hold a BM x BN tile in accumulators; a step of 64
+// reduction indices is staged in one half of LDS while the other is used.  A
+// step's two halves of 32 are read into registers one half ahead of the matrix
+// instructions that use them, so the only wait is for a step's loads, issued a
+// whole step before:
+//     read F1 (second half of the step)   | products of F0
+//     first products of F1; wait; barrier
+//     read F0 of the next step, stage the step after it | other products of F1
+template <int BM, int BN, bool ACONTIG, bool BCONTIG>
+__global__ void __launch_bounds__(kGemmThreads, BM * BN >= 65536 ? 1 : 2) rar_gemm_bf16(const GemmParams p)
+{
+// (the host pass needs the kernel's name only)
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int FM = BM / 32, FN = BN / 32;  // 16-row fragments of a wave
+    constexpr int kHalf = (BM + BN) * kRowBytes;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kHalf];
+    RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
+
+    int64_t tm, tn;
+    int split;
+    tile_of(p, tm, tn, split);
+    const int64_t m0 = tm * BM, n0 = tn * BN;
+    const int64_t k0 = split * p.steps_per_split * 64;
+    const int64_t kend = k0 + p.steps_per_split * 64 < p.K ? k0 + p.steps_per_split * 64 : p.K;
+    const int steps = k0 < kend ? (int)((kend - k0 + 63) / 64) : 0;
+    const int wave = threadIdx.x >> 6, wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+
+    Stage<2, BM, ACONTIG> sa;
+    Stage<2, BN, BCONTIG> sb;
+    sa.init(p.a, p.lda, m0, p.M, k0, kend);
+    sb.init(p.b, p.ldb, n0, p.N, k0, kend);
+    Frag16<BM, ACONTIG, FM> fa;
+    Frag16<BN, BCONTIG, FN> fb;
+    fa.init(wm);
+    fb.init(wn);
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto stage = [&](int s) __attribute__((always_inline)) {
+        if (s < steps) {
+            if (s == steps - 1) {
+                sa.cut(kend - k0 - (int64_t)s * 64);
+                sb.cut(kend - k0 - (int64_t)s * 64);
+            }
+            RAR_LDS char *to = lds + (s & 1) * kHalf;
+            sa.load(to);
+            sb.load(to + BM * kRowBytes);
+        }
+    };
+    bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
+    auto read = [&](int s, int sub, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) __attribute__((always_inline)) {
+        const RAR_LDS char *from = lds + (s & 1) * kHalf;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            b[j] = fb.read(from + BM * kRowBytes, sub, j);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            a[i] = fa.read(from, sub, i);
+    };
+    if (steps > 0) {
+        stage(0);
+        wait_loads_and_meet();
+        read(0, 0, a0, b0);
+        stage(1);
+    }
+    for (int s = 0; s < steps; ++s) {
+        read(s, 1, a1, b1);
+        products<FM, FN, 0, FM>(acc, a0, b0);
+        __builtin_amdgcn_sched_barrier(0);
+        products<FM, FN, 0, FM / 2>(acc, a1, b1);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads_and_meet();
+        read(s + 1, 0, a0, b0);  // behind the last step: unused
+        stage(s + 2);
+        products<FM, FN, FM / 2, FM>(acc, a1, b1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // every wave has read its last fragments: LDS is free for the results
+    wait_loads_and_meet();
+    const int lane = threadIdx.x & 63;
+    RAR_LDS char *const tile = lds + wave * (32 * FN * 16 * 4);
+#pragma unroll
+    for (int i = 0; i < FM; i += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                *tile_slot<FN * 16>(tile, h * 16 + (lane & 15), j * 4 + (lane >> 4)) = acc[i + h][j];
+        finish_rows<bf16, FN * 16>(p, split, tile, m0 + wm + i * 16, n0 + wn);
+    }
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// binary32 product
+// ---------------------------------------------------------------------------
+//
+// The binary32 matrix instruction does a sixteenth of the bf16 one's work per
+// cycle, so a 128 x 128 tile with plain double buffering keeps the matrix cores
+// fed: per instruction (64 cycles) a wave reads a quarter of a kilobyte of LDS.
+template <bool ACONTIG, bool BCONTIG>
+__global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = 128, BN = 128, kStep = 32;
+    constexpr int kHalf = (BM + BN) * kRowBytes;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kHalf];
+    RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
+
+    int64_t tm, tn;
+    int split;
+    tile_of(p, tm, tn, split);
+    const int64_t m0 = tm * BM, n0 = tn * BN;
+    const int64_t k0 = split * p.steps_per_split * kStep;
+    const int64_t kend = k0 + p.steps_per_split * kStep < p.K ? k0 + p.steps_per_split * kStep : p.K;
+    const int steps = k0 < kend ? (int)((kend - k0 + kStep - 1) / kStep) : 0;
+    const int wave = threadIdx.x >> 6, wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+
+    Stage<4, BM, ACONTIG> sa;
+    Stage<4, BN, BCONTIG> sb;
+    sa.init(p.a, p.lda, m0, p.M, k0, kend);
+    sb.init(p.b, p.ldb, n0, p.N, k0, kend);
+    Frag32<BM, ACONTIG> fa;
+    Frag32<BN, BCONTIG> fb;
+    fa.init(wm);
+    fb.init(wn);
+
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[i][j][e] = 0.0f;
+
+    auto stage = [&](int s) __attribute__((always_inline)) {
+        if (s < steps) {
+            if (s == steps - 1) {
+                sa.cut(kend - k0 - (int64_t)s * kStep);
+                sb.cut(kend - k0 - (int64_t)s * kStep);
+            }
+            RAR_LDS char *to = lds + (s & 1) * kHalf;
+            sa.load(to);
+            sb.load(to + BM * kRowBytes);
+        }
+    };
+
+    stage(0);
+    for (int s = 0; s < steps; ++s) {
+        wait_loads_and_meet();
+        stage(s + 1);
+        const RAR_LDS char *from = lds + (s & 1) * kHalf;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            f32x4 a[2], b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[i] = fa.read(from, c, i);
+                b[i] = fb.read(from + BM * kRowBytes, c, i);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j][e], a[i][e], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    wait_loads_and_meet();
+    const int lane = threadIdx.x & 63;
+    RAR_LDS char *const tile = lds + wave * (32 * 64 * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *tile_slot<64>(tile, lane & 31, j * 8 + q * 2 + (lane >> 5)) =
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        finish_rows<float, 64>(p, split, tile, m0 + wm + i * 32, n0 + wn);
+    }
+#endif
+}
+
+// Partial products of a split reduction, joined in the order of the splits:
+// the result does not depend on which workgroup finished first.
+template <class T>
+__global__ void __launch_bounds__(256) rar_gemm_join(const GemmParams p)
+{
+    const int64_t per_row = p.pitch / 8;  // pitch is whole groups, so a group's four lanes are neighbours
+    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = g / per_row, n = (g - m * per_row) * 8;
+    float v[8] = {};
+    if (m < p.M && n < p.N) {
+        const float *at = p.part + m * p.pitch + n;
+        for (int s = 0; s < p.splits; ++s, at += p.M * p.pitch) {
+            const f32x4 lo = load4(at), hi = load4(at + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] += lo[i];
+                v[4 + i] += hi[i];
+            }
+        }
+    }
+    epilogue<T>(p, m, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// Streaming passes
+// ---------------------------------------------------------------------------
+
+template <class T>
+__device__ __forceinline__ f32x4 get4(const T *p, int cnt, bool vec)
+{
+    if (vec && cnt == 4)
+        return load4(p);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < cnt)
+            v[i] = to_f32(p[i]);
+    return v;
+}
+
+// A copy with whole 16-byte rows for operands whose rows are not: the products
+// read 16 bytes at a time.  Bound by HBM bandwidth; the copy is small against
+// the product that reads it.
+template <class T>
+__global__ void __launch_bounds__(256) rar_pack_rows(const PackParams p)
+{
+    const int64_t row = blockIdx.x;
+    const T *src = (const T *)p.src + row * p.ld;
+    T *dst = (T *)p.dst + row * p.pitch;
+    for (int64_t c = (int64_t)blockIdx.y * 1024 + threadIdx.x * 4; c < p.pitch; c += (int64_t)gridDim.y * 1024) {
+        const int cnt = p.cols - c < 4 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 4;
+        store4(dst + c, get4(src + c, cnt, false));
+    }
+}
+
+// dz = dy * act'(z) and the column sums of dz in one pass over dy and z.  A
+// workgroup takes 256 columns (a lane four, a wave one row at a time) of
+// rows_per_chunk rows; its sums go to part[chunk], joined in chunk order by
+// rar_column_sum.  Sums are of the binary32 dz; the dz that the matrix
+// products read is rounded to the layer's type.
+template <class T>
+__global__ void __launch_bounds__(256) rar_dz(const DzParams p)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_chunk;
+    const int64_t r1 = r0 + p.rows_per_chunk < p.rows ? r0 + p.rows_per_chunk : p.rows;
+    const int cnt = p.cols - c < 4 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 4;
+    const bool vdy = ((uintptr_t)p.dy % (4 * sizeof(T)) == 0) && p.ldy % 4 == 0;
+    const bool vpre = ((uintptr_t)p.pre % (4 * sizeof(T)) == 0) && p.ldp % 4 == 0;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < p.cols || (p.dz && c < p.pitch)) {
+        for (int64_t r = r0 + wave; r < r1; r += 4) {
+            f32x4 d = get4((const T *)p.dy + r * p.ldy + c, cnt, vdy);
+            if (p.act != RAR_ACT_NONE && cnt > 0) {
+                f32x4 z;
+                if (p.pre_scales) {
+                    const int64_t groups = (p.cols + kCkptGroup - 1) / kCkptGroup;
+                    const uint32_t w = *(const uint32_t *)((const uint8_t *)p.pre + r * groups * kCkptGroup + c);
+                    z = ckpt_values4(w, p.pre_scales[r * groups + c / kCkptGroup]);
+                } else {
+                    z = get4((const T *)p.pre + r * p.ldp + c, cnt, vpre);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    d[i] = i < cnt ? d[i] * act_grad(p.act, z[i]) : 0.0f;
+            }
+            sum += d;
+            if (p.dz)
+                store4((T *)p.dz + r * p.pitch + c, d);
+        }
+    }
+    if (!p.part)
+        return;
+    __shared__ f32x4 sums[4][64];
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave == 0) {
+        const f32x4 t = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < cnt)
+                p.part[blockIdx.y * p.cols + c + i] = t[i];
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) rar_column_sum(const SumParams p)
+{
+    // 64 columns a workgroup; each wave sums every fourth chunk
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (c < p.cols)
+        for (int64_t k = wave; k < p.chunks; k += 4)
+            s += p.part[k * p.cols + c];
+    __shared__ float sums[4][64];
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < p.cols) {
+        float t = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+        T *out = (T *)p.out + c;
+        if (p.accumulate)
+            t += to_f32(*out);
+        *out = from_f32<T>(t);
+    }
+}
+
+template <int BM, int BN>
+hipError_t run_bf16(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_t st)
+{
+    if (l == kGemmForward)
+        rar_gemm_bf16<BM, BN, true, false><<<grid, kGemmThreads, 0, st>>>(p);
+    else if (l == kGemmGradX)
+        rar_gemm_bf16<BM, BN, true, true><<<grid, kGemmThreads, 0, st>>>(p);
+    else
+        rar_gemm_bf16<BM, BN, false, false><<<grid, kGemmThreads, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+
+hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big, hipStream_t st)
+{
+    const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * p.splits);
+    if (dt == RAR_BF16)
+        return big ? run_bf16<256, 256>(l, p, grid, st) : run_bf16<128, 128>(l, p, grid, st);
+    if (l == kGemmForward)
+        rar_gemm_f32<true, false><<<grid, kGemmThreads, 0, st>>>(p);
+    else if (l == kGemmGradX)
+        rar_gemm_f32<true, true><<<grid, kGemmThreads, 0, st>>>(p);
+    else
+        rar_gemm_f32<false, false><<<grid, kGemmThreads, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st)
+{
+    const int64_t groups = p.M * (p.pitch / 8);
+    const unsigned grid = (unsigned)((groups + 255) / 256);
+    if (dt == RAR_BF16)
+        rar_gemm_join<bf16><<<grid, 256, 0, st>>>(p);
+    else
+        rar_gemm_join<float><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st)
+{
+    const dim3 grid((unsigned)p.rows, (unsigned)((p.pitch + 1023) / 1024 < 64 ? (p.pitch + 1023) / 1024 : 64));
+    if (dt == RAR_BF16)
+        rar_pack_rows<bf16><<<grid, 256, 0, st>>>(p);
+    else
+        rar_pack_rows<float><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st)
+{
+    const int64_t width = p.dz && p.pitch > p.cols ? p.pitch : p.cols;
+    const dim3 grid((unsigned)((width + 255) / 256), (unsigned)((p.rows + p.rows_per_chunk - 1) / p.rows_per_chunk));
+    if (dt == RAR_BF16)
+        rar_dz<bf16><<<grid, 256, 0, st>>>(p);
+    else
+        rar_dz<float><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_sum(rar_dtype dt, const SumParams &p, hipStream_t st)
+{
+    const unsigned grid = (unsigned)((p.cols + 63) / 64);
+    if (dt == RAR_BF16)
+        rar_column_sum<bf16><<<grid, 256, 0, st>>>(p);
+    else
+        rar_column_sum<float><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace rar

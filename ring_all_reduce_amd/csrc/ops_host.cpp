@@ -1,0 +1,579 @@
+// ops_host.cpp -- host side of the gradient-producing operators of librar.so:
+// argument checks, workspace layout and the launch sequence of each call.  No
+// device work is enqueued before every argument has been checked, and nothing
+// is allocated on the device.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+#include <new>
+
+#include "ops_internal.h"
+
+using rar::GemmParams;
+
+struct rar_linear_s {
+    int64_t K = 0;
+    int64_t N = 0;
+    rar_dtype dtype = RAR_F32;
+    rar_act act = RAR_ACT_NONE;
+};
+
+namespace {
+
+constexpr int64_t kMaxWidth = int64_t(1) << 20;   // K, N, D
+constexpr int64_t kMaxLd = int64_t(1) << 22;      // offsets inside a 256-row tile stay under 2^31 bytes
+constexpr int64_t kMaxRows = int64_t(1) << 24;    // T
+constexpr int64_t kMaxVocab = int64_t(1) << 30;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+
+int esize(rar_dtype d) { return d == RAR_BF16 ? 2 : 4; }
+bool valid_dtype(int d) { return d == RAR_F32 || d == RAR_BF16; }
+bool valid_act(int a) { return a == RAR_ACT_NONE || a == RAR_ACT_RELU || a == RAR_ACT_GELU; }
+bool valid_rows(int64_t T) { return T >= 0 && T <= kMaxRows; }
+bool valid_width(int64_t n) { return n >= 1 && n <= kMaxWidth; }
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t div_up(int64_t v, int64_t by) { return (v + by - 1) / by; }
+
+rar_status launched(hipError_t e)
+{
+    if (e == hipSuccess)
+        return RAR_OK;
+    (void)hipGetLastError();  // the caller's next HIP call must not report it again
+    return RAR_EHIP;
+}
+
+// A matrix argument: rows x cols elements of es bytes, ld elements apart.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+    int es;
+    uintptr_t lo() const { return (uintptr_t)p; }
+    uintptr_t hi() const { return lo() + (uintptr_t)(((rows - 1) * ld + cols) * es); }
+    bool empty() const { return !p || rows <= 0 || cols <= 0; }
+};
+
+// Whether two matrices share memory.  Views of one leading dimension may lie
+// side by side: then only their columns count.
+bool overlap(const Mat &a, const Mat &b)
+{
+    if (a.empty() || b.empty() || a.lo() >= b.hi() || b.lo() >= a.hi())
+        return false;
+    const int64_t pa = a.ld * a.es, pb = b.ld * b.es;
+    if (pa == pb) {
+        const int64_t d = (int64_t)((b.lo() >= a.lo() ? b.lo() - a.lo() : a.lo() - b.lo()) % (uint64_t)pa);
+        const int64_t first = (b.lo() >= a.lo() ? a.cols * a.es : b.cols * b.es);
+        const int64_t second = (b.lo() >= a.lo() ? b.cols * b.es : a.cols * a.es);
+        return !(d >= first && pa - d >= second);
+    }
+    return true;
+}
+
+// Outputs must be apart from each other and from the inputs.
+bool apart(std::initializer_list<Mat> outs, std::initializer_list<Mat> ins)
+{
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (auto q = o + 1; q != outs.end(); ++q)
+            if (overlap(*o, *q))
+                return false;
+        for (const Mat &i : ins)
+            if (overlap(*o, i))
+                return false;
+    }
+    return true;
+}
+
+bool aligned(const void *p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }
+
+bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
+
+// Rows that the products may read 16 bytes at a time.
+bool direct(const Mat &m) { return aligned(m.p, 16) && (m.ld * m.es) % 16 == 0 && (m.cols * m.es) % 16 == 0; }
+
+// ---------------------------------------------------------------------------
+// Shape of a product
+// ---------------------------------------------------------------------------
+
+struct Shape {
+    bool big;
+    int64_t tiles_m, tiles_n, splits, steps;
+    int64_t pitch;
+    int64_t part_bytes;
+};
+
+Shape shape_of(rar_dtype dt, int64_t M, int64_t N, int64_t K)
+{
+    Shape s{};
+    const int64_t total = div_up(K * esize(dt), 128);
+    const int64_t big_tiles = div_up(M, 256) * div_up(N, 256);
+    s.big = dt == RAR_BF16 && big_tiles >= 192;
+    const int64_t tile = s.big ? 256 : 128;
+    s.tiles_m = div_up(M, tile);
+    s.tiles_n = div_up(N, tile);
+    s.splits = 1;
+    s.steps = total;
+    if (!s.big) {
+        const int64_t want = 512 / std::max<int64_t>(1, s.tiles_m * s.tiles_n);
+        const int64_t splits = std::min<int64_t>(want, total / 4);
+        if (splits > 1) {
+            s.steps = div_up(total, splits);
+            s.splits = div_up(total, s.steps);
+        }
+    }
+    s.pitch = up(N, rar::kCkptGroup);
+    s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
+    return s;
+}
+
+// Bytes of the workspace's parts, each a multiple of 256.
+struct Carve {
+    char *at;
+    int64_t used = 0;
+    void *take(int64_t bytes)
+    {
+        void *p = at ? at + used : nullptr;
+        used += up(bytes, 256);
+        return p;
+    }
+};
+
+int64_t packed(int64_t cols, rar_dtype dt) { return up(cols, 16 / esize(dt)); }
+
+struct Layer {
+    int64_t T, K, N;
+    rar_dtype dt;
+};
+
+// Chunks of rows whose column sums are kept apart: about 2048 workgroups of 256
+// columns, at least 16 rows each.
+int64_t sum_rows(int64_t T, int64_t N)
+{
+    const int64_t chunks = std::max<int64_t>(1, std::min(div_up(T, 16), 2048 / div_up(N, 256)));
+    return std::max<int64_t>(1, div_up(T, chunks));
+}
+
+struct ForwardWs {
+    void *x, *w;
+    float *part;
+    int64_t bytes;
+};
+
+ForwardWs forward_ws(const Layer &l, void *ws)
+{
+    Carve c{(char *)ws};
+    ForwardWs f{};
+    const int es = esize(l.dt);
+    f.x = c.take(l.T * packed(l.K, l.dt) * es);
+    f.w = c.take(l.K * packed(l.N, l.dt) * es);
+    f.part = (float *)c.take(shape_of(l.dt, l.T, l.N, l.K).part_bytes);
+    f.bytes = l.T ? c.used : 0;
+    return f;
+}
+
+struct BackwardWs {
+    void *dz, *x, *w;
+    float *sums, *part;
+    int64_t bytes;
+};
+
+BackwardWs backward_ws(const Layer &l, void *ws)
+{
+    Carve c{(char *)ws};
+    BackwardWs b{};
+    const int es = esize(l.dt);
+    b.dz = c.take(l.T * packed(l.N, l.dt) * es);
+    b.x = c.take(l.T * packed(l.K, l.dt) * es);
+    b.w = c.take(l.K * packed(l.N, l.dt) * es);
+    b.sums = (float *)c.take(div_up(l.T, sum_rows(l.T, l.N)) * l.N * 4);
+    b.part = (float *)c.take(std::max(shape_of(l.dt, l.T, l.K, l.N).part_bytes, shape_of(l.dt, l.K, l.N, l.T).part_bytes));
+    b.bytes = l.T ? c.used : 0;
+    return b;
+}
+
+rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *part, hipStream_t st)
+{
+    const Shape s = shape_of(dt, p.M, p.N, p.K);
+    if (s.tiles_m * s.tiles_n * s.splits > kMaxBlocks)
+        return RAR_EINVAL;
+    p.tiles_m = s.tiles_m;
+    p.tiles_n = s.tiles_n;
+    p.splits = (int)s.splits;
+    p.steps_per_split = s.steps;
+    p.pitch = s.pitch;
+    p.part = part;
+    const int es = esize(dt);
+    const auto wide = [es](const void *q, int64_t ld) { return aligned(q, 16) && (ld * es) % 16 == 0; };
+    p.vec = wide(p.out, p.ldo) && (!p.pre || p.pre_scales || wide(p.pre, p.ldp)) && (!p.res || wide(p.res, p.ldr)) &&
+            aligned(p.bias, 16);
+    if (s.splits == 1)
+        return launched(rar::launch_gemm(dt, layout, p, s.big, st));
+    GemmParams q = p;
+    q.mode = rar::kModePartial;
+    rar_status rc = launched(rar::launch_gemm(dt, layout, q, s.big, st));
+    return rc != RAR_OK ? rc : launched(rar::launch_join(dt, p, st));
+}
+
+// The matrix itself where its rows can be read directly, else a packed copy.
+rar_status readable(const Mat &m, rar_dtype dt, void *copy, const void **p, int64_t *ld, hipStream_t st)
+{
+    *p = m.p;
+    *ld = m.ld;
+    if (m.rows == 0 || direct(m))
+        return RAR_OK;
+    rar::PackParams k{m.p, copy, m.ld, packed(m.cols, dt), m.rows, m.cols};
+    *p = copy;
+    *ld = k.pitch;
+    return launched(rar::launch_pack(dt, k, st));
+}
+
+// Where both extents are whole 16-byte groups nothing is packed for its width.
+int64_t groups_of(int64_t cols) { return div_up(cols, rar::kCkptGroup); }
+
+}  // namespace
+
+// =============================================================================
+// Embedding
+// =============================================================================
+
+extern "C" rar_status rar_embed_lookup(int64_t V, int64_t D, rar_dtype dtype, const void *table, int64_t T,
+                                       const int64_t *ids, float scale, void *out, int64_t ldo, void *stream)
+{
+    if (V < 1 || V > kMaxVocab || !valid_width(D) || !valid_dtype(dtype) || !valid_rows(T) || !valid_ld(ldo, D))
+        return RAR_EINVAL;
+    if (T == 0)
+        return RAR_OK;
+    if (!table || !ids || !out)
+        return RAR_EINVAL;
+    const int es = esize(dtype);
+    if (!aligned(table, es) || !aligned(out, es) || !aligned(ids, 8))
+        return RAR_EALIGN;
+    if (!apart({{out, T, D, ldo, es}}, {{table, V, D, D, es}, {ids, 1, T, T, 8}}) || div_up(T * D, 1024) > kMaxBlocks)
+        return RAR_EINVAL;
+    rar::EmbedParams p{table, ids, out, T, V, D, ldo, scale};
+    return launched(rar::launch_embed_lookup(dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" rar_status rar_embed_grad_workspace(int64_t V, int64_t D, int64_t T, int64_t *bytes)
+{
+    if (!bytes || V < 1 || V > kMaxVocab || !valid_width(D) || !valid_rows(T))
+        return RAR_EINVAL;
+    *bytes = rar::embed_grad_workspace(T, V, D);
+    return RAR_OK;
+}
+
+extern "C" rar_status rar_embed_grad(int64_t V, int64_t D, rar_dtype dtype, int64_t T, const int64_t *ids,
+                                     const void *dy, int64_t lddy, float scale, int accumulate, void *grad, void *ws,
+                                     int64_t ws_bytes, void *stream)
+{
+    if (V < 1 || V > kMaxVocab || !valid_width(D) || !valid_dtype(dtype) || !valid_rows(T) || !valid_ld(lddy, D))
+        return RAR_EINVAL;
+    if (!grad || !ws || (T > 0 && (!ids || !dy)))
+        return RAR_EINVAL;
+    const int es = esize(dtype);
+    if (!aligned(grad, es) || !aligned(dy, es) || !aligned(ids, 8) || !aligned(ws, 16))
+        return RAR_EALIGN;
+    const int64_t need = rar::embed_grad_workspace(T, V, D);
+    if (ws_bytes < need || div_up(V * div_up(D, 512), 4) > kMaxBlocks)
+        return RAR_EINVAL;
+    if (!apart({{grad, V, D, D, es}, {ws, 1, need, need, 1}}, {{dy, T, D, lddy, es}, {ids, 1, T, T, 8}}))
+        return RAR_EINVAL;
+    rar::EmbedGradParams p{ids, dy, lddy, grad, T, V, D, scale, accumulate, ws};
+    return launched(rar::launch_embed_grad(dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+// =============================================================================
+// Linear layer
+// =============================================================================
+
+extern "C" rar_status rar_linear_plan(int64_t K, int64_t N, rar_dtype dtype, rar_act act, rar_linear_t *out)
+{
+    if (!out)
+        return RAR_EINVAL;
+    *out = nullptr;
+    if (!valid_width(K) || !valid_width(N) || !valid_dtype(dtype) || !valid_act(act))
+        return RAR_EINVAL;
+    rar_linear_s *p = new (std::nothrow) rar_linear_s;
+    if (!p)
+        return RAR_ENOMEM;
+    p->K = K;
+    p->N = N;
+    p->dtype = dtype;
+    p->act = act;
+    *out = p;
+    return RAR_OK;
+}
+
+extern "C" rar_status rar_linear_destroy(rar_linear_t plan)
+{
+    delete plan;
+    return RAR_OK;
+}
+
+extern "C" rar_status rar_linear_workspace(rar_linear_t plan, int64_t T, int64_t *forward_bytes,
+                                           int64_t *backward_bytes)
+{
+    if (!plan || !valid_rows(T))
+        return RAR_EINVAL;
+    const Layer l{T, plan->K, plan->N, plan->dtype};
+    if (forward_bytes)
+        *forward_bytes = forward_ws(l, nullptr).bytes;
+    if (backward_bytes)
+        *backward_bytes = backward_ws(l, nullptr).bytes;
+    return RAR_OK;
+}
+
+extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const void *x, int64_t ldx, const void *w,
+                                         const void *bias, const void *residual, int64_t ldr, void *y, int64_t ldy,
+                                         void *pre, int64_t ldp, uint8_t *pre_scales, void *ws, int64_t ws_bytes,
+                                         void *stream)
+{
+    if (!plan || !valid_rows(T))
+        return RAR_EINVAL;
+    if (T == 0)
+        return RAR_OK;
+    const int64_t K = plan->K, N = plan->N;
+    const rar_dtype dt = plan->dtype;
+    const int es = esize(dt);
+    if (!x || !w || !y || !ws || (pre_scales && !pre))
+        return RAR_EINVAL;
+    if (!valid_ld(ldx, K) || !valid_ld(ldy, N) || (residual && !valid_ld(ldr, N)) ||
+        (pre && !pre_scales && !valid_ld(ldp, N)))
+        return RAR_EINVAL;
+    if (!aligned(x, es) || !aligned(w, es) || !aligned(bias, es) || !aligned(residual, es) || !aligned(y, es) ||
+        !aligned(pre, pre_scales ? 16 : es) || !aligned(ws, 16))
+        return RAR_EALIGN;
+    const Layer l{T, K, N, dt};
+    const ForwardWs f = forward_ws(l, ws);
+    if (ws_bytes < f.bytes)
+        return RAR_EINVAL;
+    const int64_t groups = groups_of(N), pitch = groups * rar::kCkptGroup;
+    const Mat mx{x, T, K, ldx, es}, mw{w, K, N, N, es}, my{y, T, N, ldy, es}, mb{bias, 1, N, N, es};
+    const Mat mr{residual, T, N, ldr, es};
+    const Mat mp = pre_scales ? Mat{pre, 1, T * pitch, T * pitch, 1} : Mat{pre, T, N, ldp, es};
+    const Mat ms{pre_scales, 1, T * groups, T * groups, 1}, mws{ws, 1, f.bytes, f.bytes, 1};
+    const bool in_place = residual == y && ldr == ldy;
+    if (!apart({my, mp, ms, mws}, {mx, mw, mb}) || (residual && !in_place && !apart({my}, {mr})) ||
+        (residual && !apart({mp, ms, mws}, {mr})))
+        return RAR_EINVAL;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    GemmParams p{};
+    rar_status rc = readable(mx, dt, f.x, &p.a, &p.lda, st);
+    if (rc == RAR_OK)
+        rc = readable(mw, dt, f.w, &p.b, &p.ldb, st);
+    if (rc != RAR_OK)
+        return rc;
+    p.M = T;
+    p.N = N;
+    p.K = K;
+    p.out = y;
+    p.ldo = ldy;
+    p.pre = pre;
+    p.ldp = ldp;
+    p.pre_scales = pre_scales;
+    p.bias = bias;
+    p.res = residual;
+    p.ldr = ldr;
+    p.mode = rar::kModeForward;
+    p.act = plan->act;
+    return product(dt, rar::kGemmForward, p, f.part, st);
+}
+
+extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const void *dy, int64_t lddy, const void *x,
+                                          int64_t ldx, const uint8_t *x_scales, const void *w, const void *pre,
+                                          int64_t ldp, const uint8_t *pre_scales, void *dx, int64_t lddx, void *dw,
+                                          void *db, int accumulate, void *ws, int64_t ws_bytes, void *stream)
+{
+    if (!plan || !valid_rows(T))
+        return RAR_EINVAL;
+    const int64_t K = plan->K, N = plan->N;
+    const rar_dtype dt = plan->dtype;
+    const int es = esize(dt);
+    const bool act = plan->act != RAR_ACT_NONE;
+    if (!act) {
+        pre = nullptr;
+        pre_scales = nullptr;
+    }
+    const Layer l{T, K, N, dt};
+    const BackwardWs b = backward_ws(l, ws);
+    if (T > 0) {
+        if (!dy || !ws || (dx && !w) || (dw && !x) || (act && !pre))
+            return RAR_EINVAL;
+        if (!valid_ld(lddy, N) || (dx && !valid_ld(lddx, K)) || (dw && !x_scales && !valid_ld(ldx, K)) ||
+            (act && !pre_scales && !valid_ld(ldp, N)))
+            return RAR_EINVAL;
+    } else {
+        dx = nullptr;
+    }
+    if (!aligned(dy, es) || !aligned(x, x_scales ? 16 : es) || !aligned(w, es) || !aligned(pre, pre_scales ? 16 : es) ||
+        !aligned(dx, es) || !aligned(dw, es) || !aligned(db, es) || !aligned(ws, 16))
+        return RAR_EALIGN;
+    if (ws_bytes < b.bytes)
+        return RAR_EINVAL;
+    const int64_t gk = groups_of(K), gn = groups_of(N);
+    const Mat mdy{dy, T, N, lddy, es}, mw{dx ? w : nullptr, K, N, N, es};
+    Mat mx{dw ? x : nullptr, T, K, ldx, es}, mp{pre, T, N, ldp, es};
+    if (x_scales)
+        mx = Mat{dw ? x : nullptr, 1, T * gk * rar::kCkptGroup, T * gk * rar::kCkptGroup, 1};
+    if (pre_scales)
+        mp = Mat{pre, 1, T * gn * rar::kCkptGroup, T * gn * rar::kCkptGroup, 1};
+    const Mat mxs{dw ? x_scales : nullptr, 1, T * gk, T * gk, 1}, mps{pre_scales, 1, T * gn, T * gn, 1};
+    const Mat mdx{dx, T, K, lddx, es}, mdw{dw, K, N, N, es}, mdb{db, 1, N, N, es}, mws{ws, 1, b.bytes, b.bytes, 1};
+    if (!apart({mdx, mdw, mdb, mws}, {mdy, mx, mw, mp, mxs, mps}))
+        return RAR_EINVAL;
+
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    rar_status rc = RAR_OK;
+    const void *dz = dy;
+    int64_t lddz = lddy;
+    const bool need_dz = (dx || dw) && T > 0 && (act || !direct(mdy));
+    if (T > 0 && (need_dz || db)) {
+        rar::DzParams d{};
+        d.dy = dy;
+        d.ldy = lddy;
+        d.pre = pre;
+        d.ldp = ldp;
+        d.pre_scales = pre_scales;
+        d.pitch = packed(N, dt);
+        d.dz = need_dz ? b.dz : nullptr;
+        d.part = db ? b.sums : nullptr;
+        d.rows = T;
+        d.cols = N;
+        d.rows_per_chunk = sum_rows(T, N);
+        d.act = plan->act;
+        rc = launched(rar::launch_dz(dt, d, st));
+        if (rc != RAR_OK)
+            return rc;
+        if (need_dz) {
+            dz = b.dz;
+            lddz = d.pitch;
+        }
+    }
+    if (db) {
+        rar::SumParams s{b.sums, T > 0 ? div_up(T, sum_rows(T, N)) : 0, N, db, accumulate};
+        rc = launched(rar::launch_sum(dt, s, st));
+        if (rc != RAR_OK)
+            return rc;
+    }
+    if (dx) {
+        GemmParams p{};
+        p.a = dz;
+        p.lda = lddz;
+        rc = readable(mw, dt, b.w, &p.b, &p.ldb, st);
+        if (rc != RAR_OK)
+            return rc;
+        p.M = T;
+        p.N = K;
+        p.K = N;
+        p.out = dx;
+        p.ldo = lddx;
+        p.mode = rar::kModeStore;
+        rc = product(dt, rar::kGemmGradX, p, b.part, st);
+        if (rc != RAR_OK)
+            return rc;
+    }
+    if (dw) {
+        GemmParams p{};
+        if (T > 0 && x_scales) {
+            rar::CkptParams c{};
+            c.codes = (uint8_t *)x;
+            c.scales = (uint8_t *)x_scales;
+            c.y = b.x;
+            c.ldy = packed(K, dt);
+            c.pitch_zero = c.ldy;
+            c.rows = T;
+            c.cols = K;
+            c.act = RAR_ACT_NONE;
+            rc = launched(rar::launch_ckpt_load(dt, c, st));
+            p.a = b.x;
+            p.lda = c.ldy;
+        } else {
+            rc = readable(mx, dt, b.x, &p.a, &p.lda, st);
+        }
+        if (rc != RAR_OK)
+            return rc;
+        p.b = dz;
+        p.ldb = lddz;
+        p.M = K;
+        p.N = N;
+        p.K = T;
+        p.out = dw;
+        p.ldo = N;
+        p.mode = rar::kModeStore;
+        p.accumulate = accumulate;
+        rc = product(dt, rar::kGemmGradW, p, b.part, st);
+    }
+    return rc;
+}
+
+// =============================================================================
+// 8-bit checkpoints
+// =============================================================================
+
+extern "C" rar_status rar_ckpt_size(int64_t D, int64_t *pitch, int64_t *groups)
+{
+    if (!valid_width(D))
+        return RAR_EINVAL;
+    if (pitch)
+        *pitch = groups_of(D) * rar::kCkptGroup;
+    if (groups)
+        *groups = groups_of(D);
+    return RAR_OK;
+}
+
+namespace {
+
+rar_status check_ckpt(int64_t T, int64_t D, rar_dtype dt, const void *m, int64_t ld, const uint8_t *codes,
+                      const uint8_t *scales, bool store)
+{
+    if (!valid_rows(T) || !valid_width(D) || !valid_dtype(dt) || !valid_ld(ld, D))
+        return RAR_EINVAL;
+    if (T == 0)
+        return RAR_OK;
+    if (!m || !codes || !scales)
+        return RAR_EINVAL;
+    const int es = esize(dt);
+    if (!aligned(m, es) || !aligned(codes, 16))
+        return RAR_EALIGN;
+    const int64_t g = groups_of(D) * T, c = g * rar::kCkptGroup;
+    const Mat mm{m, T, D, ld, es}, mc{codes, 1, c, c, 1}, ms{scales, 1, g, g, 1};
+    if (store ? !apart({mc, ms}, {mm}) : !apart({mm}, {mc, ms}))
+        return RAR_EINVAL;
+    return RAR_OK;
+}
+
+}  // namespace
+
+extern "C" rar_status rar_ckpt_store(int64_t T, int64_t D, rar_dtype dtype, const void *x, int64_t ldx, uint8_t *codes,
+                                     uint8_t *scales, void *stream)
+{
+    const rar_status rc = check_ckpt(T, D, dtype, x, ldx, codes, scales, true);
+    if (rc != RAR_OK || T == 0)
+        return rc;
+    rar::CkptParams p{};
+    p.x = x;
+    p.ldx = ldx;
+    p.codes = codes;
+    p.scales = scales;
+    p.rows = T;
+    p.cols = D;
+    return launched(rar::launch_ckpt_store(dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" rar_status rar_ckpt_load(int64_t T, int64_t D, rar_dtype dtype, const uint8_t *codes, const uint8_t *scales,
+                                    rar_act act, void *y, int64_t ldy, void *stream)
+{
+    if (!valid_act(act))
+        return RAR_EINVAL;
+    const rar_status rc = check_ckpt(T, D, dtype, y, ldy, codes, scales, false);
+    if (rc != RAR_OK || T == 0)
+        return rc;
+    rar::CkptParams p{};
+    p.codes = (uint8_t *)codes;
+    p.scales = (uint8_t *)scales;
+    p.y = y;
+    p.ldy = ldy;
+    p.rows = T;
+    p.cols = D;
+    p.act = act;
+    return launched(rar::launch_ckpt_load(dtype, p, static_cast<hipStream_t>(stream)));
+}

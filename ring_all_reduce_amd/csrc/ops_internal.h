@@ -1,0 +1,127 @@
+// ops_internal.h -- declarations shared by the host code (ops_host.cpp) and the
+// kernels (linear.hip, embed.hip, ckpt.hip) of the gradient-producing operators
+// of librar.so.  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rar.h"
+
+namespace rar {
+
+constexpr int kCkptGroup = RAR_CKPT_GROUP;
+
+// One matrix product D[m][n] = sum_k A(m,k) B(n,k).  An operand is stored either
+// with its reduction index contiguous (element (r,k) at r*ld + k) or with the
+// reduction index slow (at k*ld + r); which one is the kernel's layout.
+enum GemmLayout {
+    kGemmForward = 0,  // A = x [T][K] contiguous, B = W [K][N] slow
+    kGemmGradX = 1,    // A = dz [T][N] contiguous, B = W [K][N] contiguous
+    kGemmGradW = 2     // A = x [T][K] slow, B = dz [T][N] slow
+};
+
+enum GemmMode {
+    kModeStore = 0,    // out = D (+ out when accumulate)
+    kModeForward = 1,  // z = D + bias; pre = z; out = act(z) + residual
+    kModePartial = 2   // part[split] = D in binary32 (joined by launch_join)
+};
+
+struct GemmParams {
+    const void *a;
+    const void *b;
+    int64_t lda, ldb;        // elements
+    int64_t M, N, K;         // K: the reduction
+    void *out;
+    int64_t ldo;
+    void *pre;               // forward: z, or checkpoint codes with pre_scales, or nullptr
+    int64_t ldp;
+    uint8_t *pre_scales;
+    const void *bias;        // or nullptr
+    const void *res;         // or nullptr
+    int64_t ldr;
+    float *part;             // [splits][M][pitch]
+    int64_t pitch;
+    int mode;
+    int act;
+    int accumulate;
+    int vec;                 // outputs, bias and residual may be accessed 16 bytes at a time
+    int splits;
+    int64_t steps_per_split; // K steps of one split
+    int64_t tiles_m, tiles_n;
+};
+
+// Copy of a [rows][cols] matrix with leading dimension ld into one with pitch
+// `pitch` whose columns [cols, pitch) are zero.
+struct PackParams {
+    const void *src;
+    void *dst;
+    int64_t ld, pitch, rows, cols;
+};
+
+// dz = dy * act'(z) and column sums of dz, for a [rows][cols] block.
+struct DzParams {
+    const void *dy;
+    int64_t ldy;
+    const void *pre;         // z in the plan's type, or checkpoint codes; nullptr when act is none
+    int64_t ldp;
+    const uint8_t *pre_scales;
+    void *dz;                // nullptr: only the sums
+    int64_t pitch;           // dz's row length; columns [cols, pitch) are set to zero
+    float *part;             // [chunks][cols] partial column sums, or nullptr
+    int64_t rows, cols;
+    int64_t rows_per_chunk;
+    int act;
+};
+
+struct SumParams {
+    const float *part;
+    int64_t chunks, cols;
+    void *out;
+    int accumulate;
+};
+
+struct CkptParams {
+    const void *x;           // store: source; load: unused
+    int64_t ldx;
+    uint8_t *codes;
+    uint8_t *scales;
+    void *y;                 // load: destination
+    int64_t ldy;
+    int64_t pitch_zero;      // load: columns [cols, pitch_zero) of y are set to zero
+    int64_t rows, cols;
+    int act;
+};
+
+struct EmbedParams {
+    const void *table;       // lookup
+    const int64_t *ids;
+    void *out;
+    int64_t T, V, D, ldo;
+    float scale;
+};
+
+struct EmbedGradParams {
+    const int64_t *ids;
+    const void *dy;
+    int64_t ldy;
+    void *grad;
+    int64_t T, V, D;
+    float scale;
+    int accumulate;
+    void *ws;
+};
+
+hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big, hipStream_t st);
+hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st);
+hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st);
+hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st);
+hipError_t launch_sum(rar_dtype dt, const SumParams &p, hipStream_t st);
+hipError_t launch_ckpt_store(rar_dtype dt, const CkptParams &p, hipStream_t st);
+hipError_t launch_ckpt_load(rar_dtype dt, const CkptParams &p, hipStream_t st);
+hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t st);
+hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t st);
+// Bytes of workspace rar_embed_grad needs.
+int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D);
+
+}  // namespace rar

@@ -1384,4 +1384,4 @@ extern "C" const char *rar_strerror(rar_status s)
     return "unknown status";
 }
 
-extern "C" int rar_version(void) { return 600; }  // 0.6.0: rar_rank_stride_candidate, wider stride search
+extern "C" int rar_version(void) { return 700; }  // 0.7.0: rar_embed_*, rar_linear_*, rar_ckpt_*

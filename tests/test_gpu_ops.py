@@ -1,0 +1,515 @@
+"""The embedding, the linear layer and 8-bit checkpoints on the GPU, against
+plain 64-bit forms at the sizes, layouts and values where they can go wrong.
+Bounds count roundings (see ops_ref.py); nothing is fitted to results."""
+import numpy as np
+import pytest
+import torch
+
+import ops_ref as R
+from ring_all_reduce_amd import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+CODE = {"f32": api.F32, "bf16": api.BF16}
+BOTH = ["f32", "bf16"]
+
+
+def rand(gen, *shape, dtype="f32", scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).to(R.DT[dtype])
+
+
+def nan_like(*shape, dtype):
+    return torch.full(shape, float("nan"), dtype=R.DT[dtype], device=DEV)
+
+
+def strided(t, extra, offset=0):
+    """t on the GPU as a view of a wider matrix (rows t.shape[1] + extra apart), NaN around it."""
+    big = torch.full((t.shape[0] + 1, t.shape[1] + extra), float("nan"), dtype=t.dtype, device=DEV)
+    v = big[:t.shape[0], offset:offset + t.shape[1]]
+    v.copy_(t.to(DEV))
+    return v
+
+
+# ---------------------------------------------------------------------------
+# Linear layer
+# ---------------------------------------------------------------------------
+
+# (T, K, N): one element, one token, odd sizes, whole and broken tiles, split reductions, more than 192 tiles of 256
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (17, 64, 32), (1, 2048, 520), (7, 300, 1000), (129, 257, 131),
+          (300, 512, 264), (64, 1000, 72), (515, 96, 640), (5001, 40, 24), (130, 8, 4096)]
+BIG = [(3000, 72, 4200), (2900, 136, 4104)]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("shape", SHAPES + BIG, ids=str)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+def test_linear_forward(shape, dtype, act):
+    T, K, N = shape
+    if shape in BIG and (act == "relu" or dtype == "f32"):
+        pytest.skip("the other combinations cover it")
+    g = torch.Generator().manual_seed(T * 31 + K + N)
+    x, w = rand(g, T, K, dtype=dtype), rand(g, K, N, dtype=dtype, scale=K ** -0.5)
+    b, r = rand(g, N, dtype=dtype), rand(g, T, N, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], R.ACTS[act])
+    for bias, res in ((b, r), (None, None)) if shape not in BIG else ((b, r),):
+        y, z = nan_like(T, N, dtype=dtype), nan_like(T, N, dtype=dtype)
+        api.rar_linear_forward(plan, T, x.to(DEV), w.to(DEV), None if bias is None else bias.to(DEV),
+                               None if res is None else res.to(DEV), y, pre=z)
+        (ry, ey), (rz, ez) = R.forward(x, w, bias, res, act, dtype)
+        R.check(z, rz, ez, "z")
+        R.check(y, ry, ey, "y")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("shape", SHAPES + BIG, ids=str)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+def test_linear_backward(shape, dtype, act):
+    T, K, N = shape
+    if shape in BIG and (act == "relu" or dtype == "f32"):
+        pytest.skip("the other combinations cover it")
+    g = torch.Generator().manual_seed(T * 37 + K + N)
+    dy, x, z = (rand(g, T, n, dtype=dtype) for n in (N, K, N))
+    w = rand(g, K, N, dtype=dtype, scale=K ** -0.5)
+    dw0, db0 = rand(g, K, N, dtype=dtype), rand(g, N, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], R.ACTS[act])
+    for acc in (False, True):
+        dx = nan_like(T, K, dtype=dtype)
+        dw = dw0.to(DEV) if acc else nan_like(K, N, dtype=dtype)
+        db = db0.to(DEV) if acc else nan_like(N, dtype=dtype)
+        api.rar_linear_backward(plan, T, dy.to(DEV), x.to(DEV), w.to(DEV), z.to(DEV), dx, dw, db, accumulate=acc)
+        ref = R.backward(dy, x, w, z, act, dtype, *((dw0, db0) if acc else ()))
+        for got, (want, bound), what in zip((dx, dw, db), ref, ("dx", "dw", "db")):
+            R.check(got, want, bound, f"{what} accumulate={acc}")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_big_dw_tiles(dtype):
+    # more than 192 tiles of 256 in K x N, and a reduction over few and odd rows
+    T, K, N = 67, 3400, 4104
+    g = torch.Generator().manual_seed(5)
+    dy, x = rand(g, T, N, dtype=dtype), rand(g, T, K, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_NONE)
+    dw = nan_like(K, N, dtype=dtype)
+    api.rar_linear_backward(plan, T, dy.to(DEV), x.to(DEV), None, None, None, dw, None)
+    want, bound = R.backward(dy, x, torch.zeros(K, N), torch.zeros(T, N), "none", dtype)[1]
+    R.check(dw, want, bound, "dw")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("extra,offset", [(8, 0), (8, 8), (3, 1), (1, 0)])
+def test_linear_strides_and_surroundings(dtype, extra, offset):
+    # every matrix a view of a wider one with NaN around it: nothing outside is read into a result or written
+    T, K, N = 150, 136, 200
+    g = torch.Generator().manual_seed(11)
+    x, r, dy, z0 = (rand(g, T, n, dtype=dtype) for n in (K, N, N, N))
+    w, b = rand(g, K, N, dtype=dtype, scale=0.1), rand(g, N, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_GELU)
+    xs, rs, dys, zs = (strided(t, extra, offset) for t in (x, r, dy, z0))
+    y, z, dx = (strided(torch.zeros(T, n, dtype=R.DT[dtype]), extra, offset) for n in (N, N, K))
+    api.rar_linear_forward(plan, T, xs, w.to(DEV), b.to(DEV), rs, y, pre=z)
+    (ry, ey), (rz, ez) = R.forward(x, w, b, r, "gelu", dtype)
+    R.check(y, ry, ey, "y")
+    R.check(z, rz, ez, "z")
+    dw, db = nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)
+    api.rar_linear_backward(plan, T, dys, xs, w.to(DEV), zs, dx, dw, db)
+    for got, (want, bound), what in zip((dx, dw, db), R.backward(dy, x, w, z0, "gelu", dtype), ("dx", "dw", "db")):
+        R.check(got, want, bound, what)
+    for view in (y, z, dx):
+        cols = view.shape[1]
+        base = view._base
+        outside = torch.ones_like(base, dtype=torch.bool)
+        outside[:T, offset:offset + cols] = False
+        assert torch.isnan(base[outside].float()).all()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_residual_in_place_and_side_by_side_outputs(dtype):
+    T, K, N = 70, 64, 96
+    g = torch.Generator().manual_seed(3)
+    x, w, r = rand(g, T, K, dtype=dtype), rand(g, K, N, dtype=dtype), rand(g, T, N, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_RELU)
+    both = torch.zeros(T, 2 * N, dtype=R.DT[dtype], device=DEV)
+    y, z = both[:, :N], both[:, N:]
+    y.copy_(r)
+    api.rar_linear_forward(plan, T, x.to(DEV), w.to(DEV), None, y, y, pre=z)
+    (ry, ey), (rz, ez) = R.forward(x, w, None, r, "relu", dtype)
+    R.check(y, ry, ey, "y")
+    R.check(z, rz, ez, "z")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_backward_parts_alone_equal_the_whole(dtype):
+    T, K, N = 90, 72, 56
+    g = torch.Generator().manual_seed(9)
+    dy, x, z, w = (rand(g, *s, dtype=dtype).to(DEV) for s in ((T, N), (T, K), (T, N), (K, N)))
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_GELU)
+    whole = [nan_like(T, K, dtype=dtype), nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)]
+    api.rar_linear_backward(plan, T, dy, x, w, z, *whole)
+    for k, (xx, ww) in enumerate(((None, w), (x, None), (None, None))):
+        part = [None] * 3
+        part[k] = torch.full_like(whole[k], float("nan"))
+        api.rar_linear_backward(plan, T, dy, xx, ww, z, *part)
+        assert torch.equal(part[k], whole[k])
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_no_rows(dtype):
+    K, N = 24, 40
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_GELU)
+    td = R.DT[dtype]
+    e = lambda n: torch.empty(0, n, dtype=td, device=DEV)
+    w = torch.ones(K, N, dtype=td, device=DEV)
+    api.rar_linear_forward(plan, 0, e(K), w, None, None, e(N), pre=e(N))
+    dw, db = nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)
+    api.rar_linear_backward(plan, 0, e(N), e(K), w, e(N), e(K), dw, db)
+    assert not dw.any() and not db.any()
+    dw.fill_(3)
+    api.rar_linear_backward(plan, 0, e(N), e(K), w, e(N), e(K), dw, None, accumulate=True)
+    assert (dw == 3).all()
+    grad = nan_like(7, 5, dtype=dtype)
+    ids = torch.empty(0, dtype=torch.int64, device=DEV)
+    api.rar_embed_grad(7, 5, CODE[dtype], 0, ids, e(5), grad)
+    assert not grad.any()
+    api.rar_embed_lookup(7, 5, CODE[dtype], grad, 0, ids, e(5))
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+def test_activation_values(dtype, act):
+    # the activation and its derivative over every bf16 value: z = x * 1, dx = act'(z)
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(torch.bfloat16)
+    v = v[torch.isfinite(v)]
+    x = v.to(R.DT[dtype]).reshape(-1, 1)
+    T = x.shape[0]
+    one = torch.ones(1, 1, dtype=R.DT[dtype])
+    plan = api.rar_linear_plan(1, 1, CODE[dtype], R.ACTS[act])
+    y, dx = nan_like(T, 1, dtype=dtype), nan_like(T, 1, dtype=dtype)
+    api.rar_linear_forward(plan, T, x.to(DEV), one.to(DEV), None, None, y)
+    api.rar_linear_backward(plan, T, torch.ones(T, 1, dtype=R.DT[dtype], device=DEV), None, one.to(DEV), x.to(DEV), dx,
+                            None, None)
+    z = x.double()
+    u = R.U[dtype]
+    want = R.act(z, act)
+    # relative to the value itself, far tail included: the exponential's argument carries z^2 / 2 * 2^-22, and
+    # results under 2^-126 may be flushed to zero
+    rel = (2.0 ** -20 + z * z * 2.0 ** -22 if act == "gelu" else 0 * z)
+    R.check(y, want, (rel + 1.01 * u) * want.abs() + 2.0 ** -120, "act")
+    want = R.act_grad(z, act)
+    slack = rel * (R.phi(z) + (z.abs() * torch.exp(-z * z / 2) * 0.4)) if act == "gelu" else 0 * z
+    R.check(dx, want, slack + 2.02 * u * want.abs() + 2.0 ** -120, "act'")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_infinities_and_nan(dtype):
+    inf, nan = float("inf"), float("nan")
+    x = torch.tensor([[inf], [-inf], [nan], [2.0]], dtype=R.DT[dtype], device=DEV)
+    one = torch.ones(1, 1, dtype=R.DT[dtype], device=DEV)
+    for act, y_want, d_want in (("relu", [inf, 0, nan, 2], [1, 0, nan, 1]), ("gelu", [inf, 0, nan, None], [1, 0, nan, None]),
+                                ("none", [inf, -inf, nan, 2], [1, 1, 1, 1])):
+        plan = api.rar_linear_plan(1, 1, CODE[dtype], R.ACTS[act])
+        y, dx = nan_like(4, 1, dtype=dtype), nan_like(4, 1, dtype=dtype)
+        api.rar_linear_forward(plan, 4, x, one, None, None, y)
+        api.rar_linear_backward(plan, 4, torch.ones_like(y), None, one, x, dx, None, None)
+        for got, want in ((y, y_want), (dx, d_want)):
+            for a, b in zip(got.flatten().tolist(), want):
+                assert b is None or a == b or (a != a and b != b), (act, got, want)
+    # a NaN row stays in its row, a NaN column of W in its column, whatever tile they share
+    T, K, N = 40, 72, 48
+    g = torch.Generator().manual_seed(2)
+    xs, w = rand(g, T, K, dtype=dtype), rand(g, K, N, dtype=dtype)
+    xs[7, 3] = nan
+    w[5, 11] = inf
+    plan = api.rar_linear_plan(K, N, CODE[dtype])
+    y = torch.zeros(T, N, dtype=R.DT[dtype], device=DEV)
+    api.rar_linear_forward(plan, T, xs.to(DEV), w.to(DEV), None, None, y)
+    bad = ~torch.isfinite(y).cpu()
+    want = torch.zeros(T, N, dtype=torch.bool)
+    want[7], want[:, 11] = True, True
+    assert torch.equal(bad, want)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit checkpoints
+# ---------------------------------------------------------------------------
+
+def make_ckpt(x, dtype):
+    T, D = x.shape
+    pitch, groups = api.rar_ckpt_size(D)
+    codes = torch.full((T, pitch), 0x55, dtype=torch.uint8, device=DEV)
+    scales = torch.full((T, groups), 0x55, dtype=torch.uint8, device=DEV)
+    api.rar_ckpt_store(T, D, CODE[dtype], x, codes, scales)
+    return codes, scales
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("T,D", [(1, 1), (1, 31), (1, 32), (2, 33), (5, 77), (64, 8), (67, 1001), (300, 512), (3, 8200)])
+def test_ckpt_store_and_load(T, D, dtype):
+    g = torch.Generator().manual_seed(T + D)
+    x = rand(g, T, D, dtype=dtype) * torch.exp2(torch.randint(-20, 20, (T, D), generator=g)).to(R.DT[dtype])
+    x[torch.rand(T, D, generator=g) < 0.1] = 0
+    codes, scales, vals = R.quantise(x)
+    for view in (x.to(DEV), strided(x, 8, 8), strided(x, 3, 1)):
+        c, s = make_ckpt(view, dtype)
+        assert np.array_equal(s.cpu().numpy(), scales)
+        got = c.cpu().numpy()
+        zero = (codes & 127) == 0
+        assert np.array_equal(np.where(zero, 0, got), np.where(zero, 0, codes)) and not (got[zero] & 127).any()
+    for act in ("none", "relu", "gelu"):
+        want = R.act(torch.from_numpy(vals), act)
+        for y in (nan_like(T, D, dtype=dtype), strided(torch.zeros(T, D, dtype=R.DT[dtype]), 3, 1)):
+            api.rar_ckpt_load(T, D, CODE[dtype], c, s, y, act=R.ACTS[act])
+            if act == "gelu":
+                v = torch.from_numpy(vals)
+                rel = 2.0 ** -20 + v * v * 2.0 ** -22
+                R.check(y, want, (rel + 1.01 * R.U[dtype]) * want.abs() + 2.0 ** -120, "gelu")
+            else:
+                # four significant bits: exact in either type
+                assert torch.equal(y.double().cpu(), want)
+
+
+def test_ckpt_every_bf16_value_and_scale():
+    # every finite bf16 magnitude against group maxima across the exponent range
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = bits[torch.randperm(65536, generator=torch.Generator().manual_seed(1))].reshape(-1, 32).clone()
+    y = bits.reshape(-1, 32).clone()
+    for t in (x, y):
+        codes, scales, vals = R.quantise(t)
+        c, s = make_ckpt(t.to(DEV), "bf16")
+        assert np.array_equal(s.cpu().numpy(), scales)
+        got = R.values(c.cpu().numpy(), s.cpu().numpy(), 32).numpy()
+        assert np.array_equal(got, vals, equal_nan=True)
+        z = torch.empty(t.shape, dtype=torch.float32, device=DEV)
+        api.rar_ckpt_load(t.shape[0], 32, api.F32, c, s, z)
+        # four significant bits of a value next to 2^128 may round to 2^128, which binary32 holds as infinity
+        with np.errstate(over="ignore"):
+            assert np.array_equal(z.cpu().numpy(), vals.astype(np.float32), equal_nan=True)
+
+
+def test_ckpt_load_reads_every_code_and_scale():
+    codes = torch.arange(256, dtype=torch.uint8).reshape(8, 32).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8).repeat_interleave(8).reshape(-1, 1)
+    want = R.values(codes.numpy(), scales.numpy(), 32)
+    want[scales.flatten() == 255] = float("nan")
+    y = torch.empty(2048, 32, dtype=torch.float32, device=DEV)
+    api.rar_ckpt_load(2048, 32, api.F32, codes.to(DEV), scales.to(DEV), y)
+    f32 = want.float()
+    got = y.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(f32)) and torch.equal(got[~torch.isnan(f32)], f32[~torch.isnan(f32)])
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("shape", [(1, 1, 1), (5, 33, 70), (200, 264, 136), (67, 1000, 31), (3000, 72, 4200)], ids=str)
+def test_forward_writes_the_checkpoint_of_z(shape, dtype):
+    T, K, N = shape
+    g = torch.Generator().manual_seed(K)
+    x, w, b = rand(g, T, K, dtype=dtype), rand(g, K, N, dtype=dtype, scale=K ** -0.5), rand(g, N, dtype=dtype)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_GELU)
+    y, z, y2 = (nan_like(T, N, dtype=dtype) for _ in range(3))
+    args = plan, T, x.to(DEV), w.to(DEV), b.to(DEV), None
+    api.rar_linear_forward(*args, y, pre=z)
+    want_c, want_s = make_ckpt(z, dtype)
+    c, s = torch.full_like(want_c, 0x55), torch.full_like(want_s, 0x55)
+    api.rar_linear_forward(*args, y2, pre=c, pre_scales=s)
+    assert torch.equal(y, y2) and torch.equal(c, want_c) and torch.equal(s, want_s)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (3, 5, 7), (130, 257, 131), (515, 96, 640), (67, 3400, 4104)], ids=str)
+def test_backward_from_checkpoints(shape, act, dtype):
+    T, K, N = shape
+    if T * K * N > 1e8 and act == "relu":
+        pytest.skip("the other activations cover it")
+    g = torch.Generator().manual_seed(T + K + N)
+    dy, x, z = (rand(g, T, n, dtype=dtype) for n in (N, K, N))
+    w = rand(g, K, N, dtype=dtype, scale=K ** -0.5)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], R.ACTS[act])
+    (xc, xs), (zc, zs) = make_ckpt(x.to(DEV), dtype), make_ckpt(z.to(DEV), dtype)
+    xv = torch.from_numpy(R.quantise(x)[2])
+    zv = torch.from_numpy(R.quantise(z)[2])
+    for use_x, use_z in ((True, True), (True, False), (False, True)):
+        out = [nan_like(T, K, dtype=dtype), nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)]
+        api.rar_linear_backward(plan, T, dy.to(DEV), xc if use_x else x.to(DEV), w.to(DEV), zc if use_z else z.to(DEV),
+                                *out, x_scales=xs if use_x else None, pre_scales=zs if use_z else None)
+        ref = R.backward(dy, xv if use_x else x, w, zv if use_z else z, act, dtype)
+        for got, (want, bound), what in zip(out, ref, ("dx", "dw", "db")):
+            R.check(got, want, bound, f"{what} x8={use_x} z8={use_z}")
+
+
+# ---------------------------------------------------------------------------
+# Embedding
+# ---------------------------------------------------------------------------
+
+EMBED = [(1, 1, 1), (1, 5, 8), (63, 7, 3), (33, 300, 520), (4096, 50, 24), (4097, 300, 40), (9000, 70000, 9),
+         (20000, 11, 130), (5000, 256, 513), (4500, 66000, 16)]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("T,V,D", EMBED)
+def test_embedding(T, V, D, dtype):
+    g = torch.Generator().manual_seed(T + V + D)
+    ids = torch.randint(0, V, (T,), generator=g)
+    if T > 8:
+        ids[torch.rand(T, generator=g) < 0.5] = V // 2          # one frequent token
+        ids[torch.rand(T, generator=g) < 0.05] = -1             # padding
+        ids[3], ids[5], ids[6] = V, 2 ** 40, -2 ** 40           # outside
+    scale = 1.7
+    table, dy = rand(g, V, D, dtype=dtype), rand(g, T, D, dtype=dtype)
+    ok = (ids >= 0) & (ids < V)
+    s32 = torch.tensor(scale, dtype=torch.float32)
+    want = torch.where(ok[:, None], (table[torch.where(ok, ids, 0)].float() * s32), torch.zeros(())).to(R.DT[dtype])
+    for out in (nan_like(T, D, dtype=dtype), strided(torch.zeros(T, D, dtype=R.DT[dtype]), 3, 1)):
+        api.rar_embed_lookup(V, D, CODE[dtype], table.to(DEV), T, ids.to(DEV), out, scale)
+        assert torch.equal(out.cpu(), want)                     # one product, one rounding
+    g0 = rand(g, V, D, dtype=dtype)
+    for acc in (False, True):
+        for d in (dy.to(DEV), strided(dy, 8, 8), strided(dy, 3, 1)):
+            grad = g0.to(DEV) if acc else nan_like(V, D, dtype=dtype)
+            api.rar_embed_grad(V, D, CODE[dtype], T, ids.to(DEV), d, grad, scale, accumulate=acc)
+            want_g, bound = R.embed_grad(V, ids, dy, scale, dtype, g0 if acc else None)
+            R.check(grad, want_g, bound, f"grad accumulate={acc}")
+            if acc:
+                idle = torch.bincount(ids[ok], minlength=V) == 0
+                assert torch.equal(grad.cpu()[idle], g0[idle])
+
+
+@pytest.mark.parametrize("T", [31, 32, 1024, 1056, 3100, 5000, 70000])
+def test_embed_grad_one_token_for_all(T):
+    # a run that is the whole batch, and one that starts off the partial rows' boundaries
+    V, D = 6, 40
+    g = torch.Generator().manual_seed(T)
+    dy = rand(g, T, D)
+    for lead in (0, 1, 29):
+        ids = torch.full((T,), 4)
+        ids[:lead] = 1
+        grad = nan_like(V, D, dtype="f32")
+        api.rar_embed_grad(V, D, api.F32, T, ids.to(DEV), dy.to(DEV), grad)
+        want, bound = R.embed_grad(V, ids, dy, 1.0, "f32")
+        R.check(grad, want, bound, f"lead {lead}")
+
+
+def test_embed_grad_row_order_is_token_order():
+    # three values whose sum depends on the order: the run is summed as the tokens come
+    big = 2.0 ** 25
+    vals = torch.tensor([big, 1.0, -big, 1.0, 0.5])
+    ids = torch.tensor([3, 3, 3, 3, 0])
+    grad = nan_like(4, 1, dtype="f32")
+    api.rar_embed_grad(4, 1, api.F32, 5, ids.to(DEV), vals.reshape(-1, 1).to(DEV), grad)
+    want = np.float32(0)
+    for v in vals[:4].numpy():
+        want = np.float32(want + v)
+    assert grad.cpu().flatten().tolist() == [0.5, 0, 0, float(want)]
+
+
+def test_embedding_offsets_past_32_bits():
+    # a table of 4.4 GB: rows past 2^32 bytes and past 2^31 elements' half
+    V, D, T = 1_100_000, 1000, 600
+    ids = torch.randint(V - 1000, V, (T,), generator=torch.Generator().manual_seed(1))
+    ids[0] = V - 1
+    table = torch.zeros(V, D, device=DEV)
+    rows = torch.randn(1000, D, generator=torch.Generator().manual_seed(2))
+    table[V - 1000:] = rows.to(DEV)
+    out = nan_like(T, D, dtype="f32")
+    api.rar_embed_lookup(V, D, api.F32, table, T, ids.to(DEV), out)
+    assert torch.equal(out.cpu(), rows[ids - (V - 1000)])
+    api.rar_embed_grad(V, D, api.F32, T, ids.to(DEV), out, table)
+    want, bound = R.embed_grad(1000, ids - (V - 1000), out.cpu(), 1.0, "f32")
+    R.check(table[V - 1000:], want, bound, "grad")
+    assert not table[:V - 1000].any()
+
+
+# ---------------------------------------------------------------------------
+# Streams, graphs, repeatability
+# ---------------------------------------------------------------------------
+
+def _step(dtype):
+    """A run of all operators on fixed inputs; returns (call, outputs)."""
+    T, K, N, V = 700, 136, 264, 900
+    g = torch.Generator().manual_seed(21)
+    td = R.DT[dtype]
+    ids = torch.randint(-1, 40, (T,), generator=g).to(DEV)
+    table, w, b = (rand(g, *s, dtype=dtype, scale=0.3).to(DEV) for s in ((V, K), (K, N), (N,)))
+    dy = rand(g, T, N, dtype=dtype).to(DEV)
+    plan = api.rar_linear_plan(K, N, CODE[dtype], api.ACT_GELU)
+    x, y, dx = (torch.zeros(T, n, dtype=td, device=DEV) for n in (K, N, K))
+    (xp, xg), (zp, zg) = api.rar_ckpt_size(K), api.rar_ckpt_size(N)
+    xc, xs, zc, zs = (torch.zeros(T, n, dtype=torch.uint8, device=DEV) for n in (xp, xg, zp, zg))
+    dw, db, grad = (torch.zeros(*s, dtype=td, device=DEV) for s in ((K, N), (N,), (V, K)))
+
+    def call(stream=None):
+        c = CODE[dtype]
+        api.rar_embed_lookup(V, K, c, table, T, ids, x, 2.0, stream=stream)
+        api.rar_ckpt_store(T, K, c, x, xc, xs, stream=stream)
+        api.rar_linear_forward(plan, T, x, w, b, None, y, pre=zc, pre_scales=zs, stream=stream)
+        api.rar_linear_backward(plan, T, dy, xc, w, zc, dx, dw, db, x_scales=xs, pre_scales=zs, stream=stream)
+        api.rar_embed_grad(V, K, c, T, ids, dx, grad, 2.0, stream=stream)
+
+    return call, [x, xc, xs, y, zc, zs, dx, dw, db, grad]
+
+
+def _bits(outs):
+    return [t.clone() for t in outs]
+
+
+def _same(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_repeated_calls_give_the_same_bits(dtype):
+    call, outs = _step(dtype)
+    call()
+    torch.cuda.synchronize()
+    first = _bits(outs)
+    for _ in range(5):
+        for t in outs:
+            t.zero_()
+        call()
+        torch.cuda.synchronize()
+        assert _same(outs, first)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_other_streams_and_two_at_once(dtype):
+    (call_a, a), (call_b, b) = _step(dtype), _step(dtype)
+    call_a()
+    torch.cuda.synchronize()
+    want = _bits(a)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for t in a:
+        t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        call_a(s1)                   # a torch stream, workspace allocated on another
+        call_b(s2.cuda_stream)       # a raw stream handle
+    torch.cuda.synchronize()
+    assert _same(a, want) and _same(b, want)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_replays_from_graphs(dtype):
+    # two graphs captured from two copies, replayed together, with eager work between the replays
+    (call_a, a), (call_b, b) = _step(dtype), _step(dtype)
+    call_a()
+    call_b()
+    torch.cuda.synchronize()
+    want = _bits(a)
+    graphs = []
+    for call in (call_a, call_b):
+        gph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gph):
+            call()
+        graphs.append(gph)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for rep in range(4):
+        for t in a + b:
+            t.zero_()
+        _ = torch.randn(1000, device=DEV).sum().item()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            graphs[0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        assert _same(a, want) and _same(b, want), f"replay {rep}"
