@@ -24,18 +24,16 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kGemmThreads = 256;
-constexpr int kRowBytes = 128;             // bytes of reduction per step of a contiguous operand
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ---------------------------------------------------------------------------
 // Staging: memory -> LDS, 16 bytes a lane, without passing through registers
 // ---------------------------------------------------------------------------
 //
-// One step stages kRowBytes / ES reduction indices of R rows of an operand.
-//   contiguous: LDS row r holds its 128 bytes of k; the 16-byte chunk c lies at
-//               slot c ^ (r & 7), so 16 lanes that read one chunk of 16 rows
-//               touch every bank once.
+// One step stages RB / ES reduction indices of R rows of an operand.
+//   contiguous: LDS row r holds its RB bytes of k; the 16-byte chunk c lies at
+//               slot c ^ row_perm(r), so 16 lanes that read one chunk of 16
+//               rows touch every bank once.
 //   slow:       LDS row k holds R elements; bf16 units of 16 elements are
 //               permuted by f(k), binary32 by one bit of k, so that the four
 //               k rows of a transposing read (or the two of a binary32 read)
@@ -54,10 +52,16 @@ __device__ __forceinline__ int slow_perm(int k)
     return ES == 2 ? ((k & 3) | (((k >> 3) & 3) << 2)) : ((k >> 2) & 1);
 }
 
-template <int ES, int R, bool CONTIG>
+template <int RB>
+__device__ __forceinline__ int row_perm(int r)
+{
+    return RB == 128 ? (r & 7) : ((r >> 2) & 3);
+}
+
+template <int ES, int R, int RB, int WAVES, bool CONTIG>
 struct Stage {
-    static constexpr int kLoads = R * kRowBytes / (kGemmThreads * 16);
-    static constexpr int kStep = kRowBytes / ES;  // reduction indices of one step
+    static constexpr int kLoads = R * RB / (WAVES * 1024);
+    static constexpr int kStep = RB / ES;  // reduction indices of one step
     uint32_t voff[kLoads];
     const char *base;
     int64_t left;     // bytes from base to the end of the operand
@@ -67,28 +71,35 @@ struct Stage {
     // and the host packs rows that end inside one with zeros.
     static __device__ __forceinline__ int64_t whole(int64_t n) { return (n + 16 / ES - 1) / (16 / ES) * (16 / ES); }
 
+    // Contiguous: row and source chunk of this lane's j-th load.
+    static __device__ __forceinline__ int row_of(int j)
+    {
+        return (j * WAVES + (threadIdx.x >> 6)) * (1024 / RB) + (threadIdx.x & 63) / (RB / 16);
+    }
+    static __device__ __forceinline__ int chunk_of(int j)
+    {
+        return ((threadIdx.x & 63) % (RB / 16)) ^ row_perm<RB>(row_of(j));
+    }
+
     // rows [r0, ...) of `rows`, reduction indices [k0, ...) of `kred`
     __device__ __forceinline__ void init(const void *p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t kred)
     {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
         if (CONTIG) {
             base = (const char *)p + (r0 * ld + k0) * ES;
             left = ((rows - 1 - r0) * ld + whole(kred - k0)) * ES;
-            advance = kRowBytes;
+            advance = RB;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int r = (j * 4 + wave) * 8 + (lane >> 3);
-                voff[j] = (uint32_t)(r * ld * ES) + (((lane & 7) ^ (r & 7)) << 4);
-            }
+            for (int j = 0; j < kLoads; ++j)
+                voff[j] = (uint32_t)(row_of(j) * ld * ES) + (chunk_of(j) << 4);
         } else {
-            constexpr int RB = R * ES;
+            constexpr int kRow = R * ES;
             base = (const char *)p + (k0 * ld + r0) * ES;
             left = ((kred - 1 - k0) * ld + whole(rows - r0)) * ES;
             advance = kStep * ld * ES;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int at = (j * 4 + wave) * 1024 + lane * 16;
-                const int k = at / RB, slot = (at % RB) / 16;
+                const int at = (j * WAVES + (threadIdx.x >> 6)) * 1024 + (threadIdx.x & 63) * 16;
+                const int k = at / kRow, slot = (at % kRow) / 16;
                 int src;
                 if (ES == 2)
                     src = (((slot >> 1) ^ (slow_perm<2>(k) & (R / 16 - 1))) << 1) | (slot & 1);
@@ -99,32 +110,40 @@ struct Stage {
         }
     }
 
-    // chunks of a contiguous operand behind the last `kleft` reduction indices
+    // Chunks of a contiguous operand behind the last `kleft` reduction indices.
     __device__ __forceinline__ void cut(int64_t kleft)
     {
         if (!CONTIG)
             return;
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int r = (j * 4 + wave) * 8 + (lane >> 3);
-            const int chunk = (lane & 7) ^ (r & 7);
-            if (chunk * (16 / ES) >= kleft)
-                voff[j] = kOutOfRange;
-        }
-    }
-
-    __device__ __forceinline__ void load(RAR_LDS char *__restrict__ lds)
-    {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int64_t n = left < 0 ? 0 : (left > 0x7fffffff ? 0x7fffffff : left);
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * 4 + wave) * 1024), 16, voff[j], 0,
-                                                     0, 0);
+            if (chunk_of(j) * (16 / ES) >= kleft)
+                voff[j] = kOutOfRange;
+    }
+
+    // The descriptor of the next step (empty: it reads zeros); load() issues its j-th load.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(bool empty)
+    {
+        const int64_t n = left < 0 || empty ? 0 : (left > 0x7fffffff ? 0x7fffffff : left);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
         base += advance;
         left -= advance;
+        return r;
+    }
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, RAR_LDS char *__restrict__ lds, int j) const
+    {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * WAVES + wave) * 1024), 16, voff[j], 0,
+                                                 0, 0);
+    }
+
+    __device__ __forceinline__ void load_all(RAR_LDS char *__restrict__ lds, bool empty)
+    {
+        const __amdgpu_buffer_rsrc_t r = next(empty);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            load(r, lds, j);
     }
 };
 
@@ -133,9 +152,9 @@ struct Stage {
 // ---------------------------------------------------------------------------
 
 // bf16, v_mfma_f32_16x16x32: lane l holds row l % 16 and the eight reduction
-// indices (l / 16) * 8 .. +7 of a step's half `sub`.  A slow operand is read
-// with the transposing LDS read: each 16 lanes read four k rows of 16 columns
-// and receive their own column's four values.
+// indices (l / 16) * 8 .. +7 of a step.  A slow operand is read with the
+// transposing LDS read: each 16 lanes read four k rows of 16 columns and
+// receive their own column's four values.
 template <int R, bool CONTIG, int NF>
 struct Frag16 {
     uint32_t off[CONTIG ? 1 : NF];
@@ -144,7 +163,7 @@ struct Frag16 {
     {
         const int lane = threadIdx.x & 63;
         if (CONTIG) {
-            off[0] = (w0 + (lane & 15)) * kRowBytes + (((lane >> 4) ^ (lane & 7)) << 4);
+            off[0] = (w0 + (lane & 15)) * 64 + (((lane >> 4) ^ row_perm<64>(lane & 15)) << 4);
         } else {
             const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
             const int f = slow_perm<2>(k) & (R / 16 - 1);
@@ -154,11 +173,11 @@ struct Frag16 {
         }
     }
 
-    __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int sub, int i) const
+    __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int i) const
     {
         if (CONTIG)
-            return *(const RAR_LDS bf16x8 *)(lds + (off[0] ^ (sub << 6)) + i * 16 * kRowBytes);
-        const RAR_LDS char *p = lds + off[CONTIG ? 0 : i] + sub * 32 * (R * 2);
+            return *(const RAR_LDS bf16x8 *)(lds + off[0] + i * 16 * 64);
+        const RAR_LDS char *p = lds + off[CONTIG ? 0 : i];
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)p);
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)(p + 4 * (R * 2)));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -177,7 +196,7 @@ struct Frag32 {
         const int lane = threadIdx.x & 63;
         const int row = w0 + (lane & 31), half = lane >> 5;
         if (CONTIG)
-            off = row * kRowBytes + ((half ^ (row & 7)) << 4);
+            off = row * 128 + ((half ^ (row & 7)) << 4);
         else
             off = half * 4 * (R * 4) + ((row * 4) ^ (half << 7));
     }
@@ -185,7 +204,7 @@ struct Frag32 {
     __device__ __forceinline__ f32x4 read(const RAR_LDS char *__restrict__ lds, int c, int i) const
     {
         if (CONTIG)
-            return *(const RAR_LDS f32x4 *)(lds + (off ^ (c << 5)) + i * 32 * kRowBytes);
+            return *(const RAR_LDS f32x4 *)(lds + (off ^ (c << 5)) + i * 32 * 128);
         // 32 columns are 128 bytes: an odd block of them flips the permuted bit
         const RAR_LDS char *p = lds + (off ^ (i << 7)) + c * 8 * (R * 4);
         return f32x4{*(const RAR_LDS float *)p, *(const RAR_LDS float *)(p + R * 4),
@@ -308,45 +327,58 @@ __device__ __forceinline__ void tile_of(const GemmParams &p, int64_t &tm, int64_
     tn = in / rows;
 }
 
-__device__ __forceinline__ void wait_loads_and_meet()
+// Own loads into LDS but the last N have arrived; then everyone's.  LDS reads
+// in flight are no concern inside the ring: a buffer is loaded again two
+// meetings after its reads, whose results were used before the second.
+template <int N>
+__device__ __forceinline__ void wait_loads()
 {
-    // own loads into LDS have arrived and own LDS reads are done; then everyone's
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Own loads into LDS and LDS reads are done; then everyone's.
+__device__ __forceinline__ void drain()
+{
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// Rows I0 .. I1 - 1 of a wave's fragments, one step of 32 reduction indices.
-template <int FM, int FN, int I0, int I1>
-__device__ __forceinline__ void products(f32x4 (&acc)[FM][FN], const bf16x8 (&a)[FM], const bf16x8 (&b)[FN])
+// acc += b a, with the accumulator kept in an accumulation register: left to
+// itself the compiler moves the 256 of a large tile back and forth between the
+// two register files, about two moves a product.  The statements keep their
+// order among each other and among the LDS accesses between them, so the
+// kernel's text is its schedule.
+__device__ __forceinline__ void product(f32x4 &acc, bf16x8 b, bf16x8 a)
 {
-#pragma unroll
-    for (int i = I0; i < I1; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
 // ---------------------------------------------------------------------------
 // bf16 product
 // ---------------------------------------------------------------------------
 //
-// Four waves as 2 x 2 hold a BM x BN tile in accumulators; a step of 64
-// reduction indices is staged in one half of LDS while the other is used.  A
-// step's two halves of 32 are read into registers one half ahead of the matrix
-// instructions that use them, so the only wait is for a step's loads, issued a
-// whole step before:
-//     read F1 (second half of the step)   | products of F0
-//     first products of F1; wait; barrier
-//     read F0 of the next step, stage the step after it | other products of F1
-template <int BM, int BN, bool ACONTIG, bool BCONTIG>
-__global__ void __launch_bounds__(kGemmThreads, BM * BN >= 65536 ? 1 : 2) rar_gemm_bf16(const GemmParams p)
+// WM x WN waves hold a BM x BN tile in accumulators.  Steps of 32 reduction
+// indices pass through a ring of kRing LDS buffers.  In step s a wave
+//   waits for its own loads of step s + 1 (those of later steps stay in
+//   flight), meets the others, and then runs its products of step s, between
+//   which it replaces its fragments by those of step s + 1 and issues the loads
+//   of step s + kRing - 1 into the buffer of step s - 1.
+// Fragments of A are replaced in place once their row of products is issued;
+// those of B need two sets.  Loads are spread over the step: a 1 KiB load
+// occupies the CU's address unit for 16 cycles, the time of one product, and a
+// burst of them holds the products up.
+template <int BM, int BN, int WM, int WN, bool ACONTIG, bool BCONTIG>
+__global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParams p)
 {
 // (the host pass needs the kernel's name only)
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int FM = BM / 32, FN = BN / 32;  // 16-row fragments of a wave
-    constexpr int kHalf = (BM + BN) * kRowBytes;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kHalf];
+    constexpr int kWaves = WM * WN, kRing = 5;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
+    constexpr int kBuf = (BM + BN) * 64;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[kRing * kBuf];
     RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
     int64_t tm, tn;
@@ -355,13 +387,14 @@ __global__ void __launch_bounds__(kGemmThreads, BM * BN >= 65536 ? 1 : 2) rar_ge
     const int64_t m0 = tm * BM, n0 = tn * BN;
     const int64_t k0 = split * p.steps_per_split * 64;
     const int64_t kend = k0 + p.steps_per_split * 64 < p.K ? k0 + p.steps_per_split * 64 : p.K;
-    const int steps = k0 < kend ? (int)((kend - k0 + 63) / 64) : 0;
-    const int wave = threadIdx.x >> 6, wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+    const int steps = k0 < kend ? (int)((kend - k0 + 31) / 32) : 0;
+    const int wave = threadIdx.x >> 6, wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
 
-    Stage<2, BM, ACONTIG> sa;
-    Stage<2, BN, BCONTIG> sb;
+    Stage<2, BM, 64, kWaves, ACONTIG> sa;
+    Stage<2, BN, 64, kWaves, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
+    constexpr int kLoads = sa.kLoads + sb.kLoads;
     Frag16<BM, ACONTIG, FM> fa;
     Frag16<BN, BCONTIG, FN> fb;
     fa.init(wm);
@@ -374,48 +407,67 @@ __global__ void __launch_bounds__(kGemmThreads, BM * BN >= 65536 ? 1 : 2) rar_ge
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto stage = [&](int s) __attribute__((always_inline)) {
-        if (s < steps) {
-            if (s == steps - 1) {
-                sa.cut(kend - k0 - (int64_t)s * 64);
-                sb.cut(kend - k0 - (int64_t)s * 64);
-            }
-            RAR_LDS char *to = lds + (s & 1) * kHalf;
-            sa.load(to);
-            sb.load(to + BM * kRowBytes);
+    // The last step's reduction may end inside it; steps behind it are zeros.
+    auto cut = [&](int s) __attribute__((always_inline)) {
+        if (s == steps - 1) {
+            sa.cut(kend - k0 - (int64_t)s * 32);
+            sb.cut(kend - k0 - (int64_t)s * 32);
         }
     };
-    bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
-    auto read = [&](int s, int sub, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) __attribute__((always_inline)) {
-        const RAR_LDS char *from = lds + (s & 1) * kHalf;
+    bf16x8 a[FM], b0[FN], b1[FN];
+    int from = 0;                     // LDS offset of the step whose fragments are read next
+    int to = (kRing - 1) * kBuf;      // and of the buffer that is loaded next
+
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            b[j] = fb.read(from + BM * kRowBytes, sub, j);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            a[i] = fa.read(from, sub, i);
-    };
-    if (steps > 0) {
-        stage(0);
-        wait_loads_and_meet();
-        read(0, 0, a0, b0);
-        stage(1);
+    for (int s = 0; s < kRing - 1; ++s) {
+        cut(s);
+        sa.load_all(lds + s * kBuf, s >= steps);
+        sb.load_all(lds + s * kBuf + BM * 64, s >= steps);
     }
-    for (int s = 0; s < steps; ++s) {
-        read(s, 1, a1, b1);
-        products<FM, FN, 0, FM>(acc, a0, b0);
-        __builtin_amdgcn_sched_barrier(0);
-        products<FM, FN, 0, FM / 2>(acc, a1, b1);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_loads_and_meet();
-        read(s + 1, 0, a0, b0);  // behind the last step: unused
-        stage(s + 2);
-        products<FM, FN, FM / 2, FM>(acc, a1, b1);
-        __builtin_amdgcn_sched_barrier(0);
+    wait_loads<kLoads *(kRing - 2)>();
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        b0[j] = fb.read(lds + BM * 64, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        a[i] = fa.read(lds, i);
+    from = kBuf;
+
+    auto step = [&](int s, bf16x8 (&b)[FN], bf16x8 (&bn)[FN]) __attribute__((always_inline)) {
+        cut(s + kRing - 1);
+        const __amdgpu_buffer_rsrc_t ra = sa.next(s + kRing - 1 >= steps), rb = sb.next(s + kRing - 1 >= steps);
+        RAR_LDS char *const src = lds + from;
+        RAR_LDS char *const dst = lds + to;
+        wait_loads<kLoads *(kRing - 3)>();
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                product(acc[i][j], b[j], a[i]);
+            a[i] = fa.read(src, i);
+            // the other fragments and the loads, spread over the rows
+#pragma unroll
+            for (int e = i * (FN + kLoads) / FM; e < (i + 1) * (FN + kLoads) / FM; ++e) {
+                if (e < FN)
+                    bn[e] = fb.read(src + BM * 64, e);
+                else if (e < FN + sa.kLoads)
+                    sa.load(ra, dst, e - FN);
+                else
+                    sb.load(rb, dst + BM * 64, e - FN - sa.kLoads);
+            }
+        }
+        from = from == (kRing - 1) * kBuf ? 0 : from + kBuf;
+        to = to == (kRing - 1) * kBuf ? 0 : to + kBuf;
+    };
+    for (int s = 0; s < steps; s += 2) {
+        step(s, b0, b1);
+        step(s + 1, b1, b0);
     }
 
+    // the last products' results (the compiler does not know the statements' latency)
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // every wave has read its last fragments: LDS is free for the results
-    wait_loads_and_meet();
+    drain();
     const int lane = threadIdx.x & 63;
     RAR_LDS char *const tile = lds + wave * (32 * FN * 16 * 4);
 #pragma unroll
@@ -438,11 +490,11 @@ __global__ void __launch_bounds__(kGemmThreads, BM * BN >= 65536 ? 1 : 2) rar_ge
 // cycle, so a 128 x 128 tile with plain double buffering keeps the matrix cores
 // fed: per instruction (64 cycles) a wave reads a quarter of a kilobyte of LDS.
 template <bool ACONTIG, bool BCONTIG>
-__global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams p)
+__global__ void __launch_bounds__(256, 2) rar_gemm_f32(const GemmParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int BM = 128, BN = 128, kStep = 32;
-    constexpr int kHalf = (BM + BN) * kRowBytes;
+    constexpr int kHalf = (BM + BN) * 128;
     __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kHalf];
     RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
@@ -455,8 +507,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams
     const int steps = k0 < kend ? (int)((kend - k0 + kStep - 1) / kStep) : 0;
     const int wave = threadIdx.x >> 6, wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
 
-    Stage<4, BM, ACONTIG> sa;
-    Stage<4, BN, BCONTIG> sb;
+    Stage<4, BM, 128, 4, ACONTIG> sa;
+    Stage<4, BN, 128, 4, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
     Frag32<BM, ACONTIG> fa;
@@ -480,14 +532,14 @@ __global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams
                 sb.cut(kend - k0 - (int64_t)s * kStep);
             }
             RAR_LDS char *to = lds + (s & 1) * kHalf;
-            sa.load(to);
-            sb.load(to + BM * kRowBytes);
+            sa.load_all(to, false);
+            sb.load_all(to + BM * 128, false);
         }
     };
 
     stage(0);
     for (int s = 0; s < steps; ++s) {
-        wait_loads_and_meet();
+        drain();
         stage(s + 1);
         const RAR_LDS char *from = lds + (s & 1) * kHalf;
 #pragma unroll
@@ -496,7 +548,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 a[i] = fa.read(from, c, i);
-                b[i] = fb.read(from + BM * kRowBytes, c, i);
+                b[i] = fb.read(from + BM * 128, c, i);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -508,7 +560,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) rar_gemm_f32(const GemmParams
         }
     }
 
-    wait_loads_and_meet();
+    drain();
     const int lane = threadIdx.x & 63;
     RAR_LDS char *const tile = lds + wave * (32 * 64 * 4);
 #pragma unroll
@@ -652,15 +704,15 @@ __global__ void __launch_bounds__(256) rar_column_sum(const SumParams p)
     }
 }
 
-template <int BM, int BN>
+template <int B, int WM, int WN>
 hipError_t run_bf16(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_t st)
 {
     if (l == kGemmForward)
-        rar_gemm_bf16<BM, BN, true, false><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_bf16<B, B, WM, WN, true, false><<<grid, 64 * WM * WN, 0, st>>>(p);
     else if (l == kGemmGradX)
-        rar_gemm_bf16<BM, BN, true, true><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_bf16<B, B, WM, WN, true, true><<<grid, 64 * WM * WN, 0, st>>>(p);
     else
-        rar_gemm_bf16<BM, BN, false, false><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_bf16<B, B, WM, WN, false, false><<<grid, 64 * WM * WN, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -671,13 +723,13 @@ hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big
 {
     const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * p.splits);
     if (dt == RAR_BF16)
-        return big ? run_bf16<256, 256>(l, p, grid, st) : run_bf16<128, 128>(l, p, grid, st);
+        return big ? run_bf16<256, 2, 4>(l, p, grid, st) : run_bf16<128, 2, 2>(l, p, grid, st);
     if (l == kGemmForward)
-        rar_gemm_f32<true, false><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_f32<true, false><<<grid, 256, 0, st>>>(p);
     else if (l == kGemmGradX)
-        rar_gemm_f32<true, true><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_f32<true, true><<<grid, 256, 0, st>>>(p);
     else
-        rar_gemm_f32<false, false><<<grid, kGemmThreads, 0, st>>>(p);
+        rar_gemm_f32<false, false><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
 }
 

@@ -176,13 +176,13 @@ def test_binding_checks_tensors_before_the_call():
     with pytest.raises(TypeError):
         fwd(x="no")
     with pytest.raises(ValueError, match="dtype"):
-        api.rar_embed_lookup(5, 8, api.F32, f(5, 8), 3, torch.zeros(3, dtype=torch.int32), f(3, 8))
+        api.rar_embed_lookup(5, 8, api.F32, A[0], 3, torch.zeros(3, dtype=torch.int32), A[1])
     with pytest.raises(ValueError, match="elements"):
-        api.rar_embed_grad(5, 8, api.F32, 3, 0x1000, 0x2000, f(5, 7))
+        api.rar_embed_grad(5, 8, api.F32, 3, A[0], A[1], f(5, 7))
     with pytest.raises(ValueError, match="elements"):
-        api.rar_ckpt_store(3, 40, api.F32, 0x1000, torch.zeros(3, 40, dtype=torch.uint8), torch.zeros(3, 2, dtype=torch.uint8))
+        api.rar_ckpt_store(3, 40, api.F32, A[0], torch.zeros(3, 40, dtype=torch.uint8), A[1])
     with pytest.raises(TypeError):
-        api.rar_embed_grad(5, 8, api.F32, 3, 0x1000, 0x2000, 0x3000, ws=0x4000)
+        api.rar_embed_grad(5, 8, api.F32, 3, A[0], A[1], A[2], ws=A[3])
 
 
 def test_plain_checkpoint_definition():
