@@ -152,10 +152,10 @@ struct Stage {
 // ---------------------------------------------------------------------------
 
 // bf16, v_mfma_f32_16x16x32: lane l holds row l % 16 and the eight reduction
-// indices (l / 16) * 8 .. +7 of a step.  A slow operand is read with the
+// indices (l / 16) * 8 .. +7 of a half step of 32.  A slow operand is read with the
 // transposing LDS read: each 16 lanes read four k rows of 16 columns and
 // receive their own column's four values.
-template <int R, bool CONTIG, int NF>
+template <int R, int RB, bool CONTIG, int NF>
 struct Frag16 {
     uint32_t off[CONTIG ? 1 : NF];
 
@@ -163,7 +163,7 @@ struct Frag16 {
     {
         const int lane = threadIdx.x & 63;
         if (CONTIG) {
-            off[0] = (w0 + (lane & 15)) * 64 + (((lane >> 4) ^ row_perm<64>(lane & 15)) << 4);
+            off[0] = (w0 + (lane & 15)) * RB + (((lane >> 4) ^ row_perm<RB>(lane & 15)) << 4);
         } else {
             const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
             const int f = slow_perm<2>(k) & (R / 16 - 1);
@@ -173,11 +173,11 @@ struct Frag16 {
         }
     }
 
-    __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int i) const
+    __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int half, int i) const
     {
         if (CONTIG)
-            return *(const RAR_LDS bf16x8 *)(lds + off[0] + i * 16 * 64);
-        const RAR_LDS char *p = lds + off[CONTIG ? 0 : i];
+            return *(const RAR_LDS bf16x8 *)(lds + (off[0] ^ (half << 6)) + i * 16 * RB);
+        const RAR_LDS char *p = lds + off[CONTIG ? 0 : i] + half * 32 * (R * 2);
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)p);
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)(p + 4 * (R * 2)));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -360,25 +360,24 @@ __device__ __forceinline__ void product(f32x4 &acc, bf16x8 b, bf16x8 a)
 // bf16 product
 // ---------------------------------------------------------------------------
 //
-// WM x WN waves hold a BM x BN tile in accumulators.  Steps of 32 reduction
-// indices pass through a ring of kRing LDS buffers.  In step s a wave
-//   waits for its own loads of step s + 1 (those of later steps stay in
-//   flight), meets the others, and then runs its products of step s, between
-//   which it replaces its fragments by those of step s + 1 and issues the loads
-//   of step s + kRing - 1 into the buffer of step s - 1.
+// WM x WN waves hold a BM x BN tile in accumulators.  A step of 64 reduction
+// indices is staged in one half of LDS while the other is used; its two halves
+// of 32 pass through registers:
+//   half 0   products of half 0, reading the fragments of half 1
+//   half 1   wait for the next step's loads, meet the other waves; products of
+//            half 1, reading the next step's half 0, and issuing the loads of
+//            the step after it into the LDS half that everyone has now read
 // Fragments of A are replaced in place once their row of products is issued;
-// those of B need two sets.  Loads are spread over the step: a 1 KiB load
-// occupies the CU's address unit for 16 cycles, the time of one product, and a
-// burst of them holds the products up.
+// those of B need two sets.
 template <int BM, int BN, int WM, int WN, bool ACONTIG, bool BCONTIG>
 __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParams p)
 {
 // (the host pass needs the kernel's name only)
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int kWaves = WM * WN, kRing = 5;
+    constexpr int kWaves = WM * WN;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
-    constexpr int kBuf = (BM + BN) * 64;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[kRing * kBuf];
+    constexpr int kBuf = (BM + BN) * 128;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kBuf];
     RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
     int64_t tm, tn;
@@ -387,16 +386,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
     const int64_t m0 = tm * BM, n0 = tn * BN;
     const int64_t k0 = split * p.steps_per_split * 64;
     const int64_t kend = k0 + p.steps_per_split * 64 < p.K ? k0 + p.steps_per_split * 64 : p.K;
-    const int steps = k0 < kend ? (int)((kend - k0 + 31) / 32) : 0;
+    const int steps = k0 < kend ? (int)((kend - k0 + 63) / 64) : 0;
     const int wave = threadIdx.x >> 6, wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
 
-    Stage<2, BM, 64, kWaves, ACONTIG> sa;
-    Stage<2, BN, 64, kWaves, BCONTIG> sb;
+    Stage<2, BM, 128, kWaves, ACONTIG> sa;
+    Stage<2, BN, 128, kWaves, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
     constexpr int kLoads = sa.kLoads + sb.kLoads;
-    Frag16<BM, ACONTIG, FM> fa;
-    Frag16<BN, BCONTIG, FN> fb;
+    Frag16<BM, 128, ACONTIG, FM> fa;
+    Frag16<BN, 128, BCONTIG, FN> fb;
     fa.init(wm);
     fb.init(wn);
 
@@ -407,61 +406,60 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // The last step's reduction may end inside it; steps behind it are zeros.
+    // The last step's reduction may end inside it.
     auto cut = [&](int s) __attribute__((always_inline)) {
         if (s == steps - 1) {
-            sa.cut(kend - k0 - (int64_t)s * 32);
-            sb.cut(kend - k0 - (int64_t)s * 32);
+            sa.cut(kend - k0 - (int64_t)s * 64);
+            sb.cut(kend - k0 - (int64_t)s * 64);
         }
     };
     bf16x8 a[FM], b0[FN], b1[FN];
-    int from = 0;                     // LDS offset of the step whose fragments are read next
-    int to = (kRing - 1) * kBuf;      // and of the buffer that is loaded next
-
 #pragma unroll
-    for (int s = 0; s < kRing - 1; ++s) {
+    for (int s = 0; s < 2; ++s) {
         cut(s);
         sa.load_all(lds + s * kBuf, s >= steps);
-        sb.load_all(lds + s * kBuf + BM * 64, s >= steps);
+        sb.load_all(lds + s * kBuf + BM * 128, s >= steps);
     }
-    wait_loads<kLoads *(kRing - 2)>();
+    wait_loads<kLoads>();
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-        b0[j] = fb.read(lds + BM * 64, j);
+        b0[j] = fb.read(lds + BM * 128, 0, j);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-        a[i] = fa.read(lds, i);
-    from = kBuf;
+        a[i] = fa.read(lds, 0, i);
 
-    auto step = [&](int s, bf16x8 (&b)[FN], bf16x8 (&bn)[FN]) __attribute__((always_inline)) {
-        cut(s + kRing - 1);
-        const __amdgpu_buffer_rsrc_t ra = sa.next(s + kRing - 1 >= steps), rb = sb.next(s + kRing - 1 >= steps);
-        RAR_LDS char *const src = lds + from;
-        RAR_LDS char *const dst = lds + to;
-        wait_loads<kLoads *(kRing - 3)>();
+    for (int s = 0; s < steps; ++s) {
+        RAR_LDS char *const here = lds + (s & 1) * kBuf;
+        RAR_LDS char *const next = lds + (kBuf - (s & 1) * kBuf);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                product(acc[i][j], b[j], a[i]);
-            a[i] = fa.read(src, i);
-            // the other fragments and the loads, spread over the rows
+                product(acc[i][j], b0[j], a[i]);
+            a[i] = fa.read(here, 1, i);
 #pragma unroll
-            for (int e = i * (FN + kLoads) / FM; e < (i + 1) * (FN + kLoads) / FM; ++e) {
-                if (e < FN)
-                    bn[e] = fb.read(src + BM * 64, e);
-                else if (e < FN + sa.kLoads)
-                    sa.load(ra, dst, e - FN);
-                else
-                    sb.load(rb, dst + BM * 64, e - FN - sa.kLoads);
-            }
+            for (int e = i * FN / FM; e < (i + 1) * FN / FM; ++e)
+                b1[e] = fb.read(here + BM * 128, 1, e);
         }
-        from = from == (kRing - 1) * kBuf ? 0 : from + kBuf;
-        to = to == (kRing - 1) * kBuf ? 0 : to + kBuf;
-    };
-    for (int s = 0; s < steps; s += 2) {
-        step(s, b0, b1);
-        step(s + 1, b1, b0);
+        cut(s + 2);
+        const __amdgpu_buffer_rsrc_t ra = sa.next(s + 2 >= steps), rb = sb.next(s + 2 >= steps);
+        drain();
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                product(acc[i][j], b1[j], a[i]);
+            a[i] = fa.read(next, 0, i);
+#pragma unroll
+            for (int e = i * FN / FM; e < (i + 1) * FN / FM; ++e)
+                b0[e] = fb.read(next + BM * 128, 0, e);
+#pragma unroll
+            for (int e = i * kLoads / FM; e < (i + 1) * kLoads / FM; ++e)
+                if (e < sa.kLoads)
+                    sa.load(ra, here, e);
+                else
+                    sb.load(rb, here + BM * 128, e - sa.kLoads);
+        }
     }
 
     // the last products' results (the compiler does not know the statements' latency)
