@@ -109,65 +109,82 @@ __device__ __forceinline__ void store8(bf16 *p, int cnt, bool vec, const float (
             p[i] = from_f32<bf16>(v[i]);
 }
 
-// exp(-x^2) erfc-style tail of the normal distribution: with a = |z|,
-//   erfc(a / sqrt 2) = exp(-a^2 / 2) * q(a / sqrt 2),  q(x) = exp(x^2) erfc(x).
-// q is smooth and falls like 1/x, so it is a polynomial in t = 1 / (1 + 0.33 x)
-// without a constant term; the eight coefficients are a least-maximum fit made
-// for this file (relative error 9.4e-8 for 0 <= x <= 10; beyond that
-// exp(-x^2) < 2^-144).  The relative error stays small in the far tail, where
-// 1 + erf(z / sqrt 2) would cancel.  About 20 instructions, two of them
-// transcendental, against about 60 for erfcf: at 8192 x 8192 outputs the
-// evaluation otherwise takes a sizeable part of the matrix product's time.
+// Upper tail of the normal distribution: with a = |z|,
+//   1 - Phi(a) = exp(-a^2 / 2) * q(a / sqrt 2) / 2,  q(x) = exp(x^2) erfc(x).
+// q is smooth and falls like 1/x, so q/2 is a polynomial in t = 1 / (1 + c x)
+// without a constant term.  The coefficients are least-maximum fits made for
+// this file: degree 8 for binary32 (relative error 9.4e-8 for 0 <= x <= 10;
+// beyond that exp(-x^2) < 2^-144), degree 6 for bf16 (5.2e-6, a hundredth of
+// its half step).  The relative error stays small in the far tail, where
+// 1 + erf(z / sqrt 2) would cancel.  About 17 instructions, two of them
+// transcendental, against about 60 for erfcf: the epilogue of a matrix product
+// evaluates it with the matrix cores idle.
+template <class T>
 __device__ __forceinline__ void normal_tail(float z, float &tail, float &e)
 {
-    const float a = __builtin_fabsf(z);
-    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.33f * 0.70710678118654752f, 1.0f));
-    float q = -0.1353447437286377f;
-    q = __builtin_fmaf(q, t, 0.4602333605289459f);
-    q = __builtin_fmaf(q, t, -0.3511435091495514f);
-    q = __builtin_fmaf(q, t, 0.4084944725036621f);
-    q = __builtin_fmaf(q, t, 0.04722348973155022f);
-    q = __builtin_fmaf(q, t, 0.20122304558753967f);
-    q = __builtin_fmaf(q, t, 0.18295608460903168f);
-    q = __builtin_fmaf(q, t, 0.1863577961921692f);
-    tail = 0.5f * e * (q * t);  // 1 - Phi(|z|)
+    constexpr bool kWide = sizeof(T) == 4;
+    constexpr float kC = (kWide ? 0.33f : 0.44f) * 0.70710678118654752f;
+    e = __builtin_amdgcn_exp2f(z * (z * -0.72134752044448170f));
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(z), kC, 1.0f));
+    float q;
+    if (kWide) {
+        q = 0.5f * -0.1353447437286377f;
+        q = __builtin_fmaf(q, t, 0.5f * 0.4602333605289459f);
+        q = __builtin_fmaf(q, t, 0.5f * -0.3511435091495514f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.4084944725036621f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.04722348973155022f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.20122304558753967f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.18295608460903168f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.1863577961921692f);
+    } else {
+        q = 0.5f * -0.14610587060451508f;
+        q = __builtin_fmaf(q, t, 0.5f * 0.3506527841091156f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.04073116183280945f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.2635860741138458f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.2425696849822998f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.24856099486351013f);
+    }
+    tail = e * (q * t);
 }
 
-// Phi(z) and the normal density; the limits at +-infinity, NaN at NaN.
+// z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the limits at +-infinity (the tail
+// is zero long before the bound on |z|), NaN at NaN.
+template <class T>
 __device__ __forceinline__ float gelu(float z)
 {
     float tail, e;
-    normal_tail(z, tail, e);
-    const float v = z * (z < 0.0f ? tail : 1.0f - tail);
-    return z < -40.0f ? 0.0f : v;
+    normal_tail<T>(z, tail, e);
+    return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 40.0f), tail, __builtin_fmaxf(z, 0.0f));
 }
 
+template <class T>
 __device__ __forceinline__ float gelu_grad(float z)
 {
     float tail, e;
-    normal_tail(z, tail, e);
+    normal_tail<T>(z, tail, e);
     const float phi = z < 0.0f ? tail : 1.0f - tail;
     const float pdf = __builtin_fabsf(z) > 40.0f ? 0.0f : z * (e * 0.39894228040143268f);
     return phi + pdf;
 }
 
+template <class T>
 __device__ __forceinline__ float act_value(int act, float z)
 {
     if (act == RAR_ACT_RELU)
         return z < 0.0f ? 0.0f : z;  // NaN stays NaN
     if (act == RAR_ACT_GELU)
-        return gelu(z);
+        return gelu<T>(z);
     return z;
 }
 
 // act'(z); relu'(0) = 0, NaN at NaN.
+template <class T>
 __device__ __forceinline__ float act_grad(int act, float z)
 {
     if (act == RAR_ACT_RELU)
         return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if (act == RAR_ACT_GELU)
-        return gelu_grad(z);
+        return gelu_grad<T>(z);
     return 1.0f;
 }
 

@@ -257,7 +257,7 @@ __device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = act_value(p.act, v[i]);
+            v[i] = act_value<T>(p.act, v[i]);
         if (p.res) {
             load8((const T *)p.res + m * p.ldr + n, cnt, vec, t);
 #pragma unroll
@@ -273,37 +273,100 @@ __device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t
     store8(out, cnt, vec, v);
 }
 
-// A wave's 32 rows of W columns pass through LDS, so that a lane finishes eight
-// consecutive columns of one row and a row's lanes access whole lines.  The
-// 16-byte chunk c of row r lies at slot c ^ (r & 15): a column of rows spreads
-// over the banks.
+// A wave's ROWS rows of W columns pass through LDS, so that a lane finishes
+// eight consecutive columns of one row and a row's lanes access whole lines.
+// The 16-byte chunk c of row r lies at slot c ^ (r & 15): a column of rows
+// spreads over the banks.
 template <int W>
 __device__ __forceinline__ RAR_LDS f32x4 *tile_slot(RAR_LDS char *tile, int r, int c)
 {
     return (RAR_LDS f32x4 *)(tile + r * (W * 4) + ((c ^ (r & 15)) << 4));
 }
 
-template <class T, int W>
+template <int W>
+__device__ __forceinline__ void tile_row(RAR_LDS char *tile, int r, int q, float (&v)[8])
+{
+    const f32x4 lo = *tile_slot<W>(tile, r, 2 * q), hi = *tile_slot<W>(tile, r, 2 * q + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
+    }
+}
+
+// The usual tile: wholly inside the matrix, rows of whole 16-byte groups, z
+// kept in the layer's type or not at all.  The same results as epilogue(),
+// with the addresses and the bias out of the loop.
+template <class T, int W, int ROWS, int ACT>
+__device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char *tile, int64_t m0, int64_t n0)
+{
+    constexpr int kLanes = W / 8, kRows = 64 / kLanes;
+    const int lane = threadIdx.x & 63, q = lane % kLanes;
+    const int64_t m = m0 + lane / kLanes, n = n0 + q * 8;
+    float bias[8] = {};
+    if (p.bias)
+        load8((const T *)p.bias + n, 8, true, bias);
+    T *out = (T *)p.out + m * p.ldo + n;
+    T *pre = (T *)p.pre + m * p.ldp + n;
+    const T *res = (const T *)p.res + m * p.ldr + n;
+    const int64_t so = kRows * p.ldo, sp = kRows * p.ldp, sr = kRows * p.ldr;
+#pragma unroll 2
+    for (int r = lane / kLanes; r < ROWS; r += kRows) {
+        float v[8], t[8];
+        if (p.res)
+            load8(res, 8, true, t);
+        tile_row<W>(tile, r, q, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += bias[i];
+        if (p.pre)
+            store8(pre, 8, true, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = act_value<T>(ACT, v[i]);
+        if (p.res)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += t[i];
+        store8(out, 8, true, v);
+        out += so;
+        pre += sp;
+        res += sr;
+    }
+}
+
+template <class T, int W, int ROWS>
 __device__ __forceinline__ void finish_rows(const GemmParams &p, int split, RAR_LDS char *tile, int64_t m0, int64_t n0)
 {
     constexpr int kLanes = W / 8, kRows = 64 / kLanes;
     const int lane = threadIdx.x & 63, q = lane % kLanes;
     const int64_t n = n0 + q * 8;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (p.vec && m0 + ROWS <= p.M && n0 + W <= p.N && !p.pre_scales &&
+        (p.mode == kModeForward || (p.mode == kModeStore && !p.accumulate))) {
+        // a plain store has no bias, residual, z or activation
+        if (p.act == RAR_ACT_GELU)
+            finish_inside<T, W, ROWS, RAR_ACT_GELU>(p, tile, m0, n0);
+        else if (p.act == RAR_ACT_RELU)
+            finish_inside<T, W, ROWS, RAR_ACT_RELU>(p, tile, m0, n0);
+        else
+            finish_inside<T, W, ROWS, RAR_ACT_NONE>(p, tile, m0, n0);
+    } else {
 #pragma unroll 1
-    for (int r = lane / kLanes; r < 32; r += kRows) {
-        const f32x4 lo = *tile_slot<W>(tile, r, 2 * q), hi = *tile_slot<W>(tile, r, 2 * q + 1);
-        const int64_t m = m0 + r;
-        if (p.mode == kModePartial) {
-            if (m < p.M && n < p.pitch) {  // pitch is whole groups; columns behind N hold anything
-                float *o = p.part + ((int64_t)split * p.M + m) * p.pitch + n;
-                store4(o, lo);
-                store4(o + 4, hi);
+        for (int r = lane / kLanes; r < ROWS; r += kRows) {
+            float v[8];
+            tile_row<W>(tile, r, q, v);
+            const int64_t m = m0 + r;
+            if (p.mode == kModePartial) {
+                if (m < p.M && n < p.pitch) {  // pitch is whole groups; columns behind N hold anything
+                    float *o = p.part + ((int64_t)split * p.M + m) * p.pitch + n;
+                    store4(o, f32x4{v[0], v[1], v[2], v[3]});
+                    store4(o + 4, f32x4{v[4], v[5], v[6], v[7]});
+                }
+                continue;
             }
-            continue;
+            epilogue<T>(p, m, n, v);
         }
-        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        epilogue<T>(p, m, n, v);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -374,7 +437,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
 {
 // (the host pass needs the kernel's name only)
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int kWaves = WM * WN;
+    constexpr int kWaves = WM * WN, kEarly = 1;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
     constexpr int kBuf = (BM + BN) * 128;
     __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kBuf];
@@ -443,18 +506,27 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
         }
         cut(s + 2);
         const __amdgpu_buffer_rsrc_t ra = sa.next(s + 2 >= steps), rb = sb.next(s + 2 >= steps);
-        drain();
+        // a few rows first: the meeting then finds the last reads done
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
+            if (i == kEarly)
+                drain();
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 product(acc[i][j], b1[j], a[i]);
-            a[i] = fa.read(next, 0, i);
+            if (i < kEarly)
+                continue;
+            constexpr int kReads = FM + FN, kRows = FM - kEarly;
 #pragma unroll
-            for (int e = i * FN / FM; e < (i + 1) * FN / FM; ++e)
-                b0[e] = fb.read(next + BM * 128, 0, e);
+            for (int e = (i - kEarly) * kReads / kRows; e < (i - kEarly + 1) * kReads / kRows; ++e) {
+                // B's fragments, then A's as far as their products are issued
+                if (e < FN)
+                    b0[e] = fb.read(next + BM * 128, 0, e);
+                else
+                    a[e - FN] = fa.read(next, 0, e - FN);
+            }
 #pragma unroll
-            for (int e = i * kLoads / FM; e < (i + 1) * kLoads / FM; ++e)
+            for (int e = (i - kEarly) * kLoads / kRows; e < (i - kEarly + 1) * kLoads / kRows; ++e)
                 if (e < sa.kLoads)
                     sa.load(ra, here, e);
                 else
@@ -467,15 +539,17 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
     // every wave has read its last fragments: LDS is free for the results
     drain();
     const int lane = threadIdx.x & 63;
-    RAR_LDS char *const tile = lds + wave * (32 * FN * 16 * 4);
+    constexpr int kPass = 64;  // rows of a pass: as many as fit
+    static_assert(kWaves * kPass * FN * 16 * 4 <= 2 * kBuf, "results pass through the operands' LDS");
+    RAR_LDS char *const tile = lds + wave * (kPass * FN * 16 * 4);
 #pragma unroll
-    for (int i = 0; i < FM; i += 2) {
+    for (int i = 0; i < FM; i += kPass / 16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kPass / 16; ++h)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 *tile_slot<FN * 16>(tile, h * 16 + (lane & 15), j * 4 + (lane >> 4)) = acc[i + h][j];
-        finish_rows<bf16, FN * 16>(p, split, tile, m0 + wm + i * 16, n0 + wn);
+        finish_rows<bf16, FN * 16, kPass>(p, split, tile, m0 + wm + i * 16, n0 + wn);
     }
 #endif
 }
@@ -560,17 +634,16 @@ __global__ void __launch_bounds__(256, 2) rar_gemm_f32(const GemmParams p)
 
     drain();
     const int lane = threadIdx.x & 63;
-    RAR_LDS char *const tile = lds + wave * (32 * 64 * 4);
+    RAR_LDS char *const tile = lds + wave * (64 * 64 * 4);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                *tile_slot<64>(tile, lane & 31, j * 8 + q * 2 + (lane >> 5)) =
+                *tile_slot<64>(tile, i * 32 + (lane & 31), j * 8 + q * 2 + (lane >> 5)) =
                     f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        finish_rows<float, 64>(p, split, tile, m0 + wm + i * 32, n0 + wn);
-    }
+    finish_rows<float, 64, 64>(p, split, tile, m0 + wm, n0 + wn);
 #endif
 }
 
@@ -659,7 +732,7 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    d[i] = i < cnt ? d[i] * act_grad(p.act, z[i]) : 0.0f;
+                    d[i] = i < cnt ? d[i] * act_grad<T>(p.act, z[i]) : 0.0f;
             }
             sum += d;
             if (p.dz)
