@@ -400,13 +400,38 @@ def rar_bucket_allreduce_arena(b: Buckets, arenas: Sequence, ready_events=None, 
 # Producers of the gradients: embedding, linear layer, 8-bit checkpoints
 # ---------------------------------------------------------------------------
 
+_get_device = None
+
+
+def _here() -> int:
+    """The current device's index, -1 without a GPU."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -1
+        torch.cuda.init()
+        _get_device = torch._C._cuda_getDevice
+    return _get_device()
+
+
+def _on(stream) -> int:
+    """The call's stream; torch's current one costs a tenth of building its Stream object."""
+    if stream is None:
+        dev = _here()
+        if dev >= 0:
+            import torch
+            return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
 def _device_of(x, what: str) -> None:
-    import torch
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         if x.numel():
             raise ValueError(f"{what}: tensor must be on the GPU")
-    elif x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensor is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    elif dev != _here():
+        raise ValueError(f"{what}: tensor is on {x.device}, the current device is cuda:{_here()}")
 
 
 def _matrix(x, what: str, tdtype, rows: int, cols: int):
@@ -417,9 +442,9 @@ def _matrix(x, what: str, tdtype, rows: int, cols: int):
         return x, cols
     if not hasattr(x, "data_ptr"):
         raise TypeError(f"{what}: not a device buffer: {type(x)!r}")
-    if x.dtype != tdtype:
+    if x.dtype is not tdtype:
         raise ValueError(f"{what}: dtype {x.dtype}, expected {tdtype}")
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+    if x.shape != (rows, cols):
         raise ValueError(f"{what}: shape {tuple(x.shape)}, expected ({rows}, {cols})")
     if rows == 0:
         return 0, cols
@@ -440,7 +465,7 @@ def _dense(x, what: str, tdtype, numel: int) -> int:
         return x or 0
     if not hasattr(x, "data_ptr"):
         raise TypeError(f"{what}: not a device buffer: {type(x)!r}")
-    if x.dtype != tdtype:
+    if x.dtype is not tdtype:
         raise ValueError(f"{what}: dtype {x.dtype}, expected {tdtype}")
     if x.numel() != numel:
         raise ValueError(f"{what}: {x.numel()} elements, expected {numel}")
@@ -476,7 +501,7 @@ def rar_embed_lookup(V: int, D: int, dtype: int, table, T: int, ids, out, scale:
     td = _torch_dtype(dtype)
     ptr, ldo = _matrix(out, "out", td, T, D)
     _check(lib().rar_embed_lookup(V, D, dtype, _dense(table, "table", td, V * D), T,
-                                  _dense(ids, "ids", torch.int64, T), scale, ptr, ldo, _stream(stream)),
+                                  _dense(ids, "ids", torch.int64, T), scale, ptr, ldo, _on(stream)),
            "rar_embed_lookup")
 
 
@@ -495,7 +520,7 @@ def rar_embed_grad(V: int, D: int, dtype: int, T: int, ids, dy, grad, scale: flo
     gptr, iptr = _dense(grad, "grad", td, V * D), _dense(ids, "ids", torch.int64, T)
     wptr, wbytes, _own = _workspace(ws, 0 if ws is not None else rar_embed_grad_workspace(V, D, T), stream)
     _check(lib().rar_embed_grad(V, D, dtype, T, iptr, dptr, lddy, scale, int(bool(accumulate)), gptr, wptr, wbytes,
-                                _stream(stream)), "rar_embed_grad")
+                                _on(stream)), "rar_embed_grad")
 
 
 class Linear:
@@ -528,7 +553,7 @@ def rar_linear_destroy(plan: Linear) -> None:
 def rar_linear_workspace(plan: Linear, T: int):
     """(forward bytes, backward bytes) for T rows."""
     f, b = ctypes.c_int64(), ctypes.c_int64()
-    _check(lib().rar_linear_workspace(plan.handle, int(T), ctypes.byref(f), ctypes.byref(b)), "rar_linear_workspace")
+    _check(lib().rar_linear_workspace(plan.handle, T, ctypes.byref(f), ctypes.byref(b)), "rar_linear_workspace")
     return f.value, b.value
 
 
@@ -554,7 +579,7 @@ def rar_linear_forward(plan: Linear, T: int, x, w, bias, residual, y, pre=None, 
     pp, ldp, sp = _kept(pre, pre_scales, "pre", td, T, N)
     wsp, wsb, _own = _workspace(ws, 0 if ws is not None else rar_linear_workspace(plan, T)[0], stream)
     _check(lib().rar_linear_forward(plan.handle, T, xp, ldx, wp, bp, rp, ldr, yp, ldy, pp, ldp, sp, wsp, wsb,
-                                    _stream(stream)), "rar_linear_forward")
+                                    _on(stream)), "rar_linear_forward")
 
 
 def rar_linear_backward(plan: Linear, T: int, dy, x, w, pre, dx, dw, db, x_scales=None, pre_scales=None,
@@ -570,7 +595,7 @@ def rar_linear_backward(plan: Linear, T: int, dy, x, w, pre, dx, dw, db, x_scale
     dwp, dbp = _dense(dw, "dw", td, K * N), _dense(db, "db", td, N)
     wsp, wsb, _own = _workspace(ws, 0 if ws is not None else rar_linear_workspace(plan, T)[1], stream)
     _check(lib().rar_linear_backward(plan.handle, T, dyp, lddy, xp, ldx, xs, wp, pp, ldp, ps, dxp, lddx, dwp, dbp,
-                                     int(bool(accumulate)), wsp, wsb, _stream(stream)), "rar_linear_backward")
+                                     int(bool(accumulate)), wsp, wsb, _on(stream)), "rar_linear_backward")
 
 
 def rar_ckpt_size(D: int):
@@ -583,13 +608,13 @@ def rar_ckpt_size(D: int):
 def rar_ckpt_store(T: int, D: int, dtype: int, x, codes, scales, stream=None) -> None:
     """codes (T x pitch) and scales (T x groups), both uint8, receive the 8-bit checkpoint of x (T x D)."""
     xp, ldx, cp, sp = *_matrix(x, "x", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
-    _check(lib().rar_ckpt_store(T, D, dtype, xp, ldx, cp, sp, _stream(stream)), "rar_ckpt_store")
+    _check(lib().rar_ckpt_store(T, D, dtype, xp, ldx, cp, sp, _on(stream)), "rar_ckpt_store")
 
 
 def rar_ckpt_load(T: int, D: int, dtype: int, codes, scales, y, act: int = ACT_NONE, stream=None) -> None:
     """y (T x D) = act(what the checkpoint holds)."""
     yp, ldy, cp, sp = *_matrix(y, "y", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
-    _check(lib().rar_ckpt_load(T, D, dtype, cp, sp, act, yp, ldy, _stream(stream)), "rar_ckpt_load")
+    _check(lib().rar_ckpt_load(T, D, dtype, cp, sp, act, yp, ldy, _on(stream)), "rar_ckpt_load")
 
 
 def _ckpt(codes, scales, T: int, D: int):

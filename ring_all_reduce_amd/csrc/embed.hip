@@ -7,14 +7,15 @@
 // (every row of the vocabulary is written) or accumulated into the rows that
 // occur.  The token positions are sorted by id, stably, so each row's terms
 // stand together in token order; no floating-point atomic is used and the
-// result does not depend on timing.  A row is then summed by one wave per 512
-// columns.  A frequent token's run can be most of the batch, so runs are
-// summed in two levels beforehand: every aligned 32 sorted positions that hold
-// one id give a partial row, and every aligned 32 of those again; the wave adds
-// the ragged ends and the partial rows, at most about 64 + 64 + T / 1024 terms.
-// The order of the terms depends on the ids alone.
+// result does not depend on timing.  Then one wave sums every 32 sorted
+// positions of 512 columns, whatever ids they hold: dy is read once, evenly,
+// however often a token occurs.  A run of one id inside a chunk is finished
+// there; the parts of a run that crosses chunks go to memory and are added in
+// order, of long runs first 32 at a time.  The order of the terms depends on
+// the ids alone.
 //
-// Bound: dy read once, grad written once; the sort moves 16 bytes a token.
+// Bound: dy read once, grad written once; the sort moves 16 bytes a token, and
+// its launches also clear the gradient.
 #include "act.h"
 #include "ops_internal.h"
 
@@ -74,9 +75,10 @@ __global__ void __launch_bounds__(256) rar_embed_rows(const EmbedParams p)
 
 constexpr int kSortThreads = 1024;                      // sixteen waves
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortKeys = 4096;                         // keys of a workgroup: four rounds of 64 a wave
-constexpr int kRounds = kSortKeys / kSortThreads;
-constexpr int kChunk = 32;                              // sorted positions of a first-level partial row
+constexpr int kRounds = 4;                              // keys of a lane
+constexpr int kSortKeys = kRounds * kSortThreads;       // keys of a workgroup
+constexpr int kSmallKeys = 2 * kSortKeys;               // batches that one workgroup sorts
+constexpr int kChunk = 32;                              // sorted positions that a wave sums
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V)
 {
@@ -91,8 +93,9 @@ struct SortShared {
 
 // Ranks of this wave's keys among the wave's equal digits (in order), counting
 // them in count[wave].  Lanes with `live` false take no part.
-__device__ __forceinline__ void wave_ranks(SortShared &s, const uint32_t (&digit)[kRounds], const bool (&live)[kRounds],
-                                           uint32_t (&rank)[kRounds])
+template <int N>
+__device__ __forceinline__ void wave_ranks(SortShared &s, const uint32_t (&digit)[N], const bool (&live)[N],
+                                           uint32_t (&rank)[N])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < kSortWaves * 256; i += kSortThreads)
@@ -100,7 +103,7 @@ __device__ __forceinline__ void wave_ranks(SortShared &s, const uint32_t (&digit
     __syncthreads();
     volatile uint32_t *count = s.count[wave];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < N; ++r) {
         uint64_t peers = __ballot(live[r]);
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -157,31 +160,64 @@ __device__ __forceinline__ void scan_digits(SortShared &s, uint32_t v, uint32_t 
     __syncthreads();
 }
 
-// A whole batch of at most kSortKeys tokens in one workgroup.
-__global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *ids, int T, int64_t V, int passes,
-                                                               uint32_t *keys, uint32_t *pos)
+// The gradient's rows are cleared by workgroups beside the sort's, which leaves
+// the memory idle: share `part` of `parts` of the bytes, kClearBytes a
+// workgroup.
+constexpr int64_t kClearBytes = 64 * 1024;
+
+struct Clear {
+    char *at;
+    int64_t bytes;
+};
+
+__device__ __forceinline__ void clear(const Clear &c, int64_t block)
 {
+    const int64_t lo = block * kClearBytes, hi = lo + kClearBytes < c.bytes ? lo + kClearBytes : c.bytes;
+    // whole 16-byte groups, and what lies before and behind them by two bytes
+    const int64_t a = lo + (16 - (int64_t)((uintptr_t)(c.at + lo) & 15)) % 16, b = hi - (int64_t)((uintptr_t)(c.at + hi) & 15);
+    if (a > b) {
+        for (int64_t i = lo + threadIdx.x * 2; i < hi; i += kSortThreads * 2)
+            *reinterpret_cast<uint16_t *>(c.at + i) = 0;
+        return;
+    }
+    if (lo + threadIdx.x * 2 < a)
+        *reinterpret_cast<uint16_t *>(c.at + lo + threadIdx.x * 2) = 0;
+    if (b + threadIdx.x * 2 < hi)
+        *reinterpret_cast<uint16_t *>(c.at + b + threadIdx.x * 2) = 0;
+    for (int64_t i = a + threadIdx.x * 16; i < b; i += kSortThreads * 16)
+        *reinterpret_cast<u32x4 *>(c.at + i) = u32x4{0, 0, 0, 0};
+}
+
+// A whole batch of at most N * kSortThreads tokens in one workgroup.
+template <int N>
+__global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *ids, int T, int64_t V, int passes,
+                                                               uint32_t *keys, uint32_t *pos, Clear c)
+{
+    if (blockIdx.x > 0) {
+        clear(c, blockIdx.x - 1);
+        return;
+    }
     __shared__ SortShared s;
-    __shared__ uint32_t k_lds[kSortKeys], p_lds[kSortKeys];
+    __shared__ uint32_t k_lds[N * kSortThreads], p_lds[N * kSortThreads];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t key[kRounds], at[kRounds], digit[kRounds], rank[kRounds];
-    bool live[kRounds];
+    uint32_t key[N], at[N], digit[N], rank[N];
+    bool live[N];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int i = wave * (64 * kRounds) + r * 64 + lane;
+    for (int r = 0; r < N; ++r) {
+        const int i = wave * (64 * N) + r * 64 + lane;
         live[r] = i < T;
         key[r] = live[r] ? key_of(ids[i], V) : 0;
         at[r] = i;
     }
     for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
+        for (int r = 0; r < N; ++r)
             digit[r] = (key[r] >> (8 * pass)) & 255;
         wave_ranks(s, digit, live, rank);
         const uint32_t total = scan_waves(s);
         scan_digits(s, total, 0);
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
+        for (int r = 0; r < N; ++r)
             if (live[r]) {
                 const uint32_t to = s.base[digit[r]] + s.count[wave][digit[r]] + rank[r];
                 k_lds[to] = key[r];
@@ -189,8 +225,8 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
             }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int i = wave * (64 * kRounds) + r * 64 + lane;
+        for (int r = 0; r < N; ++r) {
+            const int i = wave * (64 * N) + r * 64 + lane;
             if (live[r]) {
                 key[r] = k_lds[i];
                 at[r] = p_lds[i];
@@ -199,8 +235,8 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
         __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int i = wave * (64 * kRounds) + r * 64 + lane;
+    for (int r = 0; r < N; ++r) {
+        const int i = wave * (64 * N) + r * 64 + lane;
         if (live[r]) {
             keys[i] = key[r];
             pos[i] = at[r];
@@ -210,8 +246,13 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
 
 // Larger batches: digit counts of each kSortKeys tokens, then their placement.
 __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *ids, const uint32_t *keys, int64_t T,
-                                                               int64_t V, int shift, uint32_t *hist)
+                                                               int64_t V, int shift, uint32_t *hist, unsigned blocks,
+                                                               Clear c)
 {
+    if (blockIdx.x >= blocks) {
+        clear(c, blockIdx.x - blocks);
+        return;
+    }
     __shared__ uint32_t count[256];
     if (threadIdx.x < 256)
         count[threadIdx.x] = 0;
@@ -230,8 +271,12 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *id
 __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *ids, const uint32_t *keys,
                                                                const uint32_t *pos, int64_t T, int64_t V, int shift,
                                                                const uint32_t *hist, uint32_t *keys_out,
-                                                               uint32_t *pos_out)
+                                                               uint32_t *pos_out, unsigned blocks, Clear c)
 {
+    if (blockIdx.x >= blocks) {
+        clear(c, blockIdx.x - blocks);
+        return;
+    }
     __shared__ SortShared s;
     __shared__ uint32_t part[2][4][256];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *id
     // digit totals of all workgroups and of those before this one
     const int d = threadIdx.x & 255, quarter = threadIdx.x >> 8;
     uint32_t all = 0, before = 0;
-    for (int b = quarter; b < (int)gridDim.x; b += 4) {
+    for (int b = quarter; b < (int)blocks; b += 4) {
         const uint32_t c = hist[(int64_t)b * 256 + d];
         all += c;
         before += b < (int)blockIdx.x ? c : 0;
@@ -277,212 +322,259 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *id
 // Sums
 // ---------------------------------------------------------------------------
 
-constexpr int kCols = 512;  // columns of a wave: eight a lane
-
-template <class T>
-__device__ __forceinline__ void row8(const T *row, int64_t c, int cnt, bool vec, float (&v)[8])
-{
-    if (vec && cnt == 8) {
-        const f32x4 a = load4(row + c), b = load4(row + c + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = i < cnt ? to_f32(row[c + i]) : 0.0f;
-}
-
-// acc += rows of dy at the `n` <= 64 sorted positions from `at`, in order; the
-// positions are loaded together, four rows are in flight at a time.
-template <class T>
-__device__ __forceinline__ void add_rows(const EmbedGradParams &p, const uint32_t *pos, int64_t at, int n, int64_t c,
-                                         int cnt, bool vec, float (&acc)[8])
-{
-    const int lane = threadIdx.x & 63;
-    const uint32_t mine = lane < n ? pos[at + lane] : 0;
-    const T *dy = (const T *)p.dy;
-    int i = 0;
-    for (; i + 4 <= n; i += 4) {
-        float v[4][8];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            row8(dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane(mine, i + u) * p.ldy, c, cnt, vec, v[u]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                acc[e] += v[u][e];
-    }
-    for (; i < n; ++i) {
-        float v[8];
-        row8(dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane(mine, i) * p.ldy, c, cnt, vec, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            acc[e] += v[e];
-    }
-}
-
-__device__ __forceinline__ void add_partials(const float *part, int64_t pitch, int64_t at, int64_t n, int64_t c, int cnt,
-                                             float (&acc)[8])
-{
-    if (cnt <= 0)
-        return;
-    const float *row = part + at * pitch + c;  // pitch is whole eights, so every lane's eight exist
-#pragma unroll 4
-    for (int64_t i = 0; i < n; ++i, row += pitch) {
-        const f32x4 a = load4(row), b = load4(row + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[e] += a[e];
-            acc[4 + e] += b[e];
-        }
-    }
-}
+// A wave sums a strip of kCols columns.  Column of lane l's i-th value: l * 8 +
+// i where rows of dy are whole 16-byte groups, else i * 64 + l, so that either
+// way a wave reads consecutive memory.
+constexpr int kCols = 512;
 
 struct GradWs {
-    uint32_t *keys, *pos;    // sorted
-    uint32_t *start;         // [V + 1] first sorted position of each id
-    float *part1, *part2;    // [T / 32][pitch], [T / 1024][pitch]
-    int64_t pitch;
+    uint32_t *keys, *pos;  // sorted
+    // [chunk][pitch]: the part of a run that crosses into the chunk from the
+    // left, and of one that starts in it and goes on to the right; [T / 1024]:
+    // the sum of 32 aligned chunks' `from_left` that hold one id
+    float *from_left, *to_right, *long_run;
+    int64_t pitch;         // whole strips, in the lanes' order
 };
 
-// First workgroups: start[v] by binary search.  The others: one first-level
-// partial row each wave, where 32 aligned positions hold one id.
+// Eight values of a row as they were loaded: widened only when they are added,
+// which halves the registers of bf16 rows in flight.
+template <class T, bool VEC>
+struct Raw {
+    T v[8];
+    __device__ __forceinline__ float at(int i) const { return to_f32(v[i]); }
+};
+
 template <class T>
-__global__ void __launch_bounds__(256) rar_embed_part1(const EmbedGradParams p, const GradWs w, int64_t start_blocks,
-                                                       int strips)
-{
-    if ((int64_t)blockIdx.x < start_blocks) {
-        const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        if (v > p.V)
-            return;
-        int64_t lo = 0, hi = p.T;  // first position with key >= v
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (w.keys[mid] < (uint32_t)v)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        w.start[v] = (uint32_t)lo;
-        return;
+struct Raw<T, true> {
+    u32x4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float at(int i) const
+    {
+        if (sizeof(T) == 4)
+            return __uint_as_float(v[i / 4][i % 4]);
+        return __uint_as_float(i % 2 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
     }
-    const int64_t job = ((int64_t)blockIdx.x - start_blocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+};
+
+template <class T, bool VEC>
+struct Columns {
+    int64_t c0;  // first column of the strip
+    int64_t D;
+
+    __device__ __forceinline__ int64_t col(int i) const
+    {
+        const int lane = threadIdx.x & 63;
+        return c0 + (VEC ? lane * 8 + i : i * 64 + lane);
+    }
+
+    __device__ __forceinline__ void load(const T *row, Raw<T, VEC> &v) const
+    {
+        if constexpr (VEC) {
+            // D is whole eights; lanes behind it read the row's first values
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (col(0) < D ? col(0) : 0));
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                v.v[h] = p[h];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v.v[i] = row[col(i) < D ? col(i) : 0];
+        }
+    }
+
+    // Partial rows are kept in the lanes' order: eight consecutive floats a lane.
+    __device__ __forceinline__ int64_t place() const { return c0 + (threadIdx.x & 63) * 8; }
+
+    __device__ __forceinline__ void add_partials(const float *part, int64_t pitch, int64_t at, int64_t n,
+                                                 float (&acc)[8]) const
+    {
+        const float *row = part + at * pitch + place();
+#pragma unroll 8
+        for (int64_t i = 0; i < n; ++i, row += pitch) {
+            const f32x4 a = load4(row), b = load4(row + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[e] += a[e];
+                acc[4 + e] += b[e];
+            }
+        }
+    }
+
+    __device__ __forceinline__ void put_partial(float *row, const float (&acc)[8]) const
+    {
+        store4(row + place(), f32x4{acc[0], acc[1], acc[2], acc[3]});
+        store4(row + place() + 4, f32x4{acc[4], acc[5], acc[6], acc[7]});
+    }
+
+    // The finished sum of row `key` of the gradient.
+    __device__ __forceinline__ void put_row(const EmbedGradParams &p, uint32_t key, float (&acc)[8]) const
+    {
+        T *out = (T *)p.grad + (int64_t)key * D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[i] *= p.scale;
+        if (p.accumulate) {
+            Raw<T, VEC> old;
+            load(out, old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[i] += old.at(i);
+        }
+        if constexpr (VEC) {
+            store8(out + col(0), col(0) < D ? 8 : 0, true, acc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col(i) < D)
+                    out[col(i)] = from_f32<T>(acc[i]);
+        }
+    }
+};
+
+__device__ __forceinline__ int64_t wave_job(int64_t block) { return block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// One wave: 32 sorted positions of one strip, two batches of rows in flight.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) rar_embed_chunks(const EmbedGradParams p, const GradWs w, int strips)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t job = wave_job(blockIdx.x);
     const int64_t chunk = job / strips;
     const int64_t at = chunk * kChunk;
-    if (at + kChunk > p.T)
+    if (at >= p.T)
         return;
-    const uint32_t k = w.keys[at];
-    if (k >= (uint32_t)p.V || k != w.keys[at + kChunk - 1])
+    // lane l: position at - 1 + l, for one position on either side of the chunk
+    const int64_t i = at - 1 + lane;
+    const bool have = i >= 0 && i < p.T && lane <= kChunk + 1;
+    const uint32_t none = 0xffffffffu;
+    const uint32_t key = have ? w.keys[i] : none;
+    const uint32_t pos = have ? w.pos[i] : 0;
+    // ids outside the vocabulary stand at the end
+    const int n = __popcll(__ballot(lane >= 1 && lane <= kChunk && key < (uint32_t)p.V));
+    if (n == 0)
         return;
-    const int64_t c = (job - chunk * strips) * kCols + (threadIdx.x & 63) * 8;
-    const int cnt = p.D - c >= 8 ? 8 : (p.D - c < 0 ? 0 : (int)(p.D - c));
-    const bool vec = (uintptr_t)p.dy % 16 == 0 && (p.ldy * sizeof(T)) % 16 == 0;
+    const Columns<T, VEC> cols{(job - chunk * strips) * kCols, p.D};
+    const T *dy = (const T *)p.dy;
     float acc[8] = {};
-    add_rows<T>(p, w.pos, at, kChunk, c, cnt, vec, acc);
-    if (cnt > 0) {
-        float *o = w.part1 + chunk * w.pitch + c;
-        store4(o, f32x4{acc[0], acc[1], acc[2], acc[3]});
-        store4(o + 4, f32x4{acc[4], acc[5], acc[6], acc[7]});
+    bool left = __builtin_amdgcn_readlane(key, 0) == __builtin_amdgcn_readlane(key, 1);
+    constexpr int B = sizeof(Raw<T, VEC>) <= 16 ? 8 : 4;  // rows of a batch
+    const auto fetch = [&](Raw<T, VEC>(&v)[B], int r) __attribute__((always_inline)) {
+        // the last row again in place of rows behind it: no branch between the loads
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            cols.load(dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane(pos, 1 + (r + u < n ? r + u : n - 1)) * p.ldy,
+                      v[u]);
+    };
+    const auto add = [&](const Raw<T, VEC>(&v)[B], int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            if (r + u >= n)
+                break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                acc[e] += v[u].at(e);
+            const uint32_t k = __builtin_amdgcn_readlane(key, 1 + r + u), next = __builtin_amdgcn_readlane(key, 2 + r + u);
+            const bool right = r + u == n - 1 && k == next;
+            if (k == next && !right)
+                continue;
+            if (left)
+                cols.put_partial(w.from_left + chunk * w.pitch, acc);
+            else if (right)
+                cols.put_partial(w.to_right + chunk * w.pitch, acc);
+            else
+                cols.put_row(p, k, acc);
+            left = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                acc[e] = 0.0f;
+        }
+    };
+    // A batch is loaded before the one before it is added: loads that follow
+    // that one's stores would wait for them.
+    Raw<T, VEC> v0[B], v1[B];
+    fetch(v0, 0);
+    for (int r = 0; r < n; r += 2 * B) {
+        fetch(v1, r + B);
+        add(v0, r);
+        if (r + B >= n)
+            break;
+        fetch(v0, r + 2 * B);
+        add(v1, r + B);
     }
 }
 
-// Second-level partial rows: 32 aligned first-level rows of one id.
-__global__ void __launch_bounds__(256) rar_embed_part2(const EmbedGradParams p, const GradWs w, int strips)
+// The sum of 32 aligned chunks that hold one id which came in from the left.
+__global__ void __launch_bounds__(256) rar_embed_long(const EmbedGradParams p, const GradWs w, int strips)
 {
-    const int64_t job = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t big = job / strips;
-    const int64_t at = big * (kChunk * kChunk);
-    if (at + kChunk * kChunk > p.T)
+    constexpr int64_t kLong = kChunk * kChunk;
+    const int64_t job = wave_job(blockIdx.x);
+    const int64_t group = job / strips;
+    const int64_t at = group * kLong;
+    if (at + kLong > p.T || at == 0)
         return;
     const uint32_t k = w.keys[at];
-    if (k >= (uint32_t)p.V || k != w.keys[at + kChunk * kChunk - 1])
+    if (k >= (uint32_t)p.V || k != w.keys[at - 1] || k != w.keys[at + kLong - 1])
         return;
-    const int64_t c = (job - big * strips) * kCols + (threadIdx.x & 63) * 8;
-    const int cnt = p.D - c >= 8 ? 8 : (p.D - c < 0 ? 0 : (int)(p.D - c));
+    const Columns<float, true> cols{(job - group * strips) * kCols, p.D};
     float acc[8] = {};
-    add_partials(w.part1, w.pitch, big * kChunk, kChunk, c, cnt, acc);
-    if (cnt > 0) {
-        float *o = w.part2 + big * w.pitch + c;
-        store4(o, f32x4{acc[0], acc[1], acc[2], acc[3]});
-        store4(o + 4, f32x4{acc[4], acc[5], acc[6], acc[7]});
-    }
+    cols.add_partials(w.from_left, w.pitch, group * kChunk, kChunk, acc);
+    cols.put_partial(w.long_run + group * w.pitch, acc);
 }
 
-// One wave per vocabulary row and 512 columns.
-template <class T>
-__global__ void __launch_bounds__(256) rar_embed_sum(const EmbedGradParams p, const GradWs w, int strips)
+// Runs that cross chunks: the wave of the chunk in which a run starts adds its
+// parts in order.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) rar_embed_join(const EmbedGradParams p, const GradWs w, int strips)
 {
-    const int64_t job = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t v = job / strips;
-    if (v >= p.V)
+    const int lane = threadIdx.x & 63;
+    const int64_t job = wave_job(blockIdx.x);
+    const int64_t chunk = job / strips;
+    const int64_t next = (chunk + 1) * kChunk;
+    if (next >= p.T)
         return;
-    int64_t at = w.start[v];
-    const int64_t end = w.start[v + 1];
-    if (at == end && p.accumulate)
+    const uint32_t k = w.keys[next];
+    if (k >= (uint32_t)p.V || w.keys[next - 1] != k)
         return;
-    const int64_t c = (job - v * strips) * kCols + (threadIdx.x & 63) * 8;
-    const int cnt = p.D - c >= 8 ? 8 : (p.D - c < 0 ? 0 : (int)(p.D - c));
-    const bool vec = (uintptr_t)p.dy % 16 == 0 && (p.ldy * sizeof(T)) % 16 == 0;
-    constexpr int64_t kBig = kChunk * kChunk;
+    // a run that also fills this chunk from the left starts in an earlier one
+    if (chunk > 0 && w.keys[chunk * kChunk - 1] == k)
+        return;
+    // the last chunk whose first position still holds the id
+    int64_t last = chunk;
+    for (;;) {
+        const int64_t c = last + 1 + lane;
+        const uint64_t same = __ballot(c * kChunk < p.T && w.keys[c * kChunk < p.T ? c * kChunk : 0] == k);
+        const int run = __builtin_ctzll(~same | (1ull << 63)) + (same == ~0ull ? 1 : 0);
+        last += run;
+        if (run < 64)
+            break;
+    }
+    const Columns<T, VEC> cols{(job - chunk * strips) * kCols, p.D};
     float acc[8] = {};
-    while (at < end) {
-        const int64_t left = end - at;
-        if (at % kBig == 0 && left >= kBig) {
-            const int64_t n = left / kBig;
-            add_partials(w.part2, w.pitch, at / kBig, n, c, cnt, acc);
-            at += n * kBig;
-        } else if (at % kChunk == 0 && left >= kChunk) {
-            int64_t n = left / kChunk;
-            const int64_t to_big = kChunk - at / kChunk % kChunk;  // rows up to the next second-level one
-            n = n < to_big ? n : to_big;
-            add_partials(w.part1, w.pitch, at / kChunk, n, c, cnt, acc);
-            at += n * kChunk;
+    cols.add_partials(w.to_right, w.pitch, chunk, 1, acc);
+    int64_t c = chunk + 1;
+    while (c <= last) {
+        // whole aligned groups of 32 chunks: the run fills all but its last chunk
+        if (c % kChunk == 0 && last - c >= kChunk) {
+            const int64_t n = (last - c) / kChunk;
+            cols.add_partials(w.long_run, w.pitch, c / kChunk, n, acc);
+            c += n * kChunk;
         } else {
-            const int64_t to_chunk = kChunk - at % kChunk;
-            const int n = (int)(left < to_chunk ? left : to_chunk);
-            add_rows<T>(p, w.pos, at, n, c, cnt, vec, acc);
-            at += n;
+            int64_t n = kChunk - c % kChunk;
+            n = n < last - c + 1 ? n : last - c + 1;
+            cols.add_partials(w.from_left, w.pitch, c, n, acc);
+            c += n;
         }
     }
-    if (cnt <= 0)
-        return;
-    T *out = (T *)p.grad + v * p.D + c;
-    const bool vout = cnt == 8 && ((uintptr_t)out % 16 == 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        acc[i] *= p.scale;
-        if (p.accumulate && i < cnt)
-            acc[i] += to_f32(out[i]);
-    }
-    if (vout) {
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<u32x4 *>(out) = u32x4{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
-                                                    pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7])};
-        } else {
-            store4(out, f32x4{acc[0], acc[1], acc[2], acc[3]});
-            store4(out + 4, f32x4{acc[4], acc[5], acc[6], acc[7]});
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < cnt)
-            out[i] = from_f32<T>(acc[i]);
+    cols.put_row(p, k, acc);
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Byte offsets of the workspace's parts.
 struct Layout {
-    int64_t keys[2], pos[2], hist, start, part1, part2, total, pitch;
+    int64_t keys[2], pos[2], hist, from_left, to_right, long_run, total, pitch;
 };
 
-Layout layout(int64_t T, int64_t V, int64_t D)
+Layout layout(int64_t T, int64_t D)
 {
     Layout l{};
     int64_t at = 0;
@@ -491,35 +583,38 @@ Layout layout(int64_t T, int64_t V, int64_t D)
         at += up(bytes, 256);
         return here;
     };
-    l.pitch = up(D, 8);
-    const bool small = T <= kSortKeys;
+    l.pitch = up(D, kCols);
+    const bool small = T <= kSmallKeys;
     for (int i = 0; i < 2; ++i) {
         l.keys[i] = i && small ? l.keys[0] : take(4 * T);
         l.pos[i] = i && small ? l.pos[0] : take(4 * T);
     }
     l.hist = take(small ? 0 : (T + kSortKeys - 1) / kSortKeys * 1024);
-    l.start = take(4 * (V + 1));
-    l.part1 = take(T / kChunk * l.pitch * 4);
-    l.part2 = take(T / (kChunk * kChunk) * l.pitch * 4);
+    const int64_t chunks = T > kChunk ? (T + kChunk - 1) / kChunk : 0;
+    l.from_left = take(chunks * l.pitch * 4);
+    l.to_right = take(chunks * l.pitch * 4);
+    l.long_run = take(T / (kChunk * kChunk) * l.pitch * 4);
     l.total = at;
     return l;
 }
 
-template <class T>
+template <class T, bool VEC>
 void sums(const EmbedGradParams &p, const GradWs &w, hipStream_t st)
 {
-    const int strips = (int)((p.D + kCols - 1) / kCols);
-    const int64_t start_blocks = (p.V + 1 + 255) / 256;
-    const int64_t jobs1 = p.T / kChunk * strips, jobs2 = p.T / (kChunk * kChunk) * strips;
-    rar_embed_part1<T><<<(unsigned)(start_blocks + (jobs1 + 3) / 4), 256, 0, st>>>(p, w, start_blocks, strips);
-    if (jobs2)
-        rar_embed_part2<<<(unsigned)((jobs2 + 3) / 4), 256, 0, st>>>(p, w, strips);
-    rar_embed_sum<T><<<(unsigned)((p.V * strips + 3) / 4), 256, 0, st>>>(p, w, strips);
+    const int64_t strips = (p.D + kCols - 1) / kCols;
+    const int64_t chunks = (p.T + kChunk - 1) / kChunk, longs = p.T / (kChunk * kChunk);
+    const auto grid = [strips](int64_t n) { return (unsigned)((n * strips + 3) / 4); };
+    if (chunks > 0)
+        rar_embed_chunks<T, VEC><<<grid(chunks), 256, 0, st>>>(p, w, (int)strips);
+    if (longs > 1)  // the first group has nothing on its left
+        rar_embed_long<<<grid(longs), 256, 0, st>>>(p, w, (int)strips);
+    if (chunks > 1)
+        rar_embed_join<T, VEC><<<grid(chunks - 1), 256, 0, st>>>(p, w, (int)strips);
 }
 
 }  // namespace
 
-int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D) { return layout(T, V, D).total; }
+int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D) { return layout(T, D).total; }
 
 hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t st)
 {
@@ -538,7 +633,7 @@ hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t s
 
 hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t st)
 {
-    const Layout l = layout(p.T, p.V, p.D);
+    const Layout l = layout(p.T, p.D);
     char *const ws = (char *)p.ws;
     uint32_t *keys[2], *pos[2];
     for (int i = 0; i < 2; ++i) {
@@ -549,27 +644,47 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
     while (bits < 32 && (p.V >> bits) != 0)
         ++bits;
     const int passes = (bits + 7) / 8;
+    // the gradient in as many shares as the sort has launches
+    const int64_t bytes = p.accumulate ? 0 : p.V * p.D * (dt == RAR_BF16 ? 2 : 4);
+    int share = 0;
+    const int shares = p.T <= kSmallKeys ? 1 : 2 * passes;
+    auto next_clear = [&]() {
+        const int64_t lo = bytes / 256 * share / shares * 256, hi = share + 1 == shares ? bytes : bytes / 256 * (share + 1) / shares * 256;
+        ++share;
+        return Clear{(char *)p.grad + lo, hi - lo};
+    };
+    auto clear_blocks = [](const Clear &c) { return (unsigned)((c.bytes + kClearBytes - 1) / kClearBytes); };
     int last = 0;
-    if (p.T <= kSortKeys) {
-        rar_sort_small<<<1, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, keys[0], pos[0]);
+    if (p.T <= kSmallKeys) {
+        const Clear c = next_clear();
+        const unsigned grid = 1 + clear_blocks(c);
+        if (p.T <= kSortKeys)
+            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, keys[0], pos[0], c);
+        else
+            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, keys[0], pos[0], c);
     } else {
         const unsigned blocks = (unsigned)((p.T + kSortKeys - 1) / kSortKeys);
         uint32_t *const hist = (uint32_t *)(ws + l.hist);
         for (int pass = 0; pass < passes; ++pass) {
             const int64_t *ids = pass == 0 ? p.ids : nullptr;
             const int from = (pass + 1) & 1, to = pass & 1;
-            rar_sort_count<<<blocks, kSortThreads, 0, st>>>(ids, keys[from], p.T, p.V, 8 * pass, hist);
-            rar_sort_place<<<blocks, kSortThreads, 0, st>>>(ids, keys[from], pos[from], p.T, p.V, 8 * pass, hist,
-                                                            keys[to], pos[to]);
+            const Clear c0 = next_clear();
+            rar_sort_count<<<blocks + clear_blocks(c0), kSortThreads, 0, st>>>(ids, keys[from], p.T, p.V, 8 * pass, hist,
+                                                                              blocks, c0);
+            const Clear c1 = next_clear();
+            rar_sort_place<<<blocks + clear_blocks(c1), kSortThreads, 0, st>>>(
+                ids, keys[from], pos[from], p.T, p.V, 8 * pass, hist, keys[to], pos[to], blocks, c1);
             last = to;
         }
     }
-    const GradWs w{keys[last], pos[last], (uint32_t *)(ws + l.start), (float *)(ws + l.part1), (float *)(ws + l.part2),
-                   l.pitch};
+    const GradWs w{keys[last], pos[last], (float *)(ws + l.from_left), (float *)(ws + l.to_right),
+                   (float *)(ws + l.long_run), l.pitch};
+    const int es = dt == RAR_BF16 ? 2 : 4;
+    const bool vec = (uintptr_t)p.dy % 16 == 0 && p.ldy * es % 16 == 0 && (uintptr_t)p.grad % 16 == 0 && p.D % 8 == 0;
     if (dt == RAR_BF16)
-        sums<bf16>(p, w, st);
+        vec ? sums<bf16, true>(p, w, st) : sums<bf16, false>(p, w, st);
     else
-        sums<float>(p, w, st);
+        vec ? sums<float, true>(p, w, st) : sums<float, false>(p, w, st);
     return hipGetLastError();
 }
 

@@ -647,6 +647,110 @@ __global__ void __launch_bounds__(256, 2) rar_gemm_f32(const GemmParams p)
 #endif
 }
 
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+//
+// For up to R rows of x the layer is bound by reading W once, and what counts
+// is how much of W is in flight.  A workgroup takes 64 columns and all of K:
+// the lanes of a wave read whole 128-byte lines of several rows of W, a lane
+// kGemvK consecutive k of its columns and the same k of x in one vector each.
+// Partial sums are joined by lane exchanges and through LDS, in an order fixed
+// by the sizes; nothing passes through memory.
+constexpr int kGemvCols = 64, kGemvK = 8;
+
+template <class T, int E>
+__device__ __forceinline__ float element(const u32x4 (&v)[E], int i)
+{
+    if (sizeof(T) == 4)
+        return __uint_as_float(v[i / 4][i % 4]);
+    return __uint_as_float(i % 2 ? v[i / 8][i / 2 % 4] & 0xffff0000u : v[i / 8][i / 2 % 4] << 16);
+}
+
+template <class T, int R, bool VEC>
+__global__ void __launch_bounds__(1024) rar_gemv(const GemmParams p)
+{
+    constexpr int kPer = 16 / sizeof(T);               // columns of a lane
+    constexpr int kLanes = kGemvCols / kPer;           // lanes of a row of W
+    constexpr int kGroups = 64 / kLanes;               // rows of W a wave reads at once
+    constexpr int kWaves = 16;
+    __shared__ float sums[kWaves][R][kGemvCols];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int q = lane % kLanes, g = lane / kLanes;
+    const int64_t n0 = (int64_t)blockIdx.x * kGemvCols;
+    const T *const w = (const T *)p.b + n0;
+    const T *x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        x[r] = (const T *)p.a + (r < p.M ? r : 0) * p.lda;
+    float acc[R][kPer] = {};
+    // columns of this lane: neighbours, or kLanes apart where W is read by the element
+    const auto column = [&](int i) __attribute__((always_inline)) { return VEC ? q * kPer + i : q + i * kLanes; };
+    const bool live = n0 + column(0) < p.N;            // vectors are inside or outside as a whole
+    int64_t k = (wave * kGroups + g) * kGemvK;
+    constexpr int kStride = kWaves * kGroups * kGemvK;
+    if constexpr (VEC) {
+        constexpr int kUnroll = R > 2 ? 1 : 2;
+#pragma unroll kUnroll
+        for (; k + kGemvK <= p.K; k += kStride) {
+            u32x4 wv[kGemvK][1], xv[R][kGemvK / kPer];
+            const T *const at = w + k * p.ldb + q * kPer;
+#pragma unroll
+            for (int j = 0; j < kGemvK; ++j)
+                wv[j][0] = live ? *reinterpret_cast<const u32x4 *>(at + j * p.ldb) : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int j = 0; j < kGemvK / kPer; ++j)
+                    xv[r][j] = *reinterpret_cast<const u32x4 *>(x[r] + k + j * kPer);
+#pragma unroll
+            for (int j = 0; j < kGemvK; ++j)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const float e = element<T>(wv[j], i);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        acc[r][i] = __builtin_fmaf(element<T>(xv[r], j), e, acc[r][i]);
+                }
+        }
+    }
+    // by the element: the end of K, and everything where rows are not whole vectors
+#pragma unroll 1
+    for (; k < p.K; k += kStride)
+#pragma unroll 4
+        for (int64_t kk = k; kk < (k + kGemvK < p.K ? k + kGemvK : p.K); ++kk)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float e = n0 + column(i) < p.N ? to_f32(w[kk * p.ldb + column(i)]) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r][i] = __builtin_fmaf(to_f32(x[r][kk]), e, acc[r][i]);
+            }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+            for (int d = kLanes; d < 64; d *= 2)
+                acc[r][i] += __shfl_xor(acc[r][i], d);
+            if (g == 0)
+                sums[wave][r][column(i)] = acc[r][i];
+        }
+    __syncthreads();
+    if (threadIdx.x >= 64)
+        return;
+    // eight lanes finish a row, four of them a group of a checkpoint
+    const int r = lane / 8;
+    float v[8] = {};
+    if (r < R)
+#pragma unroll
+        for (int s = 0; s < kWaves; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += sums[s][r][lane % 8 * 8 + i];
+    epilogue<T>(p, r < R ? r : p.M, n0 + lane % 8 * 8, v);
+}
+
 // Partial products of a split reduction, joined in the order of the splits:
 // the result does not depend on which workgroup finished first.
 template <class T>
@@ -703,53 +807,85 @@ __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams p)
 }
 
 // dz = dy * act'(z) and the column sums of dz in one pass over dy and z.  A
-// workgroup takes 256 columns (a lane four, a wave one row at a time) of
-// rows_per_chunk rows; its sums go to part[chunk], joined in chunk order by
-// rar_column_sum.  Sums are of the binary32 dz; the dz that the matrix
-// products read is rounded to the layer's type.
-template <class T>
+// workgroup takes 512 columns (a lane eight, a wave four rows at a time, so
+// that eight 16-byte loads are in flight) of rows_per_chunk rows; its sums go
+// to part[chunk], joined in chunk order by rar_column_sum.  Sums are of the
+// binary32 dz; the dz that the matrix products read is rounded to the layer's
+// type.
+enum DzSource { kDzNone = 0, kDzPre = 1, kDzCkpt = 2 };
+constexpr int kDzRows = 4;
+
+template <class T, int ACT, int SOURCE>
 __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
     const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_chunk;
     const int64_t r1 = r0 + p.rows_per_chunk < p.rows ? r0 + p.rows_per_chunk : p.rows;
-    const int cnt = p.cols - c < 4 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 4;
-    const bool vdy = ((uintptr_t)p.dy % (4 * sizeof(T)) == 0) && p.ldy % 4 == 0;
-    const bool vpre = ((uintptr_t)p.pre % (4 * sizeof(T)) == 0) && p.ldp % 4 == 0;
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < p.cols || (p.dz && c < p.pitch)) {
-        for (int64_t r = r0 + wave; r < r1; r += 4) {
-            f32x4 d = get4((const T *)p.dy + r * p.ldy + c, cnt, vdy);
-            if (p.act != RAR_ACT_NONE && cnt > 0) {
-                f32x4 z;
-                if (p.pre_scales) {
-                    const int64_t groups = (p.cols + kCkptGroup - 1) / kCkptGroup;
-                    const uint32_t w = *(const uint32_t *)((const uint8_t *)p.pre + r * groups * kCkptGroup + c);
-                    z = ckpt_values4(w, p.pre_scales[r * groups + c / kCkptGroup]);
-                } else {
-                    z = get4((const T *)p.pre + r * p.ldp + c, cnt, vpre);
-                }
+    const int cnt = p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8;
+    const int put = p.pitch - c < 8 ? (p.pitch - c < 0 ? 0 : (int)(p.pitch - c)) : 8;
+    const bool vdy = (uintptr_t)p.dy % 16 == 0 && p.ldy * sizeof(T) % 16 == 0;
+    const bool vpre = (uintptr_t)p.pre % 16 == 0 && p.ldp * sizeof(T) % 16 == 0;
+    const int64_t groups = (p.cols + kCkptGroup - 1) / kCkptGroup;
+    float sum[8] = {};
+    if (cnt > 0 || (p.dz && put > 0)) {
+        for (int64_t r = r0 + wave; r < r1; r += 4 * kDzRows) {
+            float d[kDzRows][8], z[kDzRows][8];
+            u32x2 w[kDzRows];
+            uint32_t e[kDzRows];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    d[i] = i < cnt ? d[i] * act_grad<T>(p.act, z[i]) : 0.0f;
+            for (int u = 0; u < kDzRows; ++u) {
+                const int64_t row = r + 4 * u;
+                const int n = row < r1 ? cnt : 0;
+                load8((const T *)p.dy + row * p.ldy + c, n, vdy, d[u]);
+                if (SOURCE == kDzPre)
+                    load8((const T *)p.pre + row * p.ldp + c, n, vpre, z[u]);
+                w[u] = u32x2{0, 0};
+                e[u] = 0;
+                if (SOURCE == kDzCkpt && n > 0) {
+                    w[u] = *(const u32x2 *)((const uint8_t *)p.pre + row * groups * kCkptGroup + c);
+                    e[u] = p.pre_scales[row * groups + c / kCkptGroup];
+                }
             }
-            sum += d;
-            if (p.dz)
-                store4((T *)p.dz + r * p.pitch + c, d);
+#pragma unroll
+            for (int u = 0; u < kDzRows; ++u) {
+                const int64_t row = r + 4 * u;
+                if (row >= r1)
+                    continue;
+                if (SOURCE == kDzCkpt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const f32x4 x = ckpt_values4(w[u][h], e[u]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            z[u][4 * h + i] = x[i];
+                    }
+                if (SOURCE != kDzNone)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[u][i] = i < cnt ? d[u][i] * act_grad<T>(ACT, z[u][i]) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sum[i] += d[u][i];
+                if (p.dz)
+                    store8((T *)p.dz + row * p.pitch + c, put, true, d[u]);
+            }
         }
     }
     if (!p.part)
         return;
-    __shared__ f32x4 sums[4][64];
-    sums[wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0) {
-        const f32x4 t = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+    __shared__ float sums[4][8][64];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < cnt)
-                p.part[blockIdx.y * p.cols + c + i] = t[i];
+    for (int i = 0; i < 8; ++i)
+        sums[wave][i][lane] = sum[i];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int j = threadIdx.x + k * 256;  // column of the workgroup
+        const int64_t col = (int64_t)blockIdx.x * 512 + j;
+        if (col < p.cols)
+            p.part[blockIdx.y * p.cols + col] = (sums[0][j % 8][j / 8] + sums[1][j % 8][j / 8]) +
+                                                (sums[2][j % 8][j / 8] + sums[3][j % 8][j / 8]);
     }
 }
 
@@ -761,6 +897,7 @@ __global__ void __launch_bounds__(256) rar_column_sum(const SumParams p)
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (c < p.cols)
+#pragma unroll 16
         for (int64_t k = wave; k < p.chunks; k += 4)
             s += p.part[k * p.cols + c];
     __shared__ float sums[4][64];
@@ -804,6 +941,31 @@ hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big
     return hipGetLastError();
 }
 
+namespace {
+
+template <class T, bool VEC>
+void run_gemv(const GemmParams &p, unsigned grid, hipStream_t st)
+{
+    if (p.M == 1)
+        rar_gemv<T, 1, VEC><<<grid, 1024, 0, st>>>(p);
+    else if (p.M == 2)
+        rar_gemv<T, 2, VEC><<<grid, 1024, 0, st>>>(p);
+    else
+        rar_gemv<T, kGemvRows, VEC><<<grid, 1024, 0, st>>>(p);
+}
+
+}  // namespace
+
+hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t st)
+{
+    const unsigned grid = (unsigned)((p.N + kGemvCols - 1) / kGemvCols);
+    if (dt == RAR_BF16)
+        vec ? run_gemv<bf16, true>(p, grid, st) : run_gemv<bf16, false>(p, grid, st);
+    else
+        vec ? run_gemv<float, true>(p, grid, st) : run_gemv<float, false>(p, grid, st);
+    return hipGetLastError();
+}
+
 hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st)
 {
     const int64_t groups = p.M * (p.pitch / 8);
@@ -825,14 +987,31 @@ hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st)
     return hipGetLastError();
 }
 
+namespace {
+
+template <class T>
+void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
+{
+    if (p.act == RAR_ACT_NONE)
+        rar_dz<T, RAR_ACT_NONE, kDzNone><<<grid, 256, 0, st>>>(p);
+    else if (p.act == RAR_ACT_RELU)
+        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_RELU, kDzPre><<<grid, 256, 0, st>>>(p);
+    else
+        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_GELU, kDzPre><<<grid, 256, 0, st>>>(p);
+}
+
+}  // namespace
+
 hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st)
 {
     const int64_t width = p.dz && p.pitch > p.cols ? p.pitch : p.cols;
-    const dim3 grid((unsigned)((width + 255) / 256), (unsigned)((p.rows + p.rows_per_chunk - 1) / p.rows_per_chunk));
+    const dim3 grid((unsigned)((width + 511) / 512), (unsigned)((p.rows + p.rows_per_chunk - 1) / p.rows_per_chunk));
     if (dt == RAR_BF16)
-        rar_dz<bf16><<<grid, 256, 0, st>>>(p);
+        run_dz<bf16>(p, grid, st);
     else
-        rar_dz<float><<<grid, 256, 0, st>>>(p);
+        run_dz<float>(p, grid, st);
     return hipGetLastError();
 }
 

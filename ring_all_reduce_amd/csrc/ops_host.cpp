@@ -144,11 +144,11 @@ struct Layer {
     rar_dtype dt;
 };
 
-// Chunks of rows whose column sums are kept apart: about 2048 workgroups of 256
+// Chunks of rows whose column sums are kept apart: about 2048 workgroups of 512
 // columns, at least 16 rows each.
 int64_t sum_rows(int64_t T, int64_t N)
 {
-    const int64_t chunks = std::max<int64_t>(1, std::min(div_up(T, 16), 2048 / div_up(N, 256)));
+    const int64_t chunks = std::max<int64_t>(1, std::min(div_up(T, 16), 2048 / div_up(N, 512)));
     return std::max<int64_t>(1, div_up(T, chunks));
 }
 
@@ -190,6 +190,14 @@ BackwardWs backward_ws(const Layer &l, void *ws)
     return b;
 }
 
+// Whether the outputs, the bias and the residual can be accessed 16 bytes at a time.
+int wide_outputs(const GemmParams &p, int es)
+{
+    const auto wide = [es](const void *q, int64_t ld) { return aligned(q, 16) && (ld * es) % 16 == 0; };
+    return wide(p.out, p.ldo) && (!p.pre || p.pre_scales || wide(p.pre, p.ldp)) && (!p.res || wide(p.res, p.ldr)) &&
+           aligned(p.bias, 16);
+}
+
 rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *part, hipStream_t st)
 {
     const Shape s = shape_of(dt, p.M, p.N, p.K);
@@ -201,10 +209,7 @@ rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *pa
     p.steps_per_split = s.steps;
     p.pitch = s.pitch;
     p.part = part;
-    const int es = esize(dt);
-    const auto wide = [es](const void *q, int64_t ld) { return aligned(q, 16) && (ld * es) % 16 == 0; };
-    p.vec = wide(p.out, p.ldo) && (!p.pre || p.pre_scales || wide(p.pre, p.ldp)) && (!p.res || wide(p.res, p.ldr)) &&
-            aligned(p.bias, 16);
+    p.vec = wide_outputs(p, esize(dt));
     if (s.splits == 1)
         return launched(rar::launch_gemm(dt, layout, p, s.big, st));
     GemmParams q = p;
@@ -267,13 +272,13 @@ extern "C" rar_status rar_embed_grad(int64_t V, int64_t D, rar_dtype dtype, int6
 {
     if (V < 1 || V > kMaxVocab || !valid_width(D) || !valid_dtype(dtype) || !valid_rows(T) || !valid_ld(lddy, D))
         return RAR_EINVAL;
-    if (!grad || !ws || (T > 0 && (!ids || !dy)))
+    if (!grad || (T > 0 && (!ids || !dy || !ws)))
         return RAR_EINVAL;
     const int es = esize(dtype);
     if (!aligned(grad, es) || !aligned(dy, es) || !aligned(ids, 8) || !aligned(ws, 16))
         return RAR_EALIGN;
     const int64_t need = rar::embed_grad_workspace(T, V, D);
-    if (ws_bytes < need || div_up(V * div_up(D, 512), 4) > kMaxBlocks)
+    if (ws_bytes < need || div_up(T, 32) * div_up(D, 512) > kMaxBlocks || V * D * es / 65536 > kMaxBlocks)
         return RAR_EINVAL;
     if (!apart({{grad, V, D, D, es}, {ws, 1, need, need, 1}}, {{dy, T, D, lddy, es}, {ids, 1, T, T, 8}}))
         return RAR_EINVAL;
@@ -357,11 +362,6 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
         return RAR_EINVAL;
     hipStream_t st = static_cast<hipStream_t>(stream);
     GemmParams p{};
-    rar_status rc = readable(mx, dt, f.x, &p.a, &p.lda, st);
-    if (rc == RAR_OK)
-        rc = readable(mw, dt, f.w, &p.b, &p.ldb, st);
-    if (rc != RAR_OK)
-        return rc;
     p.M = T;
     p.N = N;
     p.K = K;
@@ -375,6 +375,19 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
     p.ldr = ldr;
     p.mode = rar::kModeForward;
     p.act = plan->act;
+    if (T <= rar::kGemvRows) {
+        p.a = x;
+        p.lda = ldx;
+        p.b = w;
+        p.ldb = N;
+        p.vec = wide_outputs(p, es);
+        return launched(rar::launch_gemv(dt, p, direct(mx) && direct(mw), st));
+    }
+    rar_status rc = readable(mx, dt, f.x, &p.a, &p.lda, st);
+    if (rc == RAR_OK)
+        rc = readable(mw, dt, f.w, &p.b, &p.ldb, st);
+    if (rc != RAR_OK)
+        return rc;
     return product(dt, rar::kGemmForward, p, f.part, st);
 }
 

@@ -113,6 +113,9 @@ struct EmbedGradParams {
 };
 
 hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big, hipStream_t st);
+// A forward product of at most kGemvRows rows; vec: rows of x and W can be read 16 bytes at a time.
+constexpr int kGemvRows = 4;
+hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t st);
 hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st);
 hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st);
 hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st);

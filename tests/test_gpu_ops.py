@@ -36,7 +36,7 @@ def strided(t, extra, offset=0):
 
 # (T, K, N): one element, one token, odd sizes, whole and broken tiles, split reductions, more than 192 tiles of 256
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (17, 64, 32), (1, 2048, 520), (7, 300, 1000), (129, 257, 131),
-          (300, 512, 264), (64, 1000, 72), (515, 96, 640), (5001, 40, 24), (130, 8, 4096)]
+          (300, 512, 264), (64, 1000, 72), (515, 96, 640), (5001, 40, 24), (130, 8, 4096), (2, 2056, 72), (4, 1000, 136), (3, 4104, 200)]
 BIG = [(3000, 72, 4200), (2900, 136, 4104)]
 
 
@@ -342,7 +342,7 @@ def test_backward_from_checkpoints(shape, act, dtype):
 # ---------------------------------------------------------------------------
 
 EMBED = [(1, 1, 1), (1, 5, 8), (63, 7, 3), (33, 300, 520), (4096, 50, 24), (4097, 300, 40), (9000, 70000, 9),
-         (20000, 11, 130), (5000, 256, 513), (4500, 66000, 16)]
+         (20000, 11, 130), (5000, 256, 513), (4500, 66000, 16), (8192, 40, 1536), (8193, 30, 2056), (700, 9, 1024)]
 
 
 @pytest.mark.parametrize("dtype", BOTH)
