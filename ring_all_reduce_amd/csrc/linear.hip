@@ -275,12 +275,12 @@ __device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t
 
 // A wave's ROWS rows of W columns pass through LDS, so that a lane finishes
 // eight consecutive columns of one row and a row's lanes access whole lines.
-// The 16-byte chunk c of row r lies at slot c ^ (r & 15): a column of rows
-// spreads over the banks.
+// The 16-byte chunk c of row r lies at slot c ^ r (of the low bits of r): a
+// column of rows spreads over the banks.
 template <int W>
 __device__ __forceinline__ RAR_LDS f32x4 *tile_slot(RAR_LDS char *tile, int r, int c)
 {
-    return (RAR_LDS f32x4 *)(tile + r * (W * 4) + ((c ^ (r & 15)) << 4));
+    return (RAR_LDS f32x4 *)(tile + r * (W * 4) + ((c ^ (r & (W >= 64 ? 15 : W / 4 - 1))) << 4));
 }
 
 template <int W>
@@ -559,91 +559,106 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
 // ---------------------------------------------------------------------------
 //
 // The binary32 matrix instruction does a sixteenth of the bf16 one's work per
-// cycle, so a 128 x 128 tile with plain double buffering keeps the matrix cores
-// fed: per instruction (64 cycles) a wave reads a quarter of a kilobyte of LDS.
-template <bool ACONTIG, bool BCONTIG>
-__global__ void __launch_bounds__(256, 2) rar_gemm_f32(const GemmParams p)
+// cycle, so its operands come from LDS with time to spare; what is left is to
+// keep the instruction fed across steps.  Four waves as 2 x 2 hold a B x B
+// tile; a step of 32 reduction indices is staged in one half of LDS while the
+// other is used, in four groups of eight whose fragments are read one group
+// ahead.  In the last group of a step the waves meet: the next step has then
+// arrived, and this one's half is free for the step after it.
+template <int B, bool ACONTIG, bool BCONTIG>
+__global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_gemm_f32(const GemmParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 128, BN = 128, kStep = 32;
-    constexpr int kHalf = (BM + BN) * 128;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kHalf];
+    constexpr int kStep = 32, F = B / 64;
+    constexpr int kBuf = 2 * B * 128;
+    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kBuf];
     RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
     int64_t tm, tn;
     int split;
     tile_of(p, tm, tn, split);
-    const int64_t m0 = tm * BM, n0 = tn * BN;
+    const int64_t m0 = tm * B, n0 = tn * B;
     const int64_t k0 = split * p.steps_per_split * kStep;
     const int64_t kend = k0 + p.steps_per_split * kStep < p.K ? k0 + p.steps_per_split * kStep : p.K;
     const int steps = k0 < kend ? (int)((kend - k0 + kStep - 1) / kStep) : 0;
-    const int wave = threadIdx.x >> 6, wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const int wave = threadIdx.x >> 6, wm = (wave & 1) * (B / 2), wn = (wave >> 1) * (B / 2);
 
-    Stage<4, BM, 128, 4, ACONTIG> sa;
-    Stage<4, BN, 128, 4, BCONTIG> sb;
+    Stage<4, B, 128, 4, ACONTIG> sa;
+    Stage<4, B, 128, 4, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
-    Frag32<BM, ACONTIG> fa;
-    Frag32<BN, BCONTIG> fb;
+    Frag32<B, ACONTIG> fa;
+    Frag32<B, BCONTIG> fb;
     fa.init(wm);
     fb.init(wn);
 
-    f32x16 acc[2][2];
+    f32x16 acc[F][F];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < F; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
 
     auto stage = [&](int s) __attribute__((always_inline)) {
-        if (s < steps) {
-            if (s == steps - 1) {
-                sa.cut(kend - k0 - (int64_t)s * kStep);
-                sb.cut(kend - k0 - (int64_t)s * kStep);
-            }
-            RAR_LDS char *to = lds + (s & 1) * kHalf;
-            sa.load_all(to, false);
-            sb.load_all(to + BM * 128, false);
+        if (s == steps - 1) {
+            sa.cut(kend - k0 - (int64_t)s * kStep);
+            sb.cut(kend - k0 - (int64_t)s * kStep);
+        }
+        RAR_LDS char *to = lds + (s & 1) * kBuf;
+        sa.load_all(to, s >= steps);
+        sb.load_all(to + B * 128, s >= steps);
+    };
+    f32x4 a[2][F], b[2][F];
+    auto read = [&](int s, int c, int set) __attribute__((always_inline)) {
+        const RAR_LDS char *from = lds + (s & 1) * kBuf;
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            a[set][i] = fa.read(from, c, i);
+            b[set][i] = fb.read(from + B * 128, c, i);
         }
     };
 
     stage(0);
+    stage(1);
+    wait_loads<sa.kLoads + sb.kLoads>();
+    read(0, 0, 0);
     for (int s = 0; s < steps; ++s) {
-        drain();
-        stage(s + 1);
-        const RAR_LDS char *from = lds + (s & 1) * kHalf;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            f32x4 a[2], b[2];
+            if (c < 3)
+                read(s, c + 1, (c + 1) & 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                a[i] = fa.read(from, c, i);
-                b[i] = fb.read(from + BM * 128, c, i);
+            for (int e = 0; e < 4; ++e) {
+                if (c == 3 && e == 1) {
+                    drain();
+                    read(s + 1, 0, 0);  // behind the last step: zeros
+                    stage(s + 2);
+                }
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+#pragma unroll
+                    for (int j = 0; j < F; ++j)
+                        acc[i][j] =
+                            __builtin_amdgcn_mfma_f32_32x32x2f32(b[c & 1][j][e], a[c & 1][i][e], acc[i][j], 0, 0, 0);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j][e], a[i][e], acc[i][j], 0, 0, 0);
         }
     }
 
     drain();
     const int lane = threadIdx.x & 63;
-    RAR_LDS char *const tile = lds + wave * (64 * 64 * 4);
+    constexpr int W = B / 2;
+    RAR_LDS char *const tile = lds + wave * (W * W * 4);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < F; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                *tile_slot<64>(tile, i * 32 + (lane & 31), j * 8 + q * 2 + (lane >> 5)) =
+                *tile_slot<W>(tile, i * 32 + (lane & 31), j * 8 + q * 2 + (lane >> 5)) =
                     f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    finish_rows<float, 64, 64>(p, split, tile, m0 + wm, n0 + wn);
+    finish_rows<float, W, W>(p, split, tile, m0 + wm, n0 + wn);
 #endif
 }
 
@@ -924,21 +939,26 @@ hipError_t run_bf16(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_
     return hipGetLastError();
 }
 
+template <int B>
+hipError_t run_f32(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_t st)
+{
+    if (l == kGemmForward)
+        rar_gemm_f32<B, true, false><<<grid, 256, 0, st>>>(p);
+    else if (l == kGemmGradX)
+        rar_gemm_f32<B, true, true><<<grid, 256, 0, st>>>(p);
+    else
+        rar_gemm_f32<B, false, false><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-
-hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big, hipStream_t st)
+hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, int tile, hipStream_t st)
 {
     const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * p.splits);
     if (dt == RAR_BF16)
-        return big ? run_bf16<256, 2, 4>(l, p, grid, st) : run_bf16<128, 2, 2>(l, p, grid, st);
-    if (l == kGemmForward)
-        rar_gemm_f32<true, false><<<grid, 256, 0, st>>>(p);
-    else if (l == kGemmGradX)
-        rar_gemm_f32<true, true><<<grid, 256, 0, st>>>(p);
-    else
-        rar_gemm_f32<false, false><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+        return tile == 256 ? run_bf16<256, 2, 4>(l, p, grid, st) : run_bf16<128, 2, 2>(l, p, grid, st);
+    return tile == 128 ? run_f32<128>(l, p, grid, st) : run_f32<64>(l, p, grid, st);
 }
 
 namespace {

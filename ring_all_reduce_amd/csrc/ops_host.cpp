@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <initializer_list>
 #include <new>
 
@@ -95,34 +96,77 @@ bool direct(const Mat &m) { return aligned(m.p, 16) && (m.ld * m.es) % 16 == 0 &
 // ---------------------------------------------------------------------------
 
 struct Shape {
-    bool big;
+    int tile;
     int64_t tiles_m, tiles_n, splits, steps;
     int64_t pitch;
     int64_t part_bytes;
 };
 
+// Microseconds of a product at a shape, from a sweep of tiles and splits on
+// MI355X over 13 layers from 333 x 501 x 259 to 8192 x 2048 x 8192: the most
+// loaded compute unit runs `rounds` workgroups, whose steps take `step` each
+// when several share the unit and at least `alone` by themselves; a split
+// reduction also writes its partial sums, reads them and launches the join.
+// Both ends, bf16: 2048 x 4096 -> 4096 forward takes 62 us in 128-tiles and 94
+// in 256-tiles (256 of them would leave half the chip idle), its weight
+// gradient 66 and 54; binary32: 2048^3 takes 139 us in 128-tiles and 132 in
+// 64-tiles, 8192 x 2048 -> 2048 500 and 510.  128 x 2048 -> 2048 in bf16 takes
+// 15 us split in four and 23 unsplit; 2048 x 512 -> 512 10 unsplit, 15 in two.
+double cost(rar_dtype dt, const Shape &s)
+{
+    double step, alone, fixed;
+    if (dt == RAR_BF16) {
+        step = s.tile == 256 ? 1.45 : 0.445;
+        alone = s.tile == 256 ? 1.45 : 0.66;
+        fixed = s.tile == 256 ? 8 : 5;
+    } else {
+        step = s.tile == 128 ? 1.9 : 0.495;
+        alone = s.tile == 128 ? 2.12 : 0.72;
+        fixed = s.tile == 128 ? 5 : 3;
+    }
+    const double rounds = std::ceil((double)(s.tiles_m * s.tiles_n * s.splits) / 256);
+    const double t = std::max(rounds * step, alone) * (double)s.steps + fixed;
+    return s.splits > 1 ? t + 4 + 0.35e-6 * (double)s.part_bytes : t;
+}
+
 Shape shape_of(rar_dtype dt, int64_t M, int64_t N, int64_t K)
 {
-    Shape s{};
-    const int64_t total = div_up(K * esize(dt), 128);
-    const int64_t big_tiles = div_up(M, 256) * div_up(N, 256);
-    s.big = dt == RAR_BF16 && big_tiles >= 192;
-    const int64_t tile = s.big ? 256 : 128;
-    s.tiles_m = div_up(M, tile);
-    s.tiles_n = div_up(N, tile);
-    s.splits = 1;
-    s.steps = total;
-    if (!s.big) {
-        const int64_t want = 512 / std::max<int64_t>(1, s.tiles_m * s.tiles_n);
-        const int64_t splits = std::min<int64_t>(want, total / 4);
-        if (splits > 1) {
-            s.steps = div_up(total, splits);
+    const int64_t total = std::max<int64_t>(1, div_up(K * esize(dt), 128));
+    const int large = dt == RAR_BF16 ? 256 : 128;
+    Shape best{};
+    double least = 0;
+    for (int tile = large; tile >= large / 2; tile /= 2) {
+        Shape s{};
+        s.tile = tile;
+        s.tiles_m = div_up(M, tile);
+        s.tiles_n = div_up(N, tile);
+        s.pitch = up(N, rar::kCkptGroup);
+        const int64_t tiles = s.tiles_m * s.tiles_n;
+        for (int64_t want = 1; want <= 32 && (want == 1 || (total / want >= 2 && tiles * want <= 2048)); ++want) {
+            s.steps = div_up(total, want);
             s.splits = div_up(total, s.steps);
+            s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
+            const double t = cost(dt, s);
+            if (best.tile == 0 || t < least) {
+                best = s;
+                least = t;
+            }
         }
     }
-    s.pitch = up(N, rar::kCkptGroup);
-    s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
-    return s;
+#ifdef RAR_FORCE
+    if (getenv("RAR_TILE")) {
+        Shape s{};
+        s.tile = atoi(getenv("RAR_TILE"));
+        s.tiles_m = div_up(M, s.tile);
+        s.tiles_n = div_up(N, s.tile);
+        s.pitch = up(N, rar::kCkptGroup);
+        s.steps = div_up(total, atoi(getenv("RAR_SPLIT")));
+        s.splits = div_up(total, s.steps);
+        s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
+        return s;
+    }
+#endif
+    return best;
 }
 
 // Bytes of the workspace's parts, each a multiple of 256.
@@ -211,10 +255,10 @@ rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *pa
     p.part = part;
     p.vec = wide_outputs(p, esize(dt));
     if (s.splits == 1)
-        return launched(rar::launch_gemm(dt, layout, p, s.big, st));
+        return launched(rar::launch_gemm(dt, layout, p, s.tile, st));
     GemmParams q = p;
     q.mode = rar::kModePartial;
-    rar_status rc = launched(rar::launch_gemm(dt, layout, q, s.big, st));
+    rar_status rc = launched(rar::launch_gemm(dt, layout, q, s.tile, st));
     return rc != RAR_OK ? rc : launched(rar::launch_join(dt, p, st));
 }
 

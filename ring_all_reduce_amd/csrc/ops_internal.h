@@ -112,7 +112,7 @@ struct EmbedGradParams {
     void *ws;
 };
 
-hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, bool big, hipStream_t st);
+hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, int tile, hipStream_t st);
 // A forward product of at most kGemvRows rows; vec: rows of x and W can be read 16 bytes at a time.
 constexpr int kGemvRows = 4;
 hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t st);
