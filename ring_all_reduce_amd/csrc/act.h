@@ -120,13 +120,12 @@ __device__ __forceinline__ void store8(bf16 *p, int cnt, bool vec, const float (
 // transcendental, against about 60 for erfcf: the epilogue of a matrix product
 // evaluates it with the matrix cores idle.
 template <class T>
-__device__ __forceinline__ void normal_tail(float z, float &tail, float &e)
+__device__ __forceinline__ void normal_tail(float z, float &q, float &e)
 {
     constexpr bool kWide = sizeof(T) == 4;
     constexpr float kC = (kWide ? 0.33f : 0.44f) * 0.70710678118654752f;
     e = __builtin_amdgcn_exp2f(z * (z * -0.72134752044448170f));
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(z), kC, 1.0f));
-    float q;
     if (kWide) {
         q = 0.5f * -0.1353447437286377f;
         q = __builtin_fmaf(q, t, 0.5f * 0.4602333605289459f);
@@ -144,27 +143,32 @@ __device__ __forceinline__ void normal_tail(float z, float &tail, float &e)
         q = __builtin_fmaf(q, t, 0.5f * 0.2425696849822998f);
         q = __builtin_fmaf(q, t, 0.5f * 0.24856099486351013f);
     }
-    tail = e * (q * t);
+    q *= t;  // 1 - Phi(|z|) = e q
 }
 
-// z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the limits at +-infinity (the tail
-// is zero long before the bound on |z|), NaN at NaN.
+// |z|, bounded where the density is zero anyway, so that infinity times zero
+// does not arise.  (The minimum with a NaN is the bound; z reaches the result
+// as a NaN through e.)
+__device__ __forceinline__ float bounded(float z) { return __builtin_fminf(__builtin_fabsf(z), 40.0f); }
+
+// z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the limits at +-infinity, NaN at NaN.
 template <class T>
 __device__ __forceinline__ float gelu(float z)
 {
-    float tail, e;
-    normal_tail<T>(z, tail, e);
-    return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 40.0f), tail, __builtin_fmaxf(z, 0.0f));
+    float q, e;
+    normal_tail<T>(z, q, e);
+    return __builtin_fmaf(-bounded(z), e * q, __builtin_fmaxf(z, 0.0f));
 }
 
+// Phi(z) + z phi(z): with h = (1 - Phi(|z|)) - |z| phi(z), h for z < 0 and
+// 1 - h else.
 template <class T>
 __device__ __forceinline__ float gelu_grad(float z)
 {
-    float tail, e;
-    normal_tail<T>(z, tail, e);
-    const float phi = z < 0.0f ? tail : 1.0f - tail;
-    const float pdf = __builtin_fabsf(z) > 40.0f ? 0.0f : z * (e * 0.39894228040143268f);
-    return phi + pdf;
+    float q, e;
+    normal_tail<T>(z, q, e);
+    const float h = e * __builtin_fmaf(-0.39894228040143268f, bounded(z), q);
+    return z < 0.0f ? h : 1.0f - h;
 }
 
 template <class T>

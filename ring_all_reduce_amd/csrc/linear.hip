@@ -373,10 +373,9 @@ __device__ __forceinline__ void finish_rows(const GemmParams &p, int split, RAR_
 
 // Workgroups go to the eight XCDs in turn; each XCD gets one run of tiles, in
 // bands of four tile rows, so that its L2 holds the operands they share.
-__device__ __forceinline__ void tile_of(const GemmParams &p, int64_t &tm, int64_t &tn, int &split)
+__device__ __forceinline__ void tile_of(const GemmParams &p, int64_t id, int64_t &tm, int64_t &tn, int &split)
 {
     const int64_t tiles = p.tiles_m * p.tiles_n, total = tiles * p.splits;
-    int64_t id = blockIdx.x;
     const int64_t per = total / 8;
     if (id < per * 8)
         id = (id % 8) * per + id / 8;
@@ -433,19 +432,15 @@ __device__ __forceinline__ void product(f32x4 &acc, bf16x8 b, bf16x8 a)
 // Fragments of A are replaced in place once their row of products is issued;
 // those of B need two sets.
 template <int BM, int BN, int WM, int WN, bool ACONTIG, bool BCONTIG>
-__global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParams p)
+__device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RAR_LDS char *const lds)
 {
-// (the host pass needs the kernel's name only)
-#if defined(__HIP_DEVICE_COMPILE__)
     constexpr int kWaves = WM * WN, kEarly = 1;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
     constexpr int kBuf = (BM + BN) * 128;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kBuf];
-    RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
     int64_t tm, tn;
     int split;
-    tile_of(p, tm, tn, split);
+    tile_of(p, block, tm, tn, split);
     const int64_t m0 = tm * BM, n0 = tn * BN;
     const int64_t k0 = split * p.steps_per_split * 64;
     const int64_t kend = k0 + p.steps_per_split * 64 < p.K ? k0 + p.steps_per_split * 64 : p.K;
@@ -551,7 +546,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
                 *tile_slot<FN * 16>(tile, h * 16 + (lane & 15), j * 4 + (lane >> 4)) = acc[i + h][j];
         finish_rows<bf16, FN * 16, kPass>(p, split, tile, m0 + wm + i * 16, n0 + wn);
     }
-#endif
 }
 
 // ---------------------------------------------------------------------------
@@ -566,17 +560,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) rar_gemm_bf16(const GemmParam
 // ahead.  In the last group of a step the waves meet: the next step has then
 // arrived, and this one's half is free for the step after it.
 template <int B, bool ACONTIG, bool BCONTIG>
-__global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_gemm_f32(const GemmParams p)
+__device__ __forceinline__ void gemm_f32(const GemmParams &p, int64_t block, RAR_LDS char *const lds)
 {
-#if defined(__HIP_DEVICE_COMPILE__)
     constexpr int kStep = 32, F = B / 64;
     constexpr int kBuf = 2 * B * 128;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * kBuf];
-    RAR_LDS char *const lds = (RAR_LDS char *)lds_mem;
 
     int64_t tm, tn;
     int split;
-    tile_of(p, tm, tn, split);
+    tile_of(p, block, tm, tn, split);
     const int64_t m0 = tm * B, n0 = tn * B;
     const int64_t k0 = split * p.steps_per_split * kStep;
     const int64_t kend = k0 + p.steps_per_split * kStep < p.K ? k0 + p.steps_per_split * kStep : p.K;
@@ -659,6 +650,54 @@ __global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_gemm_f32(const Gemm
                 *tile_slot<W>(tile, i * 32 + (lane & 31), j * 8 + q * 2 + (lane >> 5)) =
                     f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     finish_rows<float, W, W>(p, split, tile, m0 + wm, n0 + wn);
+}
+
+// ---------------------------------------------------------------------------
+// The layer's launches
+// ---------------------------------------------------------------------------
+
+// (The host pass needs the kernels' names only.)
+template <int B, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) rar_forward_bf16(const GemmParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    gemm_bf16<B, B, WM, WN, true, false>(p, blockIdx.x, (RAR_LDS char *)lds);
+#endif
+}
+
+// Both products of a backward pass in one launch: they need only dz, and of a
+// small layer each leaves most of the chip idle.
+template <int B, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) rar_backward_bf16(const GemmPair p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    if (blockIdx.x < p.x_blocks)
+        gemm_bf16<B, B, WM, WN, true, true>(p.x, blockIdx.x, (RAR_LDS char *)lds);
+    else
+        gemm_bf16<B, B, WM, WN, false, false>(p.w, blockIdx.x - p.x_blocks, (RAR_LDS char *)lds);
+#endif
+}
+
+template <int B>
+__global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_forward_f32(const GemmParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    gemm_f32<B, true, false>(p, blockIdx.x, (RAR_LDS char *)lds);
+#endif
+}
+
+template <int B>
+__global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_backward_f32(const GemmPair p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    if (blockIdx.x < p.x_blocks)
+        gemm_f32<B, true, true>(p.x, blockIdx.x, (RAR_LDS char *)lds);
+    else
+        gemm_f32<B, false, false>(p.w, blockIdx.x - p.x_blocks, (RAR_LDS char *)lds);
 #endif
 }
 
@@ -769,10 +808,10 @@ __global__ void __launch_bounds__(1024) rar_gemv(const GemmParams p)
 // Partial products of a split reduction, joined in the order of the splits:
 // the result does not depend on which workgroup finished first.
 template <class T>
-__global__ void __launch_bounds__(256) rar_gemm_join(const GemmParams p)
+__device__ __forceinline__ void join(const GemmParams &p, int64_t block)
 {
     const int64_t per_row = p.pitch / 8;  // pitch is whole groups, so a group's four lanes are neighbours
-    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t g = block * 256 + threadIdx.x;
     const int64_t m = g / per_row, n = (g - m * per_row) * 8;
     float v[8] = {};
     if (m < p.M && n < p.N) {
@@ -809,10 +848,13 @@ __device__ __forceinline__ f32x4 get4(const T *p, int cnt, bool vec)
 // A copy with whole 16-byte rows for operands whose rows are not: the products
 // read 16 bytes at a time.  Bound by HBM bandwidth; the copy is small against
 // the product that reads it.
+// Two matrices in one launch, the second's rows behind the first's.
 template <class T>
-__global__ void __launch_bounds__(256) rar_pack_rows(const PackParams p)
+__global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, const PackParams second)
 {
-    const int64_t row = blockIdx.x;
+    const bool is_second = blockIdx.x >= first.rows;
+    const PackParams &p = is_second ? second : first;
+    const int64_t row = blockIdx.x - (is_second ? first.rows : 0);
     const T *src = (const T *)p.src + row * p.ld;
     T *dst = (T *)p.dst + row * p.pitch;
     for (int64_t c = (int64_t)blockIdx.y * 1024 + threadIdx.x * 4; c < p.pitch; c += (int64_t)gridDim.y * 1024) {
@@ -904,12 +946,12 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
     }
 }
 
+// db: 64 columns a workgroup; each wave sums every fourth chunk.
 template <class T>
-__global__ void __launch_bounds__(256) rar_column_sum(const SumParams p)
+__device__ __forceinline__ void column_sum(const SumParams &p, int64_t block)
 {
-    // 64 columns a workgroup; each wave sums every fourth chunk
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t c = block * 64 + lane;
     float s = 0.0f;
     if (c < p.cols)
 #pragma unroll 16
@@ -927,38 +969,44 @@ __global__ void __launch_bounds__(256) rar_column_sum(const SumParams p)
     }
 }
 
-template <int B, int WM, int WN>
-hipError_t run_bf16(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_t st)
+// What is left after the products, in one launch: the joins of split
+// reductions and db.
+template <class T>
+__global__ void __launch_bounds__(256) rar_finish(const FinishParams p)
 {
-    if (l == kGemmForward)
-        rar_gemm_bf16<B, B, WM, WN, true, false><<<grid, 64 * WM * WN, 0, st>>>(p);
-    else if (l == kGemmGradX)
-        rar_gemm_bf16<B, B, WM, WN, true, true><<<grid, 64 * WM * WN, 0, st>>>(p);
-    else
-        rar_gemm_bf16<B, B, WM, WN, false, false><<<grid, 64 * WM * WN, 0, st>>>(p);
-    return hipGetLastError();
-}
-
-template <int B>
-hipError_t run_f32(GemmLayout l, const GemmParams &p, unsigned grid, hipStream_t st)
-{
-    if (l == kGemmForward)
-        rar_gemm_f32<B, true, false><<<grid, 256, 0, st>>>(p);
-    else if (l == kGemmGradX)
-        rar_gemm_f32<B, true, true><<<grid, 256, 0, st>>>(p);
-    else
-        rar_gemm_f32<B, false, false><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+    int64_t block = blockIdx.x;
+    if (block < p.a_blocks) {
+        join<T>(p.a, block);
+        return;
+    }
+    block -= p.a_blocks;
+    if (block < p.b_blocks) {
+        join<T>(p.b, block);
+        return;
+    }
+    column_sum<T>(p.sum, block - p.b_blocks);
 }
 
 }  // namespace
 
-hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, int tile, hipStream_t st)
+hipError_t launch_forward(rar_dtype dt, const GemmParams &p, int tile, hipStream_t st)
 {
-    const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * p.splits);
+    const unsigned grid = blocks_of(p);
     if (dt == RAR_BF16)
-        return tile == 256 ? run_bf16<256, 2, 4>(l, p, grid, st) : run_bf16<128, 2, 2>(l, p, grid, st);
-    return tile == 128 ? run_f32<128>(l, p, grid, st) : run_f32<64>(l, p, grid, st);
+        tile == 256 ? rar_forward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p) : rar_forward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
+    else
+        tile == 128 ? rar_forward_f32<128><<<grid, 256, 0, st>>>(p) : rar_forward_f32<64><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_backward(rar_dtype dt, const GemmPair &p, unsigned w_blocks, int tile, hipStream_t st)
+{
+    const unsigned grid = p.x_blocks + w_blocks;
+    if (dt == RAR_BF16)
+        tile == 256 ? rar_backward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p) : rar_backward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
+    else
+        tile == 128 ? rar_backward_f32<128><<<grid, 256, 0, st>>>(p) : rar_backward_f32<64><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
 }
 
 namespace {
@@ -986,24 +1034,14 @@ hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st)
+hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st)
 {
-    const int64_t groups = p.M * (p.pitch / 8);
-    const unsigned grid = (unsigned)((groups + 255) / 256);
+    const int64_t pitch = a.pitch > b.pitch ? a.pitch : b.pitch;
+    const dim3 grid((unsigned)(a.rows + b.rows), (unsigned)((pitch + 1023) / 1024 < 64 ? (pitch + 1023) / 1024 : 64));
     if (dt == RAR_BF16)
-        rar_gemm_join<bf16><<<grid, 256, 0, st>>>(p);
+        rar_pack_rows<bf16><<<grid, 256, 0, st>>>(a, b);
     else
-        rar_gemm_join<float><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
-}
-
-hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st)
-{
-    const dim3 grid((unsigned)p.rows, (unsigned)((p.pitch + 1023) / 1024 < 64 ? (p.pitch + 1023) / 1024 : 64));
-    if (dt == RAR_BF16)
-        rar_pack_rows<bf16><<<grid, 256, 0, st>>>(p);
-    else
-        rar_pack_rows<float><<<grid, 256, 0, st>>>(p);
+        rar_pack_rows<float><<<grid, 256, 0, st>>>(a, b);
     return hipGetLastError();
 }
 
@@ -1035,13 +1073,13 @@ hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st)
     return hipGetLastError();
 }
 
-hipError_t launch_sum(rar_dtype dt, const SumParams &p, hipStream_t st)
+hipError_t launch_finish(rar_dtype dt, const FinishParams &p, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((p.cols + 63) / 64);
+    const unsigned grid = p.a_blocks + p.b_blocks + (unsigned)((p.sum.cols + 63) / 64);
     if (dt == RAR_BF16)
-        rar_column_sum<bf16><<<grid, 256, 0, st>>>(p);
+        rar_finish<bf16><<<grid, 256, 0, st>>>(p);
     else
-        rar_column_sum<float><<<grid, 256, 0, st>>>(p);
+        rar_finish<float><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
 }
 

@@ -216,7 +216,7 @@ ForwardWs forward_ws(const Layer &l, void *ws)
 
 struct BackwardWs {
     void *dz, *x, *w;
-    float *sums, *part;
+    float *sums, *part_x, *part_w;
     int64_t bytes;
 };
 
@@ -229,7 +229,8 @@ BackwardWs backward_ws(const Layer &l, void *ws)
     b.x = c.take(l.T * packed(l.K, l.dt) * es);
     b.w = c.take(l.K * packed(l.N, l.dt) * es);
     b.sums = (float *)c.take(div_up(l.T, sum_rows(l.T, l.N)) * l.N * 4);
-    b.part = (float *)c.take(std::max(shape_of(l.dt, l.T, l.K, l.N).part_bytes, shape_of(l.dt, l.K, l.N, l.T).part_bytes));
+    b.part_x = (float *)c.take(shape_of(l.dt, l.T, l.K, l.N).part_bytes);
+    b.part_w = (float *)c.take(shape_of(l.dt, l.K, l.N, l.T).part_bytes);
     b.bytes = l.T ? c.used : 0;
     return b;
 }
@@ -242,11 +243,10 @@ int wide_outputs(const GemmParams &p, int es)
            aligned(p.bias, 16);
 }
 
-rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *part, hipStream_t st)
+// Fills in the shape of a product; false if its grid is too large.
+bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
 {
     const Shape s = shape_of(dt, p.M, p.N, p.K);
-    if (s.tiles_m * s.tiles_n * s.splits > kMaxBlocks)
-        return RAR_EINVAL;
     p.tiles_m = s.tiles_m;
     p.tiles_n = s.tiles_n;
     p.splits = (int)s.splits;
@@ -254,28 +254,31 @@ rar_status product(rar_dtype dt, rar::GemmLayout layout, GemmParams p, float *pa
     p.pitch = s.pitch;
     p.part = part;
     p.vec = wide_outputs(p, esize(dt));
-    if (s.splits == 1)
-        return launched(rar::launch_gemm(dt, layout, p, s.tile, st));
-    GemmParams q = p;
-    q.mode = rar::kModePartial;
-    rar_status rc = launched(rar::launch_gemm(dt, layout, q, s.tile, st));
-    return rc != RAR_OK ? rc : launched(rar::launch_join(dt, p, st));
+    *tile = s.tile;
+    return s.tiles_m * s.tiles_n * s.splits <= kMaxBlocks / 2;
 }
 
-// The matrix itself where its rows can be read directly, else a packed copy.
-rar_status readable(const Mat &m, rar_dtype dt, void *copy, const void **p, int64_t *ld, hipStream_t st)
+// The product as its launch sees it: partial sums where the reduction is split.
+GemmParams launched_form(GemmParams p)
+{
+    if (p.splits > 1)
+        p.mode = rar::kModePartial;
+    return p;
+}
+
+// Sends an operand whose rows cannot be read directly to a packed copy.
+bool needs_pack(const Mat &m, rar_dtype dt, void *copy, const void **p, int64_t *ld, rar::PackParams *k)
 {
     *p = m.p;
     *ld = m.ld;
-    if (m.rows == 0 || direct(m))
-        return RAR_OK;
-    rar::PackParams k{m.p, copy, m.ld, packed(m.cols, dt), m.rows, m.cols};
+    if (m.empty() || direct(m))
+        return false;
+    *k = rar::PackParams{m.p, copy, m.ld, packed(m.cols, dt), m.rows, m.cols};
     *p = copy;
-    *ld = k.pitch;
-    return launched(rar::launch_pack(dt, k, st));
+    *ld = k->pitch;
+    return true;
 }
 
-// Where both extents are whole 16-byte groups nothing is packed for its width.
 int64_t groups_of(int64_t cols) { return div_up(cols, rar::kCkptGroup); }
 
 }  // namespace
@@ -427,12 +430,21 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
         p.vec = wide_outputs(p, es);
         return launched(rar::launch_gemv(dt, p, direct(mx) && direct(mw), st));
     }
-    rar_status rc = readable(mx, dt, f.x, &p.a, &p.lda, st);
+    rar::PackParams kx{}, kw{};
+    int tile;
+    const bool px = needs_pack(mx, dt, f.x, &p.a, &p.lda, &kx), pw = needs_pack(mw, dt, f.w, &p.b, &p.ldb, &kw);
+    if (!shape_product(dt, p, f.part, &tile))
+        return RAR_EINVAL;
+    rar_status rc = px || pw ? launched(rar::launch_pack(dt, kx, kw, st)) : RAR_OK;
     if (rc == RAR_OK)
-        rc = readable(mw, dt, f.w, &p.b, &p.ldb, st);
-    if (rc != RAR_OK)
-        return rc;
-    return product(dt, rar::kGemmForward, p, f.part, st);
+        rc = launched(rar::launch_forward(dt, launched_form(p), tile, st));
+    if (rc == RAR_OK && p.splits > 1) {
+        rar::FinishParams e{};
+        e.a = p;
+        e.a_blocks = rar::join_blocks(p);
+        rc = launched(rar::launch_finish(dt, e, st));
+    }
+    return rc;
 }
 
 extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const void *dy, int64_t lddy, const void *x,
@@ -478,12 +490,61 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
     if (!apart({mdx, mdw, mdb, mws}, {mdy, mx, mw, mp, mxs, mps}))
         return RAR_EINVAL;
 
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    rar_status rc = RAR_OK;
-    const void *dz = dy;
-    int64_t lddz = lddy;
     const bool need_dz = (dx || dw) && T > 0 && (act || !direct(mdy));
-    if (T > 0 && (need_dz || db)) {
+    const void *const dz = need_dz ? b.dz : dy;
+    const int64_t lddz = need_dz ? packed(N, dt) : lddy;
+    rar::PackParams kx{}, kw{};
+    bool px = false, pw = false;
+    GemmParams gx{}, gw{};
+    int tile_x = 0, tile_w = 0;
+    if (dx) {
+        gx.a = dz;
+        gx.lda = lddz;
+        pw = needs_pack(mw, dt, b.w, &gx.b, &gx.ldb, &kw);
+        gx.M = T;
+        gx.N = K;
+        gx.K = N;
+        gx.out = dx;
+        gx.ldo = lddx;
+        gx.mode = rar::kModeStore;
+        if (!shape_product(dt, gx, b.part_x, &tile_x))
+            return RAR_EINVAL;
+    }
+    if (dw) {
+        if (x_scales) {
+            gw.a = b.x;
+            gw.lda = packed(K, dt);
+        } else {
+            px = needs_pack(mx, dt, b.x, &gw.a, &gw.lda, &kx);
+        }
+        gw.b = dz;
+        gw.ldb = lddz;
+        gw.M = K;
+        gw.N = N;
+        gw.K = T;
+        gw.out = dw;
+        gw.ldo = N;
+        gw.mode = rar::kModeStore;
+        gw.accumulate = accumulate;
+        if (!shape_product(dt, gw, b.part_w, &tile_w))
+            return RAR_EINVAL;
+    }
+
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    rar_status rc = px || pw ? launched(rar::launch_pack(dt, kx, kw, st)) : RAR_OK;
+    if (rc == RAR_OK && dw && x_scales && T > 0) {
+        rar::CkptParams c{};
+        c.codes = (uint8_t *)x;
+        c.scales = (uint8_t *)x_scales;
+        c.y = b.x;
+        c.ldy = packed(K, dt);
+        c.pitch_zero = c.ldy;
+        c.rows = T;
+        c.cols = K;
+        c.act = RAR_ACT_NONE;
+        rc = launched(rar::launch_ckpt_load(dt, c, st));
+    }
+    if (rc == RAR_OK && T > 0 && (need_dz || db)) {
         rar::DzParams d{};
         d.dy = dy;
         d.ldy = lddy;
@@ -498,67 +559,32 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
         d.rows_per_chunk = sum_rows(T, N);
         d.act = plan->act;
         rc = launched(rar::launch_dz(dt, d, st));
-        if (rc != RAR_OK)
-            return rc;
-        if (need_dz) {
-            dz = b.dz;
-            lddz = d.pitch;
-        }
     }
-    if (db) {
-        rar::SumParams s{b.sums, T > 0 ? div_up(T, sum_rows(T, N)) : 0, N, db, accumulate};
-        rc = launched(rar::launch_sum(dt, s, st));
-        if (rc != RAR_OK)
-            return rc;
+    // the two products together where they take the same kernel
+    rar::GemmPair pair{launched_form(gx), launched_form(gw), dx ? rar::blocks_of(gx) : 0};
+    const unsigned w_blocks = dw ? rar::blocks_of(gw) : 0;
+    if (rc == RAR_OK && dx && dw && tile_x == tile_w) {
+        rc = launched(rar::launch_backward(dt, pair, w_blocks, tile_x, st));
+    } else {
+        if (rc == RAR_OK && dx)
+            rc = launched(rar::launch_backward(dt, pair, 0, tile_x, st));
+        pair.x_blocks = 0;
+        if (rc == RAR_OK && dw)
+            rc = launched(rar::launch_backward(dt, pair, w_blocks, tile_w, st));
     }
+    rar::FinishParams e{};
     if (dx) {
-        GemmParams p{};
-        p.a = dz;
-        p.lda = lddz;
-        rc = readable(mw, dt, b.w, &p.b, &p.ldb, st);
-        if (rc != RAR_OK)
-            return rc;
-        p.M = T;
-        p.N = K;
-        p.K = N;
-        p.out = dx;
-        p.ldo = lddx;
-        p.mode = rar::kModeStore;
-        rc = product(dt, rar::kGemmGradX, p, b.part, st);
-        if (rc != RAR_OK)
-            return rc;
+        e.a = gx;
+        e.a_blocks = rar::join_blocks(gx);
     }
     if (dw) {
-        GemmParams p{};
-        if (T > 0 && x_scales) {
-            rar::CkptParams c{};
-            c.codes = (uint8_t *)x;
-            c.scales = (uint8_t *)x_scales;
-            c.y = b.x;
-            c.ldy = packed(K, dt);
-            c.pitch_zero = c.ldy;
-            c.rows = T;
-            c.cols = K;
-            c.act = RAR_ACT_NONE;
-            rc = launched(rar::launch_ckpt_load(dt, c, st));
-            p.a = b.x;
-            p.lda = c.ldy;
-        } else {
-            rc = readable(mx, dt, b.x, &p.a, &p.lda, st);
-        }
-        if (rc != RAR_OK)
-            return rc;
-        p.b = dz;
-        p.ldb = lddz;
-        p.M = K;
-        p.N = N;
-        p.K = T;
-        p.out = dw;
-        p.ldo = N;
-        p.mode = rar::kModeStore;
-        p.accumulate = accumulate;
-        rc = product(dt, rar::kGemmGradW, p, b.part, st);
+        e.b = gw;
+        e.b_blocks = rar::join_blocks(gw);
     }
+    if (db)
+        e.sum = rar::SumParams{b.sums, T > 0 ? div_up(T, sum_rows(T, N)) : 0, N, db, accumulate};
+    if (rc == RAR_OK && (e.a_blocks || e.b_blocks || db))
+        rc = launched(rar::launch_finish(dt, e, st));
     return rc;
 }
 

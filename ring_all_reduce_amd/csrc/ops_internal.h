@@ -14,17 +14,14 @@ constexpr int kCkptGroup = RAR_CKPT_GROUP;
 
 // One matrix product D[m][n] = sum_k A(m,k) B(n,k).  An operand is stored either
 // with its reduction index contiguous (element (r,k) at r*ld + k) or with the
-// reduction index slow (at k*ld + r); which one is the kernel's layout.
-enum GemmLayout {
-    kGemmForward = 0,  // A = x [T][K] contiguous, B = W [K][N] slow
-    kGemmGradX = 1,    // A = dz [T][N] contiguous, B = W [K][N] contiguous
-    kGemmGradW = 2     // A = x [T][K] slow, B = dz [T][N] slow
-};
-
+// reduction index slow (at k*ld + r):
+//   forward  A = x [T][K] contiguous,  B = W [K][N] slow
+//   grad x   A = dz [T][N] contiguous, B = W [K][N] contiguous
+//   grad W   A = x [T][K] slow,        B = dz [T][N] slow
 enum GemmMode {
     kModeStore = 0,    // out = D (+ out when accumulate)
     kModeForward = 1,  // z = D + bias; pre = z; out = act(z) + residual
-    kModePartial = 2   // part[split] = D in binary32 (joined by launch_join)
+    kModePartial = 2   // part[split] = D in binary32 (joined by launch_finish)
 };
 
 struct GemmParams {
@@ -112,14 +109,31 @@ struct EmbedGradParams {
     void *ws;
 };
 
-hipError_t launch_gemm(rar_dtype dt, GemmLayout l, const GemmParams &p, int tile, hipStream_t st);
+inline unsigned blocks_of(const GemmParams &p) { return (unsigned)(p.tiles_m * p.tiles_n * p.splits); }
+
+hipError_t launch_forward(rar_dtype dt, const GemmParams &p, int tile, hipStream_t st);
+// grad x in the first x_blocks workgroups, grad W in the w_blocks behind them.
+struct GemmPair {
+    GemmParams x, w;
+    unsigned x_blocks;
+};
+hipError_t launch_backward(rar_dtype dt, const GemmPair &p, unsigned w_blocks, int tile, hipStream_t st);
 // A forward product of at most kGemvRows rows; vec: rows of x and W can be read 16 bytes at a time.
 constexpr int kGemvRows = 4;
 hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t st);
-hipError_t launch_join(rar_dtype dt, const GemmParams &p, hipStream_t st);
-hipError_t launch_pack(rar_dtype dt, const PackParams &p, hipStream_t st);
+hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st);
 hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st);
-hipError_t launch_sum(rar_dtype dt, const SumParams &p, hipStream_t st);
+// Joins of split products (a_blocks, b_blocks workgroups, 0: none) and column sums (sum.cols 0: none).
+struct FinishParams {
+    GemmParams a, b;
+    unsigned a_blocks, b_blocks;
+    SumParams sum;
+};
+inline unsigned join_blocks(const GemmParams &p)
+{
+    return p.splits > 1 ? (unsigned)((p.M * (p.pitch / 8) + 255) / 256) : 0;
+}
+hipError_t launch_finish(rar_dtype dt, const FinishParams &p, hipStream_t st);
 hipError_t launch_ckpt_store(rar_dtype dt, const CkptParams &p, hipStream_t st);
 hipError_t launch_ckpt_load(rar_dtype dt, const CkptParams &p, hipStream_t st);
 hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t st);
