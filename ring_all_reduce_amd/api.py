@@ -436,6 +436,9 @@ def _device_of(x, what: str) -> None:
 
 def _matrix(x, what: str, tdtype, rows: int, cols: int):
     """(address, leading dimension) of a rows x cols matrix argument."""
+    if getattr(x, "dtype", None) is tdtype and x.is_cuda and x.is_contiguous() and x.get_device() == _here() and rows > 0 \
+            and x.shape == (rows, cols):
+        return x.data_ptr(), cols  # the usual case; what follows finds out what is wrong with others
     if x is None:
         return 0, cols
     if isinstance(x, int):
@@ -461,6 +464,8 @@ def _matrix(x, what: str, tdtype, rows: int, cols: int):
 
 def _dense(x, what: str, tdtype, numel: int) -> int:
     """Address of a contiguous argument of exactly numel elements."""
+    if getattr(x, "dtype", None) is tdtype and x.is_cuda and x.is_contiguous() and x.get_device() == _here() and x.numel() == numel:
+        return x.data_ptr()
     if x is None or isinstance(x, int):
         return x or 0
     if not hasattr(x, "data_ptr"):
@@ -552,8 +557,13 @@ def rar_linear_destroy(plan: Linear) -> None:
 
 def rar_linear_workspace(plan: Linear, T: int):
     """(forward bytes, backward bytes) for T rows."""
+    known = plan._bytes.get(T)
+    if known is not None and plan.handle:
+        return known
     f, b = ctypes.c_int64(), ctypes.c_int64()
     _check(lib().rar_linear_workspace(plan.handle, T, ctypes.byref(f), ctypes.byref(b)), "rar_linear_workspace")
+    if len(plan._bytes) < 64:  # a layer's plan serves a few batch sizes
+        plan._bytes[T] = f.value, b.value
     return f.value, b.value
 
 

@@ -48,12 +48,26 @@ __device__ __forceinline__ void store4(bf16 *p, f32x4 v)
     *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
 }
 
+// Data that a call reads once: kept from displacing other lines.
+template <class V>
+__device__ __forceinline__ V load_once(const V *p)
+{
+    return __builtin_nontemporal_load(p);
+}
+
+template <class V>
+__device__ __forceinline__ void store_once(V *p, V v)
+{
+    __builtin_nontemporal_store(v, p);
+}
+
 // Eight consecutive elements, of which the first cnt exist; vec: 16-byte aligned.
-template <class T>
-__device__ __forceinline__ void load8(const T *p, int cnt, bool vec, float (&v)[8])
+template <bool ONCE = false>
+__device__ __forceinline__ void load8(const float *p, int cnt, bool vec, float (&v)[8])
 {
     if (vec && cnt == 8) {
-        const f32x4 a = load4(p), b = load4(p + 4);
+        const f32x4 *const w = reinterpret_cast<const f32x4 *>(p);
+        const f32x4 a = ONCE ? load_once(w) : w[0], b = ONCE ? load_once(w + 1) : w[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = a[i];
@@ -66,24 +80,32 @@ __device__ __forceinline__ void load8(const T *p, int cnt, bool vec, float (&v)[
         v[i] = i < cnt ? to_f32(p[i]) : 0.0f;
 }
 
-template <class T>
-__device__ __forceinline__ void store8(T *p, int cnt, bool vec, const float (&v)[8])
+template <bool ONCE = false>
+__device__ __forceinline__ void store8(float *p, int cnt, bool vec, const float (&v)[8])
 {
     if (vec && cnt == 8) {
-        store4(p, f32x4{v[0], v[1], v[2], v[3]});
-        store4(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+        f32x4 *const w = reinterpret_cast<f32x4 *>(p);
+        const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if (ONCE) {
+            store_once(w, a);
+            store_once(w + 1, b);
+        } else {
+            w[0] = a;
+            w[1] = b;
+        }
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < cnt)
-            p[i] = from_f32<T>(v[i]);
+            p[i] = v[i];
 }
 
+template <bool ONCE = false>
 __device__ __forceinline__ void load8(const bf16 *p, int cnt, bool vec, float (&v)[8])
 {
     if (vec && cnt == 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+        const u32x4 w = ONCE ? load_once(reinterpret_cast<const u32x4 *>(p)) : *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -96,11 +118,15 @@ __device__ __forceinline__ void load8(const bf16 *p, int cnt, bool vec, float (&
         v[i] = i < cnt ? to_f32(p[i]) : 0.0f;
 }
 
+template <bool ONCE = false>
 __device__ __forceinline__ void store8(bf16 *p, int cnt, bool vec, const float (&v)[8])
 {
     if (vec && cnt == 8) {
-        *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                              pack_bf16(v[6], v[7])};
+        const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        if (ONCE)
+            store_once(reinterpret_cast<u32x4 *>(p), w);
+        else
+            *reinterpret_cast<u32x4 *>(p) = w;
         return;
     }
 #pragma unroll

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) rar_ckpt_store_rows(const CkptParams p)
         const int64_t c = (int64_t)at.group * kCkptGroup + q * kLane;
         const int cnt = p.cols - c >= kLane ? kLane : (p.cols - c < 0 ? 0 : (int)(p.cols - c));
         float v[8];
-        load8((const T *)p.x + at.row * p.ldx + c, cnt, vec, v);
+        load8<true>((const T *)p.x + at.row * p.ldx + c, cnt, vec, v);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) rar_embed_rows(const EmbedParams p)
             *dst = from_f32<T>(ok ? to_f32(*src) * p.scale : 0.0f);
         } else if constexpr (sizeof(T) == 4) {
             const f32x4 v = load4(src);
-            store4(dst, ok ? v * p.scale : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            store_once(reinterpret_cast<f32x4 *>(dst), ok ? v * p.scale : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
         } else {
             const u32x4 w = *reinterpret_cast<const u32x4 *>(src);
             u32x4 o;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) rar_embed_rows(const EmbedParams p)
                 const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
                 o[i] = ok ? pack_bf16(lo * p.scale, hi * p.scale) : 0u;
             }
-            *reinterpret_cast<u32x4 *>(dst) = o;
+            store_once(reinterpret_cast<u32x4 *>(dst), o);
         }
     }
 }
@@ -185,7 +185,7 @@ __device__ __forceinline__ void clear(const Clear &c, int64_t block)
     if (b + threadIdx.x * 2 < hi)
         *reinterpret_cast<uint16_t *>(c.at + b + threadIdx.x * 2) = 0;
     for (int64_t i = a + threadIdx.x * 16; i < b; i += kSortThreads * 16)
-        *reinterpret_cast<u32x4 *>(c.at + i) = u32x4{0, 0, 0, 0};
+        store_once(reinterpret_cast<u32x4 *>(c.at + i), u32x4{0, 0, 0, 0});
 }
 
 // A whole batch of at most N * kSortThreads tokens in one workgroup.
@@ -373,7 +373,7 @@ struct Columns {
             const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (col(0) < D ? col(0) : 0));
 #pragma unroll
             for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-                v.v[h] = p[h];
+                v.v[h] = load_once(p + h);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -420,7 +420,7 @@ struct Columns {
                 acc[i] += old.at(i);
         }
         if constexpr (VEC) {
-            store8(out + col(0), col(0) < D ? 8 : 0, true, acc);
+            store8<true>(out + col(0), col(0) < D ? 8 : 0, true, acc);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

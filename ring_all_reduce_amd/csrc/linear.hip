@@ -320,7 +320,7 @@ __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char 
         for (int i = 0; i < 8; ++i)
             v[i] += bias[i];
         if (p.pre)
-            store8(pre, 8, true, v);
+            store8<true>(pre, 8, true, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = act_value<T>(ACT, v[i]);
@@ -328,7 +328,7 @@ __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += t[i];
-        store8(out, 8, true, v);
+        store8<true>(out, 8, true, v);
         out += so;
         pre += sp;
         res += sr;
@@ -381,9 +381,10 @@ __device__ __forceinline__ void tile_of(const GemmParams &p, int64_t id, int64_t
         id = (id % 8) * per + id / 8;
     split = (int)(id / tiles);
     id -= split * tiles;
-    const int64_t band = 4 * p.tiles_n;
-    const int64_t first = id / band * 4;
-    const int64_t rows = p.tiles_m - first < 4 ? p.tiles_m - first : 4;
+    constexpr int kBand = 4;  // tile rows: 8 and 2 measured 1-2% slower at 8192 x 2048 x 8192
+    const int64_t band = kBand * p.tiles_n;
+    const int64_t first = id / band * kBand;
+    const int64_t rows = p.tiles_m - first < kBand ? p.tiles_m - first : kBand;
     const int64_t in = id % band;
     tm = first + in % rows;
     tn = in / rows;
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_backward_f32(const 
 // kGemvK consecutive k of its columns and the same k of x in one vector each.
 // Partial sums are joined by lane exchanges and through LDS, in an order fixed
 // by the sizes; nothing passes through memory.
-constexpr int kGemvCols = 64, kGemvK = 8;
+constexpr int kGemvCols = 64, kGemvK = 8;  // 32 columns a workgroup measured the same
 
 template <class T, int E>
 __device__ __forceinline__ float element(const u32x4 (&v)[E], int i)
@@ -793,16 +794,17 @@ __global__ void __launch_bounds__(1024) rar_gemv(const GemmParams p)
     __syncthreads();
     if (threadIdx.x >= 64)
         return;
-    // eight lanes finish a row, four of them a group of a checkpoint
-    const int r = lane / 8;
+    // a few lanes finish a row, four of them a group of a checkpoint
+    constexpr int kEnd = kGemvCols / 8;
+    const int r = lane / kEnd;
     float v[8] = {};
     if (r < R)
 #pragma unroll
         for (int s = 0; s < kWaves; ++s)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] += sums[s][r][lane % 8 * 8 + i];
-    epilogue<T>(p, r < R ? r : p.M, n0 + lane % 8 * 8, v);
+                v[i] += sums[s][r][lane % kEnd * 8 + i];
+    epilogue<T>(p, r < R ? r : p.M, n0 + lane % kEnd * 8, v);
 }
 
 // Partial products of a split reduction, joined in the order of the splits:
@@ -894,9 +896,9 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
             for (int u = 0; u < kDzRows; ++u) {
                 const int64_t row = r + 4 * u;
                 const int n = row < r1 ? cnt : 0;
-                load8((const T *)p.dy + row * p.ldy + c, n, vdy, d[u]);
+                load8<true>((const T *)p.dy + row * p.ldy + c, n, vdy, d[u]);
                 if (SOURCE == kDzPre)
-                    load8((const T *)p.pre + row * p.ldp + c, n, vpre, z[u]);
+                    load8<true>((const T *)p.pre + row * p.ldp + c, n, vpre, z[u]);
                 w[u] = u32x2{0, 0};
                 e[u] = 0;
                 if (SOURCE == kDzCkpt && n > 0) {

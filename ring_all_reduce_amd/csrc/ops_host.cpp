@@ -210,7 +210,7 @@ ForwardWs forward_ws(const Layer &l, void *ws)
     f.x = c.take(l.T * packed(l.K, l.dt) * es);
     f.w = c.take(l.K * packed(l.N, l.dt) * es);
     f.part = (float *)c.take(shape_of(l.dt, l.T, l.N, l.K).part_bytes);
-    f.bytes = l.T ? c.used : 0;
+    f.bytes = l.T > rar::kGemvRows ? c.used : 0;  // few rows need none
     return f;
 }
 
@@ -386,7 +386,7 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
     const int64_t K = plan->K, N = plan->N;
     const rar_dtype dt = plan->dtype;
     const int es = esize(dt);
-    if (!x || !w || !y || !ws || (pre_scales && !pre))
+    if (!x || !w || !y || (!ws && T > rar::kGemvRows) || (pre_scales && !pre))
         return RAR_EINVAL;
     if (!valid_ld(ldx, K) || !valid_ld(ldy, N) || (residual && !valid_ld(ldr, N)) ||
         (pre && !pre_scales && !valid_ld(ldp, N)))

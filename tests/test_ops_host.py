@@ -36,10 +36,11 @@ def test_linear_plan_refuses(K, N, dt, act):
 def test_linear_workspace():
     p = linear()
     assert api.rar_linear_workspace(p, 0) == (0, 0)
+    assert api.rar_linear_workspace(p, 1)[0] == 0     # few rows: nothing is split or copied
     f, b = api.rar_linear_workspace(p, 100)
     assert f > 0 and b > f
     last = (0, 0)
-    for T in (1, 10, 100, 1000, 100_000, 1 << 24):
+    for T in (5, 10, 100, 1000, 100_000, 1 << 24):
         f, b = api.rar_linear_workspace(p, T)
         assert f % 16 == 0 and b % 16 == 0 and f > 0 and b > last[1] // 64
         last = (f, b)
