@@ -7,7 +7,7 @@
 // (every row of the vocabulary is written) or accumulated into the rows that
 // occur.  The token positions are sorted by id, stably, so each row's terms
 // stand together in token order; no floating-point atomic is used and the
-// result does not depend on timing.  Then one wave sums every 32 sorted
+// result does not depend on timing.  Then one wave sums every 32 (or 8) sorted
 // positions of 512 columns, whatever ids they hold: dy is read once, evenly,
 // however often a token occurs.  A run of one id inside a chunk is finished
 // there; the parts of a run that crosses chunks go to memory and are added in
@@ -78,7 +78,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRounds = 4;                              // keys of a lane
 constexpr int kSortKeys = kRounds * kSortThreads;       // keys of a workgroup
 constexpr int kSmallKeys = 2 * kSortKeys;               // batches that one workgroup sorts
-constexpr int kChunk = 32;                              // sorted positions that a wave sums
+constexpr int kGroup = 32;                              // chunks of a long run that are added beforehand
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V)
 {
@@ -95,7 +95,7 @@ struct SortShared {
 // them in count[wave].  Lanes with `live` false take no part.
 template <int N>
 __device__ __forceinline__ void wave_ranks(SortShared &s, const uint32_t (&digit)[N], const bool (&live)[N],
-                                           uint32_t (&rank)[N])
+                                           uint32_t (&rank)[N], int rounds, int bits)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < kSortWaves * 256; i += kSortThreads)
@@ -104,9 +104,10 @@ __device__ __forceinline__ void wave_ranks(SortShared &s, const uint32_t (&digit
     volatile uint32_t *count = s.count[wave];
 #pragma unroll
     for (int r = 0; r < N; ++r) {
+        if (r >= rounds)
+            break;
         uint64_t peers = __ballot(live[r]);
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
+        for (int b = 0; b < bits; ++b) {
             const uint64_t set = __ballot((digit[r] >> b) & 1);
             peers &= (digit[r] >> b) & 1 ? set : ~set;
         }
@@ -188,10 +189,11 @@ __device__ __forceinline__ void clear(const Clear &c, int64_t block)
         store_once(reinterpret_cast<u32x4 *>(c.at + i), u32x4{0, 0, 0, 0});
 }
 
-// A whole batch of at most N * kSortThreads tokens in one workgroup.
+// A whole batch of at most N * kSortThreads tokens in one workgroup, a wave
+// `rounds` times 64 of them in a row.
 template <int N>
 __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *ids, int T, int64_t V, int passes,
-                                                               uint32_t *keys, uint32_t *pos, Clear c)
+                                                               int bits, uint32_t *keys, uint32_t *pos, Clear c)
 {
     if (blockIdx.x > 0) {
         clear(c, blockIdx.x - 1);
@@ -202,18 +204,19 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t key[N], at[N], digit[N], rank[N];
     bool live[N];
+    const int rounds = (T + kSortThreads - 1) / kSortThreads;
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const int i = wave * (64 * N) + r * 64 + lane;
-        live[r] = i < T;
+        const int i = wave * (64 * rounds) + r * 64 + lane;
+        live[r] = r < rounds && i < T;
         key[r] = live[r] ? key_of(ids[i], V) : 0;
         at[r] = i;
     }
     for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll
         for (int r = 0; r < N; ++r)
-            digit[r] = (key[r] >> (8 * pass)) & 255;
-        wave_ranks(s, digit, live, rank);
+            digit[r] = (key[r] >> (bits * pass)) & ((1u << bits) - 1);
+        wave_ranks(s, digit, live, rank, rounds, bits);
         const uint32_t total = scan_waves(s);
         scan_digits(s, total, 0);
 #pragma unroll
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-            const int i = wave * (64 * N) + r * 64 + lane;
+            const int i = wave * (64 * rounds) + r * 64 + lane;
             if (live[r]) {
                 key[r] = k_lds[i];
                 at[r] = p_lds[i];
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
     }
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const int i = wave * (64 * N) + r * 64 + lane;
+        const int i = wave * (64 * rounds) + r * 64 + lane;
         if (live[r]) {
             keys[i] = key[r];
             pos[i] = at[r];
@@ -246,8 +249,8 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
 
 // Larger batches: digit counts of each kSortKeys tokens, then their placement.
 __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *ids, const uint32_t *keys, int64_t T,
-                                                               int64_t V, int shift, uint32_t *hist, unsigned blocks,
-                                                               Clear c)
+                                                               int64_t V, int shift, int bits, uint32_t *hist,
+                                                               unsigned blocks, Clear c)
 {
     if (blockIdx.x >= blocks) {
         clear(c, blockIdx.x - blocks);
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *id
     for (int i = threadIdx.x; i < kSortKeys; i += kSortThreads)
         if (first + i < T) {
             const uint32_t key = ids ? key_of(ids[first + i], V) : keys[first + i];
-            atomicAdd(&count[(key >> shift) & 255], 1u);
+            atomicAdd(&count[(key >> shift) & ((1u << bits) - 1)], 1u);
         }
     __syncthreads();
     if (threadIdx.x < 256)
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *id
 }
 
 __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *ids, const uint32_t *keys,
-                                                               const uint32_t *pos, int64_t T, int64_t V, int shift,
+                                                               const uint32_t *pos, int64_t T, int64_t V, int shift, int bits,
                                                                const uint32_t *hist, uint32_t *keys_out,
                                                                uint32_t *pos_out, unsigned blocks, Clear c)
 {
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *id
         live[r] = i < T;
         key[r] = live[r] ? (ids ? key_of(ids[i], V) : keys[i]) : 0;
         at[r] = live[r] ? (ids ? (uint32_t)i : pos[i]) : 0;
-        digit[r] = (key[r] >> shift) & 255;
+        digit[r] = (key[r] >> shift) & ((1u << bits) - 1);
     }
     // digit totals of all workgroups and of those before this one
     const int d = threadIdx.x & 255, quarter = threadIdx.x >> 8;
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *id
     }
     part[0][quarter][d] = all;
     part[1][quarter][d] = before;
-    wave_ranks(s, digit, live, rank);  // synchronises
+    wave_ranks(s, digit, live, rank, kRounds, bits);  // synchronises
     scan_waves(s);
     uint32_t total = 0, mine = 0;
     if (threadIdx.x < 256) {
@@ -330,10 +333,11 @@ constexpr int kCols = 512;
 struct GradWs {
     uint32_t *keys, *pos;  // sorted
     // [chunk][pitch]: the part of a run that crosses into the chunk from the
-    // left, and of one that starts in it and goes on to the right; [T / 1024]:
-    // the sum of 32 aligned chunks' `from_left` that hold one id
+    // left, and of one that starts in it and goes on to the right; [group]: the
+    // sum of kGroup aligned chunks' `from_left` that hold one id
     float *from_left, *to_right, *long_run;
     int64_t pitch;         // whole strips, in the lanes' order
+    int chunk;             // sorted positions that a wave sums
 };
 
 // Eight values of a row as they were loaded: widened only when they are added,
@@ -432,24 +436,25 @@ struct Columns {
 
 __device__ __forceinline__ int64_t wave_job(int64_t block) { return block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// One wave: 32 sorted positions of one strip, two batches of rows in flight.
+// One wave: a chunk of sorted positions of one strip, two batches of rows in
+// flight.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) rar_embed_chunks(const EmbedGradParams p, const GradWs w, int strips)
 {
     const int lane = threadIdx.x & 63;
     const int64_t job = wave_job(blockIdx.x);
     const int64_t chunk = job / strips;
-    const int64_t at = chunk * kChunk;
+    const int64_t at = chunk * w.chunk;
     if (at >= p.T)
         return;
     // lane l: position at - 1 + l, for one position on either side of the chunk
     const int64_t i = at - 1 + lane;
-    const bool have = i >= 0 && i < p.T && lane <= kChunk + 1;
+    const bool have = i >= 0 && i < p.T && lane <= w.chunk + 1;
     const uint32_t none = 0xffffffffu;
     const uint32_t key = have ? w.keys[i] : none;
     const uint32_t pos = have ? w.pos[i] : 0;
     // ids outside the vocabulary stand at the end
-    const int n = __popcll(__ballot(lane >= 1 && lane <= kChunk && key < (uint32_t)p.V));
+    const int n = __popcll(__ballot(lane >= 1 && lane <= w.chunk && key < (uint32_t)p.V));
     if (n == 0)
         return;
     const Columns<T, VEC> cols{(job - chunk * strips) * kCols, p.D};
@@ -502,21 +507,21 @@ __global__ void __launch_bounds__(256) rar_embed_chunks(const EmbedGradParams p,
     }
 }
 
-// The sum of 32 aligned chunks that hold one id which came in from the left.
+// The sum of kGroup aligned chunks that hold one id which came in from the left.
 __global__ void __launch_bounds__(256) rar_embed_long(const EmbedGradParams p, const GradWs w, int strips)
 {
-    constexpr int64_t kLong = kChunk * kChunk;
+    const int64_t len = (int64_t)kGroup * w.chunk;
     const int64_t job = wave_job(blockIdx.x);
     const int64_t group = job / strips;
-    const int64_t at = group * kLong;
-    if (at + kLong > p.T || at == 0)
+    const int64_t at = group * len;
+    if (at + len > p.T || at == 0)
         return;
     const uint32_t k = w.keys[at];
-    if (k >= (uint32_t)p.V || k != w.keys[at - 1] || k != w.keys[at + kLong - 1])
+    if (k >= (uint32_t)p.V || k != w.keys[at - 1] || k != w.keys[at + len - 1])
         return;
     const Columns<float, true> cols{(job - group * strips) * kCols, p.D};
     float acc[8] = {};
-    cols.add_partials(w.from_left, w.pitch, group * kChunk, kChunk, acc);
+    cols.add_partials(w.from_left, w.pitch, group * kGroup, kGroup, acc);
     cols.put_partial(w.long_run + group * w.pitch, acc);
 }
 
@@ -528,20 +533,20 @@ __global__ void __launch_bounds__(256) rar_embed_join(const EmbedGradParams p, c
     const int lane = threadIdx.x & 63;
     const int64_t job = wave_job(blockIdx.x);
     const int64_t chunk = job / strips;
-    const int64_t next = (chunk + 1) * kChunk;
+    const int64_t next = (chunk + 1) * w.chunk;
     if (next >= p.T)
         return;
     const uint32_t k = w.keys[next];
     if (k >= (uint32_t)p.V || w.keys[next - 1] != k)
         return;
     // a run that also fills this chunk from the left starts in an earlier one
-    if (chunk > 0 && w.keys[chunk * kChunk - 1] == k)
+    if (chunk > 0 && w.keys[chunk * w.chunk - 1] == k)
         return;
     // the last chunk whose first position still holds the id
     int64_t last = chunk;
     for (;;) {
         const int64_t c = last + 1 + lane;
-        const uint64_t same = __ballot(c * kChunk < p.T && w.keys[c * kChunk < p.T ? c * kChunk : 0] == k);
+        const uint64_t same = __ballot(c * w.chunk < p.T && w.keys[c * w.chunk < p.T ? c * w.chunk : 0] == k);
         const int run = __builtin_ctzll(~same | (1ull << 63)) + (same == ~0ull ? 1 : 0);
         last += run;
         if (run < 64)
@@ -552,13 +557,13 @@ __global__ void __launch_bounds__(256) rar_embed_join(const EmbedGradParams p, c
     cols.add_partials(w.to_right, w.pitch, chunk, 1, acc);
     int64_t c = chunk + 1;
     while (c <= last) {
-        // whole aligned groups of 32 chunks: the run fills all but its last chunk
-        if (c % kChunk == 0 && last - c >= kChunk) {
-            const int64_t n = (last - c) / kChunk;
-            cols.add_partials(w.long_run, w.pitch, c / kChunk, n, acc);
-            c += n * kChunk;
+        // whole aligned groups: the run fills all but its last chunk
+        if (c % kGroup == 0 && last - c >= kGroup) {
+            const int64_t n = (last - c) / kGroup;
+            cols.add_partials(w.long_run, w.pitch, c / kGroup, n, acc);
+            c += n * kGroup;
         } else {
-            int64_t n = kChunk - c % kChunk;
+            int64_t n = kGroup - c % kGroup;
             n = n < last - c + 1 ? n : last - c + 1;
             cols.add_partials(w.from_left, w.pitch, c, n, acc);
             c += n;
@@ -572,6 +577,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Byte offsets of the workspace's parts.
 struct Layout {
     int64_t keys[2], pos[2], hist, from_left, to_right, long_run, total, pitch;
+    int chunk;
 };
 
 Layout layout(int64_t T, int64_t D)
@@ -590,10 +596,15 @@ Layout layout(int64_t T, int64_t D)
         l.pos[i] = i && small ? l.pos[0] : take(4 * T);
     }
     l.hist = take(small ? 0 : (T + kSortKeys - 1) / kSortKeys * 1024);
-    const int64_t chunks = T > kChunk ? (T + kChunk - 1) / kChunk : 0;
+    // A wave sums 32 sorted positions, or 8 where 32 would leave most of the chip
+    // without a wave: 4097 positions of 509 binary32 columns take 30 us in chunks
+    // of 8 and 34 in chunks of 32, 65536 of 2048 bf16 columns 139 and 123 (the
+    // whole call).
+    l.chunk = T * (l.pitch / kCols) >= 65536 ? 32 : 8;
+    const int64_t chunks = T > l.chunk ? (T + l.chunk - 1) / l.chunk : 0;
     l.from_left = take(chunks * l.pitch * 4);
     l.to_right = take(chunks * l.pitch * 4);
-    l.long_run = take(T / (kChunk * kChunk) * l.pitch * 4);
+    l.long_run = take(T / (kGroup * l.chunk) * l.pitch * 4);
     l.total = at;
     return l;
 }
@@ -602,7 +613,7 @@ template <class T, bool VEC>
 void sums(const EmbedGradParams &p, const GradWs &w, hipStream_t st)
 {
     const int64_t strips = (p.D + kCols - 1) / kCols;
-    const int64_t chunks = (p.T + kChunk - 1) / kChunk, longs = p.T / (kChunk * kChunk);
+    const int64_t chunks = (p.T + w.chunk - 1) / w.chunk, longs = p.T / (kGroup * w.chunk);
     const auto grid = [strips](int64_t n) { return (unsigned)((n * strips + 3) / 4); };
     if (chunks > 0)
         rar_embed_chunks<T, VEC><<<grid(chunks), 256, 0, st>>>(p, w, (int)strips);
@@ -640,10 +651,10 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
         keys[i] = (uint32_t *)(ws + l.keys[i]);
         pos[i] = (uint32_t *)(ws + l.pos[i]);
     }
-    int bits = 0;  // of the keys 0..V
-    while (bits < 32 && (p.V >> bits) != 0)
-        ++bits;
-    const int passes = (bits + 7) / 8;
+    int width = 0;  // bits of the keys 0..V
+    while (width < 32 && (p.V >> width) != 0)
+        ++width;
+    const int passes = (width + 7) / 8, bits = (width + passes - 1) / passes;
     // the gradient in as many shares as the sort has launches
     const int64_t bytes = p.accumulate ? 0 : p.V * p.D * (dt == RAR_BF16 ? 2 : 4);
     int share = 0;
@@ -659,9 +670,9 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
         const Clear c = next_clear();
         const unsigned grid = 1 + clear_blocks(c);
         if (p.T <= kSortKeys)
-            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, keys[0], pos[0], c);
+            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0], c);
         else
-            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, keys[0], pos[0], c);
+            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0], c);
     } else {
         const unsigned blocks = (unsigned)((p.T + kSortKeys - 1) / kSortKeys);
         uint32_t *const hist = (uint32_t *)(ws + l.hist);
@@ -669,16 +680,16 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
             const int64_t *ids = pass == 0 ? p.ids : nullptr;
             const int from = (pass + 1) & 1, to = pass & 1;
             const Clear c0 = next_clear();
-            rar_sort_count<<<blocks + clear_blocks(c0), kSortThreads, 0, st>>>(ids, keys[from], p.T, p.V, 8 * pass, hist,
-                                                                              blocks, c0);
+            rar_sort_count<<<blocks + clear_blocks(c0), kSortThreads, 0, st>>>(ids, keys[from], p.T, p.V, bits * pass,
+                                                                              bits, hist, blocks, c0);
             const Clear c1 = next_clear();
             rar_sort_place<<<blocks + clear_blocks(c1), kSortThreads, 0, st>>>(
-                ids, keys[from], pos[from], p.T, p.V, 8 * pass, hist, keys[to], pos[to], blocks, c1);
+                ids, keys[from], pos[from], p.T, p.V, bits * pass, bits, hist, keys[to], pos[to], blocks, c1);
             last = to;
         }
     }
     const GradWs w{keys[last], pos[last], (float *)(ws + l.from_left), (float *)(ws + l.to_right),
-                   (float *)(ws + l.long_run), l.pitch};
+                   (float *)(ws + l.long_run), l.pitch, l.chunk};
     const int es = dt == RAR_BF16 ? 2 : 4;
     const bool vec = (uintptr_t)p.dy % 16 == 0 && p.ldy * es % 16 == 0 && (uintptr_t)p.grad % 16 == 0 && p.D % 8 == 0;
     if (dt == RAR_BF16)

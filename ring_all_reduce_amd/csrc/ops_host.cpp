@@ -325,7 +325,7 @@ extern "C" rar_status rar_embed_grad(int64_t V, int64_t D, rar_dtype dtype, int6
     if (!aligned(grad, es) || !aligned(dy, es) || !aligned(ids, 8) || !aligned(ws, 16))
         return RAR_EALIGN;
     const int64_t need = rar::embed_grad_workspace(T, V, D);
-    if (ws_bytes < need || div_up(T, 32) * div_up(D, 512) > kMaxBlocks || V * D * es / 65536 > kMaxBlocks)
+    if (ws_bytes < need || div_up(T, 8) * div_up(D, 512) > kMaxBlocks || V * D * es / 65536 > kMaxBlocks)
         return RAR_EINVAL;
     if (!apart({{grad, V, D, D, es}, {ws, 1, need, need, 1}}, {{dy, T, D, lddy, es}, {ids, 1, T, T, 8}}))
         return RAR_EINVAL;

@@ -374,7 +374,7 @@ def test_embedding(T, V, D, dtype):
                 assert torch.equal(grad.cpu()[idle], g0[idle])
 
 
-@pytest.mark.parametrize("T", [31, 32, 1024, 1056, 3100, 5000, 70000])
+@pytest.mark.parametrize("T", [7, 8, 9, 31, 32, 256, 264, 1024, 1056, 3100, 5000, 70000])
 def test_embed_grad_one_token_for_all(T):
     # a run that is the whole batch, and one that starts off the partial rows' boundaries
     V, D = 6, 40
