@@ -40,13 +40,12 @@ SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (17, 64, 32), (1, 2048, 520), (7, 300
 BIG = [(3000, 72, 4200), (2900, 136, 4104)]
 
 
-@pytest.mark.parametrize("dtype", BOTH)
-@pytest.mark.parametrize("shape", SHAPES + BIG, ids=str)
-@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+LINEAR = [(s, dt, a) for s in SHAPES for dt in BOTH for a in R.ACTS] + [(s, "bf16", a) for s in BIG for a in ("none", "gelu")]
+
+
+@pytest.mark.parametrize("shape,dtype,act", LINEAR, ids=str)
 def test_linear_forward(shape, dtype, act):
     T, K, N = shape
-    if shape in BIG and (act == "relu" or dtype == "f32"):
-        pytest.skip("the other combinations cover it")
     g = torch.Generator().manual_seed(T * 31 + K + N)
     x, w = rand(g, T, K, dtype=dtype), rand(g, K, N, dtype=dtype, scale=K ** -0.5)
     b, r = rand(g, N, dtype=dtype), rand(g, T, N, dtype=dtype)
@@ -60,13 +59,9 @@ def test_linear_forward(shape, dtype, act):
         R.check(y, ry, ey, "y")
 
 
-@pytest.mark.parametrize("dtype", BOTH)
-@pytest.mark.parametrize("shape", SHAPES + BIG, ids=str)
-@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+@pytest.mark.parametrize("shape,dtype,act", LINEAR, ids=str)
 def test_linear_backward(shape, dtype, act):
     T, K, N = shape
-    if shape in BIG and (act == "relu" or dtype == "f32"):
-        pytest.skip("the other combinations cover it")
     g = torch.Generator().manual_seed(T * 37 + K + N)
     dy, x, z = (rand(g, T, n, dtype=dtype) for n in (N, K, N))
     w = rand(g, K, N, dtype=dtype, scale=K ** -0.5)
@@ -319,8 +314,6 @@ def test_forward_writes_the_checkpoint_of_z(shape, dtype):
 @pytest.mark.parametrize("shape", [(1, 1, 1), (3, 5, 7), (130, 257, 131), (515, 96, 640), (67, 3400, 4104)], ids=str)
 def test_backward_from_checkpoints(shape, act, dtype):
     T, K, N = shape
-    if T * K * N > 1e8 and act == "relu":
-        pytest.skip("the other activations cover it")
     g = torch.Generator().manual_seed(T + K + N)
     dy, x, z = (rand(g, T, n, dtype=dtype) for n in (N, K, N))
     w = rand(g, K, N, dtype=dtype, scale=K ** -0.5)
@@ -513,3 +506,157 @@ def test_replays_from_graphs(dtype):
             graphs[1].replay()
         torch.cuda.synchronize()
         assert _same(a, want) and _same(b, want), f"replay {rep}"
+
+
+# ---------------------------------------------------------------------------
+# Differences, and a training step of several ranks
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu"])
+@pytest.mark.parametrize("shape", [(3, 5, 7), (40, 72, 33), (130, 96, 200)], ids=str)
+def test_gradients_against_differences(shape, act):
+    # along a direction v: (L(+h) - L(-h)) / 2h of the kernels' own forward pass, L = sum(c * y), against the
+    # gradient's product with v.  Off by h^2 / 6 * |act'''| <= h^2 / 6 a term (gelu''' is below 0.8; the other
+    # activations are linear away from 0), and by both passes' rounding over 2h.
+    T, K, N = shape
+    h = 2.0 ** -6
+    g = torch.Generator().manual_seed(K)
+    x, w, b, c = rand(g, T, K), rand(g, K, N, scale=K ** -0.5), rand(g, N), rand(g, T, N)
+    vx, vw, vb = rand(g, T, K), rand(g, K, N, scale=K ** -0.5), rand(g, N)
+    plan = api.rar_linear_plan(K, N, api.F32, R.ACTS[act])
+
+    def forward(x, w, b):
+        y, z = nan_like(T, N, dtype="f32"), nan_like(T, N, dtype="f32")
+        api.rar_linear_forward(plan, T, x.to(DEV), w.to(DEV), b.to(DEV), None, y, pre=z)
+        return y.double().cpu(), z, R.forward(x, w, b, None, act, "f32")[0][1]
+
+    _, z, _ = forward(x, w, b)
+    dx, dw, db = nan_like(T, K, dtype="f32"), nan_like(K, N, dtype="f32"), nan_like(N, dtype="f32")
+    api.rar_linear_backward(plan, T, c.to(DEV), x.to(DEV), w.to(DEV), z, dx, dw, db)
+    grads = R.backward(c, x, w, z.cpu(), act, "f32")
+    zero = lambda t: torch.zeros_like(t)
+    for k, (grad, v, d) in enumerate(((dx, vx, (vx, zero(w), zero(b))), (dw, vw, (zero(x), vw, zero(b))),
+                                      (db, vb, (zero(x), zero(w), vb)))):
+        at = lambda s: (x + s * h * d[0], w + s * h * d[1], b + s * h * d[2])
+        yp, zp, ep = forward(*at(1))
+        ym, zm, em = forward(*at(-1))
+        # relu: keep to outputs whose z has one sign on both sides
+        use = (torch.sign(zp) == torch.sign(zm)).cpu() if act == "relu" else torch.ones(T, N, dtype=torch.bool)
+        step = ((zp - zm).double().cpu() / 2).abs()
+        diff = ((yp - ym) * c.double())[use].sum() / (2 * h)
+        cut = (c * use).to(torch.float32)
+        if not use.all():
+            api.rar_linear_backward(plan, T, cut.to(DEV), x.to(DEV), w.to(DEV), z, dx, dw, db)
+            grads = R.backward(cut, x, w, z.cpu(), act, "f32")
+        want = (grad.double().cpu() * v.double()).sum()
+        bound = (cut.double().abs() * (ep + em)).sum() / (2 * h) + (grads[k][1] * v.double().abs()).sum()
+        if act == "gelu":
+            bound += (cut.double().abs() * step ** 3).sum() / (6 * h)
+        # the operands of the two passes are rounded sums x + h v: half a step each
+        moved = [2.0 ** -24 * (p.double().abs() + h * q.double().abs()) for p, q in zip((x, w, b), d)]
+        drift = moved[0] @ w.double().abs() + x.double().abs() @ moved[1] + moved[2]
+        bound += 1.3 * (cut.double().abs() * drift).sum() / h
+        assert abs(diff - want) <= bound, (k, float(diff), float(want), float(bound))
+        if not use.all():
+            api.rar_linear_backward(plan, T, c.to(DEV), x.to(DEV), w.to(DEV), z, dx, dw, db)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_training_step_of_ranks(dtype, ckpt):
+    """Embedding, two linear layers with a residual, their backward passes into per-rank arenas, and the bucketed
+    all-reduce over them, each bucket behind the event that its last gradient records: the mean of the ranks'
+    gradients."""
+    ranks, T, V, d, h = 4, 200, 300, 48, 136
+    code, td = CODE[dtype], R.DT[dtype]
+    g = torch.Generator().manual_seed(8)
+    table, w1, w2 = (rand(g, *s, dtype=dtype, scale=0.2) for s in ((V, d), (d, h), (h, d)))
+    b1, b2 = rand(g, h, dtype=dtype), rand(g, d, dtype=dtype)
+    ids = [torch.randint(-1, V, (T,), generator=g) for _ in range(ranks)]
+    dys = [rand(g, T, d, dtype=dtype) for _ in range(ranks)]
+    l1, l2 = api.rar_linear_plan(d, h, code, api.ACT_GELU), api.rar_linear_plan(h, d, code)
+    # backward order: W2, b2, W1, b1, embedding
+    shapes = [(h, d), (d,), (d, h), (h,), (V, d)]
+    numel = [int(np.prod(s)) for s in shapes]
+    total = sum(numel)
+    buckets = api.rar_bucket_plan(numel, code, 16 * 512)
+    n_buckets = api.rar_bucket_count(buckets)[0]
+    arenas = [torch.full((total,), float("nan"), dtype=td, device=DEV) for _ in range(ranks)]
+    ends = np.cumsum(numel)
+    dev = lambda t: t.to(DEV)
+    gt, gw1, gw2, gb1, gb2 = map(dev, (table, w1, w2, b1, b2))
+    producer, comm = torch.cuda.Stream(), torch.cuda.Stream()
+    want = [torch.zeros(s, dtype=torch.float64) for s in shapes]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(producer):
+        state = []
+        for r in range(ranks):
+            views, at = [], 0
+            for s, n in zip(shapes, numel):
+                views.append(arenas[r][at:at + n].view(s))
+                at += n
+            x, a, y = (torch.empty(T, n, dtype=td, device=DEV) for n in (d, h, d))
+            api.rar_embed_lookup(V, d, code, gt, T, dev(ids[r]), x, 1.5)
+            kw = {}
+            if ckpt:
+                (xp, xg), (zp, zg) = api.rar_ckpt_size(d), api.rar_ckpt_size(h)
+                xk, xs, z, zs = (torch.empty(T, n, dtype=torch.uint8, device=DEV) for n in (xp, xg, zp, zg))
+                api.rar_ckpt_store(T, d, code, x, xk, xs)
+                api.rar_linear_forward(l1, T, x, gw1, gb1, None, a, pre=z, pre_scales=zs)
+                kw = dict(x_scales=xs, pre_scales=zs)
+            else:
+                xk, z = x, torch.empty(T, h, dtype=td, device=DEV)
+                api.rar_linear_forward(l1, T, x, gw1, gb1, None, a, pre=z)
+            api.rar_linear_forward(l2, T, a, gw2, gb2, x, y)
+            state.append((views, x, xk, a, z, kw, dev(ids[r]), dev(dys[r]), y))
+        # layer by layer over the ranks, as their passes run side by side
+        das = []
+        for views, x, xk, a, z, kw, i, dy, y in state:
+            if ckpt:
+                api.rar_ckpt_load(T, h, code, z, kw["pre_scales"], a, act=api.ACT_GELU)
+            da = torch.empty(T, h, dtype=td, device=DEV)
+            api.rar_linear_backward(l2, T, dy, a, gw2, None, da, views[0], views[1])
+            das.append(da)
+        second = torch.cuda.Event()
+        second.record(producer)
+        dxs = []
+        for (views, x, xk, a, z, kw, i, dy, y), da in zip(state, das):
+            dx = torch.empty(T, d, dtype=td, device=DEV)
+            api.rar_linear_backward(l1, T, da, xk, gw1, z, dx, views[2], views[3], **kw)
+            dx += dy                                      # the residual's share
+            dxs.append(dx)
+        first = torch.cuda.Event()
+        first.record(producer)
+        for (views, x, xk, a, z, kw, i, dy, y), dx in zip(state, dxs):
+            api.rar_embed_grad(V, d, code, T, i, dx, views[4], 1.5)
+        last = torch.cuda.Event()
+        last.record(producer)
+    events = []
+    for k in range(n_buckets):
+        so, el, _ = api.rar_bucket_info(buckets, k)
+        events.append(second if so + el <= ends[1] else first if so + el <= ends[3] else last)
+    api.rar_bucket_allreduce_arena(buckets, arenas, events, stream=comm)
+    torch.cuda.synchronize()
+    # the same step in 64 bits, from what each operator reads; values kept in 8 bits from their codes
+    bound = [torch.zeros(s, dtype=torch.float64) for s in shapes]
+    for (views, x, xk, a, z, kw, i, dy, y), da, dx in zip(state, das, dxs):
+        cpu = lambda t: t.detach().cpu()
+        xv = R.values(cpu(xk).numpy(), cpu(kw["x_scales"]).numpy(), d) if ckpt else cpu(x)
+        zv = R.values(cpu(z).numpy(), cpu(kw["pre_scales"]).numpy(), h) if ckpt else cpu(z)
+        (_, _), (dw2, e2), (db2, f2) = R.backward(cpu(dy), cpu(a), w2, torch.zeros(T, d), "none", dtype)
+        (_, _), (dw1, e1), (db1, f1) = R.backward(cpu(da), xv, w1, zv, "gelu", dtype)
+        de, ee = R.embed_grad(V, cpu(i), cpu(dx), 1.5, dtype)
+        for k, (t, e) in enumerate(((dw2, e2), (db2, f2), (dw1, e1), (db1, f1), (de, ee))):
+            want[k] += t / ranks
+            bound[k] += (e + 2 ** -22 * t.abs()) / ranks
+        # and the forward pass
+        if not ckpt:  # (with checkpoints `a` was made again since)
+            (ry, ey), _ = R.forward(cpu(a), w2, b2, cpu(x), "none", dtype)
+            R.check(y, ry, ey, "y")
+    for r in range(ranks):
+        at = 0
+        for k, (s, n) in enumerate(zip(shapes, numel)):
+            got = arenas[r][at:at + n].view(s)
+            R.check(got, want[k], bound[k] * (1 + R.U[dtype]) + R.U[dtype] * want[k].abs(), f"rank {r} tensor {k}")
+            at += n
+        assert torch.equal(arenas[r], arenas[0])
