@@ -665,7 +665,108 @@ def secondary_rows(dev, stream, reps=5):
             rows.append(r)
             log(f"row {r['row']}: {r}")
     optional_rows(rows, f"{wl.name}_overlap", overlap)
+
+    def backward():
+        r = backward_row(wl, b, specs, infos, arenas, dev, stream)
+        rows.append(r)
+        log(f"row {r['row']}: {r}")
+    optional_rows(rows, f"{wl.name}_overlap_linear_backward", backward)
     return rows
+
+
+def backward_row(wl, b, specs, infos, arenas, dev, stream, T=128, reps=2):
+    """The overlapped all-reduce behind a real producer: every rank's backward
+    pass through the Transformer's linear layers (rar_linear_backward) and its
+    embedding (rar_embed_grad), T tokens a rank, writing each gradient into the
+    rank's arena in backward order; LayerNorm gradients are filled.  A bucket's
+    event follows the last of its tensors.  Activations and weights are one
+    buffer of each size, shared by the layers."""
+    import torch
+    from ring_all_reduce_amd import api
+    N = len(arenas)
+    widest = max(max(s.shape) for s in specs)
+    gen = torch.Generator(device=dev).manual_seed(1)
+    flat = torch.randn(T * widest, device=dev, generator=gen)
+    weights = torch.randn(max(s.numel for s in specs if len(s.shape) == 2), device=dev, generator=gen)
+    dx = torch.empty(T * widest, device=dev)
+    ends, at = [], 0
+    for s in specs:
+        at += s.numel
+        ends.append(at)
+    ready, k = [0] * len(infos), 0     # the tensor that completes each bucket
+    for t, e in enumerate(ends):
+        while k < len(infos) and infos[k][0] + infos[k][1] <= e:
+            ready[k] = t
+            k += 1
+    def is_bias(s):
+        return len(s.shape) == 1 and s.name.split(".")[-1] not in ("gamma", "beta")
+
+    plans, calls = {}, []
+    for t, s in enumerate(specs):
+        at = ends[t] - s.numel
+        if len(s.shape) == 1:
+            if is_bias(s):
+                continue                # a bias: its layer's call below writes it
+            calls.append((t, lambda n, at=at, s=s: arenas[n][at:at + s.numel].fill_(1e-3)))
+        elif s.name == "embed":
+            V, D = s.shape
+            ids = torch.randint(0, V, (T,), device=dev, generator=gen)
+            ws = torch.empty(api.rar_embed_grad_workspace(V, D, T), dtype=torch.uint8, device=dev)
+            calls.append((t, lambda n, at=at, s=s, V=V, D=D: api.rar_embed_grad(
+                V, D, api.F32, T, ids, flat[:T * D].view(T, D), arenas[n][at:at + s.numel].view(V, D), ws=ws)))
+        else:
+            K, M = s.shape
+            if s.shape not in plans:
+                p = api.rar_linear_plan(K, M, api.F32)
+                plans[s.shape] = p, torch.empty(api.rar_linear_workspace(p, T)[1], dtype=torch.uint8, device=dev)
+            p, ws = plans[s.shape]
+            # the list holds the bias before its weight
+            bias = at - M if t and is_bias(specs[t - 1]) else None
+
+            def call(n, at=at, s=s, K=K, M=M, p=p, ws=ws, bias=bias):
+                api.rar_linear_backward(p, T, flat[:T * M].view(T, M), flat[:T * K].view(T, K), weights[:K * M].view(K, M),
+                                        None, dx[:T * K].view(T, K), arenas[n][at:at + s.numel].view(K, M),
+                                        None if bias is None else arenas[n][bias:bias + M], ws=ws)
+            calls.append((t, call))
+
+    def produce(producer, events):
+        with torch.cuda.stream(producer):
+            k = 0
+            for t, call in calls:
+                for n in range(N):
+                    call(n)
+                while events is not None and k < len(infos) and ready[k] <= t:
+                    events[k].record(producer)
+                    k += 1
+
+    def timed(run_prod, run_comm):
+        best = None
+        for _ in range(reps):
+            producer, comm = torch.cuda.Stream(), torch.cuda.Stream()
+            events = [torch.cuda.Event() for _ in infos] if run_prod and run_comm else None
+            torch.cuda.synchronize()
+            t0, tp, tc = (torch.cuda.Event(enable_timing=True) for _ in range(3))
+            t0.record(stream)
+            producer.wait_event(t0)
+            comm.wait_event(t0)
+            if run_prod:
+                produce(producer, events)
+            tp.record(producer)
+            if run_comm:
+                api.rar_bucket_allreduce_arena(b, arenas, events, stream=comm)
+            tc.record(comm)
+            torch.cuda.synchronize()
+            ms = max(t0.elapsed_time(tp), t0.elapsed_time(tc))
+            best = ms if best is None else min(best, ms)
+        return best
+
+    t_prod, t_comm, t_both = timed(True, False), timed(False, True), timed(True, True)
+    flops = N * sum(4 * T * s.numel for s in specs if len(s.shape) == 2 and s.name != "embed")
+    return {"row": f"{wl.name}_overlap_linear_backward", "buckets": len(infos), "tokens_per_rank": T,
+            "producer_ms": round(t_prod, 3), "producer_TFLOPs": round(flops / t_prod / 1e9, 1),
+            "allreduce_ms": round(t_comm, 3), "overlapped_ms": round(t_both, 3),
+            "fraction_of_allreduce_hidden": round((t_prod + t_comm - t_both) / t_comm, 3),
+            "producer": "rar_linear_backward of every layer and rar_embed_grad, binary32, into the arenas"}
 
 
 def optional_rows(rows, name, fn):

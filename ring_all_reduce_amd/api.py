@@ -434,10 +434,13 @@ def _device_of(x, what: str) -> None:
         raise ValueError(f"{what}: tensor is on {x.device}, the current device is cuda:{_here()}")
 
 
+def _plain(x) -> bool:
+    return x.is_cuda and x.is_contiguous() and x.get_device() == _here()
+
+
 def _matrix(x, what: str, tdtype, rows: int, cols: int):
     """(address, leading dimension) of a rows x cols matrix argument."""
-    if getattr(x, "dtype", None) is tdtype and x.is_cuda and x.is_contiguous() and x.get_device() == _here() and rows > 0 \
-            and x.shape == (rows, cols):
+    if getattr(x, "dtype", None) is tdtype and rows > 0 and x.shape == (rows, cols) and _plain(x):
         return x.data_ptr(), cols  # the usual case; what follows finds out what is wrong with others
     if x is None:
         return 0, cols
@@ -464,7 +467,7 @@ def _matrix(x, what: str, tdtype, rows: int, cols: int):
 
 def _dense(x, what: str, tdtype, numel: int) -> int:
     """Address of a contiguous argument of exactly numel elements."""
-    if getattr(x, "dtype", None) is tdtype and x.is_cuda and x.is_contiguous() and x.get_device() == _here() and x.numel() == numel:
+    if getattr(x, "dtype", None) is tdtype and x.numel() == numel and _plain(x):
         return x.data_ptr()
     if x is None or isinstance(x, int):
         return x or 0
@@ -491,8 +494,10 @@ def _workspace(ws, nbytes: int, stream):
     import torch
     t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     if stream is not None:
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream else stream
-        if hasattr(s, "cuda_stream") and s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        s = stream
+        if isinstance(stream, int):
+            s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
             # the allocator may hand the memory out again only once this stream has used it, and this
             # stream may use it only once its last user on the current stream is done
             s.wait_stream(torch.cuda.current_stream())

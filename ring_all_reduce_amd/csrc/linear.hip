@@ -464,6 +464,11 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            asm volatile("" : "+a"(acc[i][j]));
 
     // The last step's reduction may end inside it.
     auto cut = [&](int s) __attribute__((always_inline)) {
@@ -472,6 +477,8 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
             sb.cut(kend - k0 - (int64_t)s * 64);
         }
     };
+    // (the same before the first: the zeros have been written)
+    asm volatile("s_nop 7" ::: "memory");
     bf16x8 a[FM], b0[FN], b1[FN];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -530,8 +537,14 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
         }
     }
 
-    // the last products' results (the compiler does not know the statements' latency)
+    // The compiler does not know the statements' latency: wait for the last
+    // products, and tie every use of the accumulators to what follows the wait.
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            asm volatile("" : "+a"(acc[i][j]));
     // every wave has read its last fragments: LDS is free for the results
     drain();
     const int lane = threadIdx.x & 63;
