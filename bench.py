@@ -724,8 +724,8 @@ def backward_row(wl, b, specs, infos, arenas, dev, stream, T=128, reps=2):
             bias = at - M if t and is_bias(specs[t - 1]) else None
 
             def call(n, at=at, s=s, K=K, M=M, p=p, ws=ws, bias=bias):
-                api.rar_linear_backward(p, T, flat[:T * M].view(T, M), flat[:T * K].view(T, K), weights[:K * M].view(K, M),
-                                        None, dx[:T * K].view(T, K), arenas[n][at:at + s.numel].view(K, M),
+                api.rar_linear_backward(p, T, flat[:T * M].view(T, M), flat[:T * K].view(T, K),
+                                        weights[:K * M].view(K, M), None, dx[:T * K].view(T, K), arenas[n][at:at + s.numel].view(K, M),
                                         None if bias is None else arenas[n][bias:bias + M], ws=ws)
             calls.append((t, call))
 

@@ -175,7 +175,8 @@ __device__ __forceinline__ void clear(const Clear &c, int64_t block)
 {
     const int64_t lo = block * kClearBytes, hi = lo + kClearBytes < c.bytes ? lo + kClearBytes : c.bytes;
     // whole 16-byte groups, and what lies before and behind them by two bytes
-    const int64_t a = lo + (16 - (int64_t)((uintptr_t)(c.at + lo) & 15)) % 16, b = hi - (int64_t)((uintptr_t)(c.at + hi) & 15);
+    const int64_t a = lo + (16 - (int64_t)((uintptr_t)(c.at + lo) & 15)) % 16;
+    const int64_t b = hi - (int64_t)((uintptr_t)(c.at + hi) & 15);
     if (a > b) {
         for (int64_t i = lo + threadIdx.x * 2; i < hi; i += kSortThreads * 2)
             *reinterpret_cast<uint16_t *>(c.at + i) = 0;
@@ -272,7 +273,8 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *id
 }
 
 __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *ids, const uint32_t *keys,
-                                                               const uint32_t *pos, int64_t T, int64_t V, int shift, int bits,
+                                                               const uint32_t *pos, int64_t T, int64_t V, int shift,
+                                                               int bits,
                                                                const uint32_t *hist, uint32_t *keys_out,
                                                                uint32_t *pos_out, unsigned blocks, Clear c)
 {
@@ -434,7 +436,10 @@ struct Columns {
     }
 };
 
-__device__ __forceinline__ int64_t wave_job(int64_t block) { return block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+__device__ __forceinline__ int64_t wave_job(int64_t block)
+{
+    return block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
 
 // One wave: a chunk of sorted positions of one strip, two batches of rows in
 // flight.
@@ -477,7 +482,8 @@ __global__ void __launch_bounds__(256) rar_embed_chunks(const EmbedGradParams p,
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 acc[e] += v[u].at(e);
-            const uint32_t k = __builtin_amdgcn_readlane(key, 1 + r + u), next = __builtin_amdgcn_readlane(key, 2 + r + u);
+            const uint32_t k = __builtin_amdgcn_readlane(key, 1 + r + u);
+            const uint32_t next = __builtin_amdgcn_readlane(key, 2 + r + u);
             const bool right = r + u == n - 1 && k == next;
             if (k == next && !right)
                 continue;
@@ -600,7 +606,7 @@ Layout layout(int64_t T, int64_t D)
     // without a wave: 4097 positions of 509 binary32 columns take 30 us in chunks
     // of 8 and 34 in chunks of 32, 65536 of 2048 bf16 columns 139 and 123 (the
     // whole call).
-    l.chunk = T * (l.pitch / kCols) >= 65536 ? 32 : 8;
+    l.chunk = T <= 32 || T * (l.pitch / kCols) >= 65536 ? 32 : 8;  // up to 32 need no join
     const int64_t chunks = T > l.chunk ? (T + l.chunk - 1) / l.chunk : 0;
     l.from_left = take(chunks * l.pitch * 4);
     l.to_right = take(chunks * l.pitch * 4);
@@ -635,7 +641,8 @@ hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t s
     const int64_t items = p.T * (vec ? p.D * es / 16 : p.D);
     const unsigned grid = (unsigned)((items + 1023) / 1024);
     if (dt == RAR_BF16)
-        vec ? rar_embed_rows<bf16, true><<<grid, 256, 0, st>>>(p) : rar_embed_rows<bf16, false><<<grid, 256, 0, st>>>(p);
+        vec ? rar_embed_rows<bf16, true><<<grid, 256, 0, st>>>(p)
+            : rar_embed_rows<bf16, false><<<grid, 256, 0, st>>>(p);
     else
         vec ? rar_embed_rows<float, true><<<grid, 256, 0, st>>>(p)
             : rar_embed_rows<float, false><<<grid, 256, 0, st>>>(p);
@@ -660,7 +667,8 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
     int share = 0;
     const int shares = p.T <= kSmallKeys ? 1 : 2 * passes;
     auto next_clear = [&]() {
-        const int64_t lo = bytes / 256 * share / shares * 256, hi = share + 1 == shares ? bytes : bytes / 256 * (share + 1) / shares * 256;
+        const int64_t lo = bytes / 256 * share / shares * 256;
+        const int64_t hi = share + 1 == shares ? bytes : bytes / 256 * (share + 1) / shares * 256;
         ++share;
         return Clear{(char *)p.grad + lo, hi - lo};
     };
@@ -670,9 +678,11 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
         const Clear c = next_clear();
         const unsigned grid = 1 + clear_blocks(c);
         if (p.T <= kSortKeys)
-            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0], c);
+            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0],
+                                                                   c);
         else
-            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0], c);
+            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0],
+                                                                       pos[0], c);
     } else {
         const unsigned blocks = (unsigned)((p.T + kSortKeys - 1) / kSortKeys);
         uint32_t *const hist = (uint32_t *)(ws + l.hist);

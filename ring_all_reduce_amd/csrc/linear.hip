@@ -25,15 +25,18 @@ typedef short i16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
+constexpr int kRow = 128;  // bytes of reduction of a contiguous operand's row in one step
 
 // ---------------------------------------------------------------------------
 // Staging: memory -> LDS, 16 bytes a lane, without passing through registers
 // ---------------------------------------------------------------------------
 //
-// One step stages RB / ES reduction indices of R rows of an operand.
-//   contiguous: LDS row r holds its RB bytes of k; the 16-byte chunk c lies at
-//               slot c ^ row_perm(r), so 16 lanes that read one chunk of 16
-//               rows touch every bank once.
+// One step stages kRow / ES reduction indices of R rows of an operand.
+//   contiguous: LDS row r holds its 128 bytes of k; the 16-byte chunk c lies at
+//               slot c ^ (r & 7), so 16 lanes that read one chunk of 16 rows
+//               touch every bank once.  (Rows of 64 bytes, for more and smaller
+//               steps in flight, cost twice the requests a byte and were 6%
+//               slower.)
 //   slow:       LDS row k holds R elements; bf16 units of 16 elements are
 //               permuted by f(k), binary32 by one bit of k, so that the four
 //               k rows of a transposing read (or the two of a binary32 read)
@@ -52,16 +55,10 @@ __device__ __forceinline__ int slow_perm(int k)
     return ES == 2 ? ((k & 3) | (((k >> 3) & 3) << 2)) : ((k >> 2) & 1);
 }
 
-template <int RB>
-__device__ __forceinline__ int row_perm(int r)
-{
-    return RB == 128 ? (r & 7) : ((r >> 2) & 3);
-}
-
-template <int ES, int R, int RB, int WAVES, bool CONTIG>
+template <int ES, int R, int WAVES, bool CONTIG>
 struct Stage {
-    static constexpr int kLoads = R * RB / (WAVES * 1024);
-    static constexpr int kStep = RB / ES;  // reduction indices of one step
+    static constexpr int kLoads = R * kRow / (WAVES * 1024);
+    static constexpr int kStep = kRow / ES;  // reduction indices of one step
     uint32_t voff[kLoads];
     const char *base;
     int64_t left;     // bytes from base to the end of the operand
@@ -74,12 +71,9 @@ struct Stage {
     // Contiguous: row and source chunk of this lane's j-th load.
     static __device__ __forceinline__ int row_of(int j)
     {
-        return (j * WAVES + (threadIdx.x >> 6)) * (1024 / RB) + (threadIdx.x & 63) / (RB / 16);
+        return (j * WAVES + (threadIdx.x >> 6)) * 8 + ((threadIdx.x & 63) >> 3);
     }
-    static __device__ __forceinline__ int chunk_of(int j)
-    {
-        return ((threadIdx.x & 63) % (RB / 16)) ^ row_perm<RB>(row_of(j));
-    }
+    static __device__ __forceinline__ int chunk_of(int j) { return (threadIdx.x & 7) ^ (row_of(j) & 7); }
 
     // rows [r0, ...) of `rows`, reduction indices [k0, ...) of `kred`
     __device__ __forceinline__ void init(const void *p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t kred)
@@ -87,19 +81,19 @@ struct Stage {
         if (CONTIG) {
             base = (const char *)p + (r0 * ld + k0) * ES;
             left = ((rows - 1 - r0) * ld + whole(kred - k0)) * ES;
-            advance = RB;
+            advance = kRow;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
                 voff[j] = (uint32_t)(row_of(j) * ld * ES) + (chunk_of(j) << 4);
         } else {
-            constexpr int kRow = R * ES;
+            constexpr int kCols = R * ES;
             base = (const char *)p + (k0 * ld + r0) * ES;
             left = ((kred - 1 - k0) * ld + whole(rows - r0)) * ES;
             advance = kStep * ld * ES;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int at = (j * WAVES + (threadIdx.x >> 6)) * 1024 + (threadIdx.x & 63) * 16;
-                const int k = at / kRow, slot = (at % kRow) / 16;
+                const int k = at / kCols, slot = (at % kCols) / 16;
                 int src;
                 if (ES == 2)
                     src = (((slot >> 1) ^ (slow_perm<2>(k) & (R / 16 - 1))) << 1) | (slot & 1);
@@ -155,7 +149,7 @@ struct Stage {
 // indices (l / 16) * 8 .. +7 of a half step of 32.  A slow operand is read with the
 // transposing LDS read: each 16 lanes read four k rows of 16 columns and
 // receive their own column's four values.
-template <int R, int RB, bool CONTIG, int NF>
+template <int R, bool CONTIG, int NF>
 struct Frag16 {
     uint32_t off[CONTIG ? 1 : NF];
 
@@ -163,7 +157,7 @@ struct Frag16 {
     {
         const int lane = threadIdx.x & 63;
         if (CONTIG) {
-            off[0] = (w0 + (lane & 15)) * RB + (((lane >> 4) ^ row_perm<RB>(lane & 15)) << 4);
+            off[0] = (w0 + (lane & 15)) * kRow + (((lane >> 4) ^ (lane & 7)) << 4);
         } else {
             const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
             const int f = slow_perm<2>(k) & (R / 16 - 1);
@@ -176,7 +170,7 @@ struct Frag16 {
     __device__ __forceinline__ bf16x8 read(const RAR_LDS char *__restrict__ lds, int half, int i) const
     {
         if (CONTIG)
-            return *(const RAR_LDS bf16x8 *)(lds + (off[0] ^ (half << 6)) + i * 16 * RB);
+            return *(const RAR_LDS bf16x8 *)(lds + (off[0] ^ (half << 6)) + i * 16 * kRow);
         const RAR_LDS char *p = lds + off[CONTIG ? 0 : i] + half * 32 * (R * 2);
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)p);
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)(p + 4 * (R * 2)));
@@ -196,7 +190,7 @@ struct Frag32 {
         const int lane = threadIdx.x & 63;
         const int row = w0 + (lane & 31), half = lane >> 5;
         if (CONTIG)
-            off = row * 128 + ((half ^ (row & 7)) << 4);
+            off = row * kRow + ((half ^ (row & 7)) << 4);
         else
             off = half * 4 * (R * 4) + ((row * 4) ^ (half << 7));
     }
@@ -204,7 +198,7 @@ struct Frag32 {
     __device__ __forceinline__ f32x4 read(const RAR_LDS char *__restrict__ lds, int c, int i) const
     {
         if (CONTIG)
-            return *(const RAR_LDS f32x4 *)(lds + (off ^ (c << 5)) + i * 32 * 128);
+            return *(const RAR_LDS f32x4 *)(lds + (off ^ (c << 5)) + i * 32 * kRow);
         // 32 columns are 128 bytes: an odd block of them flips the permuted bit
         const RAR_LDS char *p = lds + (off ^ (i << 7)) + c * 8 * (R * 4);
         return f32x4{*(const RAR_LDS float *)p, *(const RAR_LDS float *)(p + R * 4),
@@ -390,9 +384,7 @@ __device__ __forceinline__ void tile_of(const GemmParams &p, int64_t id, int64_t
     tn = in / rows;
 }
 
-// Own loads into LDS but the last N have arrived; then everyone's.  LDS reads
-// in flight are no concern inside the ring: a buffer is loaded again two
-// meetings after its reads, whose results were used before the second.
+// Own loads into LDS but the last N have arrived; then everyone's.
 template <int N>
 __device__ __forceinline__ void wait_loads()
 {
@@ -437,7 +429,7 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
 {
     constexpr int kWaves = WM * WN, kEarly = 1;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16-row fragments of a wave
-    constexpr int kBuf = (BM + BN) * 128;
+    constexpr int kBuf = (BM + BN) * kRow;
 
     int64_t tm, tn;
     int split;
@@ -448,13 +440,13 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
     const int steps = k0 < kend ? (int)((kend - k0 + 63) / 64) : 0;
     const int wave = threadIdx.x >> 6, wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
 
-    Stage<2, BM, 128, kWaves, ACONTIG> sa;
-    Stage<2, BN, 128, kWaves, BCONTIG> sb;
+    Stage<2, BM, kWaves, ACONTIG> sa;
+    Stage<2, BN, kWaves, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
     constexpr int kLoads = sa.kLoads + sb.kLoads;
-    Frag16<BM, 128, ACONTIG, FM> fa;
-    Frag16<BN, 128, BCONTIG, FN> fb;
+    Frag16<BM, ACONTIG, FM> fa;
+    Frag16<BN, BCONTIG, FN> fb;
     fa.init(wm);
     fb.init(wn);
 
@@ -484,12 +476,12 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
     for (int s = 0; s < 2; ++s) {
         cut(s);
         sa.load_all(lds + s * kBuf, s >= steps);
-        sb.load_all(lds + s * kBuf + BM * 128, s >= steps);
+        sb.load_all(lds + s * kBuf + BM * kRow, s >= steps);
     }
     wait_loads<kLoads>();
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-        b0[j] = fb.read(lds + BM * 128, 0, j);
+        b0[j] = fb.read(lds + BM * kRow, 0, j);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
         a[i] = fa.read(lds, 0, i);
@@ -505,7 +497,7 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
             a[i] = fa.read(here, 1, i);
 #pragma unroll
             for (int e = i * FN / FM; e < (i + 1) * FN / FM; ++e)
-                b1[e] = fb.read(here + BM * 128, 1, e);
+                b1[e] = fb.read(here + BM * kRow, 1, e);
         }
         cut(s + 2);
         const __amdgpu_buffer_rsrc_t ra = sa.next(s + 2 >= steps), rb = sb.next(s + 2 >= steps);
@@ -524,7 +516,7 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
             for (int e = (i - kEarly) * kReads / kRows; e < (i - kEarly + 1) * kReads / kRows; ++e) {
                 // B's fragments, then A's as far as their products are issued
                 if (e < FN)
-                    b0[e] = fb.read(next + BM * 128, 0, e);
+                    b0[e] = fb.read(next + BM * kRow, 0, e);
                 else
                     a[e - FN] = fa.read(next, 0, e - FN);
             }
@@ -533,7 +525,7 @@ __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RA
                 if (e < sa.kLoads)
                     sa.load(ra, here, e);
                 else
-                    sb.load(rb, here + BM * 128, e - sa.kLoads);
+                    sb.load(rb, here + BM * kRow, e - sa.kLoads);
         }
     }
 
@@ -577,7 +569,7 @@ template <int B, bool ACONTIG, bool BCONTIG>
 __device__ __forceinline__ void gemm_f32(const GemmParams &p, int64_t block, RAR_LDS char *const lds)
 {
     constexpr int kStep = 32, F = B / 64;
-    constexpr int kBuf = 2 * B * 128;
+    constexpr int kBuf = 2 * B * kRow;
 
     int64_t tm, tn;
     int split;
@@ -588,8 +580,8 @@ __device__ __forceinline__ void gemm_f32(const GemmParams &p, int64_t block, RAR
     const int steps = k0 < kend ? (int)((kend - k0 + kStep - 1) / kStep) : 0;
     const int wave = threadIdx.x >> 6, wm = (wave & 1) * (B / 2), wn = (wave >> 1) * (B / 2);
 
-    Stage<4, B, 128, 4, ACONTIG> sa;
-    Stage<4, B, 128, 4, BCONTIG> sb;
+    Stage<4, B, 4, ACONTIG> sa;
+    Stage<4, B, 4, BCONTIG> sb;
     sa.init(p.a, p.lda, m0, p.M, k0, kend);
     sb.init(p.b, p.ldb, n0, p.N, k0, kend);
     Frag32<B, ACONTIG> fa;
@@ -613,7 +605,7 @@ __device__ __forceinline__ void gemm_f32(const GemmParams &p, int64_t block, RAR
         }
         RAR_LDS char *to = lds + (s & 1) * kBuf;
         sa.load_all(to, s >= steps);
-        sb.load_all(to + B * 128, s >= steps);
+        sb.load_all(to + B * kRow, s >= steps);
     };
     f32x4 a[2][F], b[2][F];
     auto read = [&](int s, int c, int set) __attribute__((always_inline)) {
@@ -621,7 +613,7 @@ __device__ __forceinline__ void gemm_f32(const GemmParams &p, int64_t block, RAR
 #pragma unroll
         for (int i = 0; i < F; ++i) {
             a[set][i] = fa.read(from, c, i);
-            b[set][i] = fb.read(from + B * 128, c, i);
+            b[set][i] = fb.read(from + B * kRow, c, i);
         }
     };
 
@@ -675,7 +667,7 @@ template <int B, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) rar_forward_bf16(const GemmParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * kRow];
     gemm_bf16<B, B, WM, WN, true, false>(p, blockIdx.x, (RAR_LDS char *)lds);
 #endif
 }
@@ -686,7 +678,7 @@ template <int B, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) rar_backward_bf16(const GemmPair p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * kRow];
     if (blockIdx.x < p.x_blocks)
         gemm_bf16<B, B, WM, WN, true, true>(p.x, blockIdx.x, (RAR_LDS char *)lds);
     else
@@ -698,7 +690,7 @@ template <int B>
 __global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_forward_f32(const GemmParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * kRow];
     gemm_f32<B, true, false>(p, blockIdx.x, (RAR_LDS char *)lds);
 #endif
 }
@@ -707,7 +699,7 @@ template <int B>
 __global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_backward_f32(const GemmPair p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * 128];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * B * kRow];
     if (blockIdx.x < p.x_blocks)
         gemm_f32<B, true, true>(p.x, blockIdx.x, (RAR_LDS char *)lds);
     else
@@ -1008,7 +1000,8 @@ hipError_t launch_forward(rar_dtype dt, const GemmParams &p, int tile, hipStream
 {
     const unsigned grid = blocks_of(p);
     if (dt == RAR_BF16)
-        tile == 256 ? rar_forward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p) : rar_forward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
+        tile == 256 ? rar_forward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p)
+                    : rar_forward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
     else
         tile == 128 ? rar_forward_f32<128><<<grid, 256, 0, st>>>(p) : rar_forward_f32<64><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
@@ -1018,7 +1011,8 @@ hipError_t launch_backward(rar_dtype dt, const GemmPair &p, unsigned w_blocks, i
 {
     const unsigned grid = p.x_blocks + w_blocks;
     if (dt == RAR_BF16)
-        tile == 256 ? rar_backward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p) : rar_backward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
+        tile == 256 ? rar_backward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p)
+                    : rar_backward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
     else
         tile == 128 ? rar_backward_f32<128><<<grid, 256, 0, st>>>(p) : rar_backward_f32<64><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();

@@ -5,7 +5,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 #include <initializer_list>
 #include <new>
 
@@ -153,19 +152,6 @@ Shape shape_of(rar_dtype dt, int64_t M, int64_t N, int64_t K)
             }
         }
     }
-#ifdef RAR_FORCE
-    if (getenv("RAR_TILE")) {
-        Shape s{};
-        s.tile = atoi(getenv("RAR_TILE"));
-        s.tiles_m = div_up(M, s.tile);
-        s.tiles_n = div_up(N, s.tile);
-        s.pitch = up(N, rar::kCkptGroup);
-        s.steps = div_up(total, atoi(getenv("RAR_SPLIT")));
-        s.splits = div_up(total, s.steps);
-        s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
-        return s;
-    }
-#endif
     return best;
 }
 

@@ -36,11 +36,13 @@ def strided(t, extra, offset=0):
 
 # (T, K, N): one element, one token, odd sizes, whole and broken tiles, split reductions, more than 192 tiles of 256
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (17, 64, 32), (1, 2048, 520), (7, 300, 1000), (129, 257, 131),
-          (300, 512, 264), (64, 1000, 72), (515, 96, 640), (5001, 40, 24), (130, 8, 4096), (2, 2056, 72), (4, 1000, 136), (3, 4104, 200)]
+          (300, 512, 264), (64, 1000, 72), (515, 96, 640), (5001, 40, 24), (130, 8, 4096),
+          (2, 2056, 72), (4, 1000, 136), (3, 4104, 200)]
 BIG = [(3000, 72, 4200), (2900, 136, 4104)]
 
 
-LINEAR = [(s, dt, a) for s in SHAPES for dt in BOTH for a in R.ACTS] + [(s, "bf16", a) for s in BIG for a in ("none", "gelu")]
+LINEAR = [(s, dt, a) for s in SHAPES for dt in BOTH for a in R.ACTS]
+LINEAR += [(s, "bf16", a) for s in BIG for a in ("none", "gelu")]
 
 
 @pytest.mark.parametrize("shape,dtype,act", LINEAR, ids=str)
@@ -200,7 +202,8 @@ def test_infinities_and_nan(dtype):
     inf, nan = float("inf"), float("nan")
     x = torch.tensor([[inf], [-inf], [nan], [2.0]], dtype=R.DT[dtype], device=DEV)
     one = torch.ones(1, 1, dtype=R.DT[dtype], device=DEV)
-    for act, y_want, d_want in (("relu", [inf, 0, nan, 2], [1, 0, nan, 1]), ("gelu", [inf, 0, nan, None], [1, 0, nan, None]),
+    for act, y_want, d_want in (("relu", [inf, 0, nan, 2], [1, 0, nan, 1]),
+                                ("gelu", [inf, 0, nan, None], [1, 0, nan, None]),
                                 ("none", [inf, -inf, nan, 2], [1, 1, 1, 1])):
         plan = api.rar_linear_plan(1, 1, CODE[dtype], R.ACTS[act])
         y, dx = nan_like(4, 1, dtype=dtype), nan_like(4, 1, dtype=dtype)
@@ -238,7 +241,8 @@ def make_ckpt(x, dtype):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
-@pytest.mark.parametrize("T,D", [(1, 1), (1, 31), (1, 32), (2, 33), (5, 77), (64, 8), (67, 1001), (300, 512), (3, 8200)])
+@pytest.mark.parametrize("T,D", [(1, 1), (1, 31), (1, 32), (2, 33), (5, 77), (64, 8), (67, 1001), (300, 512),
+                                 (3, 8200)])
 def test_ckpt_store_and_load(T, D, dtype):
     g = torch.Generator().manual_seed(T + D)
     x = rand(g, T, D, dtype=dtype) * torch.exp2(torch.randint(-20, 20, (T, D), generator=g)).to(R.DT[dtype])
@@ -290,7 +294,8 @@ def test_ckpt_load_reads_every_code_and_scale():
     api.rar_ckpt_load(2048, 32, api.F32, codes.to(DEV), scales.to(DEV), y)
     f32 = want.float()
     got = y.cpu()
-    assert torch.equal(torch.isnan(got), torch.isnan(f32)) and torch.equal(got[~torch.isnan(f32)], f32[~torch.isnan(f32)])
+    fine = ~torch.isnan(f32)
+    assert torch.equal(~torch.isnan(got), fine) and torch.equal(got[fine], f32[fine])
 
 
 @pytest.mark.parametrize("dtype", BOTH)
@@ -478,6 +483,14 @@ def test_other_streams_and_two_at_once(dtype):
         call_b(s2.cuda_stream)       # a raw stream handle
     torch.cuda.synchronize()
     assert _same(a, want) and _same(b, want)
+    # the default stream by its handle, from inside another stream
+    for t in a:
+        t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        call_a(0)
+    torch.cuda.synchronize()
+    assert _same(a, want)
 
 
 @pytest.mark.parametrize("dtype", BOTH)

@@ -25,7 +25,8 @@ def linear(K=64, N=96, dtype=api.F32, act=api.ACT_GELU):
 
 
 @pytest.mark.parametrize("K,N,dt,act", [(0, 4, 0, 0), (4, 0, 0, 0), (-1, 4, 0, 0), ((1 << 20) + 1, 4, 0, 0),
-                                        (4, (1 << 20) + 1, 1, 0), (4, 4, 2, 0), (4, 4, -1, 0), (4, 4, 0, 3), (4, 4, 0, -1)])
+                                        (4, (1 << 20) + 1, 1, 0), (4, 4, 2, 0), (4, 4, -1, 0), (4, 4, 0, 3),
+                                        (4, 4, 0, -1)])
 def test_linear_plan_refuses(K, N, dt, act):
     with pytest.raises(api.RarError) as e:
         api.rar_linear_plan(K, N, dt, act)
@@ -143,7 +144,8 @@ def test_ckpt_size_and_refusals():
         assert status(api.rar_ckpt_size, D) == api.EINVAL
     L = lib()
     st = lambda T=4, D=40, dt=0, x=A[0], ld=40, c=A[1], s=A[2]: L.rar_ckpt_store(T, D, dt, x, ld, c, s, None)
-    ld = lambda T=4, D=40, dt=0, c=A[1], s=A[2], act=0, y=A[0], ldy=40: L.rar_ckpt_load(T, D, dt, c, s, act, y, ldy, None)
+    ld = lambda T=4, D=40, dt=0, c=A[1], s=A[2], act=0, y=A[0], ldy=40: L.rar_ckpt_load(T, D, dt, c, s, act, y, ldy,
+                                                                                        None)
     for kw in (dict(T=-1), dict(D=0), dict(dt=2), dict(x=None), dict(c=None), dict(s=None), dict(ld=39), dict(c=A[0]),
                dict(s=A[0]), dict(s=A[1] + 255)):
         assert st(**kw) == api.EINVAL, kw
