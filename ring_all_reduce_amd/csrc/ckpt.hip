@@ -97,7 +97,11 @@ __global__ void __launch_bounds__(256) rar_ckpt_load_rows(const CkptParams p)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = c + i < p.cols ? act_value<T>(p.act, v[i]) : 0.0f;
+            v[i] = act_value<T>(p.act, v[i]);
+        if (c + kLane > p.cols)  // codes behind the matrix may hold anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = c + i < p.cols ? v[i] : 0.0f;
         const int cnt = width - c >= kLane ? kLane : (width - c < 0 ? 0 : (int)(width - c));
         store8((T *)p.y + at.row * p.ldy + c, cnt, vec, v);
     }

@@ -879,60 +879,84 @@ __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, con
 enum DzSource { kDzNone = 0, kDzPre = 1, kDzCkpt = 2 };
 constexpr int kDzRows = 4;
 
-template <class T, int ACT, int SOURCE>
+// VEC: rows of dy and z are whole 16-byte groups and a lane takes eight
+// neighbours; else it takes columns 64 apart, so that a wave still reads
+// consecutive memory.
+template <class T, int ACT, int SOURCE, bool VEC>
 __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
+    const int64_t c0 = (int64_t)blockIdx.x * 512;
     const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_chunk;
     const int64_t r1 = r0 + p.rows_per_chunk < p.rows ? r0 + p.rows_per_chunk : p.rows;
-    const int cnt = p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8;
-    const int put = p.pitch - c < 8 ? (p.pitch - c < 0 ? 0 : (int)(p.pitch - c)) : 8;
-    const bool vdy = (uintptr_t)p.dy % 16 == 0 && p.ldy * sizeof(T) % 16 == 0;
-    const bool vpre = (uintptr_t)p.pre % 16 == 0 && p.ldp * sizeof(T) % 16 == 0;
     const int64_t groups = (p.cols + kCkptGroup - 1) / kCkptGroup;
+    const auto column = [&](int i) __attribute__((always_inline)) { return c0 + (VEC ? lane * 8 + i : i * 64 + lane); };
     float sum[8] = {};
-    if (cnt > 0 || (p.dz && put > 0)) {
-        for (int64_t r = r0 + wave; r < r1; r += 4 * kDzRows) {
-            float d[kDzRows][8], z[kDzRows][8];
-            u32x2 w[kDzRows];
-            uint32_t e[kDzRows];
+    for (int64_t r = r0 + wave; r < r1; r += 4 * kDzRows) {
+        float d[kDzRows][8], z[kDzRows][8];
 #pragma unroll
-            for (int u = 0; u < kDzRows; ++u) {
-                const int64_t row = r + 4 * u;
-                const int n = row < r1 ? cnt : 0;
-                load8<true>((const T *)p.dy + row * p.ldy + c, n, vdy, d[u]);
+        for (int u = 0; u < kDzRows; ++u) {
+            const int64_t row = r + 4 * u;
+            const bool live = row < r1;
+            const T *dy = (const T *)p.dy + row * p.ldy, *pre = (const T *)p.pre + row * p.ldp;
+            if constexpr (VEC) {
+                const int n = live && column(0) < p.cols ? 8 : 0;  // columns are whole groups
+                load8<true>(dy + column(0), n, true, d[u]);
                 if (SOURCE == kDzPre)
-                    load8<true>((const T *)p.pre + row * p.ldp + c, n, vpre, z[u]);
-                w[u] = u32x2{0, 0};
-                e[u] = 0;
-                if (SOURCE == kDzCkpt && n > 0) {
-                    w[u] = *(const u32x2 *)((const uint8_t *)p.pre + row * groups * kCkptGroup + c);
-                    e[u] = p.pre_scales[row * groups + c / kCkptGroup];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kDzRows; ++u) {
-                const int64_t row = r + 4 * u;
-                if (row >= r1)
-                    continue;
-                if (SOURCE == kDzCkpt)
+                    load8<true>(pre + column(0), n, true, z[u]);
+                if (SOURCE == kDzCkpt) {
+                    u32x2 w = {0, 0};
+                    uint32_t e = 0;
+                    if (n) {
+                        w = load_once((const u32x2 *)((const uint8_t *)p.pre + row * groups * kCkptGroup + column(0)));
+                        e = p.pre_scales[row * groups + column(0) / kCkptGroup];
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const f32x4 x = ckpt_values4(w[u][h], e[u]);
+                        const f32x4 x = ckpt_values4(w[h], e);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             z[u][4 * h + i] = x[i];
                     }
-                if (SOURCE != kDzNone)
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        d[u][i] = i < cnt ? d[u][i] * act_grad<T>(ACT, z[u][i]) : 0.0f;
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = live && column(i) < p.cols;
+                    d[u][i] = in ? to_f32(dy[column(i)]) : 0.0f;
+                    z[u][i] = 0.0f;
+                    if (SOURCE == kDzPre)
+                        z[u][i] = in ? to_f32(pre[column(i)]) : 0.0f;
+                    if (SOURCE == kDzCkpt && in)
+                        z[u][i] = ckpt_values4(((const uint8_t *)p.pre)[row * groups * kCkptGroup + column(i)],
+                                               p.pre_scales[row * groups + column(i) / kCkptGroup])
+                                      .x;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kDzRows; ++u) {
+            const int64_t row = r + 4 * u;
+            if (row >= r1)
+                continue;
+            // columns behind the matrix: zero times a derivative at zero
+            if (SOURCE != kDzNone)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    sum[i] += d[u][i];
-                if (p.dz)
-                    store8((T *)p.dz + row * p.pitch + c, put, true, d[u]);
+                    d[u][i] *= act_grad<T>(ACT, z[u][i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum[i] += d[u][i];
+            if (!p.dz)
+                continue;
+            T *dz = (T *)p.dz + row * p.pitch;
+            if constexpr (VEC) {
+                store8(dz + column(0), column(0) < p.pitch ? 8 : 0, true, d[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (column(i) < p.pitch)
+                        dz[column(i)] = from_f32<T>(d[u][i]);
             }
         }
     }
@@ -946,10 +970,9 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int j = threadIdx.x + k * 256;  // column of the workgroup
-        const int64_t col = (int64_t)blockIdx.x * 512 + j;
-        if (col < p.cols)
-            p.part[blockIdx.y * p.cols + col] = (sums[0][j % 8][j / 8] + sums[1][j % 8][j / 8]) +
-                                                (sums[2][j % 8][j / 8] + sums[3][j % 8][j / 8]);
+        const int i = VEC ? j % 8 : j / 64, l = VEC ? j / 8 : j % 64;
+        if (c0 + j < p.cols)
+            p.part[blockIdx.y * p.cols + c0 + j] = (sums[0][i][l] + sums[1][i][l]) + (sums[2][i][l] + sums[3][i][l]);
     }
 }
 
@@ -1056,17 +1079,27 @@ hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, h
 
 namespace {
 
-template <class T>
+template <class T, bool VEC>
 void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
 {
     if (p.act == RAR_ACT_NONE)
-        rar_dz<T, RAR_ACT_NONE, kDzNone><<<grid, 256, 0, st>>>(p);
+        rar_dz<T, RAR_ACT_NONE, kDzNone, VEC><<<grid, 256, 0, st>>>(p);
     else if (p.act == RAR_ACT_RELU)
-        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_RELU, kDzPre><<<grid, 256, 0, st>>>(p);
+        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt, VEC><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_RELU, kDzPre, VEC><<<grid, 256, 0, st>>>(p);
     else
-        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_GELU, kDzPre><<<grid, 256, 0, st>>>(p);
+        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt, VEC><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_GELU, kDzPre, VEC><<<grid, 256, 0, st>>>(p);
+}
+
+template <class T>
+void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
+{
+    const auto whole = [](const void *m, int64_t ld) { return (uintptr_t)m % 16 == 0 && ld * sizeof(T) % 16 == 0; };
+    if (p.cols % 8 == 0 && whole(p.dy, p.ldy) && (!p.pre || p.pre_scales || whole(p.pre, p.ldp)))
+        run_dz<T, true>(p, grid, st);
+    else
+        run_dz<T, false>(p, grid, st);
 }
 
 }  // namespace
