@@ -61,13 +61,19 @@ __device__ __forceinline__ void store_once(V *p, V v)
     __builtin_nontemporal_store(v, p);
 }
 
-// Eight consecutive elements, of which the first cnt exist; vec: 16-byte aligned.
+// Eight consecutive elements, of which the first cnt exist.  Whole groups move in
+// 16-byte accesses at whatever address the element type allows (global memory
+// takes them unaligned).
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
 template <bool ONCE = false>
-__device__ __forceinline__ void load8(const float *p, int cnt, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const float *p, int cnt, float (&v)[8])
 {
-    if (vec && cnt == 8) {
-        const f32x4 *const w = reinterpret_cast<const f32x4 *>(p);
-        const f32x4 a = ONCE ? load_once(w) : w[0], b = ONCE ? load_once(w + 1) : w[1];
+    if (cnt == 8) {
+        const f32x4_any *const w = reinterpret_cast<const f32x4_any *>(p);
+        const f32x4 a = ONCE ? __builtin_nontemporal_load(w) : w[0];
+        const f32x4 b = ONCE ? __builtin_nontemporal_load(w + 1) : w[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = a[i];
@@ -81,14 +87,14 @@ __device__ __forceinline__ void load8(const float *p, int cnt, bool vec, float (
 }
 
 template <bool ONCE = false>
-__device__ __forceinline__ void store8(float *p, int cnt, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(float *p, int cnt, const float (&v)[8])
 {
-    if (vec && cnt == 8) {
-        f32x4 *const w = reinterpret_cast<f32x4 *>(p);
+    if (cnt == 8) {
+        f32x4_any *const w = reinterpret_cast<f32x4_any *>(p);
         const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
         if (ONCE) {
-            store_once(w, a);
-            store_once(w + 1, b);
+            __builtin_nontemporal_store(a, w);
+            __builtin_nontemporal_store(b, w + 1);
         } else {
             w[0] = a;
             w[1] = b;
@@ -102,10 +108,11 @@ __device__ __forceinline__ void store8(float *p, int cnt, bool vec, const float 
 }
 
 template <bool ONCE = false>
-__device__ __forceinline__ void load8(const bf16 *p, int cnt, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const bf16 *p, int cnt, float (&v)[8])
 {
-    if (vec && cnt == 8) {
-        const u32x4 w = ONCE ? load_once(reinterpret_cast<const u32x4 *>(p)) : *reinterpret_cast<const u32x4 *>(p);
+    if (cnt == 8) {
+        const u32x4_any *const q = reinterpret_cast<const u32x4_any *>(p);
+        const u32x4 w = ONCE ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -119,14 +126,15 @@ __device__ __forceinline__ void load8(const bf16 *p, int cnt, bool vec, float (&
 }
 
 template <bool ONCE = false>
-__device__ __forceinline__ void store8(bf16 *p, int cnt, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(bf16 *p, int cnt, const float (&v)[8])
 {
-    if (vec && cnt == 8) {
+    if (cnt == 8) {
         const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        u32x4_any *const q = reinterpret_cast<u32x4_any *>(p);
         if (ONCE)
-            store_once(reinterpret_cast<u32x4 *>(p), w);
+            __builtin_nontemporal_store(w, q);
         else
-            *reinterpret_cast<u32x4 *>(p) = w;
+            *q = w;
         return;
     }
 #pragma unroll

@@ -44,7 +44,6 @@ template <class T>
 __global__ void __launch_bounds__(256) rar_ckpt_store_rows(const CkptParams p)
 {
     const uint32_t groups = (uint32_t)((p.cols + kCkptGroup - 1) / kCkptGroup);
-    const bool vec = (uintptr_t)p.x % 16 == 0 && (p.ldx * sizeof(T)) % 16 == 0;
     const int q = threadIdx.x % kLanes;
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
@@ -54,7 +53,7 @@ __global__ void __launch_bounds__(256) rar_ckpt_store_rows(const CkptParams p)
         const int64_t c = (int64_t)at.group * kCkptGroup + q * kLane;
         const int cnt = p.cols - c >= kLane ? kLane : (p.cols - c < 0 ? 0 : (int)(p.cols - c));
         float v[8];
-        load8<true>((const T *)p.x + at.row * p.ldx + c, cnt, vec, v);
+        load8<true>((const T *)p.x + at.row * p.ldx + c, cnt, v);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -76,7 +75,6 @@ __global__ void __launch_bounds__(256) rar_ckpt_load_rows(const CkptParams p)
 {
     const uint32_t groups = (uint32_t)((p.cols + kCkptGroup - 1) / kCkptGroup);
     const int64_t width = p.pitch_zero > p.cols ? p.pitch_zero : p.cols;
-    const bool vec = (uintptr_t)p.y % 16 == 0 && (p.ldy * sizeof(T)) % 16 == 0;
     const int q = threadIdx.x % kLanes;
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
@@ -103,7 +101,7 @@ __global__ void __launch_bounds__(256) rar_ckpt_load_rows(const CkptParams p)
             for (int i = 0; i < 8; ++i)
                 v[i] = c + i < p.cols ? v[i] : 0.0f;
         const int cnt = width - c >= kLane ? kLane : (width - c < 0 ? 0 : (int)(width - c));
-        store8((T *)p.y + at.row * p.ldy + c, cnt, vec, v);
+        store8((T *)p.y + at.row * p.ldy + c, cnt, v);
     }
 }
 

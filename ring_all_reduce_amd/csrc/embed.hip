@@ -28,8 +28,8 @@ namespace {
 // Lookup
 // ---------------------------------------------------------------------------
 
-// 16-byte vectors of a row, or single elements where rows are not 16-byte
-// aligned.  The workgroup's first row is found by one uniform division.
+// 16-byte vectors of a row, or single elements where rows are not whole
+// vectors.  The workgroup's first row is found by one uniform division.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) rar_embed_rows(const EmbedParams p)
 {
@@ -54,17 +54,18 @@ __global__ void __launch_bounds__(256) rar_embed_rows(const EmbedParams p)
         if constexpr (!VEC) {
             *dst = from_f32<T>(ok ? to_f32(*src) * p.scale : 0.0f);
         } else if constexpr (sizeof(T) == 4) {
-            const f32x4 v = load4(src);
-            store_once(reinterpret_cast<f32x4 *>(dst), ok ? v * p.scale : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            const f32x4 v = *reinterpret_cast<const f32x4_any *>(src);
+            __builtin_nontemporal_store(ok ? v * p.scale : f32x4{0.0f, 0.0f, 0.0f, 0.0f},
+                                        reinterpret_cast<f32x4_any *>(dst));
         } else {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(src);
+            const u32x4 w = *reinterpret_cast<const u32x4_any *>(src);
             u32x4 o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
                 o[i] = ok ? pack_bf16(lo * p.scale, hi * p.scale) : 0u;
             }
-            store_once(reinterpret_cast<u32x4 *>(dst), o);
+            __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any *>(dst));
         }
     }
 }
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_place(const int64_t *id
 // ---------------------------------------------------------------------------
 
 // A wave sums a strip of kCols columns.  Column of lane l's i-th value: l * 8 +
-// i where rows of dy are whole 16-byte groups, else i * 64 + l, so that either
+// i where rows are whole eights, else i * 64 + l, so that either
 // way a wave reads consecutive memory.
 constexpr int kCols = 512;
 
@@ -376,10 +377,10 @@ struct Columns {
     {
         if constexpr (VEC) {
             // D is whole eights; lanes behind it read the row's first values
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (col(0) < D ? col(0) : 0));
+            const u32x4_any *p = reinterpret_cast<const u32x4_any *>(row + (col(0) < D ? col(0) : 0));
 #pragma unroll
             for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-                v.v[h] = load_once(p + h);
+                v.v[h] = __builtin_nontemporal_load(p + h);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -426,7 +427,7 @@ struct Columns {
                 acc[i] += old.at(i);
         }
         if constexpr (VEC) {
-            store8<true>(out + col(0), col(0) < D ? 8 : 0, true, acc);
+            store8<true>(out + col(0), col(0) < D ? 8 : 0, acc);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -636,8 +637,7 @@ int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D) { return layout(T,
 hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t st)
 {
     const int es = dt == RAR_BF16 ? 2 : 4;
-    const bool vec = (uintptr_t)p.table % 16 == 0 && (uintptr_t)p.out % 16 == 0 && (p.D * es) % 16 == 0 &&
-                     (p.ldo * es) % 16 == 0;
+    const bool vec = p.D * es % 16 == 0;  // rows of whole 16-byte groups, at any address
     const int64_t items = p.T * (vec ? p.D * es / 16 : p.D);
     const unsigned grid = (unsigned)((items + 1023) / 1024);
     if (dt == RAR_BF16)
@@ -700,8 +700,7 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
     }
     const GradWs w{keys[last], pos[last], (float *)(ws + l.from_left), (float *)(ws + l.to_right),
                    (float *)(ws + l.long_run), l.pitch, l.chunk};
-    const int es = dt == RAR_BF16 ? 2 : 4;
-    const bool vec = (uintptr_t)p.dy % 16 == 0 && p.ldy * es % 16 == 0 && (uintptr_t)p.grad % 16 == 0 && p.D % 8 == 0;
+    const bool vec = p.D % 8 == 0;
     if (dt == RAR_BF16)
         vec ? sums<bf16, true>(p, w, st) : sums<bf16, false>(p, w, st);
     else

@@ -216,13 +216,12 @@ struct Frag32 {
 template <class T>
 __device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t n, float (&v)[8])
 {
-    const bool vec = p.vec;
     const int cnt = m >= p.M || n >= p.N ? 0 : (p.N - n < 8 ? (int)(p.N - n) : 8);
     T *const out = (T *)p.out + m * p.ldo + n;
     float t[8];
     if (p.mode == kModeForward) {
         if (p.bias) {
-            load8((const T *)p.bias + n, cnt, vec, t);
+            load8((const T *)p.bias + n, cnt, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += t[i];
@@ -247,24 +246,24 @@ __device__ __forceinline__ void epilogue(const GemmParams &p, int64_t m, int64_t
                     p.pre_scales[m * groups + g] = (uint8_t)e;
             }
         } else if (p.pre) {
-            store8((T *)p.pre + m * p.ldp + n, cnt, vec, v);
+            store8((T *)p.pre + m * p.ldp + n, cnt, v);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = act_value<T>(p.act, v[i]);
         if (p.res) {
-            load8((const T *)p.res + m * p.ldr + n, cnt, vec, t);
+            load8((const T *)p.res + m * p.ldr + n, cnt, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += t[i];
         }
     } else if (p.accumulate) {
-        load8(out, cnt, vec, t);
+        load8(out, cnt, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] += t[i];
     }
-    store8(out, cnt, vec, v);
+    store8(out, cnt, v);
 }
 
 // A wave's ROWS rows of W columns pass through LDS, so that a lane finishes
@@ -288,8 +287,8 @@ __device__ __forceinline__ void tile_row(RAR_LDS char *tile, int r, int q, float
     }
 }
 
-// The usual tile: wholly inside the matrix, rows of whole 16-byte groups, z
-// kept in the layer's type or not at all.  The same results as epilogue(),
+// The usual tile: wholly inside the matrix, z kept in the layer's type or not at
+// all.  The same results as epilogue(),
 // with the addresses and the bias out of the loop.
 template <class T, int W, int ROWS, int ACT>
 __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char *tile, int64_t m0, int64_t n0)
@@ -299,7 +298,7 @@ __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char 
     const int64_t m = m0 + lane / kLanes, n = n0 + q * 8;
     float bias[8] = {};
     if (p.bias)
-        load8((const T *)p.bias + n, 8, true, bias);
+        load8((const T *)p.bias + n, 8, bias);
     T *out = (T *)p.out + m * p.ldo + n;
     T *pre = (T *)p.pre + m * p.ldp + n;
     const T *res = (const T *)p.res + m * p.ldr + n;
@@ -308,13 +307,13 @@ __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char 
     for (int r = lane / kLanes; r < ROWS; r += kRows) {
         float v[8], t[8];
         if (p.res)
-            load8(res, 8, true, t);
+            load8(res, 8, t);
         tile_row<W>(tile, r, q, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] += bias[i];
         if (p.pre)
-            store8<true>(pre, 8, true, v);
+            store8<true>(pre, 8, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = act_value<T>(ACT, v[i]);
@@ -322,7 +321,7 @@ __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += t[i];
-        store8<true>(out, 8, true, v);
+        store8<true>(out, 8, v);
         out += so;
         pre += sp;
         res += sr;
@@ -336,7 +335,7 @@ __device__ __forceinline__ void finish_rows(const GemmParams &p, int split, RAR_
     const int lane = threadIdx.x & 63, q = lane % kLanes;
     const int64_t n = n0 + q * 8;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (p.vec && m0 + ROWS <= p.M && n0 + W <= p.N && !p.pre_scales &&
+    if (m0 + ROWS <= p.M && n0 + W <= p.N && !p.pre_scales &&
         (p.mode == kModeForward || (p.mode == kModeStore && !p.accumulate))) {
         // a plain store has no bias, residual, z or activation
         if (p.act == RAR_ACT_GELU)
@@ -757,12 +756,12 @@ __global__ void __launch_bounds__(1024) rar_gemv(const GemmParams p)
             const T *const at = w + k * p.ldb + q * kPer;
 #pragma unroll
             for (int j = 0; j < kGemvK; ++j)
-                wv[j][0] = live ? *reinterpret_cast<const u32x4 *>(at + j * p.ldb) : u32x4{0, 0, 0, 0};
+                wv[j][0] = live ? *reinterpret_cast<const u32x4_any *>(at + j * p.ldb) : u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int j = 0; j < kGemvK / kPer; ++j)
-                    xv[r][j] = *reinterpret_cast<const u32x4 *>(x[r] + k + j * kPer);
+                    xv[r][j] = *reinterpret_cast<const u32x4_any *>(x[r] + k + j * kPer);
 #pragma unroll
             for (int j = 0; j < kGemvK; ++j)
 #pragma unroll
@@ -839,19 +838,6 @@ __device__ __forceinline__ void join(const GemmParams &p, int64_t block)
 // Streaming passes
 // ---------------------------------------------------------------------------
 
-template <class T>
-__device__ __forceinline__ f32x4 get4(const T *p, int cnt, bool vec)
-{
-    if (vec && cnt == 4)
-        return load4(p);
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < cnt)
-            v[i] = to_f32(p[i]);
-    return v;
-}
-
 // A copy with whole 16-byte rows for operands whose rows are not: the products
 // read 16 bytes at a time.  Bound by HBM bandwidth; the copy is small against
 // the product that reads it.
@@ -864,9 +850,10 @@ __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, con
     const int64_t row = blockIdx.x - (is_second ? first.rows : 0);
     const T *src = (const T *)p.src + row * p.ld;
     T *dst = (T *)p.dst + row * p.pitch;
-    for (int64_t c = (int64_t)blockIdx.y * 1024 + threadIdx.x * 4; c < p.pitch; c += (int64_t)gridDim.y * 1024) {
-        const int cnt = p.cols - c < 4 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 4;
-        store4(dst + c, get4(src + c, cnt, false));
+    for (int64_t c = (int64_t)blockIdx.y * 2048 + threadIdx.x * 8; c < p.pitch; c += (int64_t)gridDim.y * 2048) {
+        float v[8];
+        load8(src + c, p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8, v);
+        store8(dst + c, p.pitch - c < 8 ? (int)(p.pitch - c) : 8, v);
     }
 }
 
@@ -879,59 +866,33 @@ __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, con
 enum DzSource { kDzNone = 0, kDzPre = 1, kDzCkpt = 2 };
 constexpr int kDzRows = 4;
 
-// VEC: rows of dy and z are whole 16-byte groups and a lane takes eight
-// neighbours; else it takes columns 64 apart, so that a wave still reads
-// consecutive memory.
-template <class T, int ACT, int SOURCE, bool VEC>
+template <class T, int ACT, int SOURCE>
 __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c0 = (int64_t)blockIdx.x * 512;
+    const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
     const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_chunk;
     const int64_t r1 = r0 + p.rows_per_chunk < p.rows ? r0 + p.rows_per_chunk : p.rows;
+    const int cnt = p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8;
+    const int put = p.pitch - c < 8 ? (p.pitch - c < 0 ? 0 : (int)(p.pitch - c)) : 8;
     const int64_t groups = (p.cols + kCkptGroup - 1) / kCkptGroup;
-    const auto column = [&](int i) __attribute__((always_inline)) { return c0 + (VEC ? lane * 8 + i : i * 64 + lane); };
     float sum[8] = {};
     for (int64_t r = r0 + wave; r < r1; r += 4 * kDzRows) {
         float d[kDzRows][8], z[kDzRows][8];
+        u32x2 w[kDzRows];
+        uint32_t e[kDzRows];
 #pragma unroll
         for (int u = 0; u < kDzRows; ++u) {
             const int64_t row = r + 4 * u;
-            const bool live = row < r1;
-            const T *dy = (const T *)p.dy + row * p.ldy, *pre = (const T *)p.pre + row * p.ldp;
-            if constexpr (VEC) {
-                const int n = live && column(0) < p.cols ? 8 : 0;  // columns are whole groups
-                load8<true>(dy + column(0), n, true, d[u]);
-                if (SOURCE == kDzPre)
-                    load8<true>(pre + column(0), n, true, z[u]);
-                if (SOURCE == kDzCkpt) {
-                    u32x2 w = {0, 0};
-                    uint32_t e = 0;
-                    if (n) {
-                        w = load_once((const u32x2 *)((const uint8_t *)p.pre + row * groups * kCkptGroup + column(0)));
-                        e = p.pre_scales[row * groups + column(0) / kCkptGroup];
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const f32x4 x = ckpt_values4(w[h], e);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            z[u][4 * h + i] = x[i];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = live && column(i) < p.cols;
-                    d[u][i] = in ? to_f32(dy[column(i)]) : 0.0f;
-                    z[u][i] = 0.0f;
-                    if (SOURCE == kDzPre)
-                        z[u][i] = in ? to_f32(pre[column(i)]) : 0.0f;
-                    if (SOURCE == kDzCkpt && in)
-                        z[u][i] = ckpt_values4(((const uint8_t *)p.pre)[row * groups * kCkptGroup + column(i)],
-                                               p.pre_scales[row * groups + column(i) / kCkptGroup])
-                                      .x;
-                }
+            const int n = row < r1 ? cnt : 0;
+            load8<true>((const T *)p.dy + row * p.ldy + c, n, d[u]);
+            if (SOURCE == kDzPre)
+                load8<true>((const T *)p.pre + row * p.ldp + c, n, z[u]);
+            w[u] = u32x2{0, 0};
+            e[u] = 0;
+            if (SOURCE == kDzCkpt && n > 0) {
+                w[u] = load_once((const u32x2 *)((const uint8_t *)p.pre + row * groups * kCkptGroup + c));
+                e[u] = p.pre_scales[row * groups + c / kCkptGroup];
             }
         }
 #pragma unroll
@@ -939,25 +900,27 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
             const int64_t row = r + 4 * u;
             if (row >= r1)
                 continue;
-            // columns behind the matrix: zero times a derivative at zero
+            if (SOURCE == kDzCkpt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 x = ckpt_values4(w[u][h], e[u]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        z[u][4 * h + i] = x[i];
+                }
             if (SOURCE != kDzNone)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     d[u][i] *= act_grad<T>(ACT, z[u][i]);
+            if (SOURCE == kDzCkpt && cnt < 8)  // codes behind the matrix may hold anything
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[u][i] = i < cnt ? d[u][i] : 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 sum[i] += d[u][i];
-            if (!p.dz)
-                continue;
-            T *dz = (T *)p.dz + row * p.pitch;
-            if constexpr (VEC) {
-                store8(dz + column(0), column(0) < p.pitch ? 8 : 0, true, d[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (column(i) < p.pitch)
-                        dz[column(i)] = from_f32<T>(d[u][i]);
-            }
+            if (p.dz)
+                store8((T *)p.dz + row * p.pitch + c, put, d[u]);
         }
     }
     if (!p.part)
@@ -970,9 +933,10 @@ __global__ void __launch_bounds__(256) rar_dz(const DzParams p)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int j = threadIdx.x + k * 256;  // column of the workgroup
-        const int i = VEC ? j % 8 : j / 64, l = VEC ? j / 8 : j % 64;
-        if (c0 + j < p.cols)
-            p.part[blockIdx.y * p.cols + c0 + j] = (sums[0][i][l] + sums[1][i][l]) + (sums[2][i][l] + sums[3][i][l]);
+        const int64_t col = (int64_t)blockIdx.x * 512 + j;
+        if (col < p.cols)
+            p.part[blockIdx.y * p.cols + col] = (sums[0][j % 8][j / 8] + sums[1][j % 8][j / 8]) +
+                                                (sums[2][j % 8][j / 8] + sums[3][j % 8][j / 8]);
     }
 }
 
@@ -1069,7 +1033,7 @@ hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t 
 hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st)
 {
     const int64_t pitch = a.pitch > b.pitch ? a.pitch : b.pitch;
-    const dim3 grid((unsigned)(a.rows + b.rows), (unsigned)((pitch + 1023) / 1024 < 64 ? (pitch + 1023) / 1024 : 64));
+    const dim3 grid((unsigned)(a.rows + b.rows), (unsigned)((pitch + 2047) / 2048 < 64 ? (pitch + 2047) / 2048 : 64));
     if (dt == RAR_BF16)
         rar_pack_rows<bf16><<<grid, 256, 0, st>>>(a, b);
     else
@@ -1079,27 +1043,17 @@ hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, h
 
 namespace {
 
-template <class T, bool VEC>
-void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
-{
-    if (p.act == RAR_ACT_NONE)
-        rar_dz<T, RAR_ACT_NONE, kDzNone, VEC><<<grid, 256, 0, st>>>(p);
-    else if (p.act == RAR_ACT_RELU)
-        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt, VEC><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_RELU, kDzPre, VEC><<<grid, 256, 0, st>>>(p);
-    else
-        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt, VEC><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_GELU, kDzPre, VEC><<<grid, 256, 0, st>>>(p);
-}
-
 template <class T>
 void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
 {
-    const auto whole = [](const void *m, int64_t ld) { return (uintptr_t)m % 16 == 0 && ld * sizeof(T) % 16 == 0; };
-    if (p.cols % 8 == 0 && whole(p.dy, p.ldy) && (!p.pre || p.pre_scales || whole(p.pre, p.ldp)))
-        run_dz<T, true>(p, grid, st);
+    if (p.act == RAR_ACT_NONE)
+        rar_dz<T, RAR_ACT_NONE, kDzNone><<<grid, 256, 0, st>>>(p);
+    else if (p.act == RAR_ACT_RELU)
+        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_RELU, kDzPre><<<grid, 256, 0, st>>>(p);
     else
-        run_dz<T, false>(p, grid, st);
+        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
+                     : rar_dz<T, RAR_ACT_GELU, kDzPre><<<grid, 256, 0, st>>>(p);
 }
 
 }  // namespace

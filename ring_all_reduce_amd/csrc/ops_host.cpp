@@ -221,14 +221,6 @@ BackwardWs backward_ws(const Layer &l, void *ws)
     return b;
 }
 
-// Whether the outputs, the bias and the residual can be accessed 16 bytes at a time.
-int wide_outputs(const GemmParams &p, int es)
-{
-    const auto wide = [es](const void *q, int64_t ld) { return aligned(q, 16) && (ld * es) % 16 == 0; };
-    return wide(p.out, p.ldo) && (!p.pre || p.pre_scales || wide(p.pre, p.ldp)) && (!p.res || wide(p.res, p.ldr)) &&
-           aligned(p.bias, 16);
-}
-
 // Fills in the shape of a product; false if its grid is too large.
 bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
 {
@@ -239,7 +231,6 @@ bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
     p.steps_per_split = s.steps;
     p.pitch = s.pitch;
     p.part = part;
-    p.vec = wide_outputs(p, esize(dt));
     *tile = s.tile;
     return s.tiles_m * s.tiles_n * s.splits <= kMaxBlocks / 2;
 }
@@ -413,8 +404,7 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
         p.lda = ldx;
         p.b = w;
         p.ldb = N;
-        p.vec = wide_outputs(p, es);
-        return launched(rar::launch_gemv(dt, p, direct(mx) && direct(mw), st));
+        return launched(rar::launch_gemv(dt, p, N * es % 16 == 0, st));
     }
     rar::PackParams kx{}, kw{};
     int tile;

@@ -42,7 +42,6 @@ struct GemmParams {
     int mode;
     int act;
     int accumulate;
-    int vec;                 // outputs, bias and residual may be accessed 16 bytes at a time
     int splits;
     int64_t steps_per_split; // K steps of one split
     int64_t tiles_m, tiles_n;
@@ -118,7 +117,7 @@ struct GemmPair {
     unsigned x_blocks;
 };
 hipError_t launch_backward(rar_dtype dt, const GemmPair &p, unsigned w_blocks, int tile, hipStream_t st);
-// A forward product of at most kGemvRows rows; vec: rows of x and W can be read 16 bytes at a time.
+// A forward product of at most kGemvRows rows; vec: rows of W are whole 16-byte groups.
 constexpr int kGemvRows = 4;
 hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t st);
 hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st);
