@@ -508,6 +508,7 @@ def _workspace(ws, nbytes: int, stream):
 def rar_embed_lookup(V: int, D: int, dtype: int, table, T: int, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[ids[t]]; rows of ids outside 0..V-1 are zero."""
     import torch
+    V, D, T, scale = int(V), int(D), int(T), float(scale)
     td = _torch_dtype(dtype)
     ptr, ldo = _matrix(out, "out", td, T, D)
     _check(lib().rar_embed_lookup(V, D, dtype, _dense(table, "table", td, V * D), T,
@@ -517,7 +518,7 @@ def rar_embed_lookup(V: int, D: int, dtype: int, table, T: int, ids, out, scale:
 
 def rar_embed_grad_workspace(V: int, D: int, T: int) -> int:
     out = ctypes.c_int64()
-    _check(lib().rar_embed_grad_workspace(V, D, T, ctypes.byref(out)), "rar_embed_grad_workspace")
+    _check(lib().rar_embed_grad_workspace(int(V), int(D), int(T), ctypes.byref(out)), "rar_embed_grad_workspace")
     return out.value
 
 
@@ -525,6 +526,7 @@ def rar_embed_grad(V: int, D: int, dtype: int, T: int, ids, dy, grad, scale: flo
                    ws=None, stream=None) -> None:
     """grad[v] (+)= scale * the sum of dy[t] over the t with ids[t] == v."""
     import torch
+    V, D, T, scale = int(V), int(D), int(T), float(scale)
     td = _torch_dtype(dtype)
     dptr, lddy = _matrix(dy, "dy", td, T, D)
     gptr, iptr = _dense(grad, "grad", td, V * D), _dense(ids, "ids", torch.int64, T)
@@ -562,6 +564,7 @@ def rar_linear_destroy(plan: Linear) -> None:
 
 def rar_linear_workspace(plan: Linear, T: int):
     """(forward bytes, backward bytes) for T rows."""
+    T = int(T)
     known = plan._bytes.get(T)
     if known is not None and plan.handle:
         return known
@@ -586,6 +589,7 @@ def rar_linear_forward(plan: Linear, T: int, x, w, bias, residual, y, pre=None, 
                        stream=None) -> None:
     """z = x w + bias, y = act(z) + residual; bias and residual may be None.
     pre receives z, as an 8-bit checkpoint when pre_scales is given."""
+    T = int(T)
     td, K, N = _torch_dtype(plan.dtype), plan.K, plan.N
     xp, ldx = _matrix(x, "x", td, T, K)
     wp, bp = _dense(w, "w", td, K * N), _dense(bias, "bias", td, N)
@@ -601,6 +605,7 @@ def rar_linear_backward(plan: Linear, T: int, dy, x, w, pre, dx, dw, db, x_scale
                         accumulate: bool = False, ws=None, stream=None) -> None:
     """dz = dy act'(z); dx = dz w^T, dw (+)= x^T dz, db (+)= column sums of dz.
     dx, dw and db may each be None; x and pre may be 8-bit checkpoints."""
+    T = int(T)
     td, K, N = _torch_dtype(plan.dtype), plan.K, plan.N
     dyp, lddy = _matrix(dy, "dy", td, T, N)
     xp, ldx, xs = _kept(x, x_scales, "x", td, T, K)
@@ -622,12 +627,14 @@ def rar_ckpt_size(D: int):
 
 def rar_ckpt_store(T: int, D: int, dtype: int, x, codes, scales, stream=None) -> None:
     """codes (T x pitch) and scales (T x groups), both uint8, receive the 8-bit checkpoint of x (T x D)."""
+    T, D = int(T), int(D)
     xp, ldx, cp, sp = *_matrix(x, "x", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
     _check(lib().rar_ckpt_store(T, D, dtype, xp, ldx, cp, sp, _on(stream)), "rar_ckpt_store")
 
 
 def rar_ckpt_load(T: int, D: int, dtype: int, codes, scales, y, act: int = ACT_NONE, stream=None) -> None:
     """y (T x D) = act(what the checkpoint holds)."""
+    T, D = int(T), int(D)
     yp, ldy, cp, sp = *_matrix(y, "y", _torch_dtype(dtype), T, D), *_ckpt(codes, scales, T, D)
     _check(lib().rar_ckpt_load(T, D, dtype, cp, sp, act, yp, ldy, _on(stream)), "rar_ckpt_load")
 
