@@ -422,10 +422,13 @@ __device__ __forceinline__ void product(f32x4 &acc, bf16x8 b, bf16x8 a)
 //            half 1, reading the next step's half 0, and issuing the loads of
 //            the step after it into the LDS half that everyone has now read
 // Fragments of A are replaced in place once their row of products is issued;
-// those of B need two sets.  Bound: the matrix cores, 62% busy at 256 x 256 (the
-// clock falls to about 2.1 GHz under them).  Eight waves rather than four: two
+// those of B need two sets.  Bound: the matrix cores, 68% busy in the backward
+// products and 51% in the forward one with its epilogue, at 256 x 256 and the
+// 2.0 GHz that the clock falls to under them.  Eight waves rather than four: two
 // waves a SIMD cover each other's meeting and address work, and the epilogue's
-// arithmetic.  Measured at 8192 rows, 2048 -> 8192: both backward products in
+// arithmetic.  A ring of five smaller buffers with loads further ahead measured
+// the same; 32 x 32 x 16 instructions 3 to 5% slower, their reads of 32 rows
+// meeting in the same banks.  Measured at 8192 rows, 2048 -> 8192: both backward products in
 // one launch 393 us (1.40 PFLOP/s), the forward product with gelu and z kept
 // 256 us (1.07 PFLOP/s, about 50 us of it the epilogue).  128 x 128 tiles for
 // products with few tiles: 2048 x 4096 -> 4096 62 us (1.1 PFLOP/s).
