@@ -639,19 +639,36 @@ void sums(const EmbedGradParams &p, const GradWs &w, hipStream_t st)
 
 int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D) { return layout(T, D).total; }
 
+bool embed_grad_fits(int64_t T, int64_t D, int64_t grad_bytes, int64_t lanes)
+{
+    const int64_t chunks = T / layout(T, D).chunk + 1, strips = (D + kCols - 1) / kCols;
+    return (chunks * strips / 4 + 1) * 256 <= lanes &&
+           (grad_bytes / kClearBytes + T / kSortKeys + 3) * kSortThreads <= lanes;
+}
+
 hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t st)
 {
     const int es = dt == RAR_BF16 ? 2 : 4;
     const bool vec = p.D * es % 16 == 0;  // rows of whole 16-byte groups, at any address
-    const int64_t items = p.T * (vec ? p.D * es / 16 : p.D);
-    const unsigned grid = (unsigned)((items + 1023) / 1024);
-    if (dt == RAR_BF16)
-        vec ? rar_embed_rows<bf16, true><<<grid, 256, 0, st>>>(p)
-            : rar_embed_rows<bf16, false><<<grid, 256, 0, st>>>(p);
-    else
-        vec ? rar_embed_rows<float, true><<<grid, 256, 0, st>>>(p)
-            : rar_embed_rows<float, false><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+    const int64_t width = vec ? p.D * es / 16 : p.D;
+    const int64_t most = (int64_t(1) << 33) / width;  // rows of a launch: a grid holds 2^32 lanes, each four items
+    for (int64_t t = 0; t < p.T; t += most) {
+        EmbedParams q = p;
+        q.ids = p.ids + t;
+        q.out = (char *)p.out + t * p.ldo * es;
+        q.T = p.T - t < most ? p.T - t : most;
+        const unsigned grid = (unsigned)((q.T * width + 1023) / 1024);
+        if (dt == RAR_BF16)
+            vec ? rar_embed_rows<bf16, true><<<grid, 256, 0, st>>>(q)
+                : rar_embed_rows<bf16, false><<<grid, 256, 0, st>>>(q);
+        else
+            vec ? rar_embed_rows<float, true><<<grid, 256, 0, st>>>(q)
+                : rar_embed_rows<float, false><<<grid, 256, 0, st>>>(q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t st)

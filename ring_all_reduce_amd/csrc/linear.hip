@@ -855,19 +855,22 @@ __device__ __forceinline__ void join(const GemmParams &p, int64_t block)
 // A copy with whole 16-byte rows for operands whose rows are not: the products'
 // loads into LDS take 16 aligned bytes.  A streaming pass, 3.4 us for a layer
 // of 333 x 501 -> 259; the products it feeds take 11.
-// Two matrices in one launch, the second's rows behind the first's.
+// Two matrices in one launch, the second's rows behind the first's; a
+// workgroup takes every gridDim.x-th row.
 template <class T>
 __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, const PackParams second)
 {
-    const bool is_second = blockIdx.x >= first.rows;
-    const PackParams &p = is_second ? second : first;
-    const int64_t row = blockIdx.x - (is_second ? first.rows : 0);
-    const T *src = (const T *)p.src + row * p.ld;
-    T *dst = (T *)p.dst + row * p.pitch;
-    for (int64_t c = (int64_t)blockIdx.y * 2048 + threadIdx.x * 8; c < p.pitch; c += (int64_t)gridDim.y * 2048) {
-        float v[8];
-        load8(src + c, p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8, v);
-        store8(dst + c, p.pitch - c < 8 ? (int)(p.pitch - c) : 8, v);
+    for (int64_t at = blockIdx.x; at < first.rows + second.rows; at += gridDim.x) {
+        const bool is_second = at >= first.rows;
+        const PackParams &p = is_second ? second : first;
+        const int64_t row = at - (is_second ? first.rows : 0);
+        const T *src = (const T *)p.src + row * p.ld;
+        T *dst = (T *)p.dst + row * p.pitch;
+        for (int64_t c = (int64_t)blockIdx.y * 2048 + threadIdx.x * 8; c < p.pitch; c += (int64_t)gridDim.y * 2048) {
+            float v[8];
+            load8(src + c, p.cols - c < 8 ? (p.cols - c < 0 ? 0 : (int)(p.cols - c)) : 8, v);
+            store8(dst + c, p.pitch - c < 8 ? (int)(p.pitch - c) : 8, v);
+        }
     }
 }
 
@@ -1049,7 +1052,9 @@ hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t 
 hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st)
 {
     const int64_t pitch = a.pitch > b.pitch ? a.pitch : b.pitch;
-    const dim3 grid((unsigned)(a.rows + b.rows), (unsigned)((pitch + 2047) / 2048 < 64 ? (pitch + 2047) / 2048 : 64));
+    const int64_t rows = a.rows + b.rows;
+    const dim3 grid((unsigned)(rows < (1 << 20) ? rows : 1 << 20),  // a grid holds 2^32 lanes along x
+                    (unsigned)((pitch + 2047) / 2048 < 64 ? (pitch + 2047) / 2048 : 64));
     if (dt == RAR_BF16)
         rar_pack_rows<bf16><<<grid, 256, 0, st>>>(a, b);
     else

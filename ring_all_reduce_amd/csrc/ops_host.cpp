@@ -25,7 +25,7 @@ constexpr int64_t kMaxWidth = int64_t(1) << 20;   // K, N, D
 constexpr int64_t kMaxLd = int64_t(1) << 22;      // offsets inside a 256-row tile stay under 2^31 bytes
 constexpr int64_t kMaxRows = int64_t(1) << 24;    // T
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxLanes = (int64_t(1) << 32) - 1;  // of a grid, along x
 
 int esize(rar_dtype d) { return d == RAR_BF16 ? 2 : 4; }
 bool valid_dtype(int d) { return d == RAR_F32 || d == RAR_BF16; }
@@ -232,7 +232,7 @@ bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
     p.pitch = s.pitch;
     p.part = part;
     *tile = s.tile;
-    return s.tiles_m * s.tiles_n * s.splits <= kMaxBlocks / 2;
+    return s.tiles_m * s.tiles_n * s.splits <= kMaxLanes / 512 / 2;  // two products may share a launch
 }
 
 // The product as its launch sees it: partial sums where the reduction is split.
@@ -276,7 +276,7 @@ extern "C" rar_status rar_embed_lookup(int64_t V, int64_t D, rar_dtype dtype, co
     const int es = esize(dtype);
     if (!aligned(table, es) || !aligned(out, es) || !aligned(ids, 8))
         return RAR_EALIGN;
-    if (!apart({{out, T, D, ldo, es}}, {{table, V, D, D, es}, {ids, 1, T, T, 8}}) || div_up(T * D, 1024) > kMaxBlocks)
+    if (!apart({{out, T, D, ldo, es}}, {{table, V, D, D, es}, {ids, 1, T, T, 8}}))
         return RAR_EINVAL;
     rar::EmbedParams p{table, ids, out, T, V, D, ldo, scale};
     return launched(rar::launch_embed_lookup(dtype, p, static_cast<hipStream_t>(stream)));
@@ -302,7 +302,7 @@ extern "C" rar_status rar_embed_grad(int64_t V, int64_t D, rar_dtype dtype, int6
     if (!aligned(grad, es) || !aligned(dy, es) || !aligned(ids, 8) || !aligned(ws, 16))
         return RAR_EALIGN;
     const int64_t need = rar::embed_grad_workspace(T, V, D);
-    if (ws_bytes < need || div_up(T, 8) * div_up(D, 512) > kMaxBlocks || V * D * es / 65536 > kMaxBlocks)
+    if (ws_bytes < need || !rar::embed_grad_fits(T, D, V * D * es, kMaxLanes))
         return RAR_EINVAL;
     if (!apart({{grad, V, D, D, es}, {ws, 1, need, need, 1}}, {{dy, T, D, lddy, es}, {ids, 1, T, T, 8}}))
         return RAR_EINVAL;
@@ -594,6 +594,8 @@ rar_status check_ckpt(int64_t T, int64_t D, rar_dtype dt, const void *m, int64_t
     if (!aligned(m, es) || !aligned(codes, 16))
         return RAR_EALIGN;
     const int64_t g = groups_of(D) * T, c = g * rar::kCkptGroup;
+    if (g > kMaxLanes - 256)  // four lanes move four groups each
+        return RAR_EINVAL;
     const Mat mm{m, T, D, ld, es}, mc{codes, 1, c, c, 1}, ms{scales, 1, g, g, 1};
     if (store ? !apart({mc, ms}, {mm}) : !apart({mm}, {mc, ms}))
         return RAR_EINVAL;

@@ -139,5 +139,7 @@ hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t s
 hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t st);
 // Bytes of workspace rar_embed_grad needs.
 int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D);
+// Whether each of its launches has at most `lanes` lanes.
+bool embed_grad_fits(int64_t T, int64_t D, int64_t grad_bytes, int64_t lanes);
 
 }  // namespace rar

@@ -418,6 +418,86 @@ def test_embedding_offsets_past_32_bits():
 
 
 # ---------------------------------------------------------------------------
+# Largest sizes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_linear_most_rows(dtype):
+    """2^24 rows that have to be packed.  Small integers: every sum is exact
+    (|dw|, |db| <= 2^24) until its one rounding, so the results are compared
+    with equality."""
+    T, K, N = 1 << 24, 5, 3
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x, w, dy = (torch.randint(-1, 2, s, device=DEV, generator=g, dtype=torch.int32) for s in ((T, K), (K, N), (T, N)))
+    xf, wf, dyf = (t.to(R.DT[dtype]) for t in (x, w, dy))
+    plan = api.rar_linear_plan(K, N, CODE[dtype])
+    y, dx = nan_like(T, N, dtype=dtype), nan_like(T, K, dtype=dtype)
+    dw, db = nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)
+    api.rar_linear_forward(plan, T, xf, wf, None, None, y)
+    api.rar_linear_backward(plan, T, dyf, xf, wf, None, dx, dw, db)
+    for k in range(K):
+        assert torch.equal(dx[:, k], (dy * w[k]).sum(1).to(dx.dtype))
+        assert torch.equal(dw[k], (x[:, k:k + 1] * dy).sum(0).float().to(dw.dtype))
+    for n in range(N):
+        assert torch.equal(y[:, n], (x * w[:, n]).sum(1).to(y.dtype))
+    assert torch.equal(db, dy.sum(0).float().to(db.dtype))
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_linear_widest_rows(dtype):
+    """Rows 2^22 elements apart, the most a call takes: offsets pass 2^31 bytes
+    inside a tile's operand and 2^32 bytes behind it."""
+    T, K, N, ld = 530, 40, 24, 1 << 22
+    g = torch.Generator().manual_seed(6)
+    big = torch.full((T * ld,), float("nan"), dtype=R.DT[dtype], device=DEV).view(T, ld)
+    x, dy = rand(g, T, K, dtype=dtype), rand(g, T, N, dtype=dtype)
+    w = rand(g, K, N, dtype=dtype, scale=K ** -0.5)
+    plan = api.rar_linear_plan(K, N, CODE[dtype])
+    vx, vdy, y, dx = big[:, 64:64 + K], big[:, ld - 128:ld - 128 + N], big[:, 256:256 + N], big[:, 320:320 + K]
+    vx.copy_(x.to(DEV))
+    vdy.copy_(dy.to(DEV))
+    dw, db = nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)
+    api.rar_linear_forward(plan, T, vx, w.to(DEV), None, None, y)
+    api.rar_linear_backward(plan, T, vdy, vx, w.to(DEV), None, dx, dw, db)
+    (ry, ey), _ = R.forward(x, w, None, None, "none", dtype)
+    R.check(y, ry, ey, "y")
+    packed = [nan_like(T, K, dtype=dtype), nan_like(K, N, dtype=dtype), nan_like(N, dtype=dtype)]
+    api.rar_linear_backward(plan, T, dy.to(DEV), x.to(DEV), w.to(DEV), None, *packed)
+    for got, want in zip((dx, dw, db), packed):
+        assert torch.equal(got, want)
+    assert torch.isnan(big[:, 256 + N:320]).all() and torch.isnan(big[:, 320 + K:512]).all()
+
+
+def test_lookup_of_more_elements_than_one_launch():
+    T, D, V = 1 << 24, 1025, 7
+    ids = torch.arange(T, device=DEV) % V
+    table = torch.randn(V, D, device=DEV).bfloat16()
+    out = torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+    out[-9:] = float("nan")
+    api.rar_embed_lookup(V, D, api.BF16, table, T, ids, out)
+    at = torch.cat([torch.arange(0, T, 65537), torch.arange((1 << 33) // D - 5, (1 << 33) // D + 5),
+                    torch.arange(T - 9, T)]).to(DEV)
+    assert torch.equal(out[at], table[ids[at]])
+
+
+def test_ckpt_offsets_past_32_bits():
+    T, D = 4_200_000, 1025
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)
+    x[-100:] = torch.randn(100, D, device=DEV).bfloat16()
+    pitch, groups = api.rar_ckpt_size(D)
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    codes, scales = torch.empty(T, pitch, **u8), torch.empty(T, groups, **u8)
+    api.rar_ckpt_store(T, D, api.BF16, x, codes, scales)
+    c2, s2 = torch.empty(100, pitch, **u8), torch.empty(100, groups, **u8)
+    api.rar_ckpt_store(100, D, api.BF16, x[-100:], c2, s2)
+    assert torch.equal(codes[-100:, :D], c2[:, :D]) and torch.equal(scales[-100:], s2)
+    y2 = torch.empty(100, D, dtype=torch.bfloat16, device=DEV)
+    api.rar_ckpt_load(100, D, api.BF16, c2, s2, y2)
+    api.rar_ckpt_load(T, D, api.BF16, codes, scales, x, api.ACT_RELU)
+    assert torch.equal(x[-100:], y2.clamp_min(0)) and not x[:-100].any()
+
+
+# ---------------------------------------------------------------------------
 # Streams, graphs, repeatability
 # ---------------------------------------------------------------------------
 

@@ -129,7 +129,8 @@ def test_embed_refuses():
 
     for kw in (dict(V=0), dict(D=0), dict(dt=3), dict(T=-1), dict(lddy=7), dict(ids=None), dict(dy=None), dict(g=None),
                dict(ws=None), dict(nb=need - 1), dict(g=A[0]), dict(g=A[1]), dict(g=WS), dict(ws=A[0]),
-               dict(V=1 << 30, D=1 << 20, nb=1 << 62)):
+               dict(V=1 << 30, D=1 << 20, nb=1 << 62),
+               dict(T=1 << 24, D=1 << 20, lddy=1 << 20, nb=1 << 62)):
         assert grad(**kw) == api.EINVAL, kw
     for kw in (dict(ids=A[1] + 4), dict(dy=A[0] + 2), dict(g=A[2] + 2), dict(ws=WS + 8)):
         assert grad(**kw) == api.EALIGN, kw
