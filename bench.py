@@ -674,7 +674,7 @@ def secondary_rows(dev, stream, reps=5):
     return rows
 
 
-def backward_row(wl, b, specs, infos, arenas, dev, stream, T=128, reps=2):
+def backward_row(wl, b, specs, infos, arenas, dev, stream, T=128, reps=4):
     """The overlapped all-reduce behind a real producer: every rank's backward
     pass through the Transformer's linear layers (rar_linear_backward) and its
     embedding (rar_embed_grad), T tokens a rank, writing each gradient into the
