@@ -480,6 +480,20 @@ def test_lookup_of_more_elements_than_one_launch():
     assert torch.equal(out[at], table[ids[at]])
 
 
+@pytest.mark.parametrize("V", [5, 70_000])
+def test_embed_grad_of_most_tokens(V):
+    """2^24 tokens, some of them padding.  Small integers: every sum is exact."""
+    T, D = 1 << 24, 2
+    g = torch.Generator(device=DEV).manual_seed(8)
+    ids = torch.randint(-1, V + 1, (T,), device=DEV, generator=g)
+    dy = torch.randint(-1, 2, (T, D), device=DEV, generator=g)
+    grad = nan_like(V, D, dtype="f32")
+    api.rar_embed_grad(V, D, api.F32, T, ids, dy.float(), grad)
+    ok = (ids >= 0) & (ids < V)
+    want = torch.zeros(V, D, dtype=torch.int64, device=DEV).index_add_(0, ids[ok], dy[ok])
+    assert torch.equal(grad, want.float())
+
+
 def test_ckpt_offsets_past_32_bits():
     T, D = 4_200_000, 1025
     x = torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)
