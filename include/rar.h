@@ -374,7 +374,8 @@ rar_status rar_bucket_allreduce_arena(rar_buckets_t b, int N, rar_chunking chunk
 /* W (in x out) with biases.                                               */
 /*                                                                         */
 /* Matrices are row-major with a leading dimension in elements (ld >= the  */
-/* row length, at most 2^22; K, N, D at most 2^20; T at most 2^24).        */
+/* row length, at most 2^22; K, N, D at most 2^20; T at most 2^24; of a     */
+/* linear layer T x K, T x N and K x N at most 2^37 elements).             */
 /* Matrices in the operator's type need element alignment only; rows of    */
 /* whole 16-byte groups at 16-byte aligned addresses are read directly,    */
 /* others are copied into the workspace first.  Outputs must not overlap   */

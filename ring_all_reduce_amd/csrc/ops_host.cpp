@@ -3,11 +3,11 @@
 // device work is enqueued before every argument has been checked, and nothing
 // is allocated on the device.
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 #include <initializer_list>
 #include <new>
 
+#include "linear_shape.h"
 #include "ops_internal.h"
 
 using rar::GemmParams;
@@ -25,15 +25,19 @@ constexpr int64_t kMaxWidth = int64_t(1) << 20;   // K, N, D
 constexpr int64_t kMaxLd = int64_t(1) << 22;      // offsets inside a 256-row tile stay under 2^31 bytes
 constexpr int64_t kMaxRows = int64_t(1) << 24;    // T
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
-constexpr int64_t kMaxLanes = (int64_t(1) << 32) - 1;  // of a grid, along x
 
-int esize(rar_dtype d) { return d == RAR_BF16 ? 2 : 4; }
+using rar::div_up;
+using rar::esize;
+using rar::kMaxLanes;
+using rar::most_blocks;
+using rar::Shape;
+using rar::shape_of;
+using rar::up;
+
 bool valid_dtype(int d) { return d == RAR_F32 || d == RAR_BF16; }
 bool valid_act(int a) { return a == RAR_ACT_NONE || a == RAR_ACT_RELU || a == RAR_ACT_GELU; }
 bool valid_rows(int64_t T) { return T >= 0 && T <= kMaxRows; }
 bool valid_width(int64_t n) { return n >= 1 && n <= kMaxWidth; }
-int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-int64_t div_up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
 rar_status launched(hipError_t e)
 {
@@ -89,71 +93,6 @@ bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
 
 // Rows that the products may read 16 bytes at a time.
 bool direct(const Mat &m) { return aligned(m.p, 16) && (m.ld * m.es) % 16 == 0 && (m.cols * m.es) % 16 == 0; }
-
-// ---------------------------------------------------------------------------
-// Shape of a product
-// ---------------------------------------------------------------------------
-
-struct Shape {
-    int tile;
-    int64_t tiles_m, tiles_n, splits, steps;
-    int64_t pitch;
-    int64_t part_bytes;
-};
-
-// Microseconds of a product at a shape, from a sweep of tiles and splits on
-// MI355X over 13 layers from 333 x 501 x 259 to 8192 x 2048 x 8192: the most
-// loaded compute unit runs `rounds` workgroups, whose steps take `step` each
-// when several share the unit and at least `alone` by themselves; a split
-// reduction also writes its partial sums, reads them and launches the join.
-// Both ends, bf16: 2048 x 4096 -> 4096 forward takes 62 us in 128-tiles and 94
-// in 256-tiles (256 of them would leave half the chip idle), its weight
-// gradient 66 and 54; binary32: 2048^3 takes 139 us in 128-tiles and 132 in
-// 64-tiles, 8192 x 2048 -> 2048 500 and 510.  128 x 2048 -> 2048 in bf16 takes
-// 15 us split in four and 23 unsplit; 2048 x 512 -> 512 10 unsplit, 15 in two.
-double cost(rar_dtype dt, const Shape &s)
-{
-    double step, alone, fixed;
-    if (dt == RAR_BF16) {
-        step = s.tile == 256 ? 1.45 : 0.445;
-        alone = s.tile == 256 ? 1.45 : 0.66;
-        fixed = s.tile == 256 ? 8 : 5;
-    } else {
-        step = s.tile == 128 ? 1.9 : 0.495;
-        alone = s.tile == 128 ? 2.12 : 0.72;
-        fixed = s.tile == 128 ? 5 : 3;
-    }
-    const double rounds = std::ceil((double)(s.tiles_m * s.tiles_n * s.splits) / 256);
-    const double t = std::max(rounds * step, alone) * (double)s.steps + fixed;
-    return s.splits > 1 ? t + 4 + 0.35e-6 * (double)s.part_bytes : t;
-}
-
-Shape shape_of(rar_dtype dt, int64_t M, int64_t N, int64_t K)
-{
-    const int64_t total = std::max<int64_t>(1, div_up(K * esize(dt), 128));
-    const int large = dt == RAR_BF16 ? 256 : 128;
-    Shape best{};
-    double least = 0;
-    for (int tile = large; tile >= large / 2; tile /= 2) {
-        Shape s{};
-        s.tile = tile;
-        s.tiles_m = div_up(M, tile);
-        s.tiles_n = div_up(N, tile);
-        s.pitch = up(N, rar::kCkptGroup);
-        const int64_t tiles = s.tiles_m * s.tiles_n;
-        for (int64_t want = 1; want <= 32 && (want == 1 || (total / want >= 2 && tiles * want <= 2048)); ++want) {
-            s.steps = div_up(total, want);
-            s.splits = div_up(total, s.steps);
-            s.part_bytes = s.splits > 1 ? s.splits * M * s.pitch * 4 : 0;
-            const double t = cost(dt, s);
-            if (best.tile == 0 || t < least) {
-                best = s;
-                least = t;
-            }
-        }
-    }
-    return best;
-}
 
 // Bytes of the workspace's parts, each a multiple of 256.
 struct Carve {
@@ -221,8 +160,15 @@ BackwardWs backward_ws(const Layer &l, void *ws)
     return b;
 }
 
-// Fills in the shape of a product; false if its grid is too large.
-bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
+// Whether the layer's matrices are within the documented size: every product of
+// such a layer has a tile whose grid fits a launch.
+bool valid_layer(int64_t T, int64_t K, int64_t N)
+{
+    return T * K <= rar::kMaxOutputs && T * N <= rar::kMaxOutputs && K * N <= rar::kMaxOutputs;
+}
+
+// Fills in the shape of a product.
+void shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
 {
     const Shape s = shape_of(dt, p.M, p.N, p.K);
     p.tiles_m = s.tiles_m;
@@ -232,7 +178,6 @@ bool shape_product(rar_dtype dt, GemmParams &p, float *part, int *tile)
     p.pitch = s.pitch;
     p.part = part;
     *tile = s.tile;
-    return s.tiles_m * s.tiles_n * s.splits <= kMaxLanes / 512 / 2;  // two products may share a launch
 }
 
 // The product as its launch sees it: partial sums where the reduction is split.
@@ -341,7 +286,7 @@ extern "C" rar_status rar_linear_destroy(rar_linear_t plan)
 extern "C" rar_status rar_linear_workspace(rar_linear_t plan, int64_t T, int64_t *forward_bytes,
                                            int64_t *backward_bytes)
 {
-    if (!plan || !valid_rows(T))
+    if (!plan || !valid_rows(T) || !valid_layer(T, plan->K, plan->N))
         return RAR_EINVAL;
     const Layer l{T, plan->K, plan->N, plan->dtype};
     if (forward_bytes)
@@ -356,7 +301,7 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
                                          void *pre, int64_t ldp, uint8_t *pre_scales, void *ws, int64_t ws_bytes,
                                          void *stream)
 {
-    if (!plan || !valid_rows(T))
+    if (!plan || !valid_rows(T) || !valid_layer(T, plan->K, plan->N))
         return RAR_EINVAL;
     if (T == 0)
         return RAR_OK;
@@ -409,8 +354,7 @@ extern "C" rar_status rar_linear_forward(rar_linear_t plan, int64_t T, const voi
     rar::PackParams kx{}, kw{};
     int tile;
     const bool px = needs_pack(mx, dt, f.x, &p.a, &p.lda, &kx), pw = needs_pack(mw, dt, f.w, &p.b, &p.ldb, &kw);
-    if (!shape_product(dt, p, f.part, &tile))
-        return RAR_EINVAL;
+    shape_product(dt, p, f.part, &tile);
     rar_status rc = px || pw ? launched(rar::launch_pack(dt, kx, kw, st)) : RAR_OK;
     if (rc == RAR_OK)
         rc = launched(rar::launch_forward(dt, launched_form(p), tile, st));
@@ -428,7 +372,7 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
                                           int64_t ldp, const uint8_t *pre_scales, void *dx, int64_t lddx, void *dw,
                                           void *db, int accumulate, void *ws, int64_t ws_bytes, void *stream)
 {
-    if (!plan || !valid_rows(T))
+    if (!plan || !valid_rows(T) || !valid_layer(T, plan->K, plan->N))
         return RAR_EINVAL;
     const int64_t K = plan->K, N = plan->N;
     const rar_dtype dt = plan->dtype;
@@ -483,8 +427,7 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
         gx.out = dx;
         gx.ldo = lddx;
         gx.mode = rar::kModeStore;
-        if (!shape_product(dt, gx, b.part_x, &tile_x))
-            return RAR_EINVAL;
+        shape_product(dt, gx, b.part_x, &tile_x);
     }
     if (dw) {
         if (x_scales) {
@@ -502,8 +445,7 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
         gw.ldo = N;
         gw.mode = rar::kModeStore;
         gw.accumulate = accumulate;
-        if (!shape_product(dt, gw, b.part_w, &tile_w))
-            return RAR_EINVAL;
+        shape_product(dt, gw, b.part_w, &tile_w);
     }
 
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -536,10 +478,11 @@ extern "C" rar_status rar_linear_backward(rar_linear_t plan, int64_t T, const vo
         d.act = plan->act;
         rc = launched(rar::launch_dz(dt, d, st));
     }
-    // the two products together where they take the same kernel
+    // the two products together where they take the same kernel and fit one grid
     rar::GemmPair pair{launched_form(gx), launched_form(gw), dx ? rar::blocks_of(gx) : 0};
     const unsigned w_blocks = dw ? rar::blocks_of(gw) : 0;
-    if (rc == RAR_OK && dx && dw && tile_x == tile_w) {
+    if (rc == RAR_OK && dx && dw && tile_x == tile_w &&
+        (int64_t)pair.x_blocks + w_blocks <= most_blocks(dt, tile_x)) {
         rc = launched(rar::launch_backward(dt, pair, w_blocks, tile_x, st));
     } else {
         if (rc == RAR_OK && dx)
