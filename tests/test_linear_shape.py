@@ -9,6 +9,7 @@ import subprocess
 import pytest
 import torch
 
+import ops_sizes as S
 from ring_all_reduce_amd import api
 from ring_all_reduce_amd._lib import lib
 
@@ -94,3 +95,18 @@ def test_layers_behind_the_limits_are_refused():
                                              a[5], None, 0, a[3], 1 << 60, None) == api.EINVAL
         if T > 1:
             api.rar_linear_workspace(plan, T - (1 << 23))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sizes_of_the_large_tiles(shape, dtype):
+    # the GPU tests of the large tiles reach them only as long as this holds
+    for (T, K, N), want in S.LINEAR[dtype].items():
+        got = tuple(shape(dtype, *p)[::3] for p in ((T, N, K), (T, K, N), (K, N, T)))
+        assert got == want, (T, K, N)
+    # every large kernel with one and with several splits, and a pair of different tiles
+    large = 256 if dtype == "bf16" else 128
+    forms = S.LINEAR[dtype].values()
+    assert {f[0][1] > 1 for f in forms if f[0][0] == large} == {False, True}
+    for k in (1, 2):
+        assert {f[k][1] > 1 for f in forms if f[k][0] == large} == {False, True}
+    assert {(f[1][0] == large, f[2][0] == large) for f in forms} == {(a, b) for a in (False, True) for b in (False, True)}
