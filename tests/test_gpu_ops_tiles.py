@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import ops_ref as R
-from ops_sizes import LINEAR
+from ops_sizes import EMBED_32, LINEAR
 from ring_all_reduce_amd import api
 
 pytestmark = pytest.mark.gpu
@@ -211,3 +211,49 @@ def test_large_calls_repeat_and_replay(shape, dtype):
         call() if rep == 1 else graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, first)), rep
+
+
+# ---------------------------------------------------------------------------
+# The embedding's gradient in chunks of 32 sorted positions
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("T,V,D", EMBED_32)
+def test_embed_grad_of_a_batch(T, V, D, dtype):
+    g = torch.Generator().manual_seed(T + V + D)
+    ids = torch.randint(0, V, (T,), generator=g)
+    ids[torch.rand(T, generator=g) < 0.5] = V // 2          # one frequent token: runs of whole groups of chunks
+    ids[torch.rand(T, generator=g) < 0.05] = -1             # padding
+    ids[3], ids[5], ids[6] = V, 2 ** 40, -2 ** 40           # outside
+    dy, g0 = (torch.randn(n, D, generator=g).to(R.DT[dtype]) for n in (T, V))
+    live = (ids >= 0) & (ids < V)
+    scale, first = 1.7, None
+    want, bound = R.embed_grad(V, ids, dy, scale, dtype)
+    want_acc, bound_acc = R.embed_grad(V, ids, dy, scale, dtype, g0)
+    for extra, offset in ((0, 0), (8, 8), (3, 1)):
+        d = torch.full((T + 1, D + extra), float("nan"), dtype=R.DT[dtype], device=DEV)[:T, offset:offset + D]
+        d.copy_(dy)
+        d[(~live).to(DEV)] = float("nan")                   # rows that no sum takes
+        grad = nan_like(V, D, dtype=dtype)
+        api.rar_embed_grad(V, D, CODE[dtype], T, ids.to(DEV), d, grad, scale)
+        R.check(grad, want, bound, f"stride {D + extra}")
+        first = grad if first is None else first
+        assert torch.equal(grad, first)                     # the order of the terms is the ids' alone
+        acc = g0.to(DEV)
+        api.rar_embed_grad(V, D, CODE[dtype], T, ids.to(DEV), d, acc, scale, accumulate=True)
+        R.check(acc, want_acc, bound_acc, f"stride {D + extra}, accumulated")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("lead", [0, 1, 31, 1000])
+def test_embed_grad_one_token_for_a_batch(lead, dtype):
+    # one run over all chunks, its start on and off the borders of chunks and of groups of chunks
+    T, V, D = 22001, 6, 1544
+    g = torch.Generator().manual_seed(lead)
+    dy = torch.randn(T, D, generator=g).to(R.DT[dtype])
+    ids = torch.full((T,), 4)
+    ids[:lead] = 1
+    grad = nan_like(V, D, dtype=dtype)
+    api.rar_embed_grad(V, D, CODE[dtype], T, ids.to(DEV), dy.to(DEV), grad)
+    want, bound = R.embed_grad(V, ids, dy, 1.0, dtype)
+    R.check(grad, want, bound, f"lead {lead}")

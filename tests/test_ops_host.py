@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import ops_ref as R
+import ops_sizes as S
 from ring_all_reduce_amd import api
 from ring_all_reduce_amd._lib import lib
 
@@ -204,3 +205,15 @@ def test_plain_checkpoint_definition():
     # half a step: 2^-4 of the value, or half the smallest step
     assert (abs(vals - v)[fine] <= (abs(v) * 2.0 ** -4 + s * 2.0 ** -10)[fine]).all()
     assert vals[0, 2] == -1 and vals[0, 0] != vals[0, 0] and vals[0, 1] != vals[0, 1]
+
+
+def test_sizes_of_embedding_chunks():
+    # The workspace holds two rows of partial sums a chunk and one a group of 32 chunks, beside the sort's lists (16
+    # bytes a token and 1024 a workgroup of 4096): chunks of 32 sorted positions need a quarter of what chunks of 8 do.
+    def chunk(T, V, D):
+        part = api.rar_embed_grad_workspace(V, D, T) - 16 * T - (T + 4095) // 4096 * 1024
+        return T * 2.03 * 4 * ((D + 511) // 512 * 512) / part
+
+    for T, V, D in S.EMBED_32:
+        assert (D + 511) // 512 > 1 and 30 < chunk(T, V, D) < 34
+    assert 7 < chunk(9000, 70000, 9) < 9
