@@ -117,20 +117,12 @@ unsigned blocks_of(const CkptParams &p)
 
 hipError_t launch_ckpt_store(rar_dtype dt, const CkptParams &p, hipStream_t st)
 {
-    if (dt == RAR_BF16)
-        rar_ckpt_store_rows<bf16><<<blocks_of(p), 256, 0, st>>>(p);
-    else
-        rar_ckpt_store_rows<float><<<blocks_of(p), 256, 0, st>>>(p);
-    return hipGetLastError();
+    return launch(dt == RAR_BF16 ? rar_ckpt_store_rows<bf16> : rar_ckpt_store_rows<float>, blocks_of(p), 256, st, p);
 }
 
 hipError_t launch_ckpt_load(rar_dtype dt, const CkptParams &p, hipStream_t st)
 {
-    if (dt == RAR_BF16)
-        rar_ckpt_load_rows<bf16><<<blocks_of(p), 256, 0, st>>>(p);
-    else
-        rar_ckpt_load_rows<float><<<blocks_of(p), 256, 0, st>>>(p);
-    return hipGetLastError();
+    return launch(dt == RAR_BF16 ? rar_ckpt_load_rows<bf16> : rar_ckpt_load_rows<float>, blocks_of(p), 256, st, p);
 }
 
 }  // namespace rar

@@ -622,17 +622,19 @@ Layout layout(int64_t T, int64_t D)
 }
 
 template <class T, bool VEC>
-void sums(const EmbedGradParams &p, const GradWs &w, hipStream_t st)
+hipError_t sums(const EmbedGradParams &p, const GradWs &w, hipStream_t st)
 {
     const int64_t strips = (p.D + kCols - 1) / kCols;
     const int64_t chunks = (p.T + w.chunk - 1) / w.chunk, longs = p.T / (kGroup * w.chunk);
     const auto grid = [strips](int64_t n) { return (unsigned)((n * strips + 3) / 4); };
+    hipError_t e = hipSuccess;
     if (chunks > 0)
-        rar_embed_chunks<T, VEC><<<grid(chunks), 256, 0, st>>>(p, w, (int)strips);
-    if (longs > 1)  // the first group has nothing on its left
-        rar_embed_long<<<grid(longs), 256, 0, st>>>(p, w, (int)strips);
-    if (chunks > 1)
-        rar_embed_join<T, VEC><<<grid(chunks - 1), 256, 0, st>>>(p, w, (int)strips);
+        e = launch(rar_embed_chunks<T, VEC>, grid(chunks), 256, st, p, w, (int)strips);
+    if (e == hipSuccess && longs > 1)  // the first group has nothing on its left
+        e = launch(rar_embed_long, grid(longs), 256, st, p, w, (int)strips);
+    if (e == hipSuccess && chunks > 1)
+        e = launch(rar_embed_join<T, VEC>, grid(chunks - 1), 256, st, p, w, (int)strips);
+    return e;
 }
 
 }  // namespace
@@ -658,13 +660,10 @@ hipError_t launch_embed_lookup(rar_dtype dt, const EmbedParams &p, hipStream_t s
         q.out = (char *)p.out + t * p.ldo * es;
         q.T = p.T - t < most ? p.T - t : most;
         const unsigned grid = (unsigned)((q.T * width + 1023) / 1024);
-        if (dt == RAR_BF16)
-            vec ? rar_embed_rows<bf16, true><<<grid, 256, 0, st>>>(q)
-                : rar_embed_rows<bf16, false><<<grid, 256, 0, st>>>(q);
-        else
-            vec ? rar_embed_rows<float, true><<<grid, 256, 0, st>>>(q)
-                : rar_embed_rows<float, false><<<grid, 256, 0, st>>>(q);
-        const hipError_t e = hipGetLastError();
+        void (*const kernel)(EmbedParams) = dt == RAR_BF16
+                                                ? (vec ? rar_embed_rows<bf16, true> : rar_embed_rows<bf16, false>)
+                                                : (vec ? rar_embed_rows<float, true> : rar_embed_rows<float, false>);
+        const hipError_t e = launch(kernel, grid, 256, st, q);
         if (e != hipSuccess)
             return e;
     }
@@ -696,38 +695,35 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
     };
     auto clear_blocks = [](const Clear &c) { return (unsigned)((c.bytes + kClearBytes - 1) / kClearBytes); };
     int last = 0;
+    hipError_t e = hipSuccess;
     if (p.T <= kSmallKeys) {
         const Clear c = next_clear();
-        const unsigned grid = 1 + clear_blocks(c);
-        if (p.T <= kSortKeys)
-            rar_sort_small<kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0],
-                                                                   c);
-        else
-            rar_sort_small<2 * kRounds><<<grid, kSortThreads, 0, st>>>(p.ids, (int)p.T, p.V, passes, bits, keys[0],
-                                                                       pos[0], c);
+        e = launch(p.T <= kSortKeys ? rar_sort_small<kRounds> : rar_sort_small<2 * kRounds>, 1 + clear_blocks(c),
+                   kSortThreads, st, p.ids, (int)p.T, p.V, passes, bits, keys[0], pos[0], c);
     } else {
         const unsigned blocks = (unsigned)((p.T + kSortKeys - 1) / kSortKeys);
         uint32_t *const hist = (uint32_t *)(ws + l.hist);
-        for (int pass = 0; pass < passes; ++pass) {
+        for (int pass = 0; pass < passes && e == hipSuccess; ++pass) {
             const int64_t *ids = pass == 0 ? p.ids : nullptr;
             const int from = (pass + 1) & 1, to = pass & 1;
             const Clear c0 = next_clear();
-            rar_sort_count<<<blocks + clear_blocks(c0), kSortThreads, 0, st>>>(ids, keys[from], p.T, p.V, bits * pass,
-                                                                              bits, hist, blocks, c0);
+            e = launch(rar_sort_count, blocks + clear_blocks(c0), kSortThreads, st, ids, keys[from], p.T, p.V,
+                       bits * pass, bits, hist, blocks, c0);
             const Clear c1 = next_clear();
-            rar_sort_place<<<blocks + clear_blocks(c1), kSortThreads, 0, st>>>(
-                ids, keys[from], pos[from], p.T, p.V, bits * pass, bits, hist, keys[to], pos[to], blocks, c1);
+            if (e == hipSuccess)
+                e = launch(rar_sort_place, blocks + clear_blocks(c1), kSortThreads, st, ids, keys[from], pos[from], p.T,
+                           p.V, bits * pass, bits, hist, keys[to], pos[to], blocks, c1);
             last = to;
         }
     }
     const GradWs w{keys[last], pos[last], (float *)(ws + l.from_left), (float *)(ws + l.to_right),
                    (float *)(ws + l.long_run), l.pitch, l.chunk};
+    if (e != hipSuccess)
+        return e;
     const bool vec = p.D % 8 == 0;
     if (dt == RAR_BF16)
-        vec ? sums<bf16, true>(p, w, st) : sums<bf16, false>(p, w, st);
-    else
-        vec ? sums<float, true>(p, w, st) : sums<float, false>(p, w, st);
-    return hipGetLastError();
+        return vec ? sums<bf16, true>(p, w, st) : sums<bf16, false>(p, w, st);
+    return vec ? sums<float, true>(p, w, st) : sums<float, false>(p, w, st);
 }
 
 }  // namespace rar

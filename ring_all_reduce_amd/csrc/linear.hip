@@ -1006,35 +1006,29 @@ hipError_t launch_forward(rar_dtype dt, const GemmParams &p, int tile, hipStream
 {
     const unsigned grid = blocks_of(p);
     if (dt == RAR_BF16)
-        tile == 256 ? rar_forward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p)
-                    : rar_forward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
-    else
-        tile == 128 ? rar_forward_f32<128><<<grid, 256, 0, st>>>(p) : rar_forward_f32<64><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+        return tile == 256 ? launch(rar_forward_bf16<256, 2, 4>, grid, 512, st, p)
+                           : launch(rar_forward_bf16<128, 2, 2>, grid, 256, st, p);
+    return launch(tile == 128 ? rar_forward_f32<128> : rar_forward_f32<64>, grid, 256, st, p);
 }
 
 hipError_t launch_backward(rar_dtype dt, const GemmPair &p, unsigned w_blocks, int tile, hipStream_t st)
 {
     const unsigned grid = p.x_blocks + w_blocks;
     if (dt == RAR_BF16)
-        tile == 256 ? rar_backward_bf16<256, 2, 4><<<grid, 512, 0, st>>>(p)
-                    : rar_backward_bf16<128, 2, 2><<<grid, 256, 0, st>>>(p);
-    else
-        tile == 128 ? rar_backward_f32<128><<<grid, 256, 0, st>>>(p) : rar_backward_f32<64><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+        return tile == 256 ? launch(rar_backward_bf16<256, 2, 4>, grid, 512, st, p)
+                           : launch(rar_backward_bf16<128, 2, 2>, grid, 256, st, p);
+    return launch(tile == 128 ? rar_backward_f32<128> : rar_backward_f32<64>, grid, 256, st, p);
 }
 
 namespace {
 
 template <class T, bool VEC>
-void run_gemv(const GemmParams &p, unsigned grid, hipStream_t st)
+hipError_t run_gemv(const GemmParams &p, unsigned grid, hipStream_t st)
 {
-    if (p.M == 1)
-        rar_gemv<T, 1, VEC><<<grid, 1024, 0, st>>>(p);
-    else if (p.M == 2)
-        rar_gemv<T, 2, VEC><<<grid, 1024, 0, st>>>(p);
-    else
-        rar_gemv<T, kGemvRows, VEC><<<grid, 1024, 0, st>>>(p);
+    return launch(p.M == 1   ? rar_gemv<T, 1, VEC>
+                  : p.M == 2 ? rar_gemv<T, 2, VEC>
+                             : rar_gemv<T, kGemvRows, VEC>,
+                  grid, 1024, st, p);
 }
 
 }  // namespace
@@ -1043,10 +1037,8 @@ hipError_t launch_gemv(rar_dtype dt, const GemmParams &p, bool vec, hipStream_t 
 {
     const unsigned grid = (unsigned)((p.N + kGemvCols - 1) / kGemvCols);
     if (dt == RAR_BF16)
-        vec ? run_gemv<bf16, true>(p, grid, st) : run_gemv<bf16, false>(p, grid, st);
-    else
-        vec ? run_gemv<float, true>(p, grid, st) : run_gemv<float, false>(p, grid, st);
-    return hipGetLastError();
+        return vec ? run_gemv<bf16, true>(p, grid, st) : run_gemv<bf16, false>(p, grid, st);
+    return vec ? run_gemv<float, true>(p, grid, st) : run_gemv<float, false>(p, grid, st);
 }
 
 hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, hipStream_t st)
@@ -1055,26 +1047,20 @@ hipError_t launch_pack(rar_dtype dt, const PackParams &a, const PackParams &b, h
     const int64_t rows = a.rows + b.rows;
     const dim3 grid((unsigned)(rows < (1 << 20) ? rows : 1 << 20),  // a grid holds 2^32 lanes along x
                     (unsigned)((pitch + 2047) / 2048 < 64 ? (pitch + 2047) / 2048 : 64));
-    if (dt == RAR_BF16)
-        rar_pack_rows<bf16><<<grid, 256, 0, st>>>(a, b);
-    else
-        rar_pack_rows<float><<<grid, 256, 0, st>>>(a, b);
-    return hipGetLastError();
+    return launch(dt == RAR_BF16 ? rar_pack_rows<bf16> : rar_pack_rows<float>, grid, 256, st, a, b);
 }
 
 namespace {
 
 template <class T>
-void run_dz(const DzParams &p, dim3 grid, hipStream_t st)
+hipError_t run_dz(const DzParams &p, dim3 grid, hipStream_t st)
 {
-    if (p.act == RAR_ACT_NONE)
-        rar_dz<T, RAR_ACT_NONE, kDzNone><<<grid, 256, 0, st>>>(p);
-    else if (p.act == RAR_ACT_RELU)
-        p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_RELU, kDzPre><<<grid, 256, 0, st>>>(p);
-    else
-        p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt><<<grid, 256, 0, st>>>(p)
-                     : rar_dz<T, RAR_ACT_GELU, kDzPre><<<grid, 256, 0, st>>>(p);
+    void (*kernel)(DzParams) = rar_dz<T, RAR_ACT_NONE, kDzNone>;
+    if (p.act == RAR_ACT_RELU)
+        kernel = p.pre_scales ? rar_dz<T, RAR_ACT_RELU, kDzCkpt> : rar_dz<T, RAR_ACT_RELU, kDzPre>;
+    else if (p.act == RAR_ACT_GELU)
+        kernel = p.pre_scales ? rar_dz<T, RAR_ACT_GELU, kDzCkpt> : rar_dz<T, RAR_ACT_GELU, kDzPre>;
+    return launch(kernel, grid, 256, st, p);
 }
 
 }  // namespace
@@ -1083,21 +1069,13 @@ hipError_t launch_dz(rar_dtype dt, const DzParams &p, hipStream_t st)
 {
     const int64_t width = p.dz && p.pitch > p.cols ? p.pitch : p.cols;
     const dim3 grid((unsigned)((width + 511) / 512), (unsigned)((p.rows + p.rows_per_chunk - 1) / p.rows_per_chunk));
-    if (dt == RAR_BF16)
-        run_dz<bf16>(p, grid, st);
-    else
-        run_dz<float>(p, grid, st);
-    return hipGetLastError();
+    return dt == RAR_BF16 ? run_dz<bf16>(p, grid, st) : run_dz<float>(p, grid, st);
 }
 
 hipError_t launch_finish(rar_dtype dt, const FinishParams &p, hipStream_t st)
 {
     const unsigned grid = p.a_blocks + p.b_blocks + (unsigned)((p.sum.cols + 63) / 64);
-    if (dt == RAR_BF16)
-        rar_finish<bf16><<<grid, 256, 0, st>>>(p);
-    else
-        rar_finish<float><<<grid, 256, 0, st>>>(p);
-    return hipGetLastError();
+    return launch(dt == RAR_BF16 ? rar_finish<bf16> : rar_finish<float>, grid, 256, st, p);
 }
 
 }  // namespace rar

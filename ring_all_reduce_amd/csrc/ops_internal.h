@@ -12,6 +12,21 @@ namespace rar {
 
 constexpr int kCkptGroup = RAR_CKPT_GROUP;
 
+// A kernel launch and its own status.  (After <<<>>> the status is HIP's last
+// error, which an earlier call of the caller's may have left there: this call
+// would take it for its own and end before its next launch.)
+template <class T>
+struct Same {
+    typedef T type;
+};
+
+template <class... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, unsigned lanes, hipStream_t st, typename Same<P>::type... a)
+{
+    void *args[] = {(void *)&a...};
+    return hipLaunchKernel((const void *)kernel, grid, dim3(lanes), args, 0, st);
+}
+
 // One matrix product D[m][n] = sum_k A(m,k) B(n,k).  An operand is stored either
 // with its reduction index contiguous (element (r,k) at r*ld + k) or with the
 // reduction index slow (at k*ld + r):

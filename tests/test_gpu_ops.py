@@ -1,6 +1,8 @@
 """The embedding, the linear layer and 8-bit checkpoints on the GPU, against
 plain 64-bit forms at the sizes, layouts and values where they can go wrong.
 Bounds count roundings (see ops_ref.py); nothing is fitted to results."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -767,3 +769,52 @@ def test_training_step_of_ranks(dtype, ckpt):
             R.check(got, want[k], bound[k] * (1 + R.U[dtype]) + R.U[dtype] * want[k].abs(), f"rank {r} tensor {k}")
             at += n
         assert torch.equal(arenas[r], arenas[0])
+
+
+# ---------------------------------------------------------------------------
+# An error that an earlier HIP call left
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_an_earlier_error_is_not_taken_for_the_calls_own(dtype):
+    """A HIP call of the caller's that the host refused (no such device) leaves
+    HIP's last error set: the calls after it run to their end and report their
+    own status."""
+    hip = ctypes.CDLL("libamdhip64.so")
+    g = torch.Generator().manual_seed(17)
+    T, K, N, V = 300, 60, 1001, 40
+    code, td = CODE[dtype], R.DT[dtype]
+    x, dy, w, b = (rand(g, *s, dtype=dtype).to(DEV) for s in ((T, K), (T, N), (K, N), (N,)))
+    table, dt = (rand(g, n, K, dtype=dtype).to(DEV) for n in (V, 9000))
+    ids = torch.randint(0, V, (9000,), generator=g).to(DEV)
+    plan = api.rar_linear_plan(K, N, code, api.ACT_GELU)
+    (xp, xg) = api.rar_ckpt_size(K)
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    ws = torch.empty(max(*api.rar_linear_workspace(plan, T), api.rar_embed_grad_workspace(V, K, 9000)), **u8)
+    outs = [torch.empty(*s, dtype=td, device=DEV) for s in
+            ((T, K), (V, K), (V, K), (T, N), (T, N), (2, N), (T, K), (K, N), (N,), (T, K))]
+    look, few, many, y, z, y2, dx, dw, db, back = outs
+    codes, scales = torch.empty(T, xp, **u8), torch.empty(T, xg, **u8)
+    calls = [lambda: api.rar_embed_lookup(V, K, code, table, T, ids[:T], look),
+             lambda: api.rar_embed_grad(V, K, code, T, ids[:T], dt[:T], few, ws=ws),
+             lambda: api.rar_embed_grad(V, K, code, 9000, ids, dt, many, ws=ws),
+             lambda: api.rar_linear_forward(plan, T, x, w, b, None, y, pre=z, ws=ws),
+             lambda: api.rar_linear_forward(plan, 2, x[:2], w, b, None, y2, ws=ws),
+             lambda: api.rar_linear_backward(plan, T, dy, x, w, z, dx, dw, db, ws=ws),
+             lambda: api.rar_ckpt_store(T, K, code, x, codes, scales),
+             lambda: api.rar_ckpt_load(T, K, code, codes, scales, back)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs + [codes, scales]]
+    for t in outs + [codes, scales]:
+        t.zero_()
+    torch.cuda.synchronize()
+    try:
+        for call in calls:
+            assert hip.hipSetDevice(1 << 20) != 0
+            call()
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, v) for t, v in zip(outs + [codes, scales], want))
