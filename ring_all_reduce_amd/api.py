@@ -411,17 +411,20 @@ def _here() -> int:
         if not torch.cuda.is_available():
             return -1
         torch.cuda.init()
-        _get_device = torch._C._cuda_getDevice
+        # the call behind current_device(), where torch has it
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return _get_device()
 
 
 def _on(stream) -> int:
-    """The call's stream; torch's current one costs a tenth of building its Stream object."""
+    """The call's stream; torch's current one, where torch has it, costs a tenth of building its Stream object."""
     if stream is None:
         dev = _here()
         if dev >= 0:
             import torch
-            return torch._C._cuda_getCurrentRawStream(dev)
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:
+                return raw(dev)
     return _stream(stream)
 
 

@@ -217,3 +217,23 @@ def test_sizes_of_embedding_chunks():
     for T, V, D in S.EMBED_32:
         assert (D + 511) // 512 > 1 and 30 < chunk(T, V, D) < 34
     assert 7 < chunk(9000, 70000, 9) < 9
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_device_and_stream_by_public_calls_alone(monkeypatch, private):
+    # the binding asks torch's internal calls for the current device and stream, and the public ones where a torch
+    # lacks those
+    class Stream:
+        cuda_stream = 0x1230
+
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    for name, value in (("_cuda_getDevice", lambda: 3), ("_cuda_getCurrentRawStream", lambda dev: 0x1230 + dev - 3)):
+        if private:
+            monkeypatch.setattr(torch._C, name, value, raising=False)
+        else:
+            monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(api, "_get_device", None)
+    assert api._here() == 3 and api._on(None) == 0x1230 and api._on(Stream) == 0x1230 and api._on(7) == 7
