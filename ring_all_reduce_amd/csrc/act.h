@@ -147,12 +147,14 @@ __device__ __forceinline__ void store8(bf16 *p, int cnt, const float (&v)[8])
 //   1 - Phi(a) = exp(-a^2 / 2) * q(a / sqrt 2) / 2,  q(x) = exp(x^2) erfc(x).
 // q is smooth and falls like 1/x, so q/2 is a polynomial in t = 1 / (1 + c x)
 // without a constant term.  The coefficients are least-maximum fits made for
-// this file: degree 8 for binary32 (relative error 9.4e-8 for 0 <= x <= 10;
-// beyond that exp(-x^2) < 2^-144), degree 6 for bf16 (5.2e-6, a hundredth of
-// its half step).  The relative error stays small in the far tail, where
-// 1 + erf(z / sqrt 2) would cancel.  About 17 instructions, two of them
-// transcendental, against about 60 for erfcf: the epilogue of a matrix product
-// evaluates it with the matrix cores idle.
+// this file.  Relative error of q for 0 <= x <= 10, as the constants below are
+// rounded (beyond that exp(-x^2) < 2^-144): degree 8 for binary32, 1.02e-7;
+// degree 6 for bf16, 5.2e-6, a seven-hundredth of its half step.  The
+// exponential's argument is rounded twice, which adds z^2 * 2^-24 to the
+// relative error of the tail: 4e-6 at |z| = 8, where 1 + erf(z / sqrt 2) has no
+// digit left in binary32.  About 17 instructions, two of them transcendental,
+// against about 60 for erfcf: the epilogue of a matrix product evaluates it with
+// the matrix cores idle.
 template <class T>
 __device__ __forceinline__ void normal_tail(float z, float &q, float &e)
 {

@@ -2,7 +2,10 @@
 a GPU: every call here is refused before it would reach a kernel, or has no
 rows to work on."""
 import ctypes
+import pathlib
+import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -237,3 +240,39 @@ def test_current_device_and_stream_by_public_calls_alone(monkeypatch, private):
             monkeypatch.delattr(torch._C, name, raising=False)
     monkeypatch.setattr(api, "_get_device", None)
     assert api._here() == 3 and api._on(None) == 0x1230 and api._on(Stream) == 0x1230 and api._on(7) == 7
+
+
+@pytest.mark.parametrize("dtype,degree,fit", [("f32", 8, 1.02e-7), ("bf16", 6, 5.2e-6)])
+def test_normal_tail_is_as_good_as_its_comment_says(dtype, degree, fit):
+    # the polynomial of act.h, its constants rounded as there, against exp(x^2) erfc(x) in 64 bits
+    src = (pathlib.Path(R.__file__).parents[1] / "ring_all_reduce_amd" / "csrc" / "act.h").read_text()
+    assert f"{fit:.3g}".replace("e-0", "e-") in src
+    body = src[src.index("void normal_tail"):]
+    c = np.float32(np.float32(re.search(r"kWide \? 0\.33f : 0\.44f\) \* (0\.70710678118654752)f", body)[1]) *
+                   np.float32(0.33 if dtype == "f32" else 0.44))
+    half = body[:body.index("} else {")] if dtype == "f32" else body[body.index("} else {"):body.index("q *= t")]
+    coeff = [np.float32(0.5) * np.float32(v) for v in re.findall(r"0\.5f \* (-?[0-9.]+)f", half)]
+    assert len(coeff) == degree
+
+    def tail(z):
+        t = 1 / (1 + float(c) * z)
+        q = torch.zeros_like(t)
+        for a in coeff:
+            q = q * t + float(a)
+        return q * t
+
+    x = torch.linspace(0, 10, 400001, dtype=torch.float64)
+    rel = (tail(x * 2 ** 0.5) / (torch.special.erfcx(x) / 2) - 1).abs().max().item()
+    assert rel < fit * 1.005
+    # with the exponential's argument as binary32 rounds it: z^2 * 2^-24 more
+    z = (x * 2 ** 0.5).float()[(x > 0) & (x < 9.3)]
+    e = torch.exp2((z * (z * torch.tensor(-0.72134752044448170, dtype=torch.float32))).double())
+    z = z.double()
+    want = torch.special.erfc(z / 2 ** 0.5) / 2
+    assert ((tail(z) * e - want).abs() <= (fit * 1.05 + z * z * 2.0 ** -24) * want).all()
+    # what the header promises of gelu (|z| times the tail) and its derivative (the tail and |z| times the density)
+    off = (tail(z) * e - want).abs()
+    dens = (e - torch.exp(-z * z / 2)).abs() * (2 * np.pi) ** -0.5
+    assert (torch.maximum(z * off, off + z * dens) <= 2.0 ** (-20 if dtype == "f32" else -18) * (1 + z)).all()
+    if dtype == "bf16":
+        assert fit * 700 < R.U["bf16"]
