@@ -374,14 +374,14 @@ rar_status rar_bucket_allreduce_arena(rar_buckets_t b, int N, rar_chunking chunk
 /* W (in x out) with biases.                                               */
 /*                                                                         */
 /* Matrices are row-major with a leading dimension in elements (ld >= the  */
-/* row length, at most 2^22; K, N, D at most 2^20; T at most 2^24; of a     */
+/* row length, at most 2^22; K, N, D at most 2^20; T at most 2^24; of a    */
 /* linear layer T x K, T x N and K x N at most 2^37 elements).             */
-/* Matrices in the operator's type need element alignment only; rows of    */
-/* whole 16-byte groups at 16-byte aligned addresses are read directly,    */
-/* others are copied into the workspace first.  Outputs must not overlap   */
-/* inputs or each other, unless a call says so (RAR_EINVAL); two views of  */
-/* one leading dimension with disjoint columns do not overlap.  Device     */
-/* buffers belong to the current device.                                   */
+/* Matrices in the operator's type need element alignment only; a linear   */
+/* layer's products read rows of whole 16-byte groups at 16-byte aligned   */
+/* addresses directly and copy others into the workspace first, in every   */
+/* call.  Outputs must not overlap inputs or each other, unless a call     */
+/* says so (RAR_EINVAL); two views of one leading dimension with disjoint  */
+/* columns do not overlap.  Device buffers belong to the current device.   */
 /*                                                                         */
 /* Workspaces are the caller's: `ws` is device memory, 16-byte aligned, of */
 /* at least the bytes the matching query gives (RAR_EINVAL otherwise); it  */
@@ -435,8 +435,9 @@ rar_status rar_linear_plan(int64_t K, int64_t N, rar_dtype dtype, rar_act act, r
 
 rar_status rar_linear_destroy(rar_linear_t plan);
 
-/* Workspaces of a forward and of a backward call on T rows.  Either output
- * may be NULL. */
+/* Workspaces of a forward and of a backward call on T rows, for matrices at any
+ * address and of any leading dimension: copies of x and w are counted also
+ * where a call reads them directly.  Either output may be NULL. */
 rar_status rar_linear_workspace(rar_linear_t plan, int64_t T, int64_t *forward_bytes, int64_t *backward_bytes);
 
 /* z = x W + bias, y = act(z) + residual.  x is T x K, w K x N contiguous, bias

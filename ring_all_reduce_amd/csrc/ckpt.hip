@@ -11,8 +11,9 @@
 // Both directions are streaming passes bound by HBM bandwidth: four lanes share
 // a group, a lane moves eight values (16 bytes of bf16), and the group's
 // maximum takes two lane exchanges.  8192 x 8192 in bf16: store 36 us (5.7
-// TB/s); load with gelu 47 us, bound by the activation's arithmetic; 8192 x
-// 2048 without an activation 11 us (4.7 TB/s).
+// TB/s); load with gelu 47 us, bound by the activation's arithmetic (its waves
+// wait 25% of their cycles, the store's 60%); 8192 x 2048 without an activation 11
+// us (4.6 TB/s).
 #include "act.h"
 #include "ops_internal.h"
 

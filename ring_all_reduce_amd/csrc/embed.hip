@@ -1,9 +1,13 @@
 // embed.hip -- CDNA4 (gfx950) kernels of the embedding: lookup with scaling, and
 // its gradient by sorted tokens.
 //
-// Lookup: out[t] = scale * table[ids[t]], a gather bound by HBM bandwidth; out is
-// written past the caches (65536 rows of 2048 bf16: 58 us, 6.8 TB/s; with
-// ordinary stores 85).
+// Lookup: out[t] = scale * table[ids[t]], a gather bound by HBM bandwidth: 65536
+// rows of 2048 bf16, 59 us for 131 MB of distinct rows and 268 MB of out (6.8
+// TB/s).  out is written past the caches, which pays for large calls and costs
+// the reader of small ones up to 3%.  Lookup alone and with the 2048 -> 2048
+// product that reads out, in brackets with ordinary stores: 65536 rows 59 and
+// 523 us (82 and 542), 4096 rows 5.6 and 51 (6.7 and 49), 512 rows 4.0 and 29.4
+// (4.3 and 28.7).
 //
 // Gradient: grad[v] = scale * sum of dy[t] over the t with ids[t] == v, dense
 // (every row of the vocabulary is written) or accumulated into the rows that
@@ -18,9 +22,9 @@
 //
 // Bound: dy read once, grad written once; the sort moves 16 bytes a token, and
 // its launches also clear the gradient.  65536 tokens of 2048 bf16 columns into
-// 32000 rows: 121 us, of them the sort with the clearing 39, the chunks 66 (200
-// MB at 3 TB/s: the rows of dy are read in the order of their ids, 4 KB here and
-// there), the joins 16.
+// 32000 rows: 121 us, of them the sort with the clearing 39 (16 workgroups of
+// 4096 keys, two passes), the chunks 68 (268 MB of dy read, 72 MB of finished and
+// partial rows written, 5.0 TB/s together), the joins 16.
 #include "act.h"
 #include "ops_internal.h"
 
@@ -83,7 +87,11 @@ constexpr int kSortThreads = 1024;                      // sixteen waves
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRounds = 4;                              // keys of a lane
 constexpr int kSortKeys = kRounds * kSortThreads;       // keys of a workgroup
-constexpr int kSmallKeys = 2 * kSortKeys;               // batches that one workgroup sorts
+// Batches that one workgroup sorts.  The whole call with one workgroup and with
+// one for every 4096 keys: 2000 tokens of 509 binary32 columns 20 and 29 us, 4096
+// 27 and 36, 8192 38 and 42; 8192 of 2048 bf16 columns 51 and 60.  Up to 1024 they
+// take the same; more than 8192 in one were not measured.
+constexpr int kSmallKeys = 2 * kSortKeys;
 constexpr int kGroup = 32;                              // chunks of a long run that are added beforehand
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V)
@@ -254,7 +262,10 @@ __global__ void __launch_bounds__(kSortThreads) rar_sort_small(const int64_t *id
     }
 }
 
-// Larger batches: digit counts of each kSortKeys tokens, then their placement.
+// Larger batches: digit counts of each kSortKeys tokens, then their placement,
+// for which every workgroup adds up all workgroups' counts.  That is a read of
+// 16 KB a workgroup at 65536 tokens and of 4 MB at 2^24: a placement takes 11 us at
+// 2^16 tokens, 31 at 2^20 and 2.2 ms at 2^24, where it is most of the call.
 __global__ void __launch_bounds__(kSortThreads) rar_sort_count(const int64_t *ids, const uint32_t *keys, int64_t T,
                                                                int64_t V, int shift, int bits, uint32_t *hist,
                                                                unsigned blocks, Clear c)
@@ -609,9 +620,12 @@ Layout layout(int64_t T, int64_t D)
     }
     l.hist = take(small ? 0 : (T + kSortKeys - 1) / kSortKeys * 1024);
     // A wave sums 32 sorted positions, or 8 where 32 would leave most of the chip
-    // without a wave: 4097 positions of 509 binary32 columns take 30 us in chunks
-    // of 8 and 34 in chunks of 32, 65536 of 2048 bf16 columns 139 and 123 (the
-    // whole call).
+    // without a wave.  The whole call in chunks of 8 and of 32, by positions times
+    // strips: 4097 (509 binary32 columns) 29 and 36 us, 8192 (bf16) 36 and 37 to
+    // 37 and 42, 16384 (either type) 45 and 45 to 54 and 53, 32768 55 and 48 (bf16)
+    // to 94 and 80 (binary32), 65536 68 and 60 to 118 and 107, 262144 139 and 124.
+    // The two cross near 16384; between there and the border chunks of 8 cost up to
+    // 16%.
     l.chunk = T <= 32 || T * (l.pitch / kCols) >= 65536 ? 32 : 8;  // up to 32 need no join
     const int64_t chunks = T > l.chunk ? (T + l.chunk - 1) / l.chunk : 0;
     l.from_left = take(chunks * l.pitch * 4);

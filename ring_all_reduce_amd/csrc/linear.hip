@@ -288,8 +288,13 @@ __device__ __forceinline__ void tile_row(RAR_LDS char *tile, int r, int q, float
 }
 
 // The usual tile: wholly inside the matrix, z kept in the layer's type or not at
-// all.  The same results as epilogue(),
-// with the addresses and the bias out of the loop.
+// all.  The same results as epilogue(), with the addresses and the bias out of
+// the loop.  Rows are written past the caches.  Forward and backward of two bf16
+// layers, 2048 -> 8192 with gelu and back, with such stores and with ordinary
+// ones: 8192 rows 1342 and 1364 us, 512 rows 165 and 172, 128 rows 105 and 107;
+// the first layer's forward call and then the second's, which reads it: 453 and
+// 473, 62 and 63, 42.6 and 42.4.  Rows that start off the 128-byte lines lose by
+// it: 7178 x 177 -> 2023 takes 45 and 37 in bf16, 115 and 76 in binary32.
 template <class T, int W, int ROWS, int ACT>
 __device__ __forceinline__ void finish_inside(const GemmParams &p, RAR_LDS char *tile, int64_t m0, int64_t n0)
 {
@@ -424,14 +429,16 @@ __device__ __forceinline__ void product(f32x4 &acc, bf16x8 b, bf16x8 a)
 // Fragments of A are replaced in place once their row of products is issued;
 // those of B need two sets.  Bound: the matrix cores, 68% busy in the backward
 // products and 51% in the forward one with its epilogue, at 256 x 256 and the
-// 2.0 GHz that the clock falls to under them.  Eight waves rather than four: two
+// 1.9 to 2.0 GHz that the clock falls to under them.  Eight waves rather than four: two
 // waves a SIMD cover each other's meeting and address work, and the epilogue's
 // arithmetic.  A ring of five smaller buffers with loads further ahead measured
 // the same; 32 x 32 x 16 instructions 3 to 5% slower, their reads of 32 rows
-// meeting in the same banks.  Measured at 8192 rows, 2048 -> 8192: both backward products in
-// one launch 393 us (1.40 PFLOP/s), the forward product with gelu and z kept
-// 256 us (1.07 PFLOP/s, about 50 us of it the epilogue).  128 x 128 tiles for
-// products with few tiles: 2048 x 4096 -> 4096 62 us (1.1 PFLOP/s).
+// meeting in the same banks.  Measured at 8192 rows, 2048 -> 8192, under a
+// profiler (median of 30 passes, and the least): both backward products in one
+// launch 412 us (389; 1.33 PFLOP/s), the forward product with gelu and z kept 284
+// (253; 0.97 PFLOP/s).  The forward call timed without it takes 250 (1.10
+// PFLOP/s), about 50 of it the epilogue.  128 x 128 tiles for products with few
+// tiles: 2048 x 4096 -> 4096 62 us (1.1 PFLOP/s).
 template <int BM, int BN, int WM, int WN, bool ACONTIG, bool BCONTIG>
 __device__ __forceinline__ void gemm_bf16(const GemmParams &p, int64_t block, RAR_LDS char *const lds)
 {
@@ -728,8 +735,14 @@ __global__ void __launch_bounds__(256, B == 128 ? 2 : 4) rar_backward_f32(const 
 // kGemvK consecutive k of its columns and the same k of x in one vector each.
 // Partial sums are joined by lane exchanges and through LDS, in an order fixed
 // by the sizes; nothing passes through memory.
-// 2048 -> 8192 in bf16: 11 us, 3.1 TB/s, bound by latency; the tiled product and
-// its join take 18.
+// 2048 -> 8192 in bf16, one row: 11 us, 3.1 TB/s, with 128 workgroups on the 256
+// units and the waves waiting 54% of their cycles; 8.5 where W is left in the
+// Infinity Cache, as for the figures that follow.  This kernel and the tiled
+// product with its join, for 1, 2 and 4 rows: 2048 -> 8192 bf16 8.5, 10 and 14
+// against 15 us, binary32 14.6, 15.2 and 16.7 against 27; 2048 -> 2048 bf16 7.5,
+// 8.8 and 12.5 against 12 to 13.5; 512 -> 512 bf16 5.5, 6.8 and 9.4 against 14.
+// Eight rows in one pass took 13 to 45, more than the tiles.  Deep narrow layers
+// would do better in tiles: 8192 -> 2048 bf16 20.5, 23 and 28 against 20 to 23.
 constexpr int kGemvCols = 64, kGemvK = 8;  // 32 columns a workgroup measured the same
 
 template <class T, int E>
@@ -854,7 +867,7 @@ __device__ __forceinline__ void join(const GemmParams &p, int64_t block)
 
 // A copy with whole 16-byte rows for operands whose rows are not: the products'
 // loads into LDS take 16 aligned bytes.  A streaming pass, 3.4 us for a layer
-// of 333 x 501 -> 259; the products it feeds take 11.
+// of 333 x 501 -> 259; the products it feeds take 11.5.
 // Two matrices in one launch, the second's rows behind the first's; a
 // workgroup takes every gridDim.x-th row.
 template <class T>
@@ -880,8 +893,8 @@ __global__ void __launch_bounds__(256) rar_pack_rows(const PackParams first, con
 // to part[chunk], joined in chunk order by rar_column_sum.  Sums are of the
 // binary32 dz; the dz that the matrix products read is rounded to the layer's
 // type.
-// 8192 x 8192 in bf16, gelu: 79-82 us, 403 MB at 5 TB/s; z in 8 bits 75 us,
-// where the derivative's arithmetic takes about 60.
+// 8192 x 8192 in bf16, gelu: 82 us, 406 MB at 5 TB/s; z in 8 bits 79 us, 341 MB at
+// 4.3 TB/s.
 enum DzSource { kDzNone = 0, kDzPre = 1, kDzCkpt = 2 };
 constexpr int kDzRows = 4;
 
