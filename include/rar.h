@@ -483,6 +483,156 @@ rar_status rar_ckpt_load(int64_t T, int64_t D, rar_dtype dtype, const uint8_t *c
                          rar_act act, void *y, int64_t ldy, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Between the linear layers and behind them: the norms around a block,     */
+/* dropout, cross attention and the loss.  The rules of the operators above */
+/* on matrices, leading dimensions, overlap, workspaces, capture and        */
+/* numerics hold here too.  Matrices need element alignment only.           */
+/* Exponentials under 2^-126 count as zero.                                 */
+/* ---------------------------------------------------------------------- */
+
+/* ---- the norms before and after a block, with its gate and residual ---- */
+
+typedef struct rar_norm_s *rar_norm_t;
+
+typedef enum {
+    RAR_NORM_NONE = 0,  /* v itself; its weight and bias are ignored */
+    RAR_NORM_LAYER = 1, /* w (v - mean) / sqrt(var + eps) + b, var = mean of (v - mean)^2 */
+    RAR_NORM_RMS = 2    /* w v / sqrt(mean of v^2 + eps) + b */
+} rar_norm_kind;
+
+/* What stands between two blocks of D columns: `post` norms a block's output,
+ * `pre` the next block's input.  eps > 0.  Host memory only, immutable, any
+ * number of threads and streams. */
+rar_status rar_norm_plan(int64_t D, rar_dtype dtype, rar_norm_kind post, rar_norm_kind pre, float eps,
+                         rar_norm_t *out);
+
+rar_status rar_norm_destroy(rar_norm_t plan);
+
+/* Workspace of a backward call on T rows. */
+rar_status rar_norm_workspace(rar_norm_t plan, int64_t T, int64_t *bytes);
+
+/* n = post(o),  h = a x + s (gate . n),  u = pre(h), all T x D.
+ * x is the residual stream, o the block's output or NULL (h = a x: the norm
+ * before the first block).  gate and the norms' weights and biases are vectors
+ * of D or NULL (gate and weights one, biases zero).  h may be x itself, or NULL
+ * when only u is wanted; u may be NULL.  u is the norm of the unrounded h.
+ * T == 0 is a no-op. */
+rar_status rar_norm_forward(rar_norm_t plan, int64_t T, const void *x, int64_t ldx, const void *o, int64_t ldo,
+                            const void *post_w, const void *post_b, const void *gate, float a, float s,
+                            const void *pre_w, const void *pre_b, void *h, int64_t ldh, void *u, int64_t ldu,
+                            void *stream);
+
+/* The gradients, from o and h as the forward call read and wrote them (the
+ * statistics are made again from the rows, nothing else is kept):
+ *   g = dh + pre'(du; h),  dx = a g,  do = post'(s gate . g; o)
+ *   dpre_w = sum du . h^, dpre_b = sum du, dgate = sum s g . n,
+ *   dpost_w = sum s gate . g . o^, dpost_b = sum s gate . g   (sums over rows,
+ *   of the unrounded g; h^ and o^ the normalised rows without weight and bias)
+ * dh, the gradient that reaches h from further on, may be NULL (zero), and so
+ * may du; of a plan with RAR_NORM_NONE before the block pre(h) is h.  Every
+ * output may be NULL.  With o NULL there are no do, dgate and dpost_* (they
+ * must be NULL).  dpost_* need a post norm, dpre_* a pre norm (RAR_EINVAL).  dx
+ * may be dh itself and do may be o itself.  With accumulate != 0 the five
+ * vectors are added to (dx and do are not). */
+rar_status rar_norm_backward(rar_norm_t plan, int64_t T, const void *dh, int64_t lddh, const void *du, int64_t lddu,
+                             const void *o, int64_t ldo, const void *h, int64_t ldh, const void *post_w,
+                             const void *post_b, const void *gate, float a, float s, const void *pre_w, void *dx,
+                             int64_t lddx, void *d_o, int64_t lddo, void *dpost_w, void *dpost_b, void *dgate,
+                             void *dpre_w, void *dpre_b, int accumulate, void *ws, int64_t ws_bytes, void *stream);
+
+/* ---- dropout ------------------------------------------------------------ */
+
+/* y = r + keep . x / (1 - p), T x D; r NULL stands for zero.  The mask is a
+ * function of its place, the seed and the step, and is never stored: element
+ * (t, c) is kept when the 16-bit draw c % 8 of Philox4x32-10 (Salmon et al.,
+ * 2011) with key (seed low, seed high) and counter (g low, g high, step low,
+ * step high), g = t * ceil(D / 8) + c / 8, is at least round(65536 p).  (Draw i
+ * is the half i % 2, lower first, of word i / 2.)  1 - p is taken as kept draws
+ * over 65536, so the mean is exact; p = 1 keeps nothing.  A dropped element
+ * counts as zero whatever it holds.  step is one int64 on the device (a captured
+ * call reads it in every replay) or NULL for zero.  The backward pass is the
+ * same call on dy without r.  y may be x or r itself.  0 <= p <= 1.  T == 0 is a
+ * no-op. */
+rar_status rar_dropout(int64_t T, int64_t D, rar_dtype dtype, float p, uint64_t seed, const int64_t *step,
+                       const void *x, int64_t ldx, const void *r, int64_t ldr, void *y, int64_t ldy, void *stream);
+
+/* ---- cross attention ---------------------------------------------------- */
+
+typedef struct rar_attn_s *rar_attn_t;
+
+#define RAR_ATTN_MAX_WIDTH 128
+
+/* Attention of H query heads of dh columns (1..RAR_ATTN_MAX_WIDTH) to an
+ * encoder's states projected to Hkv key and value heads; Hkv divides H, and H /
+ * Hkv neighbouring query heads share one.  H dh at most 2^20.  scale multiplies
+ * the scores.  Host memory only, immutable, any number of threads and streams. */
+rar_status rar_attn_plan(int64_t H, int64_t Hkv, int64_t dh, rar_dtype dtype, float scale, rar_attn_t *out);
+
+rar_status rar_attn_destroy(rar_attn_t plan);
+
+/* Workspaces of a forward and of a backward call on B sequences of Tq queries
+ * and Tk keys (B Tq and B Tk at most 2^24, B at most 65535), for matrices at any
+ * address and of any leading dimension.  Either output may be NULL. */
+rar_status rar_attn_workspace(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, int64_t *forward_bytes,
+                              int64_t *backward_bytes);
+
+/* o = softmax(scale q k^T) v for every sequence and head.  q and o are B Tq rows
+ * of H heads side by side, k and v B Tk rows of Hkv heads: what the linear layers
+ * write.  qlen and klen are B int64 on the device or NULL (whole): of sequence b
+ * the first qlen[b] queries and klen[b] keys count, taken into 0..Tq and 0..Tk.
+ * What lies behind them is not used, whatever it holds.  o and lse of queries
+ * behind qlen, and of queries that no key is left for (klen 0, or every score
+ * -infinity), are zero and -infinity.  lse (B Tq x H binary32, contiguous, or
+ * NULL) receives the logarithm of the sum of the scores' exponentials, which the
+ * backward call reads.  bf16: the weights are rounded to bf16 for their product
+ * with v, their sum is not.  B Tq == 0 is a no-op. */
+rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, const void *q, int64_t ldq,
+                            const void *k, int64_t ldk, const void *v, int64_t ldv, const int64_t *qlen,
+                            const int64_t *klen, void *o, int64_t ldo, float *lse, void *ws, int64_t ws_bytes,
+                            void *stream);
+
+/* The gradients of q, k and v, given d_o and the forward call's inputs, o and
+ * lse.  Rows of dq behind qlen and of dk and dv behind klen become zero; shared
+ * heads' gradients are summed in a fixed order.  dq, dk and dv may each be NULL.
+ * bf16: weights and score gradients are rounded to bf16 for their products. */
+rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, const void *d_o, int64_t lddo,
+                             const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                             const int64_t *qlen, const int64_t *klen, const void *o, int64_t ldo, const float *lse,
+                             void *dq, int64_t lddq, void *dk, int64_t lddk, void *dv, int64_t lddv, void *ws,
+                             int64_t ws_bytes, void *stream);
+
+/* ---- the loss ----------------------------------------------------------- */
+
+#define RAR_LOGPROB_MAX_TOP 32
+
+/* With z = scale * logits (T x V, scale > 0) and p = softmax(z) of a row:
+ *   logp[t]    = log p at targets[t]; zero for a target outside 0..V-1 (padding)
+ *   entropy[t] = -sum p log p
+ *   top_ids[t][k], top_logp[t][k], k < K: the K largest logits in falling order,
+ *                ties to the lowest index, and their log probabilities
+ * (T binary32, T binary32, T x K int64 and binary32, all contiguous; each may be
+ * NULL, targets too when logp is).  0 <= K <= RAR_LOGPROB_MAX_TOP; K > 0 needs
+ * top_ids and top_logp.  A logit of -infinity is masked: p = 0, and no
+ * alternative; where fewer than K are left the rest are -1 and -infinity.  A row
+ * that has nothing left gives logp -infinity and entropy zero.  A NaN or
+ * +infinity in a row makes its log probabilities and entropy NaN (its
+ * alternatives -1 and NaN).  T == 0 is a no-op. */
+rar_status rar_logprob(int64_t T, int64_t V, rar_dtype dtype, const void *logits, int64_t ldz, float scale,
+                       const int64_t *targets, float *logp, float *entropy, int K, int64_t *top_ids, float *top_logp,
+                       void *stream);
+
+/* The gradient of sum_t dlogp[t] logp[t] + dentropy[t] entropy[t] in the logits:
+ *   dz[t][j] = scale (dlogp [j = target] - p (dlogp + dentropy (log p + entropy)))
+ * dlogp and dentropy are T binary32 or NULL (zero); targets may be NULL without
+ * dlogp.  dz may be the logits themselves.  logp and entropy, or NULL, receive
+ * what rar_logprob gives: a loss whose dlogp is known beforehand (-1 / T of a
+ * mean) needs this call only.  A row that has nothing left has a gradient of
+ * zero.  dlogp of a padded target is ignored. */
+rar_status rar_logprob_grad(int64_t T, int64_t V, rar_dtype dtype, const void *logits, int64_t ldz, float scale,
+                            const int64_t *targets, const float *dlogp, const float *dentropy, float *logp,
+                            float *entropy, void *dz, int64_t lddz, void *stream);
+
+/* ---------------------------------------------------------------------- */
 
 /* Static description of a status code; never NULL. */
 const char *rar_strerror(rar_status s);
@@ -491,7 +641,8 @@ const char *rar_strerror(rar_status s);
  * rar_rank_stride, 0.3.0 = 300 rar_rank_stride_tune, 0.4.0 = 400
  * rar_allreduce_ring_noalloc, 0.5.0 = 500 rar_rank_stride_tune_stats,
  * 0.6.0 = 600 rar_rank_stride_candidate and the wider stride search,
- * 0.7.0 = 700 rar_embed_*, rar_linear_* and rar_ckpt_*). */
+ * 0.7.0 = 700 rar_embed_*, rar_linear_* and rar_ckpt_*, 0.8.0 = 800
+ * rar_norm_*, rar_dropout, rar_attn_* and rar_logprob*). */
 int rar_version(void);
 
 #ifdef __cplusplus

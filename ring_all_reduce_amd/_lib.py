@@ -57,6 +57,23 @@ SIGNATURES = {
     "rar_ckpt_size": (_int, [_i64, _i64p, _i64p]),
     "rar_ckpt_store": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _vp, _vp]),
     "rar_ckpt_load": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _i64, _vp]),
+    "rar_norm_plan": (_int, [_i64, _int, _int, _int, _f, ctypes.POINTER(_vp)]),
+    "rar_norm_destroy": (_int, [_vp]),
+    "rar_norm_workspace": (_int, [_vp, _i64, _i64p]),
+    "rar_norm_forward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _f, _f, _vp, _vp, _vp, _i64, _vp,
+                                _i64, _vp]),
+    "rar_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _f, _f, _vp,
+                                 _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _vp]),
+    "rar_dropout": (_int, [_i64, _i64, _int, _f, ctypes.c_uint64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "rar_attn_plan": (_int, [_i64, _i64, _i64, _int, _f, ctypes.POINTER(_vp)]),
+    "rar_attn_destroy": (_int, [_vp]),
+    "rar_attn_workspace": (_int, [_vp, _i64, _i64, _i64, _i64p, _i64p]),
+    "rar_attn_forward": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp,
+                                _i64, _vp]),
+    "rar_attn_backward": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                 _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "rar_logprob": (_int, [_i64, _i64, _int, _vp, _i64, _f, _vp, _vp, _vp, _int, _vp, _vp, _vp]),
+    "rar_logprob_grad": (_int, [_i64, _i64, _int, _vp, _i64, _f, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "rar_strerror": (ctypes.c_char_p, [_int]),
     "rar_version": (_int, []),
 }

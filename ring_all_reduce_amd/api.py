@@ -9,8 +9,8 @@ unchecked.  ``stream`` may be a torch stream, an
 integer hipStream_t, or None for torch's current stream on the current
 device (the default stream when torch has no GPU).
 
-The operators on matrices (rar_embed_*, rar_linear_*, rar_ckpt_*) take 2-D
-tensors whose rows are contiguous; the distance between rows is the leading
+The operators on matrices (rar_embed_*, rar_linear_*, rar_ckpt_*, rar_norm_*,
+rar_dropout, rar_attn_*, rar_logprob*) take 2-D tensors whose rows are contiguous; the distance between rows is the leading
 dimension.  An integer address stands for a contiguous matrix.  Their tensors
 must be on the current device.  ``ws`` is a uint8 tensor of at least the
 queried bytes, or None: then one is allocated for the call, and returned to
@@ -35,6 +35,9 @@ MAX_STRIDE_CANDIDATES = 64
 STATIC_WS_ELEMS = 1 << 24
 ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
 CKPT_GROUP = 32
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2
+ATTN_MAX_WIDTH = 128
+LOGPROB_MAX_TOP = 32
 
 
 class RarError(RuntimeError):
@@ -647,3 +650,203 @@ def _ckpt(codes, scales, T: int, D: int):
     groups = -(-D // CKPT_GROUP)
     return (_dense(codes, "codes", torch.uint8, T * groups * CKPT_GROUP),
             _dense(scales, "scales", torch.uint8, T * groups))
+
+
+# ---------------------------------------------------------------------------
+# Between the linear layers and behind them: norms around a block, dropout,
+# cross attention, log probabilities
+# ---------------------------------------------------------------------------
+
+class Norm:
+    """Owner of a rar_norm_t; destroyed with the object or by rar_norm_destroy."""
+
+    def __init__(self, handle: int, D: int, dtype: int, post: int, pre: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.D, self.dtype, self.post, self.pre = D, dtype, post, pre
+
+    def __del__(self):
+        try:
+            rar_norm_destroy(self)
+        except Exception:
+            pass
+
+
+def rar_norm_plan(D: int, dtype: int = F32, post: int = NORM_NONE, pre: int = NORM_LAYER, eps: float = 1e-5) -> Norm:
+    """What stands between two blocks: a norm of a block's output and one of the next block's input."""
+    out = ctypes.c_void_p()
+    _check(lib().rar_norm_plan(int(D), int(dtype), int(post), int(pre), float(eps), ctypes.byref(out)),
+           "rar_norm_plan")
+    return Norm(out.value, int(D), int(dtype), int(post), int(pre))
+
+
+def rar_norm_destroy(plan: Norm) -> None:
+    if plan.handle:
+        h, plan.handle = plan.handle, ctypes.c_void_p()
+        _check(lib().rar_norm_destroy(h), "rar_norm_destroy")
+
+
+def rar_norm_workspace(plan: Norm, T: int) -> int:
+    """Bytes of a backward call on T rows."""
+    out = ctypes.c_int64()
+    _check(lib().rar_norm_workspace(plan.handle, int(T), ctypes.byref(out)), "rar_norm_workspace")
+    return out.value
+
+
+def rar_norm_forward(plan: Norm, T: int, x, o, post_w, post_b, gate, pre_w, pre_b, h, u, a: float = 1.0,
+                     s: float = 1.0, stream=None) -> None:
+    """n = post(o), h = a x + s gate n, u = pre(h).  o (then h = a x), the
+    vectors (weights and gate one, biases zero) and one of h and u may be None;
+    h may be x."""
+    T, D, td = int(T), plan.D, _torch_dtype(plan.dtype)
+    xp, ldx = _matrix(x, "x", td, T, D)
+    op, ldo = _matrix(o, "o", td, T, D)
+    hp, ldh = _matrix(h, "h", td, T, D)
+    up, ldu = _matrix(u, "u", td, T, D)
+    vs = [_dense(v, n, td, D) for v, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"), (pre_w, "pre_w"),
+                                           (pre_b, "pre_b"))]
+    _check(lib().rar_norm_forward(plan.handle, T, xp, ldx, op, ldo, vs[0], vs[1], vs[2], float(a), float(s), vs[3],
+                                  vs[4], hp, ldh, up, ldu, _on(stream)), "rar_norm_forward")
+
+
+def rar_norm_backward(plan: Norm, T: int, dh, du, o, h, post_w, post_b, gate, pre_w, dx, do, dpost_w=None,
+                      dpost_b=None, dgate=None, dpre_w=None, dpre_b=None, a: float = 1.0, s: float = 1.0,
+                      accumulate: bool = False, ws=None, stream=None) -> None:
+    """The gradients of rar_norm_forward from its o and h: dh and du (either may
+    be None) reach h and u; every output may be None.  accumulate adds to the
+    five vectors."""
+    T, D, td = int(T), plan.D, _torch_dtype(plan.dtype)
+    m = []
+    for x, name in ((dh, "dh"), (du, "du"), (o, "o"), (h, "h"), (dx, "dx"), (do, "do")):
+        m.append(_matrix(x, name, td, T, D))
+    v = [_dense(x, n, td, D) for x, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"), (pre_w, "pre_w"))]
+    d = [_dense(x, n, td, D) for x, n in ((dpost_w, "dpost_w"), (dpost_b, "dpost_b"), (dgate, "dgate"),
+                                          (dpre_w, "dpre_w"), (dpre_b, "dpre_b"))]
+    need = rar_norm_workspace(plan, T) if ws is None and any(d) else 0
+    wp, wb, _own = _workspace(ws, need, stream)
+    _check(lib().rar_norm_backward(plan.handle, T, *m[0], *m[1], *m[2], *m[3], v[0], v[1], v[2], float(a), float(s),
+                                   v[3], *m[4], *m[5], *d, int(bool(accumulate)), wp, wb, _on(stream)),
+           "rar_norm_backward")
+
+
+def rar_dropout(T: int, D: int, dtype: int, x, y, p: float, seed: int, step=None, residual=None,
+                stream=None) -> None:
+    """y = residual + x with elements dropped with probability p and the others
+    scaled by 1 / (1 - p).  The mask follows from seed (64 bits) and step (one
+    int64 on the GPU, or None for zero); the same call on dy is the backward
+    pass.  y may be x or residual."""
+    import torch
+    T, D, td = int(T), int(D), _torch_dtype(dtype)
+    xp, ldx = _matrix(x, "x", td, T, D)
+    rp, ldr = _matrix(residual, "residual", td, T, D)
+    yp, ldy = _matrix(y, "y", td, T, D)
+    if not 0 <= int(seed) < 1 << 64:
+        raise ValueError("seed: 64 bits")
+    _check(lib().rar_dropout(T, D, dtype, float(p), int(seed), _dense(step, "step", torch.int64, 1), xp, ldx, rp, ldr,
+                             yp, ldy, _on(stream)), "rar_dropout")
+
+
+class Attn:
+    """Owner of a rar_attn_t; destroyed with the object or by rar_attn_destroy."""
+
+    def __init__(self, handle: int, H: int, Hkv: int, dh: int, dtype: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.H, self.Hkv, self.dh, self.dtype = H, Hkv, dh, dtype
+
+    def __del__(self):
+        try:
+            rar_attn_destroy(self)
+        except Exception:
+            pass
+
+
+def rar_attn_plan(H: int, Hkv: int, dh: int, dtype: int = F32, scale: float = None) -> Attn:
+    """H query heads of dh columns on Hkv key and value heads; scale is dh ** -0.5 unless given."""
+    out = ctypes.c_void_p()
+    scale = float(scale) if scale is not None else (float(dh) ** -0.5 if dh > 0 else 1.0)
+    _check(lib().rar_attn_plan(int(H), int(Hkv), int(dh), int(dtype), scale, ctypes.byref(out)), "rar_attn_plan")
+    return Attn(out.value, int(H), int(Hkv), int(dh), int(dtype))
+
+
+def rar_attn_destroy(plan: Attn) -> None:
+    if plan.handle:
+        h, plan.handle = plan.handle, ctypes.c_void_p()
+        _check(lib().rar_attn_destroy(h), "rar_attn_destroy")
+
+
+def rar_attn_workspace(plan: Attn, B: int, Tq: int, Tk: int):
+    """(forward bytes, backward bytes) for B sequences of Tq queries and Tk keys."""
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().rar_attn_workspace(plan.handle, int(B), int(Tq), int(Tk), ctypes.byref(f), ctypes.byref(b)),
+           "rar_attn_workspace")
+    return f.value, b.value
+
+
+def rar_attn_forward(plan: Attn, B: int, Tq: int, Tk: int, q, k, v, o, lse=None, qlen=None, klen=None, ws=None,
+                     stream=None) -> None:
+    """o = softmax(scale q k^T) v for each sequence and head: q and o are (B Tq)
+    x (H dh), k and v (B Tk) x (Hkv dh).  qlen and klen (B int64 on the GPU, or
+    None) say how many queries and keys of a sequence count.  lse ((B Tq) x H
+    float32, or None) is what the backward call reads."""
+    import torch
+    B, Tq, Tk, td = int(B), int(Tq), int(Tk), _torch_dtype(plan.dtype)
+    wide, narrow = plan.H * plan.dh, plan.Hkv * plan.dh
+    qp, op = _matrix(q, "q", td, B * Tq, wide), _matrix(o, "o", td, B * Tq, wide)
+    kp, vp = _matrix(k, "k", td, B * Tk, narrow), _matrix(v, "v", td, B * Tk, narrow)
+    nq, nk = _dense(qlen, "qlen", torch.int64, B), _dense(klen, "klen", torch.int64, B)
+    lp = _dense(lse, "lse", torch.float32, B * Tq * plan.H)
+    need = rar_attn_workspace(plan, B, Tq, Tk)[0] if ws is None else 0
+    wp, wb, _own = _workspace(ws, need, stream)
+    _check(lib().rar_attn_forward(plan.handle, B, Tq, Tk, *qp, *kp, *vp, nq, nk, *op, lp, wp, wb, _on(stream)),
+           "rar_attn_forward")
+
+
+def rar_attn_backward(plan: Attn, B: int, Tq: int, Tk: int, do, q, k, v, o, lse, dq, dk, dv, qlen=None, klen=None,
+                      ws=None, stream=None) -> None:
+    """The gradients of q, k and v (each output may be None) from the forward call's inputs, o and lse."""
+    import torch
+    B, Tq, Tk, td = int(B), int(Tq), int(Tk), _torch_dtype(plan.dtype)
+    wide, narrow = plan.H * plan.dh, plan.Hkv * plan.dh
+    m = [_matrix(x, n, td, B * Tq, wide) for x, n in ((do, "do"), (q, "q"), (o, "o"), (dq, "dq"))]
+    n = [_matrix(x, n, td, B * Tk, narrow) for x, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv"))]
+    nq, nk = _dense(qlen, "qlen", torch.int64, B), _dense(klen, "klen", torch.int64, B)
+    lp = _dense(lse, "lse", torch.float32, B * Tq * plan.H)
+    need = rar_attn_workspace(plan, B, Tq, Tk)[1] if ws is None else 0
+    wp, wb, _own = _workspace(ws, need, stream)
+    _check(lib().rar_attn_backward(plan.handle, B, Tq, Tk, *m[0], *m[1], *n[0], *n[1], nq, nk, *m[2], lp, *m[3], *n[2],
+                                   *n[3], wp, wb, _on(stream)), "rar_attn_backward")
+
+
+def rar_logprob(T: int, V: int, dtype: int, logits, targets, logp, entropy=None, top_ids=None, top_logp=None,
+                scale: float = 1.0, stream=None) -> None:
+    """Of softmax(scale logits), T x V: logp (T float32) at targets (T int64),
+    the entropy (T float32), and the K best alternatives (T x K int64 and
+    float32).  Each may be None."""
+    import torch
+    T, V, td = int(T), int(V), _torch_dtype(dtype)
+    zp, ldz = _matrix(logits, "logits", td, T, V)
+    K = 0
+    if top_ids is not None or top_logp is not None:
+        if not all(hasattr(x, "data_ptr") and x.dim() == 2 for x in (top_ids, top_logp)):
+            raise TypeError("top_ids and top_logp must be matrices of one shape (it says how many are wanted)")
+        K = top_ids.shape[1]
+        if top_ids.shape != (T, K) or top_logp.shape != (T, K):
+            raise ValueError(f"top_ids {tuple(top_ids.shape)} and top_logp {tuple(top_logp.shape)}: expected ({T}, K)")
+    _check(lib().rar_logprob(T, V, dtype, zp, ldz, float(scale), _dense(targets, "targets", torch.int64, T),
+                             _dense(logp, "logp", torch.float32, T), _dense(entropy, "entropy", torch.float32, T), K,
+                             _dense(top_ids, "top_ids", torch.int64, T * K),
+                             _dense(top_logp, "top_logp", torch.float32, T * K), _on(stream)), "rar_logprob")
+
+
+def rar_logprob_grad(T: int, V: int, dtype: int, logits, targets, dlogp, dentropy, dz, logp=None, entropy=None,
+                     scale: float = 1.0, stream=None) -> None:
+    """dz (T x V, may be the logits): the gradient of sum(dlogp logp + dentropy
+    entropy) in the logits; dlogp and dentropy are T float32 or None.  logp and
+    entropy receive what rar_logprob gives."""
+    import torch
+    T, V, td = int(T), int(V), _torch_dtype(dtype)
+    zp, ldz = _matrix(logits, "logits", td, T, V)
+    dp, lddz = _matrix(dz, "dz", td, T, V)
+    f = [_dense(x, n, torch.float32, T) for x, n in ((dlogp, "dlogp"), (dentropy, "dentropy"), (logp, "logp"),
+                                                     (entropy, "entropy"))]
+    _check(lib().rar_logprob_grad(T, V, dtype, zp, ldz, float(scale), _dense(targets, "targets", torch.int64, T), *f,
+                                  dp, lddz, _on(stream)), "rar_logprob_grad")

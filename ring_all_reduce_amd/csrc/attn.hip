@@ -1,0 +1,974 @@
+// attn.hip -- CDNA4 (gfx950) kernels of cross attention, forward and backward.
+//
+//   S = scale q k^T over the keys that count, P = softmax(S), o = P v
+//   lse = log sum e^S,  delta = sum do . o
+//   dv = P^T do,  dP = do v^T,  dS = P (dP - delta),  dq = scale dS k,  dk = scale dS^T q
+//
+// All products are 32 x 32 tiles of the matrix cores whose reduction runs over 16
+// (lane l holds row l % 32 and elements 8 (l / 32) .. +7; the result's lane holds
+// column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4, i < 16).  The order of
+// a reduction is free as long as both operands keep it.  So scores are taken
+// transposed, one query (or, for dk and dv, one key) a lane: softmax runs along a
+// lane's registers, and the weights are, as they stand, an operand of the next
+// product, whose other operand is read from LDS in the same order of rows by
+// transposing reads.  Neither scores nor weights pass through LDS or memory.
+//
+// Query heads that share a key head are rows of one tile: row r is query r /
+// share of head r % share.
+#include <algorithm>
+
+#include "ops_internal.h"
+#include "row.h"
+
+#pragma clang fp contract(off)
+
+#define RAR_LDS __attribute__((address_space(3)))
+
+namespace rar {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr uint32_t kOutOfRange = 0x80000000u;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kInf = __builtin_inff();
+
+// ---------------------------------------------------------------------------
+// Products
+// ---------------------------------------------------------------------------
+
+template <class T> struct Frag;
+
+template <> struct Frag<bf16> {
+    bf16x8 v;
+    __device__ __forceinline__ void zero() { v = bf16x8{}; }
+    __device__ __forceinline__ void load(const bf16 *p) { v = *reinterpret_cast<const bf16x8 *>(p); }
+    // eight consecutive results of a tile, rounded for the next product
+    __device__ __forceinline__ void set(const f32x16 &s, int at)
+    {
+        const u32x4 w = {pack_bf16(s[at], s[at + 1]), pack_bf16(s[at + 2], s[at + 3]), pack_bf16(s[at + 4], s[at + 5]),
+                         pack_bf16(s[at + 6], s[at + 7])};
+        v = __builtin_bit_cast(bf16x8, w);
+    }
+};
+
+template <> struct Frag<float> {
+    f32x4 lo, hi;
+    __device__ __forceinline__ void zero() { lo = hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void load(const float *p)
+    {
+        lo = *reinterpret_cast<const f32x4 *>(p);
+        hi = *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    __device__ __forceinline__ void set(const f32x16 &s, int at)
+    {
+        lo = f32x4{s[at], s[at + 1], s[at + 2], s[at + 3]};
+        hi = f32x4{s[at + 4], s[at + 5], s[at + 6], s[at + 7]};
+    }
+};
+
+__device__ __forceinline__ void mma(f32x16 &c, const Frag<bf16> &a, const Frag<bf16> &b)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+#endif
+}
+
+__device__ __forceinline__ void mma(f32x16 &c, const Frag<float> &a, const Frag<float> &b)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.lo[j], b.lo[j], c, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.hi[j], b.hi[j], c, 0, 0, 0);
+#endif
+}
+
+__device__ __forceinline__ f32x16 zeros()
+{
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = 0.0f;
+    return v;
+}
+
+// Row of a result's register i, without the lane's 4 (l / 32).
+__device__ __forceinline__ constexpr int row_of(int i) { return 8 * (i / 4) + i % 4; }
+
+// ---------------------------------------------------------------------------
+// Tiles in LDS
+// ---------------------------------------------------------------------------
+//
+// A tile holds rows of PITCH elements.  The 16-byte chunk c of row r lies at slot
+// c ^ spread(r), so that both reads below touch every bank once in 256 bytes: one
+// chunk of 16 rows (an operand whose rows are the tile's), and, of bf16, four
+// chunks of four rows (an operand whose reduction runs over the tile's rows, by
+// the transposing read) or, of binary32, 128 bytes of two rows that lie four apart.
+template <class T, int PITCH>
+struct Tile {
+    static constexpr int ES = sizeof(T);
+    static constexpr int kBytes = PITCH * ES;   // of a row
+    static constexpr int kChunks = kBytes / 16;
+
+    static __device__ __forceinline__ int spread(int r)
+    {
+        if (ES == 4)
+            return ((r >> 2) & 1) << 3 | (r & 3) << 1 | ((r >> 3) & 1);
+        if (kBytes == 256)
+            return (r & 3) << 2 | ((r >> 2) & 3);
+        return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);  // two rows in 256 bytes
+    }
+
+    // Rows r0 + l % 32 (r0 a multiple of 32), elements 16 s + 8 (l / 32) ..
+    static __device__ __forceinline__ Frag<T> rows(const RAR_LDS char *__restrict__ lds, int r0, int s)
+    {
+        const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+        const RAR_LDS char *const at = lds + (r0 + r) * kBytes;
+        Frag<T> f;
+        if constexpr (ES == 2) {
+            f.v = *(const RAR_LDS bf16x8 *)(at + (((2 * s + half) ^ spread(r)) << 4));
+        } else {
+            f.lo = *(const RAR_LDS f32x4 *)(at + (((4 * s + 2 * half) ^ spread(r)) << 4));
+            f.hi = *(const RAR_LDS f32x4 *)(at + (((4 * s + 2 * half + 1) ^ spread(r)) << 4));
+        }
+        return f;
+    }
+
+    // Column 32 d + l % 32 of the rows that registers 8 j .. 8 j + 7 of a result
+    // stand for, in a tile of 32 rows that starts at r0.
+    static __device__ __forceinline__ Frag<T> cols(const RAR_LDS char *__restrict__ lds, int r0, int j, int d)
+    {
+        const int lane = threadIdx.x & 63, half = lane >> 5;
+        Frag<T> f;
+        if constexpr (ES == 2) {
+            i16x4 w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * j + 8 * e + 4 * half + ((lane & 15) >> 2);
+                const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+                const RAR_LDS char *const at =
+                    lds + (r0 + r) * kBytes + ((c ^ spread(r)) << 4) + ((lane & 1) << 3);
+                w[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RAR_LDS i16x4 *)at);
+            }
+            f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = 16 * j + 8 * (e / 4) + 4 * half + e % 4;
+                const int c = 8 * d + ((lane & 31) >> 2);
+                const float v =
+                    *(const RAR_LDS float *)(lds + (r0 + r) * kBytes + ((c ^ spread(r)) << 4) + ((lane & 3) << 2));
+                if (e < 4)
+                    f.lo[e & 3] = v;
+                else
+                    f.hi[e & 3] = v;
+            }
+        }
+        return f;
+    }
+};
+
+// Memory -> LDS, 16 bytes a lane, without passing through registers.  The
+// destination is linear in the lane, so the spread is applied to the address
+// that each lane reads.  The descriptor ends with the last row that counts: rows
+// behind it, and chunks behind the head's columns, read as zero.
+template <class T, int PITCH, int ROWS, int WAVES>
+struct Loader {
+    typedef Tile<T, PITCH> Lds;
+    static constexpr int kLoads = ROWS * Lds::kBytes / (WAVES * 1024);
+    static_assert(kLoads * WAVES * 1024 == ROWS * Lds::kBytes, "whole loads");
+    uint32_t voff[kLoads];
+    const char *base;
+    int64_t pitch, width;  // bytes of a row in memory, and of a head
+    int64_t left;          // rows from base that count
+
+    __device__ __forceinline__ void init(const AttnOperand &m, int64_t row, int64_t head, int64_t rows)
+    {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        base = (const char *)m.p + (row * m.ld + head * m.hs) * Lds::ES;
+        pitch = m.ld * Lds::ES;
+        width = m.cols * Lds::ES;
+        left = rows;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int at = (j * WAVES + wave) * 1024 + lane * 16;
+            const int r = at / Lds::kBytes, c = ((at % Lds::kBytes) / 16) ^ Lds::spread(r);
+            voff[j] = c * 16 < width ? (uint32_t)(r * pitch) + c * 16 : kOutOfRange;
+        }
+    }
+
+    __device__ __forceinline__ void load(RAR_LDS char *__restrict__ lds)
+    {
+#if defined(__HIP_DEVICE_COMPILE__)
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        int64_t n = left > 0 ? (left - 1) * pitch + width : 0;
+        if (n > 0x7fffffff)
+            n = 0x7fffffff;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * WAVES + wave) * 1024), 16, voff[j],
+                                                     0, 0, 0);
+#endif
+    }
+
+    // The next ROWS rows.
+    __device__ __forceinline__ void advance()
+    {
+        base += ROWS * pitch;
+        left -= ROWS;
+    }
+};
+
+// Own loads into LDS and own LDS reads are done; then everyone's.
+__device__ __forceinline__ void meet()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Workgroups go to the eight XCDs in turn; each XCD gets one run of the work, so
+// that its L2 holds the keys (or queries) that neighbours share.
+__device__ __forceinline__ int64_t in_order(int64_t id, int64_t total)
+{
+    const int64_t per = total / 8;
+    return id < per * 8 ? (id % 8) * per + id / 8 : id;
+}
+
+__device__ __forceinline__ int64_t length_of(const int64_t *lens, int64_t b, int64_t most)
+{
+    if (!lens)
+        return most;
+    const int64_t n = lens[b];
+    return n < 0 ? 0 : (n > most ? most : n);
+}
+
+// Four consecutive columns of a row, of which those before `cols` exist.
+template <class T>
+__device__ __forceinline__ void put4(T *row, int c, int cols, f32x4 v)
+{
+    if (c + 4 <= cols) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<f32x4_any *>(row + c) = v;
+        } else {
+            typedef u32x2 u32x2_any __attribute__((aligned(2)));
+            *reinterpret_cast<u32x2_any *>(row + c) = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < cols)
+            row[c + i] = from_f32<T>(v[i]);
+}
+
+// e^(scale s - shift): bf16 in one rounding of the exponent; binary32 subtracts
+// first, so that the weights near one, which carry the result, keep their digits.
+template <class T>
+__device__ __forceinline__ float weight(float s, float scale, float scale2, float shift, float shift2)
+{
+    if (sizeof(T) == 2)
+        return __builtin_amdgcn_exp2f(__builtin_fmaf(s, scale2, -shift2));
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(s, scale, -shift) * kLog2e);
+}
+
+template <class T, int W>
+struct Shape {
+    static constexpr int PITCH = W <= 2 ? 64 : 128;
+    static constexpr int STEPS = 2 * W;  // reductions of 16 over a head's columns
+    typedef Tile<T, PITCH> Lds;
+};
+
+// The fragments of one row of a matrix: row `row`, elements 16 s + 8 half ..
+template <class T, int N>
+__device__ __forceinline__ void load_row(Frag<T> (&f)[N], const AttnOperand &m, int64_t row, int64_t head, bool live)
+{
+    const int half = (threadIdx.x & 63) >> 5;
+    const T *const p = (const T *)m.p + row * m.ld + head * m.hs;
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int c = 16 * s + 8 * half;
+        if (live && c + 8 <= m.cols) {
+            f[s].load(p + c);
+        } else if (live && c < m.cols) {  // binary32: the columns are whole fours
+            f[s].zero();
+            if constexpr (sizeof(T) == 4)
+                f[s].lo = *reinterpret_cast<const f32x4 *>(p + c);
+        } else {
+            f[s].zero();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+//
+// A wave holds 32 query rows.  In the usual form the waves of a workgroup take
+// different rows and share the staged keys; with few rows (KEYS) they take the
+// same rows and different keys of a stage, and are joined through LDS at the
+// end.  Running maximum and sum stay in the lane of the row; the accumulator is
+// scaled only where some row's maximum has grown.
+template <class T>
+constexpr int forward_waves(bool keys) { return keys && sizeof(T) == 4 ? 2 : 4; }
+
+template <class T, int W, bool KEYS>
+struct Forward {
+    typedef Shape<T, W> S;
+    typedef typename S::Lds Lds;
+    static constexpr int kWaves = forward_waves<T>(KEYS);
+    static constexpr int kTiles = !KEYS && sizeof(T) == 2 ? 2 : 1;      // of 32 keys, a wave, a stage
+    static constexpr int kStage = (KEYS ? kWaves : 1) * kTiles * 32;    // keys of a stage
+    static constexpr int kRows = KEYS ? 32 : kWaves * 32;
+    static constexpr int kHalf = kStage * Lds::kBytes;                  // bytes of a stage's keys
+    static constexpr int kJoinPitch = W * 32 * 4 + 16;                  // bytes of a row in the join
+    static constexpr int kJoin = KEYS ? kWaves * 32 * (kJoinPitch + 8) : 0;
+    static constexpr int kLds = 4 * kHalf > kJoin ? 4 * kHalf : kJoin;
+};
+
+template <class T, int W, bool KEYS>
+__global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(const AttnParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef Forward<T, W, KEYS> F;
+    typedef typename F::Lds Lds;
+    constexpr int STEPS = F::S::STEPS;
+    __shared__ __attribute__((aligned(1024))) char memory[F::kLds];
+    RAR_LDS char *const lds = (RAR_LDS char *)memory;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+
+    int64_t id = in_order(blockIdx.x, p.blocks);
+    const int64_t tile = id % p.tiles;
+    id /= p.tiles;
+    const int split = (int)(id % p.splits);
+    id /= p.splits;
+    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int64_t rows = p.Tq * p.share;
+
+    const int64_t first = tile * F::kRows;
+    const int64_t row = first + (KEYS ? 0 : wave * 32) + (lane & 31);
+    const int64_t t = row / p.share, h = hk * p.share + row % p.share;
+    const bool live = row < rows && t < qlen;
+    Frag<T> q[STEPS];
+    load_row<T>(q, p.q, b * p.Tq + t, h, live);
+
+    // this workgroup's keys: whole stages
+    const int64_t k0 = (int64_t)split * p.stages * F::kStage;
+    int64_t kend = k0 + (int64_t)p.stages * F::kStage;
+    kend = kend < klen ? kend : klen;
+    const int stages = first / p.share < qlen && k0 < kend ? (int)((kend - k0 + F::kStage - 1) / F::kStage) : 0;
+
+    Loader<T, F::S::PITCH, F::kStage, F::kWaves> lk, lv;
+    lk.init(p.k, b * p.Tk + k0, hk, kend - k0);
+    lv.init(p.v, b * p.Tk + k0, hk, kend - k0);
+    f32x16 acc[W];
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+        acc[d] = zeros();
+    float m = -kInf, l = 0.0f;
+    const float scale2 = p.scale * kLog2e;
+
+    if (stages) {
+        lk.load(lds);
+        lv.load(lds + F::kHalf);
+        meet();
+    }
+    for (int n = 0; n < stages; ++n) {
+        RAR_LDS char *const here = lds + (n & 1) * 2 * F::kHalf;
+        RAR_LDS char *const next = lds + (2 - (n & 1) * 2) * F::kHalf;
+        if (n + 1 < stages) {
+            lk.advance();
+            lv.advance();
+            lk.load(next);
+            lv.load(next + F::kHalf);
+        }
+        const int r0 = KEYS ? wave * 32 : 0;
+        f32x16 s[F::kTiles];
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e) {
+            s[e] = zeros();
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+                mma(s[e], Lds::rows(here, r0 + e * 32, i), q[i]);
+        }
+        // keys behind the last one that counts
+        const int64_t rest = kend - k0 - (int64_t)n * F::kStage - r0;
+        if (rest < F::kTiles * 32)
+#pragma unroll
+            for (int e = 0; e < F::kTiles; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (e * 32 + row_of(i) + 4 * half >= rest)
+                        s[e][i] = -kInf;
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = __builtin_fmaxf(top, s[e][i]);
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        top = __builtin_fmaxf(top * p.scale, m);
+        const float base = top == -kInf ? 0.0f : top, base2 = base * kLog2e;
+        if (__any(top > m)) {
+            const float down = __builtin_amdgcn_exp2f((m - base) * kLog2e);
+            l *= down;
+#pragma unroll
+            for (int d = 0; d < W; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[d][i] *= down;
+            m = top;
+        }
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[e][i] = weight<T>(s[e][i], p.scale, scale2, base, base2);
+                l += s[e][i];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                Frag<T> w;
+                w.set(s[e], 8 * j);
+#pragma unroll
+                for (int d = 0; d < W; ++d)
+                    mma(acc[d], Lds::cols(here + F::kHalf, r0 + e * 32, j, d), w);
+            }
+        }
+        meet();
+    }
+    l += __shfl_xor(l, 32);
+
+    if constexpr (KEYS) {
+        RAR_LDS float *const mine = (RAR_LDS float *)(lds + (wave * 32 + (lane & 31)) * F::kJoinPitch);
+        RAR_LDS float *const stats = (RAR_LDS float *)(lds + F::kWaves * 32 * F::kJoinPitch);  // [wave][32][m, l]
+        if (half == 0) {
+            stats[(wave * 32 + lane) * 2] = m;
+            stats[(wave * 32 + lane) * 2 + 1] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < W; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *(RAR_LDS f32x4 *)(mine + d * 32 + 8 * i + 4 * half) =
+                    f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        meet();
+        // eight lanes a row, W quads of columns a lane
+        for (int r = threadIdx.x >> 3; r < 32; r += F::kWaves * 8) {
+            const int64_t at = first + r;
+            if (at >= rows)
+                break;
+            float top = -kInf, sum = 0.0f, w[F::kWaves];
+#pragma unroll
+            for (int i = 0; i < F::kWaves; ++i)
+                top = __builtin_fmaxf(top, stats[(i * 32 + r) * 2]);
+#pragma unroll
+            for (int i = 0; i < F::kWaves; ++i) {
+                const float mi = stats[(i * 32 + r) * 2];
+                const float li = stats[(i * 32 + r) * 2 + 1];
+                // (no key of this wave's counts, or all of their scores are -infinity)
+                w[i] = li == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((mi - (top == -kInf ? 0.0f : top)) * kLog2e);
+                sum = __builtin_fmaf(w[i], li, sum);
+            }
+            const int64_t at_t = at / p.share, at_h = hk * p.share + at % p.share;
+            const bool on = at_t < qlen;
+            const float inv = p.splits > 1 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+            const int64_t place = (b * p.Hkv + hk) * rows + at;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const int c = ((threadIdx.x & 7) + e * 8) * 4;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < F::kWaves; ++i) {
+                    const f32x4 a = *(RAR_LDS f32x4 *)((RAR_LDS float *)(lds + (i * 32 + r) * F::kJoinPitch) + c);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        v[x] = w[i] == 0.0f ? v[x] : __builtin_fmaf(w[i], a[x], v[x]);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    v[x] = on ? v[x] * inv : 0.0f;
+                if (p.splits > 1)
+                    store4(p.part + (split * p.part_rows + place) * (W * 32) + c, v);
+                else
+                    put4((T *)p.o + (b * p.Tq + at_t) * p.ldo + at_h * p.dh, c, p.dh, v);
+            }
+            if ((threadIdx.x & 7) == 0) {
+                if (p.splits > 1) {
+                    p.stats[(split * p.part_rows + place) * 2] = top;
+                    p.stats[(split * p.part_rows + place) * 2 + 1] = sum;
+                } else if (p.lse) {
+                    p.lse[(b * p.Tq + at_t) * p.H + at_h] = on && sum != 0.0f ? top + logf(sum) : -kInf;
+                }
+            }
+        }
+    } else {
+        if (row >= rows)
+            return;
+        const float inv = p.splits > 1 ? 1.0f : (l == 0.0f || !live ? 0.0f : 1.0f / l);
+        const int64_t place = (b * p.Hkv + hk) * rows + row;
+#pragma unroll
+        for (int d = 0; d < W; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 v;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    v[x] = live ? acc[d][4 * i + x] * inv : 0.0f;
+                const int c = d * 32 + 8 * i + 4 * half;
+                if (p.splits > 1)
+                    store4(p.part + (split * p.part_rows + place) * (W * 32) + c, v);
+                else
+                    put4((T *)p.o + (b * p.Tq + t) * p.ldo + h * p.dh, c, p.dh, v);
+            }
+        if (half)
+            return;
+        if (p.splits > 1) {
+            p.stats[(split * p.part_rows + place) * 2] = m;
+            p.stats[(split * p.part_rows + place) * 2 + 1] = l;
+        } else if (p.lse) {
+            p.lse[(b * p.Tq + t) * p.H + h] = live && l != 0.0f ? m + logf(l) : -kInf;
+        }
+    }
+#endif
+}
+
+// Joins the parts of a row whose keys were split: eight lanes a row.
+template <class T>
+__global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
+{
+    const int64_t rows = p.Tq * p.share;
+    const int64_t place = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    if (place >= p.part_rows)
+        return;
+    const int64_t row = place % rows, hk = place / rows % p.Hkv, b = place / rows / p.Hkv;
+    const int64_t t = row / p.share, h = hk * p.share + row % p.share;
+    const int lane = threadIdx.x & 7, pitch = p.pitch;
+    float top = -kInf, sum = 0.0f;
+    for (int s = 0; s < p.splits; ++s)
+        top = __builtin_fmaxf(top, p.stats[(s * p.part_rows + place) * 2]);
+    const float base = top == -kInf ? 0.0f : top;
+    f32x4 v[4] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const int64_t at = s * p.part_rows + place;
+        const float m = p.stats[at * 2], l = p.stats[at * 2 + 1];
+        if (l == 0.0f)
+            continue;  // no key of this part counts
+        const float w = __builtin_amdgcn_exp2f((m - base) * kLog2e);
+        sum = __builtin_fmaf(w, l, sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (lane * 4 + e * 32 < pitch) {
+                const f32x4 a = load4(p.part + at * pitch + lane * 4 + e * 32);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    v[e][x] = __builtin_fmaf(w, a[x], v[e][x]);
+            }
+    }
+    const bool on = t < length_of(p.qlen, b, p.Tq);
+    const float inv = sum == 0.0f || !on ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            v[e][x] = on ? v[e][x] * inv : 0.0f;
+        put4((T *)p.o + (b * p.Tq + t) * p.ldo + h * p.dh, lane * 4 + e * 32, p.dh, v[e]);
+    }
+    if (lane == 0 && p.lse)
+        p.lse[(b * p.Tq + t) * p.H + h] = on && sum != 0.0f ? top + logf(sum) : -kInf;
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// delta and lse of every row of a head, query after query, in whole stages: rows
+// that do not count have lse = infinity, so that their weights are zero.  Eight
+// lanes a row.
+template <class T>
+__global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
+{
+    const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    if (at >= p.B * p.H * p.padded)
+        return;
+    const int64_t t = at % p.padded, h = at / p.padded % p.H, b = at / p.padded / p.H;
+    const int lane = threadIdx.x & 7;
+    float lse = kInf, sum = 0.0f;
+    if (t < length_of(p.qlen, b, p.Tq)) {
+        const int64_t row = b * p.Tq + t;
+        lse = p.lse[row * p.H + h];
+        if (lse == -kInf) {
+            lse = kInf;  // no key was left for it
+        } else {
+            const T *const o = (const T *)p.o + row * p.ldo + h * p.dh;
+            const T *const g = (const T *)p.d_o + row * p.lddo + h * p.dh;
+            for (int c = lane * 8; c < p.dh; c += 64) {
+                float x[8], y[8];
+                const int cnt = clamp8(p.dh - c);
+                load8(o + c, cnt, x);
+                load8(g + c, cnt, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sum = __builtin_fmaf(x[i], y[i], sum);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+        sum += __shfl_xor(sum, d);
+    if (lane == 0) {
+        p.row_lse[at] = lse;
+        p.row_delta[at] = sum;
+    }
+}
+
+// dq: a wave holds 32 query rows as in the forward kernel.
+template <class T, int W>
+struct BackwardQ {
+    typedef Shape<T, W> S;
+    typedef typename S::Lds Lds;
+    static constexpr int kStage = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kHalf = kStage * Lds::kBytes;
+};
+
+template <class T, int W>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const AttnParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef BackwardQ<T, W> F;
+    typedef typename F::Lds Lds;
+    constexpr int STEPS = F::S::STEPS;
+    __shared__ __attribute__((aligned(1024))) char memory[4 * F::kHalf];
+    RAR_LDS char *const lds = (RAR_LDS char *)memory;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+
+    int64_t id = in_order(blockIdx.x, p.blocks);
+    const int64_t tile = id % p.tiles;
+    id /= p.tiles;
+    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int64_t rows = p.Tq * p.share;
+    const int64_t first = tile * 128, row = first + wave * 32 + (lane & 31);
+    const int64_t t = row / p.share, h = hk * p.share + row % p.share;
+    const bool live = row < rows && t < qlen;
+    Frag<T> q[STEPS], g[STEPS];
+    load_row<T>(q, p.q, b * p.Tq + t, h, live);
+    load_row<T>(g, p.g, b * p.Tq + t, h, live);
+    const int64_t place = (b * p.H + h) * p.padded + t;
+    const float lse = live ? p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
+    const float lse2 = lse * kLog2e, scale2 = p.scale * kLog2e;
+
+    const int stages = first / p.share < qlen ? (int)((klen + F::kStage - 1) / F::kStage) : 0;
+    Loader<T, F::S::PITCH, F::kStage, 4> lk, lv;
+    lk.init(p.k, b * p.Tk, hk, klen);
+    lv.init(p.v, b * p.Tk, hk, klen);
+    f32x16 acc[W];
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+        acc[d] = zeros();
+    if (stages) {
+        lk.load(lds);
+        lv.load(lds + F::kHalf);
+        meet();
+    }
+    for (int n = 0; n < stages; ++n) {
+        RAR_LDS char *const here = lds + (n & 1) * 2 * F::kHalf;
+        RAR_LDS char *const next = lds + (2 - (n & 1) * 2) * F::kHalf;
+        if (n + 1 < stages) {
+            lk.advance();
+            lv.advance();
+            lk.load(next);
+            lv.load(next + F::kHalf);
+        }
+        const int64_t rest = klen - (int64_t)n * F::kStage;
+#pragma unroll
+        for (int e = 0; e < F::kStage / 32; ++e) {
+            f32x16 s = zeros(), dp = zeros();
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s, Lds::rows(here, e * 32, i), q[i]);
+                mma(dp, Lds::rows(here + F::kHalf, e * 32, i), g[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float w = weight<T>(s[i], p.scale, scale2, lse, lse2);
+                s[i] = w * (dp[i] - delta);
+            }
+            if (rest < F::kStage)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (e * 32 + row_of(i) + 4 * half >= rest)
+                        s[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                Frag<T> w;
+                w.set(s, 8 * j);
+#pragma unroll
+                for (int d = 0; d < W; ++d)
+                    mma(acc[d], Lds::cols(here, e * 32, j, d), w);
+            }
+        }
+        meet();
+    }
+    if (row >= rows)
+        return;
+    T *const out = (T *)p.dq + (b * p.Tq + t) * p.lddq + h * p.dh;
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 v;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                v[x] = live ? acc[d][4 * i + x] * p.scale : 0.0f;
+            put4(out, d * 32 + 8 * i + 4 * half, p.dh, v);
+        }
+#endif
+}
+
+// dk and dv: a wave holds 32 keys, and the queries of every head that shares
+// them pass by in stages.
+template <class T, int W>
+struct BackwardK {
+    typedef Shape<T, W> S;
+    typedef typename S::Lds Lds;
+    static constexpr int kStage = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kHalf = kStage * Lds::kBytes;
+    static constexpr int kBuffer = 2 * kHalf + 1024;    // q, do, lse and delta
+};
+
+template <class T, int W>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(const AttnParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef BackwardK<T, W> F;
+    typedef typename F::Lds Lds;
+    constexpr int STEPS = F::S::STEPS;
+    __shared__ __attribute__((aligned(1024))) char memory[2 * F::kBuffer];
+    RAR_LDS char *const lds = (RAR_LDS char *)memory;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+
+    int64_t id = in_order(blockIdx.x, p.blocks);
+    const int64_t tile = id % p.tiles;
+    id /= p.tiles;
+    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int64_t key = tile * 128 + wave * 32 + (lane & 31);
+    const bool live = key < klen;
+    Frag<T> k[STEPS], v[STEPS];
+    load_row<T>(k, p.k, b * p.Tk + key, hk, live);
+    load_row<T>(v, p.v, b * p.Tk + key, hk, live);
+    f32x16 dk[W], dv[W];
+#pragma unroll
+    for (int d = 0; d < W; ++d) {
+        dk[d] = zeros();
+        dv[d] = zeros();
+    }
+    const float scale2 = p.scale * kLog2e;
+    const int per_head = (int)((qlen + F::kStage - 1) / F::kStage);
+    const int stages = tile * 128 < klen ? per_head * (int)p.share : 0;
+    Loader<T, F::S::PITCH, F::kStage, 4> lq, lg;
+    int at = 0;  // stage within the head that is loaded next
+    int64_t head = hk * p.share;
+    auto load = [&](RAR_LDS char *to) __attribute__((always_inline)) {
+        if (at == 0) {
+            lq.init(p.q, b * p.Tq, head, qlen);
+            lg.init(p.g, b * p.Tq, head, qlen);
+        }
+        lq.load(to);
+        lg.load(to + F::kHalf);
+        if (wave < 2) {
+            // lse by the first wave, delta by the second: four bytes a lane, whole stages
+            const float *const from = (wave ? p.row_delta : p.row_lse) + (b * p.H + head) * p.padded + at * F::kStage;
+            const __amdgpu_buffer_rsrc_t r =
+                __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, F::kStage * 4, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(to + 2 * F::kHalf + wave * 256), 4, lane * 4, 0,
+                                                     0, 0);
+        }
+        lq.advance();
+        lg.advance();
+        if (++at == per_head) {
+            at = 0;
+            ++head;
+        }
+    };
+    if (stages) {
+        load(lds);
+        meet();
+    }
+    for (int n = 0; n < stages; ++n) {
+        RAR_LDS char *const here = lds + (n & 1) * F::kBuffer;
+        if (n + 1 < stages)
+            load(lds + (F::kBuffer - (n & 1) * F::kBuffer));
+        const RAR_LDS float *const lse = (const RAR_LDS float *)(here + 2 * F::kHalf);
+#pragma unroll
+        for (int e = 0; e < F::kStage / 32; ++e) {
+            f32x16 s = zeros(), dp = zeros();
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s, Lds::rows(here, e * 32, i), k[i]);
+                mma(dp, Lds::rows(here + F::kHalf, e * 32, i), v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 a = *(const RAR_LDS f32x4 *)(lse + e * 32 + 8 * i + 4 * half);
+                const f32x4 c = *(const RAR_LDS f32x4 *)(lse + 64 + e * 32 + 8 * i + 4 * half);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float w = weight<T>(s[4 * i + x], p.scale, scale2, a[x], a[x] * kLog2e);
+                    s[4 * i + x] = w;
+                    dp[4 * i + x] = w * (dp[4 * i + x] - c[x]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                Frag<T> w, ds;
+                w.set(s, 8 * j);
+                ds.set(dp, 8 * j);
+#pragma unroll
+                for (int d = 0; d < W; ++d) {
+                    mma(dv[d], Lds::cols(here + F::kHalf, e * 32, j, d), w);
+                    mma(dk[d], Lds::cols(here, e * 32, j, d), ds);
+                }
+            }
+        }
+        meet();
+    }
+    if (key >= p.Tk)
+        return;
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = d * 32 + 8 * i + 4 * half;
+            f32x4 a, e;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                a[x] = live ? dk[d][4 * i + x] * p.scale : 0.0f;
+                e[x] = live ? dv[d][4 * i + x] : 0.0f;
+            }
+            if (p.dk)
+                put4((T *)p.dk + (b * p.Tk + key) * p.lddk + hk * p.dh, c, p.dh, a);
+            if (p.dv)
+                put4((T *)p.dv + (b * p.Tk + key) * p.lddv + hk * p.dh, c, p.dh, e);
+        }
+#endif
+}
+
+// Copies of operands whose heads are not whole 16-byte groups at 16-byte aligned
+// addresses: every head's columns to `cols`, zero behind dh.
+template <class T>
+__global__ void __launch_bounds__(256) rar_attn_pack(const AttnPack p)
+{
+    constexpr int kPer = 16 / sizeof(T);
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int e = 0;
+    while (e < p.count && i >= p.item[e].chunks)
+        i -= p.item[e++].chunks;
+    if (e == p.count)
+        return;
+    const AttnPack::Item &m = p.item[e];
+    const int per_head = p.cols / kPer;
+    const int64_t row = i / (m.heads * per_head);
+    const int64_t in = i - row * (m.heads * per_head);
+    const int64_t head = in / per_head, c = (in - head * per_head) * kPer;
+    const T *const from = (const T *)m.src + row * m.ld + head * p.dh + c;
+    float v[8];
+    load8(from, clamp8(p.dh - c < kPer ? p.dh - c : kPer), v);
+    T *const to = (T *)m.dst + (row * m.heads + head) * p.cols + c;
+    if constexpr (sizeof(T) == 4)
+        store4(to, f32x4{v[0], v[1], v[2], v[3]});
+    else
+        store8(to, 8, v);
+}
+
+template <class P>
+struct Kernels {
+    void (*f32)(P), (*bf)(P);
+};
+
+template <class T>
+void (*rows_kernel(int w, bool keys))(AttnParams)
+{
+    switch (w) {
+    case 1: return keys ? rar_attn_rows<T, 1, true> : rar_attn_rows<T, 1, false>;
+    case 2: return keys ? rar_attn_rows<T, 2, true> : rar_attn_rows<T, 2, false>;
+    case 3: return keys ? rar_attn_rows<T, 3, true> : rar_attn_rows<T, 3, false>;
+    default: return keys ? rar_attn_rows<T, 4, true> : rar_attn_rows<T, 4, false>;
+    }
+}
+
+template <class T>
+void (*dq_kernel(int w))(AttnParams)
+{
+    switch (w) {
+    case 1: return rar_attn_dq<T, 1>;
+    case 2: return rar_attn_dq<T, 2>;
+    case 3: return rar_attn_dq<T, 3>;
+    default: return rar_attn_dq<T, 4>;
+    }
+}
+
+template <class T>
+void (*dkv_kernel(int w))(AttnParams)
+{
+    switch (w) {
+    case 1: return rar_attn_dkv<T, 1>;
+    case 2: return rar_attn_dkv<T, 2>;
+    case 3: return rar_attn_dkv<T, 3>;
+    default: return rar_attn_dkv<T, 4>;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool keys, hipStream_t st)
+{
+    const int w = (p.dh + 31) / 32;
+    if (dt == RAR_BF16)
+        return launch(rows_kernel<bf16>(w, keys), (unsigned)p.blocks, 256, st, p);
+    return launch(rows_kernel<float>(w, keys), (unsigned)p.blocks, keys ? 128 : 256, st, p);
+}
+
+hipError_t launch_attn_join(rar_dtype dt, const AttnParams &p, hipStream_t st)
+{
+    return launch(dt == RAR_BF16 ? rar_attn_join<bf16> : rar_attn_join<float>, (unsigned)((p.part_rows + 31) / 32), 256,
+                  st, p);
+}
+
+hipError_t launch_attn_delta(rar_dtype dt, const AttnParams &p, hipStream_t st)
+{
+    return launch(dt == RAR_BF16 ? rar_attn_delta<bf16> : rar_attn_delta<float>,
+                  (unsigned)((p.B * p.H * p.padded + 31) / 32), 256, st, p);
+}
+
+hipError_t launch_attn_dq(rar_dtype dt, const AttnParams &p, hipStream_t st)
+{
+    const int w = (p.dh + 31) / 32;
+    return launch(dt == RAR_BF16 ? dq_kernel<bf16>(w) : dq_kernel<float>(w), (unsigned)p.blocks, 256, st, p);
+}
+
+hipError_t launch_attn_dkv(rar_dtype dt, const AttnParams &p, hipStream_t st)
+{
+    const int w = (p.dh + 31) / 32;
+    return launch(dt == RAR_BF16 ? dkv_kernel<bf16>(w) : dkv_kernel<float>(w), (unsigned)p.blocks, 256, st, p);
+}
+
+hipError_t launch_attn_pack(rar_dtype dt, const AttnPack &p, hipStream_t st)
+{
+    int64_t chunks = 0;
+    for (int i = 0; i < p.count; ++i)
+        chunks += p.item[i].chunks;
+    return launch(dt == RAR_BF16 ? rar_attn_pack<bf16> : rar_attn_pack<float>, (unsigned)((chunks + 255) / 256), 256, st,
+                  p);
+}
+
+}  // namespace rar

@@ -1,6 +1,7 @@
-// ops_internal.h -- declarations shared by the host code (ops_host.cpp) and the
-// kernels (linear.hip, embed.hip, ckpt.hip) of the gradient-producing operators
-// of librar.so.  Not part of the public ABI.
+// ops_internal.h -- declarations shared by the host code (ops_host.cpp,
+// block_host.cpp) and the kernels (linear.hip, embed.hip, ckpt.hip, norm.hip,
+// dropout.hip, attn.hip, logprob.hip) of the operators of librar.so.  Not part
+// of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -123,6 +124,107 @@ struct EmbedGradParams {
     void *ws;
 };
 
+struct NormParams {
+    const void *x, *o;       // o: or nullptr
+    int64_t ldx, ldo;
+    const void *post_w, *post_b, *gate, *pre_w, *pre_b;  // each or nullptr
+    void *h, *u;             // each or nullptr
+    int64_t ldh, ldu;
+    int64_t rows, cols;
+    float a, s, eps;
+    int post, pre;           // rar_norm_kind
+};
+
+struct NormGradParams {
+    const void *dh, *du, *o, *h;             // dh, du and o: or nullptr
+    int64_t lddh, lddu, ldo, ldh;
+    const void *post_w, *post_b, *gate, *pre_w;
+    void *dx, *d_o;                          // each or nullptr
+    int64_t lddx, lddo;
+    void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
+    int accumulate;
+    float *part;                             // [chunks][4][pitch] column sums: g o^, g, du h^, du
+    int64_t chunks, pitch;
+    bool sum_post, sum_pre;                  // which pairs are wanted
+    int64_t rows, cols;
+    float a, s, eps;
+    int post, pre;
+};
+
+struct DropoutParams {
+    const void *x, *r;
+    void *y;
+    int64_t ldx, ldr, ldy, rows, cols;
+    const int64_t *step;
+    uint32_t seed_lo, seed_hi;
+    uint32_t threshold;      // a draw below it drops
+    float scale;
+};
+
+// A matrix of heads: element (row, head, column) at row ld + head hs + column;
+// `cols` columns of a head, a whole number of 16-byte groups, aligned.
+struct AttnOperand {
+    const void *p;
+    int64_t ld, hs;
+    int cols;
+};
+
+struct AttnParams {
+    AttnOperand q, k, v, g;  // g: do
+    int64_t B, Tq, Tk, H, Hkv, share;
+    int dh;
+    float scale;
+    const int64_t *qlen, *klen;  // or nullptr
+    void *o;
+    int64_t ldo;
+    float *lse;              // forward: or nullptr
+    // grid: blocks = B * Hkv * splits * tiles
+    int64_t blocks, tiles;
+    int splits;
+    int stages;              // forward: stages of keys of one split
+    float *part, *stats;     // [splits][part_rows][pitch], [splits][part_rows][maximum, sum]
+    int64_t part_rows;
+    int pitch;
+    // backward
+    const void *d_o;
+    int64_t lddo;
+    float *row_lse, *row_delta;  // [B][H][padded]
+    int64_t padded;              // Tq in whole stages
+    void *dq, *dk, *dv;
+    int64_t lddq, lddk, lddv;
+};
+
+constexpr int kAttnRows = 128;       // query rows of a workgroup, or keys of one of dk and dv
+constexpr int kAttnFewRows = 32;     // rows whose keys are shared out among the waves
+constexpr int kAttnPad = 64;         // whole stages of queries
+
+// Keys of a stage of the forward kernel.
+inline int attn_stage(rar_dtype dt, bool keys) { return dt == RAR_BF16 ? (keys ? 128 : 64) : (keys ? 64 : 32); }
+
+struct AttnPack {
+    struct Item {
+        const void *src;
+        void *dst;
+        int64_t ld, heads, chunks;  // chunks: of 16 bytes, in all
+    } item[4];
+    int count, dh, cols;
+};
+
+struct LogprobParams {
+    const void *z;
+    int64_t ldz;
+    float scale;
+    const int64_t *targets;
+    const float *dlogp, *dentropy;
+    float *logp, *entropy;
+    int top;
+    int64_t *top_ids;
+    float *top_logp;
+    void *dz;                // or nullptr
+    int64_t lddz;
+    int64_t rows, cols;
+};
+
 inline unsigned blocks_of(const GemmParams &p) { return (unsigned)(p.tiles_m * p.tiles_n * p.splits); }
 
 hipError_t launch_forward(rar_dtype dt, const GemmParams &p, int tile, hipStream_t st);
@@ -156,5 +258,19 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
 int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D);
 // Whether each of its launches has at most `lanes` lanes.
 bool embed_grad_fits(int64_t T, int64_t D, int64_t grad_bytes, int64_t lanes);
+// Rows of column sums that the norms' backward kernel writes.
+int64_t norm_chunks(int64_t rows, int64_t cols);
+hipError_t launch_norm(rar_dtype dt, const NormParams &p, hipStream_t st);
+hipError_t launch_norm_grad(rar_dtype dt, const NormGradParams &p, hipStream_t st);
+hipError_t launch_norm_sums(rar_dtype dt, const NormGradParams &p, hipStream_t st);
+hipError_t launch_dropout(rar_dtype dt, const DropoutParams &p, hipStream_t st);
+// keys: rows of at most kAttnFewRows a key head, keys shared out among the waves.
+hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool keys, hipStream_t st);
+hipError_t launch_attn_join(rar_dtype dt, const AttnParams &p, hipStream_t st);
+hipError_t launch_attn_delta(rar_dtype dt, const AttnParams &p, hipStream_t st);
+hipError_t launch_attn_dq(rar_dtype dt, const AttnParams &p, hipStream_t st);
+hipError_t launch_attn_dkv(rar_dtype dt, const AttnParams &p, hipStream_t st);
+hipError_t launch_attn_pack(rar_dtype dt, const AttnPack &p, hipStream_t st);
+hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st);
 
 }  // namespace rar

@@ -1384,4 +1384,4 @@ extern "C" const char *rar_strerror(rar_status s)
     return "unknown status";
 }
 
-extern "C" int rar_version(void) { return 700; }  // 0.7.0: rar_embed_*, rar_linear_*, rar_ckpt_*
+extern "C" int rar_version(void) { return 800; }  // 0.8.0: rar_norm_*, rar_dropout, rar_attn_*, rar_logprob*
