@@ -35,6 +35,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr uint32_t kOutOfRange = 0x80000000u;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kInf = __builtin_inff();
+// How far a row's scores may pass the maximum that its weights are taken from
+// before the accumulator is scaled again: weights stay under e^8.
+constexpr float kSlack = 8.0f;
 
 // ---------------------------------------------------------------------------
 // Products
@@ -226,20 +229,56 @@ struct Loader {
     }
 };
 
-// Own loads into LDS and own LDS reads are done; then everyone's.
-__device__ __forceinline__ void meet()
+// A half of LDS, as a constant: addresses in it are then parts of the instructions.
+template <int N>
+struct Half {
+    __device__ constexpr int operator()() const { return N; }
+};
+
+// Nothing moves across: what stands before is issued before what stands behind.
+__device__ __forceinline__ void schedule_fence()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_sched_barrier(0);
+#endif
 }
 
-// Workgroups go to the eight XCDs in turn; each XCD gets one run of the work, so
-// that its L2 holds the keys (or queries) that neighbours share.
-__device__ __forceinline__ int64_t in_order(int64_t id, int64_t total)
+// Own loads into LDS and own LDS reads are done; then everyone's.  (By the builtin:
+// of a wait in assembly the compiler knows nothing, and it would wait again, in the
+// loop, for the loads before it.)
+__device__ __forceinline__ void meet()
 {
-    const int64_t per = total / 8;
-    return id < per * 8 ? (id % 8) * per + id / 8 : id;
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#endif
+}
+
+// Workgroups go to the eight XCDs in turn.  The work of one sequence and key head
+// goes to one XCD, whose L2 then holds the keys (or queries) that it shares, and
+// neighbouring heads to different ones: sequences of different lengths weigh on
+// all XCDs alike.  (Runs of whole sequences left the XCD of the longest one
+// working alone.)  What is left of the heads behind the last eight is spread out.
+struct Place {
+    int64_t b, hk, in;  // in: which of the head's workgroups
+};
+
+__device__ __forceinline__ Place place_of(int64_t heads, int64_t Hkv, int64_t each)
+{
+    const int64_t id = blockIdx.x, whole = heads / 8 * 8;
+    int64_t head, in;
+    if (id < whole * each) {
+        const int64_t j = id / 8;
+        head = j / each * 8 + id % 8;
+        in = j % each;
+    } else {
+        const int64_t j = id - whole * each;
+        head = whole + j / each;
+        in = j % each;
+    }
+    return Place{head / Hkv, head % Hkv, in};
 }
 
 __device__ __forceinline__ int64_t length_of(const int64_t *lens, int64_t b, int64_t most)
@@ -269,14 +308,17 @@ __device__ __forceinline__ void put4(T *row, int c, int cols, f32x4 v)
             row[c + i] = from_f32<T>(v[i]);
 }
 
-// e^(scale s - shift): bf16 in one rounding of the exponent; binary32 subtracts
-// first, so that the weights near one, which carry the result, keep their digits.
+// e^(scale s - shift).  bf16 takes scale and shift times log2 e and rounds the
+// exponent once; binary32 subtracts first, so that the weights near one, which
+// carry the result, keep their digits.
 template <class T>
-__device__ __forceinline__ float weight(float s, float scale, float scale2, float shift, float shift2)
+constexpr float kUnit = sizeof(T) == 2 ? kLog2e : 1.0f;
+
+template <class T>
+__device__ __forceinline__ float weight(float s, float scale, float shift)
 {
-    if (sizeof(T) == 2)
-        return __builtin_amdgcn_exp2f(__builtin_fmaf(s, scale2, -shift2));
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(s, scale, -shift) * kLog2e);
+    const float x = __builtin_fmaf(s, scale, -shift);
+    return __builtin_amdgcn_exp2f(sizeof(T) == 2 ? x : x * kLog2e);
 }
 
 template <class T, int W>
@@ -344,12 +386,9 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
-    int64_t id = in_order(blockIdx.x, p.blocks);
-    const int64_t tile = id % p.tiles;
-    id /= p.tiles;
-    const int split = (int)(id % p.splits);
-    id /= p.splits;
-    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles * p.splits);
+    const int64_t tile = at.in % p.tiles, hk = at.hk, b = at.b;
+    const int split = (int)(at.in / p.tiles);
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
     const int64_t rows = p.Tq * p.share;
 
@@ -374,16 +413,17 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
     for (int d = 0; d < W; ++d)
         acc[d] = zeros();
     float m = -kInf, l = 0.0f;
-    const float scale2 = p.scale * kLog2e;
+    const float scale = p.scale * kUnit<T>;
 
     if (stages) {
         lk.load(lds);
         lv.load(lds + F::kHalf);
-        meet();
     }
-    for (int n = 0; n < stages; ++n) {
-        RAR_LDS char *const here = lds + (n & 1) * 2 * F::kHalf;
-        RAR_LDS char *const next = lds + (2 - (n & 1) * 2) * F::kHalf;
+    meet();
+    // One stage, in the half of LDS that BUF names.
+    auto stage = [&](auto BUF, int n) __attribute__((always_inline)) {
+        RAR_LDS char *const here = lds + BUF() * 2 * F::kHalf;
+        RAR_LDS char *const next = lds + (2 - BUF() * 2) * F::kHalf;
         if (n + 1 < stages) {
             lk.advance();
             lv.advance();
@@ -391,16 +431,33 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
             lv.load(next + F::kHalf);
         }
         const int r0 = KEYS ? wave * 32 : 0;
+        // every fragment of the keys is on its way before the first product
+        Frag<T> k[F::kTiles][STEPS], v[2][W];
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e)
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+                k[e][i] = Lds::rows(here, r0 + e * 32, i);
+        schedule_fence();
         f32x16 s[F::kTiles];
 #pragma unroll
         for (int e = 0; e < F::kTiles; ++e) {
             s[e] = zeros();
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-                mma(s[e], Lds::rows(here, r0 + e * 32, i), q[i]);
+                mma(s[e], k[e][i], q[i]);
         }
+        auto values = [&](int e) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int d = 0; d < W; ++d)
+                    v[j][d] = Lds::cols(here + F::kHalf, r0 + e * 32, j, d);
+        };
+        values(0);
+        schedule_fence();
         // keys behind the last one that counts
-        const int64_t rest = kend - k0 - (int64_t)n * F::kStage - r0;
+        const int rest = (int)(kend - k0 - (int64_t)n * F::kStage) - r0;
         if (rest < F::kTiles * 32)
 #pragma unroll
             for (int e = 0; e < F::kTiles; ++e)
@@ -415,10 +472,10 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
             for (int i = 0; i < 16; ++i)
                 top = __builtin_fmaxf(top, s[e][i]);
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        top = __builtin_fmaxf(top * p.scale, m);
-        const float base = top == -kInf ? 0.0f : top, base2 = base * kLog2e;
-        if (__any(top > m)) {
-            const float down = __builtin_amdgcn_exp2f((m - base) * kLog2e);
+        top *= p.scale;
+        if (__any(top > m + kSlack || (m == -kInf && top > m))) {
+            top = __builtin_fmaxf(top, m);
+            const float down = __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
             l *= down;
 #pragma unroll
             for (int d = 0; d < W; ++d)
@@ -427,23 +484,32 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
                     acc[d][i] *= down;
             m = top;
         }
+        const float base = m == -kInf ? 0.0f : m * kUnit<T>;
 #pragma unroll
         for (int e = 0; e < F::kTiles; ++e) {
+            Frag<T> w[2];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[e][i] = weight<T>(s[e][i], p.scale, scale2, base, base2);
+                s[e][i] = weight<T>(s[e][i], scale, base);
                 l += s[e][i];
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                Frag<T> w;
-                w.set(s[e], 8 * j);
+            for (int j = 0; j < 2; ++j)
+                w[j].set(s[e], 8 * j);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int d = 0; d < W; ++d)
-                    mma(acc[d], Lds::cols(here + F::kHalf, r0 + e * 32, j, d), w);
-            }
+                    mma(acc[d], v[j][d], w[j]);
+            if (e + 1 < F::kTiles)
+                values(e + 1);
         }
         meet();
+    };
+    for (int n = 0; n < stages; n += 2) {
+        stage(Half<0>{}, n);
+        if (n + 1 < stages)
+            stage(Half<1>{}, n + 1);
     }
     l += __shfl_xor(l, 32);
 
@@ -463,8 +529,8 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
         meet();
         // eight lanes a row, W quads of columns a lane
         for (int r = threadIdx.x >> 3; r < 32; r += F::kWaves * 8) {
-            const int64_t at = first + r;
-            if (at >= rows)
+            const int64_t to = first + r;
+            if (to >= rows)
                 break;
             float top = -kInf, sum = 0.0f, w[F::kWaves];
 #pragma unroll
@@ -478,10 +544,10 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
                 w[i] = li == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((mi - (top == -kInf ? 0.0f : top)) * kLog2e);
                 sum = __builtin_fmaf(w[i], li, sum);
             }
-            const int64_t at_t = at / p.share, at_h = hk * p.share + at % p.share;
+            const int64_t at_t = to / p.share, at_h = hk * p.share + to % p.share;
             const bool on = at_t < qlen;
             const float inv = p.splits > 1 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
-            const int64_t place = (b * p.Hkv + hk) * rows + at;
+            const int64_t place = (b * p.Hkv + hk) * rows + to;
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 const int c = ((threadIdx.x & 7) + e * 8) * 4;
@@ -590,8 +656,8 @@ __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
 // Backward
 // ---------------------------------------------------------------------------
 
-// delta and lse of every row of a head, query after query, in whole stages: rows
-// that do not count have lse = infinity, so that their weights are zero.  Eight
+// delta and lse (in the weights' unit) of every row of a head, query after query, in
+// whole stages: rows that do not count have lse = infinity, so that their weights are zero.  Eight
 // lanes a row.
 template <class T>
 __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
@@ -625,7 +691,7 @@ __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
     for (int d = 1; d < 8; d *= 2)
         sum += __shfl_xor(sum, d);
     if (lane == 0) {
-        p.row_lse[at] = lse;
+        p.row_lse[at] = lse * kUnit<T>;
         p.row_delta[at] = sum;
     }
 }
@@ -635,12 +701,13 @@ template <class T, int W>
 struct BackwardQ {
     typedef Shape<T, W> S;
     typedef typename S::Lds Lds;
-    static constexpr int kStage = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;  // of 32 rows, a stage
+    static constexpr int kStage = kTiles * 32;
     static constexpr int kHalf = kStage * Lds::kBytes;
 };
 
 template <class T, int W>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const AttnParams p)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn_dq(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef BackwardQ<T, W> F;
@@ -650,10 +717,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
-    int64_t id = in_order(blockIdx.x, p.blocks);
-    const int64_t tile = id % p.tiles;
-    id /= p.tiles;
-    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles);
+    const int64_t tile = at.in, hk = at.hk, b = at.b;
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
     const int64_t rows = p.Tq * p.share;
     const int64_t first = tile * 128, row = first + wave * 32 + (lane & 31);
@@ -664,7 +729,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const
     load_row<T>(g, p.g, b * p.Tq + t, h, live);
     const int64_t place = (b * p.H + h) * p.padded + t;
     const float lse = live ? p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
-    const float lse2 = lse * kLog2e, scale2 = p.scale * kLog2e;
+    const float scale = p.scale * kUnit<T>;
 
     const int stages = first / p.share < qlen ? (int)((klen + F::kStage - 1) / F::kStage) : 0;
     Loader<T, F::S::PITCH, F::kStage, 4> lk, lv;
@@ -677,46 +742,68 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const
     if (stages) {
         lk.load(lds);
         lv.load(lds + F::kHalf);
-        meet();
     }
-    for (int n = 0; n < stages; ++n) {
-        RAR_LDS char *const here = lds + (n & 1) * 2 * F::kHalf;
-        RAR_LDS char *const next = lds + (2 - (n & 1) * 2) * F::kHalf;
+    meet();
+    auto stage = [&](auto BUF, int n) __attribute__((always_inline)) {
+        RAR_LDS char *const here = lds + BUF() * 2 * F::kHalf;
+        RAR_LDS char *const next = lds + (2 - BUF() * 2) * F::kHalf;
         if (n + 1 < stages) {
             lk.advance();
             lv.advance();
             lk.load(next);
             lv.load(next + F::kHalf);
         }
-        const int64_t rest = klen - (int64_t)n * F::kStage;
-#pragma unroll
-        for (int e = 0; e < F::kStage / 32; ++e) {
-            f32x16 s = zeros(), dp = zeros();
+        const int rest = (int)(klen - (int64_t)n * F::kStage);
+        f32x16 s[F::kTiles], dp[F::kTiles];
+        Frag<T> k[STEPS], v[STEPS], kt[2][W];
+        auto scores = [&](int e) __attribute__((always_inline)) {
+            s[e] = zeros();
+            dp[e] = zeros();
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                mma(s, Lds::rows(here, e * 32, i), q[i]);
-                mma(dp, Lds::rows(here + F::kHalf, e * 32, i), g[i]);
+                k[i] = Lds::rows(here, e * 32, i);
+                v[i] = Lds::rows(here + F::kHalf, e * 32, i);
             }
+            schedule_fence();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float w = weight<T>(s[i], p.scale, scale2, lse, lse2);
-                s[i] = w * (dp[i] - delta);
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s[e], k[i], q[i]);
+                mma(dp[e], v[i], g[i]);
             }
+        };
+        scores(0);
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int d = 0; d < W; ++d)
+                    kt[j][d] = Lds::cols(here, e * 32, j, d);
+            if (e + 1 < F::kTiles)
+                scores(e + 1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[e][i] = weight<T>(s[e][i], scale, lse) * (dp[e][i] - delta);
             if (rest < F::kStage)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (e * 32 + row_of(i) + 4 * half >= rest)
-                        s[i] = 0.0f;
+                        s[e][i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 Frag<T> w;
-                w.set(s, 8 * j);
+                w.set(s[e], 8 * j);
 #pragma unroll
                 for (int d = 0; d < W; ++d)
-                    mma(acc[d], Lds::cols(here, e * 32, j, d), w);
+                    mma(acc[d], kt[j][d], w);
             }
         }
         meet();
+    };
+    for (int n = 0; n < stages; n += 2) {
+        stage(Half<0>{}, n);
+        if (n + 1 < stages)
+            stage(Half<1>{}, n + 1);
     }
     if (row >= rows)
         return;
@@ -740,13 +827,14 @@ template <class T, int W>
 struct BackwardK {
     typedef Shape<T, W> S;
     typedef typename S::Lds Lds;
-    static constexpr int kStage = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;  // of 32 rows, a stage
+    static constexpr int kStage = kTiles * 32;
     static constexpr int kHalf = kStage * Lds::kBytes;
     static constexpr int kBuffer = 2 * kHalf + 1024;    // q, do, lse and delta
 };
 
 template <class T, int W>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(const AttnParams p)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn_dkv(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef BackwardK<T, W> F;
@@ -756,10 +844,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(cons
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
-    int64_t id = in_order(blockIdx.x, p.blocks);
-    const int64_t tile = id % p.tiles;
-    id /= p.tiles;
-    const int64_t hk = id % p.Hkv, b = id / p.Hkv;
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles);
+    const int64_t tile = at.in, hk = at.hk, b = at.b;
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
     const int64_t key = tile * 128 + wave * 32 + (lane & 31);
     const bool live = key < klen;
@@ -772,14 +858,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(cons
         dk[d] = zeros();
         dv[d] = zeros();
     }
-    const float scale2 = p.scale * kLog2e;
+    const float scale = p.scale * kUnit<T>;
     const int per_head = (int)((qlen + F::kStage - 1) / F::kStage);
     const int stages = tile * 128 < klen ? per_head * (int)p.share : 0;
     Loader<T, F::S::PITCH, F::kStage, 4> lq, lg;
-    int at = 0;  // stage within the head that is loaded next
+    int ahead = 0;  // stage within the head that is loaded next
     int64_t head = hk * p.share;
     auto load = [&](RAR_LDS char *to) __attribute__((always_inline)) {
-        if (at == 0) {
+        if (ahead == 0) {
             lq.init(p.q, b * p.Tq, head, qlen);
             lg.init(p.g, b * p.Tq, head, qlen);
         }
@@ -787,7 +873,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(cons
         lg.load(to + F::kHalf);
         if (wave < 2) {
             // lse by the first wave, delta by the second: four bytes a lane, whole stages
-            const float *const from = (wave ? p.row_delta : p.row_lse) + (b * p.H + head) * p.padded + at * F::kStage;
+            const float *const from = (wave ? p.row_delta : p.row_lse) + (b * p.H + head) * p.padded + ahead * F::kStage;
             const __amdgpu_buffer_rsrc_t r =
                 __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, F::kStage * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(to + 2 * F::kHalf + wave * 256), 4, lane * 4, 0,
@@ -795,52 +881,77 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dkv(cons
         }
         lq.advance();
         lg.advance();
-        if (++at == per_head) {
-            at = 0;
+        if (++ahead == per_head) {
+            ahead = 0;
             ++head;
         }
     };
-    if (stages) {
+    if (stages)
         load(lds);
-        meet();
-    }
-    for (int n = 0; n < stages; ++n) {
-        RAR_LDS char *const here = lds + (n & 1) * F::kBuffer;
+    meet();
+    auto stage = [&](auto BUF, int n) __attribute__((always_inline)) {
+        RAR_LDS char *const here = lds + BUF() * F::kBuffer;
         if (n + 1 < stages)
-            load(lds + (F::kBuffer - (n & 1) * F::kBuffer));
+            load(lds + (1 - BUF()) * F::kBuffer);
         const RAR_LDS float *const lse = (const RAR_LDS float *)(here + 2 * F::kHalf);
-#pragma unroll
-        for (int e = 0; e < F::kStage / 32; ++e) {
-            f32x16 s = zeros(), dp = zeros();
+        f32x16 s[F::kTiles], dp[F::kTiles];
+        Frag<T> q[STEPS], g[STEPS], qt[2][W], gt[2][W];
+        auto scores = [&](int e) __attribute__((always_inline)) {
+            s[e] = zeros();
+            dp[e] = zeros();
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                mma(s, Lds::rows(here, e * 32, i), k[i]);
-                mma(dp, Lds::rows(here + F::kHalf, e * 32, i), v[i]);
+                q[i] = Lds::rows(here, e * 32, i);
+                g[i] = Lds::rows(here + F::kHalf, e * 32, i);
             }
+            schedule_fence();
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s[e], q[i], k[i]);
+                mma(dp[e], g[i], v[i]);
+            }
+        };
+        scores(0);
+#pragma unroll
+        for (int e = 0; e < F::kTiles; ++e) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int d = 0; d < W; ++d) {
+                    gt[j][d] = Lds::cols(here + F::kHalf, e * 32, j, d);
+                    qt[j][d] = Lds::cols(here, e * 32, j, d);
+                }
+            if (e + 1 < F::kTiles)
+                scores(e + 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 a = *(const RAR_LDS f32x4 *)(lse + e * 32 + 8 * i + 4 * half);
                 const f32x4 c = *(const RAR_LDS f32x4 *)(lse + 64 + e * 32 + 8 * i + 4 * half);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float w = weight<T>(s[4 * i + x], p.scale, scale2, a[x], a[x] * kLog2e);
-                    s[4 * i + x] = w;
-                    dp[4 * i + x] = w * (dp[4 * i + x] - c[x]);
+                    const float w = weight<T>(s[e][4 * i + x], scale, a[x]);
+                    s[e][4 * i + x] = w;
+                    dp[e][4 * i + x] = w * (dp[e][4 * i + x] - c[x]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 Frag<T> w, ds;
-                w.set(s, 8 * j);
-                ds.set(dp, 8 * j);
+                w.set(s[e], 8 * j);
+                ds.set(dp[e], 8 * j);
 #pragma unroll
                 for (int d = 0; d < W; ++d) {
-                    mma(dv[d], Lds::cols(here + F::kHalf, e * 32, j, d), w);
-                    mma(dk[d], Lds::cols(here, e * 32, j, d), ds);
+                    mma(dv[d], gt[j][d], w);
+                    mma(dk[d], qt[j][d], ds);
                 }
             }
         }
         meet();
+    };
+    for (int n = 0; n < stages; n += 2) {
+        stage(Half<0>{}, n);
+        if (n + 1 < stages)
+            stage(Half<1>{}, n + 1);
     }
     if (key >= p.Tk)
         return;
