@@ -34,6 +34,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kInf = __builtin_inff();
 // How far a row's scores may pass the maximum that its weights are taken from
 // before the accumulator is scaled again: weights stay under e^8.
@@ -181,6 +182,7 @@ struct Tile {
 // destination is linear in the lane, so the spread is applied to the address
 // that each lane reads.  The descriptor ends with the last row that counts: rows
 // behind it, and chunks behind the head's columns, read as zero.
+// With WAVES = 1 a wave loads a tile of its own.
 template <class T, int PITCH, int ROWS, int WAVES>
 struct Loader {
     typedef Tile<T, PITCH> Lds;
@@ -193,7 +195,7 @@ struct Loader {
 
     __device__ __forceinline__ void init(const AttnOperand &m, int64_t row, int64_t head, int64_t rows)
     {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = WAVES > 1 ? threadIdx.x >> 6 : 0, lane = threadIdx.x & 63;
         base = (const char *)m.p + (row * m.ld + head * m.hs) * Lds::ES;
         pitch = m.ld * Lds::ES;
         width = m.cols * Lds::ES;
@@ -209,7 +211,7 @@ struct Loader {
     __device__ __forceinline__ void load(RAR_LDS char *__restrict__ lds)
     {
 #if defined(__HIP_DEVICE_COMPILE__)
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int wave = WAVES > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
         int64_t n = left > 0 ? (left - 1) * pitch + width : 0;
         if (n > 0x7fffffff)
             n = 0x7fffffff;
@@ -221,11 +223,10 @@ struct Loader {
 #endif
     }
 
-    // The next ROWS rows.
-    __device__ __forceinline__ void advance()
+    __device__ __forceinline__ void advance(int rows = ROWS)
     {
-        base += ROWS * pitch;
-        left -= ROWS;
+        base += rows * pitch;
+        left -= rows;
     }
 };
 
@@ -260,7 +261,9 @@ __device__ __forceinline__ void meet()
 // goes to one XCD, whose L2 then holds the keys (or queries) that it shares, and
 // neighbouring heads to different ones: sequences of different lengths weigh on
 // all XCDs alike.  (Runs of whole sequences left the XCD of the longest one
-// working alone.)  What is left of the heads behind the last eight is spread out.
+// working alone.)  From one eight to the next the heads move on by an XCD: a head's
+// keys lie a row of all heads apart, and the same heads on an XCD would use few of
+// its L2's channels.  What is left behind the last eight heads is spread out.
 struct Place {
     int64_t b, hk, in;  // in: which of the head's workgroups
 };
@@ -271,7 +274,7 @@ __device__ __forceinline__ Place place_of(int64_t heads, int64_t Hkv, int64_t ea
     int64_t head, in;
     if (id < whole * each) {
         const int64_t j = id / 8;
-        head = j / each * 8 + id % 8;
+        head = j / each * 8 + (id + j / each) % 8;
         in = j % each;
     } else {
         const int64_t j = id - whole * each;
@@ -353,36 +356,103 @@ __device__ __forceinline__ void load_row(Frag<T> (&f)[N], const AttnOperand &m, 
 // Forward
 // ---------------------------------------------------------------------------
 //
-// A wave holds 32 query rows.  In the usual form the waves of a workgroup take
-// different rows and share the staged keys; with few rows (KEYS) they take the
-// same rows and different keys of a stage, and are joined through LDS at the
-// end.  Running maximum and sum stay in the lane of the row; the accumulator is
-// scaled only where some row's maximum has grown.
-template <class T>
-constexpr int forward_waves(bool keys) { return keys && sizeof(T) == 4 ? 2 : 4; }
+// A wave holds 32 query rows, a row a lane and its other half; running maximum,
+// sum and accumulator stay there.
+template <class T, int W>
+struct Rows {
+    f32x16 acc[W];
+    float m, l;
 
-template <class T, int W, bool KEYS>
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int d = 0; d < W; ++d)
+            acc[d] = zeros();
+        m = -kInf;
+        l = 0.0f;
+    }
+
+    // Scores of TILES * 32 keys, of which `rest` count, become weights.  The
+    // accumulator is scaled only where some row's scores have passed its maximum
+    // by kSlack: with 32 rows to a wave, some row's maximum grows in almost every
+    // step.
+    template <int TILES>
+    __device__ __forceinline__ void weigh(f32x16 (&s)[TILES], int rest, float scale)
+    {
+        const int half = (threadIdx.x & 63) >> 5;
+        if (rest < TILES * 32)
+#pragma unroll
+            for (int e = 0; e < TILES; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (e * 32 + row_of(i) + 4 * half >= rest)
+                        s[e][i] = -kInf;
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 0; e < TILES; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = __builtin_fmaxf(top, s[e][i]);
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32)) * scale;
+        if (__any(top > m + kSlack || (m == -kInf && top > m))) {
+            top = __builtin_fmaxf(top, m);
+            const float down = __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
+            l *= down;
+#pragma unroll
+            for (int d = 0; d < W; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[d][i] *= down;
+            m = top;
+        }
+    }
+
+    // Of one tile, with the sum; to be called after weigh().
+    __device__ __forceinline__ void exponentials(f32x16 &s, float scale)
+    {
+        const float base = m == -kInf ? 0.0f : m * kUnit<T>;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[i] = weight<T>(s[i], scale * kUnit<T>, base);
+            l += s[i];
+        }
+    }
+
+    // Both halves' sums.
+    __device__ __forceinline__ void close() { l += __shfl_xor(l, 32); }
+};
+
+// Which row a lane holds, and where its results go.
+struct RowPlace {
+    int64_t row, t, h;
+    bool live;
+};
+
+__device__ __forceinline__ RowPlace row_place(const AttnParams &p, int64_t hk, int64_t row, int64_t qlen)
+{
+    const int64_t t = row / p.share;
+    return RowPlace{row, t, hk * p.share + row % p.share, row < p.Tq * p.share && t < qlen};
+}
+
+// Many rows: the four waves of a workgroup take different rows and share the
+// staged keys, two stages in turn.
+template <class T, int W>
 struct Forward {
     typedef Shape<T, W> S;
     typedef typename S::Lds Lds;
-    static constexpr int kWaves = forward_waves<T>(KEYS);
-    static constexpr int kTiles = !KEYS && sizeof(T) == 2 ? 2 : 1;      // of 32 keys, a wave, a stage
-    static constexpr int kStage = (KEYS ? kWaves : 1) * kTiles * 32;    // keys of a stage
-    static constexpr int kRows = KEYS ? 32 : kWaves * 32;
-    static constexpr int kHalf = kStage * Lds::kBytes;                  // bytes of a stage's keys
-    static constexpr int kJoinPitch = W * 32 * 4 + 16;                  // bytes of a row in the join
-    static constexpr int kJoin = KEYS ? kWaves * 32 * (kJoinPitch + 8) : 0;
-    static constexpr int kLds = 4 * kHalf > kJoin ? 4 * kHalf : kJoin;
+    static constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;   // of 32 keys, a stage
+    static constexpr int kStage = kTiles * 32;
+    static constexpr int kHalf = kStage * Lds::kBytes;      // bytes of a stage's keys
 };
 
-template <class T, int W, bool KEYS>
-__global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(const AttnParams p)
+template <class T, int W>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 && W > 2 ? 1 : 2) rar_attn_rows(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    typedef Forward<T, W, KEYS> F;
+    typedef Forward<T, W> F;
     typedef typename F::Lds Lds;
     constexpr int STEPS = F::S::STEPS;
-    __shared__ __attribute__((aligned(1024))) char memory[F::kLds];
+    __shared__ __attribute__((aligned(1024))) char memory[4 * F::kHalf];
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
@@ -390,14 +460,10 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
     const int64_t tile = at.in % p.tiles, hk = at.hk, b = at.b;
     const int split = (int)(at.in / p.tiles);
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
-    const int64_t rows = p.Tq * p.share;
-
-    const int64_t first = tile * F::kRows;
-    const int64_t row = first + (KEYS ? 0 : wave * 32) + (lane & 31);
-    const int64_t t = row / p.share, h = hk * p.share + row % p.share;
-    const bool live = row < rows && t < qlen;
+    const int64_t rows = p.Tq * p.share, first = tile * kAttnRows;
+    const RowPlace r = row_place(p, hk, first + wave * 32 + (lane & 31), qlen);
     Frag<T> q[STEPS];
-    load_row<T>(q, p.q, b * p.Tq + t, h, live);
+    load_row<T>(q, p.q, b * p.Tq + r.t, r.h, r.live);
 
     // this workgroup's keys: whole stages
     const int64_t k0 = (int64_t)split * p.stages * F::kStage;
@@ -405,15 +471,11 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
     kend = kend < klen ? kend : klen;
     const int stages = first / p.share < qlen && k0 < kend ? (int)((kend - k0 + F::kStage - 1) / F::kStage) : 0;
 
-    Loader<T, F::S::PITCH, F::kStage, F::kWaves> lk, lv;
+    Loader<T, F::S::PITCH, F::kStage, 4> lk, lv;
     lk.init(p.k, b * p.Tk + k0, hk, kend - k0);
     lv.init(p.v, b * p.Tk + k0, hk, kend - k0);
-    f32x16 acc[W];
-#pragma unroll
-    for (int d = 0; d < W; ++d)
-        acc[d] = zeros();
-    float m = -kInf, l = 0.0f;
-    const float scale = p.scale * kUnit<T>;
+    Rows<T, W> own;
+    own.init();
 
     if (stages) {
         lk.load(lds);
@@ -430,77 +492,44 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
             lk.load(next);
             lv.load(next + F::kHalf);
         }
-        const int r0 = KEYS ? wave * 32 : 0;
-        // every fragment of the keys is on its way before the first product
-        Frag<T> k[F::kTiles][STEPS], v[2][W];
+        // a tile's fragments are on their way before its first product, the next tile's follow in their place
+        Frag<T> k[STEPS], v[2][W];
 #pragma unroll
-        for (int e = 0; e < F::kTiles; ++e)
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-                k[e][i] = Lds::rows(here, r0 + e * 32, i);
+        for (int i = 0; i < STEPS; ++i)
+            k[i] = Lds::rows(here, 0, i);
         schedule_fence();
         f32x16 s[F::kTiles];
 #pragma unroll
         for (int e = 0; e < F::kTiles; ++e) {
             s[e] = zeros();
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-                mma(s[e], k[e][i], q[i]);
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s[e], k[i], q[i]);
+                if (e + 1 < F::kTiles)
+                    k[i] = Lds::rows(here, e * 32 + 32, i);
+            }
         }
         auto values = [&](int e) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int d = 0; d < W; ++d)
-                    v[j][d] = Lds::cols(here + F::kHalf, r0 + e * 32, j, d);
+                    v[j][d] = Lds::cols(here + F::kHalf, e * 32, j, d);
         };
         values(0);
         schedule_fence();
-        // keys behind the last one that counts
-        const int rest = (int)(kend - k0 - (int64_t)n * F::kStage) - r0;
-        if (rest < F::kTiles * 32)
-#pragma unroll
-            for (int e = 0; e < F::kTiles; ++e)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (e * 32 + row_of(i) + 4 * half >= rest)
-                        s[e][i] = -kInf;
-        float top = s[0][0];
-#pragma unroll
-        for (int e = 0; e < F::kTiles; ++e)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = __builtin_fmaxf(top, s[e][i]);
-        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        top *= p.scale;
-        if (__any(top > m + kSlack || (m == -kInf && top > m))) {
-            top = __builtin_fmaxf(top, m);
-            const float down = __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
-            l *= down;
-#pragma unroll
-            for (int d = 0; d < W; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    acc[d][i] *= down;
-            m = top;
-        }
-        const float base = m == -kInf ? 0.0f : m * kUnit<T>;
+        own.weigh(s, (int)(kend - k0 - (int64_t)n * F::kStage), p.scale);
 #pragma unroll
         for (int e = 0; e < F::kTiles; ++e) {
-            Frag<T> w[2];
+            own.exponentials(s[e], p.scale);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[e][i] = weight<T>(s[e][i], scale, base);
-                l += s[e][i];
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                w[j].set(s[e], 8 * j);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
+                Frag<T> w;
+                w.set(s[e], 8 * j);
 #pragma unroll
                 for (int d = 0; d < W; ++d)
-                    mma(acc[d], v[j][d], w[j]);
+                    mma(own.acc[d], v[j][d], w);
+            }
             if (e + 1 < F::kTiles)
                 values(e + 1);
         }
@@ -511,145 +540,432 @@ __global__ void __launch_bounds__(64 * forward_waves<T>(KEYS), 2) rar_attn_rows(
         if (n + 1 < stages)
             stage(Half<1>{}, n + 1);
     }
-    l += __shfl_xor(l, 32);
+    own.close();
 
-    if constexpr (KEYS) {
-        RAR_LDS float *const mine = (RAR_LDS float *)(lds + (wave * 32 + (lane & 31)) * F::kJoinPitch);
-        RAR_LDS float *const stats = (RAR_LDS float *)(lds + F::kWaves * 32 * F::kJoinPitch);  // [wave][32][m, l]
-        if (half == 0) {
-            stats[(wave * 32 + lane) * 2] = m;
-            stats[(wave * 32 + lane) * 2 + 1] = l;
+    if (r.row >= rows)
+        return;
+    const float inv = p.splits > 1 ? 1.0f : (own.l == 0.0f || !r.live ? 0.0f : 1.0f / own.l);
+    const int64_t place = split * p.part_rows + (b * p.Hkv + hk) * rows + r.row;
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 v;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                v[x] = r.live ? own.acc[d][4 * i + x] * inv : 0.0f;
+            const int c = d * 32 + 8 * i + 4 * half;
+            if (p.splits > 1)
+                store4(p.part + place * (W * 32) + c, v);
+            else
+                put4((T *)p.o + (b * p.Tq + r.t) * p.ldo + r.h * p.dh, c, p.dh, v);
         }
+    if (half)
+        return;
+    if (p.splits > 1) {
+        p.stats[place * 2] = own.m;
+        p.stats[place * 2 + 1] = own.l;
+    } else if (p.lse) {
+        p.lse[(b * p.Tq + r.t) * p.H + r.h] = r.live && own.l != 0.0f ? own.m + logf(own.l) : -kInf;
+    }
+#endif
+}
+
+// Few rows: every wave of a workgroup takes the same rows and keys of its own, 32
+// at a time, through a ring of LDS tiles that it fills itself, so that no wave
+// waits for another.  Bound by reading the keys: what counts is how much is in
+// flight, all of LDS but the tiles in use.  The waves are joined through LDS at
+// the end.
+template <class T, int W>
+struct Few {
+    typedef Shape<T, W> S;
+    typedef typename S::Lds Lds;
+    static constexpr int kHalf = 32 * Lds::kBytes;               // bytes of a tile's keys
+    static constexpr int kWaves = attn_few_waves(Lds::kBytes);
+    static constexpr int kRing = kWaves > 1 ? 5 : 3;
+    typedef Loader<T, S::PITCH, 32, 1> Load;
+    static constexpr int kBehind = (kRing - 2) * 2 * Load::kLoads;  // loads that may be in flight behind a tile
+    static_assert(kBehind < 64, "the counter of loads has six bits");
+    static constexpr int kJoinPitch = W * 32 * 4 + 16;           // bytes of a row in the join
+    static constexpr int kJoin = kWaves * 32 * (kJoinPitch + 8);
+    static constexpr int kTiles = kWaves * kRing * 2 * kHalf;
+    static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
+};
+
+template <class T, int W>
+__global__ void __launch_bounds__(64 * attn_few_waves((W <= 2 ? 64 : 128) * sizeof(T))) rar_attn_few(const AttnParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef Few<T, W> F;
+    typedef typename F::Lds Lds;
+    constexpr int STEPS = F::S::STEPS, kStep = F::kWaves * 32;
+    __shared__ __attribute__((aligned(1024))) char memory[F::kLds];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+    RAR_LDS char *const lds = (RAR_LDS char *)memory, *const ring = lds + wave * (F::kRing * 2 * F::kHalf);
+
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.splits);
+    const int64_t hk = at.hk, b = at.b;
+    const int split = (int)at.in;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int64_t rows = p.Tq * p.share;
+    const RowPlace own_row = row_place(p, hk, lane & 31, qlen);
+    Frag<T> q[STEPS];
+    load_row<T>(q, p.q, b * p.Tq + own_row.t, own_row.h, own_row.live);
+
+    const int64_t k0 = (int64_t)split * p.stages * kAttnFewStage + wave * 32;
+    int64_t kend = (int64_t)(split + 1) * p.stages * kAttnFewStage;
+    kend = kend < klen ? kend : klen;
+    const int tiles = qlen > 0 && k0 < kend ? (int)((kend - k0 + kStep - 1) / kStep) : 0;
+    typename F::Load lk, lv;
+    lk.init(p.k, b * p.Tk + k0, hk, kend - k0);
+    lv.init(p.v, b * p.Tk + k0, hk, kend - k0);
+    auto load = [&](int slot) __attribute__((always_inline)) {
+        lk.load(ring + slot * 2 * F::kHalf);
+        lv.load(ring + slot * 2 * F::kHalf + F::kHalf);
+        lk.advance(kStep);
+        lv.advance(kStep);
+    };
+    Rows<T, W> own;
+    own.init();
+    for (int n = 0; n < F::kRing - 1 && n < tiles; ++n)
+        load(n);
+    int slot = 0, fill = F::kRing - 1;
+    for (int n = 0; n < tiles; ++n) {
+        // this tile has arrived, and the reads of the tile before it, whose slot is filled next, are done
+        asm volatile("" ::: "memory");
+        if (n + F::kRing - 2 < tiles)
+            __builtin_amdgcn_s_waitcnt((F::kBehind & 15) | (F::kBehind >> 4) << 14 | 7 << 4);
+        else
+            __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        if (n + F::kRing - 1 < tiles)
+            load(fill);
+        RAR_LDS char *const here = ring + slot * 2 * F::kHalf;
+        Frag<T> k[STEPS], v[2][W];
 #pragma unroll
-        for (int d = 0; d < W; ++d)
+        for (int i = 0; i < STEPS; ++i)
+            k[i] = Lds::rows(here, 0, i);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *(RAR_LDS f32x4 *)(mine + d * 32 + 8 * i + 4 * half) =
-                    f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
-        meet();
-        // eight lanes a row, W quads of columns a lane
-        for (int r = threadIdx.x >> 3; r < 32; r += F::kWaves * 8) {
-            const int64_t to = first + r;
-            if (to >= rows)
-                break;
-            float top = -kInf, sum = 0.0f, w[F::kWaves];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < F::kWaves; ++i)
-                top = __builtin_fmaxf(top, stats[(i * 32 + r) * 2]);
+            for (int d = 0; d < W; ++d)
+                v[j][d] = Lds::cols(here + F::kHalf, 0, j, d);
+        f32x16 s[1] = {zeros()};
 #pragma unroll
-            for (int i = 0; i < F::kWaves; ++i) {
-                const float mi = stats[(i * 32 + r) * 2];
-                const float li = stats[(i * 32 + r) * 2 + 1];
-                // (no key of this wave's counts, or all of their scores are -infinity)
-                w[i] = li == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((mi - (top == -kInf ? 0.0f : top)) * kLog2e);
-                sum = __builtin_fmaf(w[i], li, sum);
-            }
-            const int64_t at_t = to / p.share, at_h = hk * p.share + to % p.share;
-            const bool on = at_t < qlen;
-            const float inv = p.splits > 1 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
-            const int64_t place = (b * p.Hkv + hk) * rows + to;
+        for (int i = 0; i < STEPS; ++i)
+            mma(s[0], k[i], q[i]);
+        own.weigh(s, (int)(kend - k0 - (int64_t)n * kStep), p.scale);
+        own.exponentials(s[0], p.scale);
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const int c = ((threadIdx.x & 7) + e * 8) * 4;
-                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < 2; ++j) {
+            Frag<T> w;
+            w.set(s[0], 8 * j);
 #pragma unroll
-                for (int i = 0; i < F::kWaves; ++i) {
-                    const f32x4 a = *(RAR_LDS f32x4 *)((RAR_LDS float *)(lds + (i * 32 + r) * F::kJoinPitch) + c);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        v[x] = w[i] == 0.0f ? v[x] : __builtin_fmaf(w[i], a[x], v[x]);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[x] = on ? v[x] * inv : 0.0f;
-                if (p.splits > 1)
-                    store4(p.part + (split * p.part_rows + place) * (W * 32) + c, v);
-                else
-                    put4((T *)p.o + (b * p.Tq + at_t) * p.ldo + at_h * p.dh, c, p.dh, v);
-            }
-            if ((threadIdx.x & 7) == 0) {
-                if (p.splits > 1) {
-                    p.stats[(split * p.part_rows + place) * 2] = top;
-                    p.stats[(split * p.part_rows + place) * 2 + 1] = sum;
-                } else if (p.lse) {
-                    p.lse[(b * p.Tq + at_t) * p.H + at_h] = on && sum != 0.0f ? top + logf(sum) : -kInf;
-                }
-            }
+            for (int d = 0; d < W; ++d)
+                mma(own.acc[d], v[j][d], w);
         }
-    } else {
-        if (row >= rows)
-            return;
-        const float inv = p.splits > 1 ? 1.0f : (l == 0.0f || !live ? 0.0f : 1.0f / l);
-        const int64_t place = (b * p.Hkv + hk) * rows + row;
+        slot = slot + 1 == F::kRing ? 0 : slot + 1;
+        fill = fill + 1 == F::kRing ? 0 : fill + 1;
+    }
+    own.close();
+
+    meet();  // the rings are free
+    RAR_LDS float *const mine = (RAR_LDS float *)(lds + (wave * 32 + (lane & 31)) * F::kJoinPitch);
+    RAR_LDS float *const stats = (RAR_LDS float *)(lds + F::kWaves * 32 * F::kJoinPitch);  // [wave][32][m, l]
+    if (half == 0) {
+        stats[(wave * 32 + lane) * 2] = own.m;
+        stats[(wave * 32 + lane) * 2 + 1] = own.l;
+    }
 #pragma unroll
-        for (int d = 0; d < W; ++d)
+    for (int d = 0; d < W; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f32x4 v;
+        for (int i = 0; i < 4; ++i)
+            *(RAR_LDS f32x4 *)(mine + d * 32 + 8 * i + 4 * half) = f32x4{
+                own.acc[d][4 * i], own.acc[d][4 * i + 1], own.acc[d][4 * i + 2], own.acc[d][4 * i + 3]};
+    meet();
+    // eight lanes a row, W quads of columns a lane
+    for (int i = threadIdx.x >> 3; i < rows; i += F::kWaves * 8) {
+        const RowPlace r = row_place(p, hk, i, qlen);
+        float top = -kInf, sum = 0.0f, w[F::kWaves];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[x] = live ? acc[d][4 * i + x] * inv : 0.0f;
-                const int c = d * 32 + 8 * i + 4 * half;
-                if (p.splits > 1)
-                    store4(p.part + (split * p.part_rows + place) * (W * 32) + c, v);
-                else
-                    put4((T *)p.o + (b * p.Tq + t) * p.ldo + h * p.dh, c, p.dh, v);
+        for (int x = 0; x < F::kWaves; ++x)
+            top = __builtin_fmaxf(top, stats[(x * 32 + i) * 2]);
+#pragma unroll
+        for (int x = 0; x < F::kWaves; ++x) {
+            const float m = stats[(x * 32 + i) * 2], l = stats[(x * 32 + i) * 2 + 1];
+            // (no key of this wave's counts, or all of their scores are -infinity)
+            w[x] = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
+            sum = __builtin_fmaf(w[x], l, sum);
+        }
+        const float inv = p.splits > 1 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+        const int64_t place = split * p.part_rows + (b * p.Hkv + hk) * rows + i;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int c = ((threadIdx.x & 7) + e * 8) * 4;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < F::kWaves; ++x) {
+                const f32x4 a = *(RAR_LDS f32x4 *)((RAR_LDS float *)(lds + (x * 32 + i) * F::kJoinPitch) + c);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    v[y] = w[x] == 0.0f ? v[y] : __builtin_fmaf(w[x], a[y], v[y]);
             }
-        if (half)
-            return;
-        if (p.splits > 1) {
-            p.stats[(split * p.part_rows + place) * 2] = m;
-            p.stats[(split * p.part_rows + place) * 2 + 1] = l;
-        } else if (p.lse) {
-            p.lse[(b * p.Tq + t) * p.H + h] = live && l != 0.0f ? m + logf(l) : -kInf;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                v[y] = r.live ? v[y] * inv : 0.0f;
+            if (p.splits > 1)
+                store4(p.part + place * (W * 32) + c, v);
+            else
+                put4((T *)p.o + (b * p.Tq + r.t) * p.ldo + r.h * p.dh, c, p.dh, v);
+        }
+        if ((threadIdx.x & 7) == 0) {
+            if (p.splits > 1) {
+                p.stats[place * 2] = top;
+                p.stats[place * 2 + 1] = sum;
+            } else if (p.lse) {
+                p.lse[(b * p.Tq + r.t) * p.H + r.h] = r.live && sum != 0.0f ? top + logf(sum) : -kInf;
+            }
         }
     }
 #endif
 }
 
-// Joins the parts of a row whose keys were split: eight lanes a row.
+// ---------------------------------------------------------------------------
+// Forward, a token at a time
+// ---------------------------------------------------------------------------
+//
+// Up to four rows a key head (a decoding step): a tile of the matrix cores would
+// be mostly padding, and its long chain of reads and products keeps a wave from
+// its next loads.  The vector units do it in two passes over registers: the lanes
+// of a wave hold 16 bytes each of several keys, a key's lanes add up its products
+// by lane exchanges, and the same lanes then weigh their 16 bytes of its value.
+// The eight waves of a workgroup take keys in turn and are joined through LDS.
+// Loads go straight to registers at any address, so no cache is copied.  Scores
+// and their maximum are in units of log 2.  Bound by HBM.
+template <class T>
+struct Piece {
+    static constexpr int N = 16 / sizeof(T);
+    u32x4 w;
+    __device__ __forceinline__ void load(const T *p, int cnt)
+    {
+        if (cnt >= N) {
+            w = *reinterpret_cast<const u32x4_any *>(p);
+            return;
+        }
+        w = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < cnt) {
+                if constexpr (sizeof(T) == 4)
+                    w[i] = __float_as_uint(p[i]);
+                else
+                    w[i >> 1] |= (uint32_t)p[i].u << (i & 1 ? 16 : 0);
+            }
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
+// The sum over a group of L neighbouring lanes, in all of them.
+template <int L>
+__device__ __forceinline__ float group_sum(float v)
+{
+    v += dpp<0xB1, 0xf>(v, 0.0f);   // the neighbour, the neighbouring pair,
+    v += dpp<0x4E, 0xf>(v, 0.0f);
+    v += dpp<0x141, 0xf>(v, 0.0f);  // the other four of eight,
+    if (L >= 16)
+        v += dpp<0x140, 0xf>(v, 0.0f);  // the other eight of sixteen
+    if (L >= 32)
+        v += __shfl_xor(v, 16);
+    return v;
+}
+
+constexpr int kTokenWaves = 8;
+
+template <class T, int PITCH, int R>
+__global__ void __launch_bounds__(64 * kTokenWaves) rar_attn_token(const AttnParams p)
+{
+    constexpr int N = Piece<T>::N, L = PITCH / N, G = 64 / L;  // lanes of a key, keys of a wave at a time
+    constexpr int U = R > 2 ? 2 : 4;                           // keys a group takes in one step
+    constexpr float kSlack2 = kSlack * kLog2e;
+    __shared__ float joined[kTokenWaves][R][PITCH + 2];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane / L, c = lane % L * N;
+
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.splits);
+    const int64_t hk = at.hk, b = at.b;
+    const int split = (int)at.in;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int rows = (int)(p.Tq * p.share), cnt = p.dh - c;
+    float q[R][N], acc[R][N], m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const RowPlace place = row_place(p, hk, r, qlen);
+        Piece<T> w;
+        w.load((const T *)p.q.p + (b * p.Tq + place.t) * p.q.ld + place.h * p.q.hs + c, place.live ? cnt : 0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            q[r][i] = w.get(i) * (p.scale * kLog2e);
+            acc[r][i] = 0.0f;
+        }
+        m[r] = -kInf;
+        l[r] = 0.0f;
+    }
+    const int64_t k0 = (int64_t)split * p.stages * kAttnFewStage;
+    int64_t kend = k0 + (int64_t)p.stages * kAttnFewStage;
+    kend = kend < klen ? kend : klen;
+    const T *const keys = (const T *)p.k.p + (b * p.Tk + k0) * p.k.ld + hk * p.k.hs + c;
+    const T *const values = (const T *)p.v.p + (b * p.Tk + k0) * p.v.ld + hk * p.v.hs + c;
+    const int64_t count = qlen > 0 ? kend - k0 : 0;
+    for (int64_t first = wave * (G * U); first < count; first += kTokenWaves * G * U) {
+        Piece<T> k[U], v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t key = first + u * G + group;
+            k[u].load(keys + key * p.k.ld, key < count ? cnt : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t key = first + u * G + group;
+            v[u].load(values + key * p.v.ld, key < count ? cnt : 0);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float s[U], top = m[r];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float t = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    t = __builtin_fmaf(q[r][i], k[u].get(i), t);
+                t = group_sum<L>(t);
+                s[u] = first + u * G + group < count ? t : -kInf;
+                top = __builtin_fmaxf(top, s[u]);
+            }
+            if (__any(top > m[r] + kSlack2 || (m[r] == -kInf && top > m[r]))) {
+                const float down = __builtin_amdgcn_exp2f(m[r] - (top == -kInf ? 0.0f : top));
+                l[r] *= down;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[r][i] *= down;
+                m[r] = top;
+            }
+            const float base = m[r] == -kInf ? 0.0f : m[r];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = __builtin_amdgcn_exp2f(s[u] - base);
+                l[r] += w;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[r][i] = __builtin_fmaf(w, v[u].get(i), acc[r][i]);
+            }
+        }
+    }
+    // the groups of a wave, then the waves
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float top = m[r];
+#pragma unroll
+        for (int d = L; d < 64; d *= 2)
+            top = __builtin_fmaxf(top, __shfl_xor(top, d));
+        const float w = l[r] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[r] - (top == -kInf ? 0.0f : top));
+        l[r] *= w;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            acc[r][i] = w == 0.0f ? 0.0f : acc[r][i] * w;
+#pragma unroll
+        for (int d = L; d < 64; d *= 2) {
+            l[r] += __shfl_xor(l[r], d);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                acc[r][i] += __shfl_xor(acc[r][i], d);
+        }
+        if (lane < L) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                joined[wave][r][c + i] = acc[r][i];
+            if (lane == 0) {
+                joined[wave][r][PITCH] = top;
+                joined[wave][r][PITCH + 1] = l[r];
+            }
+        }
+    }
+    __syncthreads();
+    const int r = threadIdx.x / PITCH, col = threadIdx.x % PITCH;
+    if (r >= rows)
+        return;
+    float top = -kInf, sum = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kTokenWaves; ++w)
+        top = __builtin_fmaxf(top, joined[w][r][PITCH]);
+#pragma unroll
+    for (int w = 0; w < kTokenWaves; ++w) {
+        const float lw = joined[w][r][PITCH + 1];
+        if (lw == 0.0f)
+            continue;  // no key of this wave's counts
+        const float x = __builtin_amdgcn_exp2f(joined[w][r][PITCH] - (top == -kInf ? 0.0f : top));
+        sum = __builtin_fmaf(x, lw, sum);
+        o = __builtin_fmaf(x, joined[w][r][col], o);
+    }
+    const RowPlace place = row_place(p, hk, r, qlen);
+    if (p.splits > 1) {
+        const int64_t part = split * p.part_rows + (b * p.Hkv + hk) * rows + r;
+        if (col < p.pitch)
+            p.part[part * p.pitch + col] = o;
+        if (col == 0) {
+            p.stats[part * 2] = top * kLn2;
+            p.stats[part * 2 + 1] = sum;
+        }
+        return;
+    }
+    if (col < p.dh)
+        ((T *)p.o)[(b * p.Tq + place.t) * p.ldo + place.h * p.dh + col] =
+            from_f32<T>(place.live && sum != 0.0f ? o / sum : 0.0f);
+    if (col == 0 && p.lse)
+        p.lse[(b * p.Tq + place.t) * p.H + place.h] = place.live && sum != 0.0f ? top * kLn2 + logf(sum) : -kInf;
+}
+
+// Joins the parts of a row whose keys were split: a wave a row, two columns a lane;
+// lane s weighs part s.
 template <class T>
 __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
 {
     const int64_t rows = p.Tq * p.share;
-    const int64_t place = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int64_t place = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (place >= p.part_rows)
         return;
-    const int64_t row = place % rows, hk = place / rows % p.Hkv, b = place / rows / p.Hkv;
-    const int64_t t = row / p.share, h = hk * p.share + row % p.share;
-    const int lane = threadIdx.x & 7, pitch = p.pitch;
-    float top = -kInf, sum = 0.0f;
-    for (int s = 0; s < p.splits; ++s)
-        top = __builtin_fmaxf(top, p.stats[(s * p.part_rows + place) * 2]);
-    const float base = top == -kInf ? 0.0f : top;
-    f32x4 v[4] = {};
+    const int64_t hk = place / rows % p.Hkv, b = place / rows / p.Hkv;
+    const RowPlace r = row_place(p, hk, place % rows, length_of(p.qlen, b, p.Tq));
+    const int lane = threadIdx.x & 63, c = lane * 2;
+    float m = -kInf, l = 0.0f;
+    if (lane < p.splits) {
+        m = p.stats[(lane * p.part_rows + place) * 2];
+        l = p.stats[(lane * p.part_rows + place) * 2 + 1];
+    }
+    const float top = wave_max(m);
+    const float w = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
+    const float sum = wave_sum(w * l);
+    f32x2 v = {0.0f, 0.0f};
+#pragma unroll 8
     for (int s = 0; s < p.splits; ++s) {
-        const int64_t at = s * p.part_rows + place;
-        const float m = p.stats[at * 2], l = p.stats[at * 2 + 1];
-        if (l == 0.0f)
-            continue;  // no key of this part counts
-        const float w = __builtin_amdgcn_exp2f((m - base) * kLog2e);
-        sum = __builtin_fmaf(w, l, sum);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (lane * 4 + e * 32 < pitch) {
-                const f32x4 a = load4(p.part + at * pitch + lane * 4 + e * 32);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[e][x] = __builtin_fmaf(w, a[x], v[e][x]);
-            }
+        const float ws = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(w), s));
+        f32x2 a = {0.0f, 0.0f};
+        if (c < p.pitch)
+            a = *reinterpret_cast<const f32x2 *>(p.part + (s * p.part_rows + place) * p.pitch + c);
+        v.x = ws == 0.0f ? v.x : __builtin_fmaf(ws, a.x, v.x);  // (no key of such a part counts)
+        v.y = ws == 0.0f ? v.y : __builtin_fmaf(ws, a.y, v.y);
     }
-    const bool on = t < length_of(p.qlen, b, p.Tq);
-    const float inv = sum == 0.0f || !on ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            v[e][x] = on ? v[e][x] * inv : 0.0f;
-        put4((T *)p.o + (b * p.Tq + t) * p.ldo + h * p.dh, lane * 4 + e * 32, p.dh, v[e]);
-    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *const o = (T *)p.o + (b * p.Tq + r.t) * p.ldo + r.h * p.dh;
+    if (c < p.dh)
+        o[c] = from_f32<T>(r.live ? v.x * inv : 0.0f);
+    if (c + 1 < p.dh)
+        o[c + 1] = from_f32<T>(r.live ? v.y * inv : 0.0f);
     if (lane == 0 && p.lse)
-        p.lse[(b * p.Tq + t) * p.H + h] = on && sum != 0.0f ? top + logf(sum) : -kInf;
+        p.lse[(b * p.Tq + r.t) * p.H + r.h] = r.live && sum != 0.0f ? top + logf(sum) : -kInf;
 }
 
 // ---------------------------------------------------------------------------
@@ -1007,14 +1323,22 @@ struct Kernels {
 };
 
 template <class T>
-void (*rows_kernel(int w, bool keys))(AttnParams)
+void (*rows_kernel(int w, bool few))(AttnParams)
 {
     switch (w) {
-    case 1: return keys ? rar_attn_rows<T, 1, true> : rar_attn_rows<T, 1, false>;
-    case 2: return keys ? rar_attn_rows<T, 2, true> : rar_attn_rows<T, 2, false>;
-    case 3: return keys ? rar_attn_rows<T, 3, true> : rar_attn_rows<T, 3, false>;
-    default: return keys ? rar_attn_rows<T, 4, true> : rar_attn_rows<T, 4, false>;
+    case 1: return few ? rar_attn_few<T, 1> : rar_attn_rows<T, 1>;
+    case 2: return few ? rar_attn_few<T, 2> : rar_attn_rows<T, 2>;
+    case 3: return few ? rar_attn_few<T, 3> : rar_attn_rows<T, 3>;
+    default: return few ? rar_attn_few<T, 4> : rar_attn_rows<T, 4>;
     }
+}
+
+template <class T>
+void (*token_kernel(int w, int rows))(AttnParams)
+{
+    if (w <= 2)
+        return rows == 1 ? rar_attn_token<T, 64, 1> : rows == 2 ? rar_attn_token<T, 64, 2> : rar_attn_token<T, 64, 4>;
+    return rows == 1 ? rar_attn_token<T, 128, 1> : rows == 2 ? rar_attn_token<T, 128, 2> : rar_attn_token<T, 128, 4>;
 }
 
 template <class T>
@@ -1041,17 +1365,22 @@ void (*dkv_kernel(int w))(AttnParams)
 
 }  // namespace
 
-hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool keys, hipStream_t st)
+hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool few, hipStream_t st)
 {
     const int w = (p.dh + 31) / 32;
-    if (dt == RAR_BF16)
-        return launch(rows_kernel<bf16>(w, keys), (unsigned)p.blocks, 256, st, p);
-    return launch(rows_kernel<float>(w, keys), (unsigned)p.blocks, keys ? 128 : 256, st, p);
+    if (p.Tq * p.share <= kAttnTokenRows) {
+        const int rows = (int)(p.Tq * p.share);
+        return launch(dt == RAR_BF16 ? token_kernel<bf16>(w, rows) : token_kernel<float>(w, rows), (unsigned)p.blocks,
+                      64 * kTokenWaves, st, p);
+    }
+    const int waves = few ? attn_few_waves((w <= 2 ? 64 : 128) * (dt == RAR_BF16 ? 2 : 4)) : 4;
+    return launch(dt == RAR_BF16 ? rows_kernel<bf16>(w, few) : rows_kernel<float>(w, few), (unsigned)p.blocks,
+                  64 * waves, st, p);
 }
 
 hipError_t launch_attn_join(rar_dtype dt, const AttnParams &p, hipStream_t st)
 {
-    return launch(dt == RAR_BF16 ? rar_attn_join<bf16> : rar_attn_join<float>, (unsigned)((p.part_rows + 31) / 32), 256,
+    return launch(dt == RAR_BF16 ? rar_attn_join<bf16> : rar_attn_join<float>, (unsigned)((p.part_rows + 3) / 4), 256,
                   st, p);
 }
 

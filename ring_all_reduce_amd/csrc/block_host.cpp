@@ -292,10 +292,12 @@ struct AttnShape {
         width = (int)up(dh, 32);
         few = rows <= kAttnFewRows;
         tiles = div_up(rows, few ? kAttnFewRows : kAttnRows);
-        // two workgroups a compute unit, each with at least two stages of keys
-        const int64_t all = std::max<int64_t>(1, div_up(Tk, attn_stage(dt, few)));
+        // two workgroups a compute unit, or one where a workgroup fills it or the caches' ports (few rows); each
+        // with at least two stages of keys.  16 x 16 heads of 128, a token on 2048 keys in bf16: 44 us unsplit,
+        // 45 in two parts and 41 in four, and the join 4 more.
+        const int64_t all = std::max<int64_t>(1, div_up(Tk, attn_stage(dt, rows)));
         const int64_t work = std::max<int64_t>(1, B * Hkv * tiles);
-        splits = std::min<int64_t>(std::min<int64_t>(div_up(512, work), std::max<int64_t>(1, all / 2)), 64);
+        splits = std::min<int64_t>(std::min<int64_t>(div_up(few ? 256 : 512, work), std::max<int64_t>(1, all / 2)), 64);
         stages = div_up(all, splits);
         splits = div_up(all, stages);
         key_tiles = div_up(Tk, kAttnRows);
@@ -450,9 +452,15 @@ extern "C" rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, i
     pack.dh = (int)s.dh;
     pack.cols = (int)s.cols;
     AttnParams p = attn_params(*plan, s, qlen, klen);
-    p.q = operand(s, mq, s.H, w.q, pack);
-    p.k = operand(s, mk, s.Hkv, w.k, pack);
-    p.v = operand(s, mv, s.Hkv, w.v, pack);
+    if (s.rows <= kAttnTokenRows) {  // read at any address
+        p.q = AttnOperand{q, ldq, s.dh, (int)s.dh};
+        p.k = AttnOperand{k, ldk, s.dh, (int)s.dh};
+        p.v = AttnOperand{v, ldv, s.dh, (int)s.dh};
+    } else {
+        p.q = operand(s, mq, s.H, w.q, pack);
+        p.k = operand(s, mk, s.Hkv, w.k, pack);
+        p.v = operand(s, mv, s.Hkv, w.v, pack);
+    }
     p.o = o;
     p.ldo = ldo;
     p.lse = lse;

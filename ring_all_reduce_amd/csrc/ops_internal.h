@@ -195,11 +195,19 @@ struct AttnParams {
 };
 
 constexpr int kAttnRows = 128;       // query rows of a workgroup, or keys of one of dk and dv
-constexpr int kAttnFewRows = 32;     // rows whose keys are shared out among the waves
+constexpr int kAttnFewRows = 32;     // rows of a key head that share one tile: the waves share out the keys
+constexpr int kAttnTokenRows = 4;    // rows of a key head that the vector units take
+constexpr int kAttnFewStage = 128;   // keys that such a call's split is a multiple of
 constexpr int kAttnPad = 64;         // whole stages of queries
 
-// Keys of a stage of the forward kernel.
-inline int attn_stage(rar_dtype dt, bool keys) { return dt == RAR_BF16 ? (keys ? 128 : 64) : (keys ? 64 : 32); }
+// Keys of a stage of the forward kernel for `rows` rows a key head.
+inline int attn_stage(rar_dtype dt, int64_t rows)
+{
+    return rows <= kAttnFewRows ? kAttnFewStage : (dt == RAR_BF16 ? 64 : 32);
+}
+
+// Waves of a workgroup that share out the keys, by the bytes of a row in LDS: what fills LDS.
+constexpr int attn_few_waves(int row_bytes) { return 512 / row_bytes; }
 
 struct AttnPack {
     struct Item {
@@ -264,8 +272,8 @@ hipError_t launch_norm(rar_dtype dt, const NormParams &p, hipStream_t st);
 hipError_t launch_norm_grad(rar_dtype dt, const NormGradParams &p, hipStream_t st);
 hipError_t launch_norm_sums(rar_dtype dt, const NormGradParams &p, hipStream_t st);
 hipError_t launch_dropout(rar_dtype dt, const DropoutParams &p, hipStream_t st);
-// keys: rows of at most kAttnFewRows a key head, keys shared out among the waves.
-hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool keys, hipStream_t st);
+// few: at most kAttnFewRows rows a key head, the keys shared out among the waves.
+hipError_t launch_attn_rows(rar_dtype dt, const AttnParams &p, bool few, hipStream_t st);
 hipError_t launch_attn_join(rar_dtype dt, const AttnParams &p, hipStream_t st);
 hipError_t launch_attn_delta(rar_dtype dt, const AttnParams &p, hipStream_t st);
 hipError_t launch_attn_dq(rar_dtype dt, const AttnParams &p, hipStream_t st);
