@@ -1,19 +1,18 @@
 // logprob.hip -- CDNA4 (gfx950) kernels of log probabilities of given tokens, with
 // entropy, top alternatives and the gradient in the logits.
 //
-// With m = max z, d = scale (m - z) >= 0, S = sum e^-d:
-//   log p = -d - log S,  entropy = log S + (sum d e^-d) / S   (no term cancels)
-//   dz = scale (dlogp [j = target] - p (dlogp + dentropy (log p + entropy)))
+// With m = max z, t = (z - m) scale log2 e <= 0, S = sum 2^t:
+//   log p = scale (z - m) - log S,  entropy = log S - ln 2 (sum t 2^t) / S   (no term cancels)
+//   dz = scale (dlogp [j = target] - p (dlogp + dentropy (log p + entropy))),  p = 2^(t - log2 S)
 //
-// Bound by HBM: a row passes once through the registers of its lanes, in its own
-// type; the exponentials are taken twice rather than kept.  Nothing but the
-// results is written, so a loss with its gradient reads the logits once and
-// writes dz.
+// A row passes once through the registers of its lanes, in its own type, and the
+// exponentials are taken twice rather than kept.  Nothing but the results is
+// written, so a loss with its gradient reads the logits once and writes dz.
 //
-// Alternatives: an element's key orders by value, then by the lower index, and
-// no two are alike.  The row is cut into 64 groups; the K-th largest of the
-// groups' best keys is at most the K-th largest key, since K keys reach it.  The
-// few keys that do (some thirty of 32000 for K = 20) are collected in LDS and
+// Alternatives: the row is cut into 64 groups of neighbouring lanes.  The K-th
+// largest of the groups' maxima is at most the K-th largest element, since K
+// elements reach it.  The few that do (some thirty of 32000 for K = 20) are
+// collected in LDS under a key that orders by value, then by the lower index, and
 // ranked by counting.  Where they are too many (rows of equal or sorted values),
 // K rounds each take the largest key under the last.
 #include "ops_internal.h"
@@ -28,16 +27,16 @@ constexpr int kMost = RAR_LOGPROB_MAX_TOP;
 constexpr int kGroups = 64;
 constexpr int kCandidates = 256;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kInf = __builtin_inff();
+constexpr float kNothing = -1000.0f;  // 2^this is zero
 
-// Larger for a larger value, then for a lower index; zero for a masked element or
-// a NaN.  The two zeros are one value.
-__device__ __forceinline__ uint32_t key_of(float v)
+// Larger for a larger value, then for a lower index, and never zero; the two zeros
+// are one value.
+__device__ __forceinline__ uint64_t key_at(float v, int64_t index)
 {
     const uint32_t b = __float_as_uint(v + 0.0f);
-    if (!(v > -kInf))
-        return 0;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~(uint32_t)index;
 }
 
 __device__ __forceinline__ float value_of(uint32_t k)
@@ -51,19 +50,37 @@ __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int d)
     return (uint64_t)hi << 32 | lo;
 }
 
+// What stands behind is not begun before what stands before: left to itself the
+// compiler takes every eight of a row at once, and runs out of registers.
+__device__ __forceinline__ void one_after_another()
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// v, of which nothing is known: what is computed from it is not kept from row to row
+// (columns, counts and masks of every eight would take more registers than the row).
+__device__ __forceinline__ int forgotten(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 template <int LANES>
 struct TopLds {
     static constexpr int kRows = LANES >= 256 ? 1 : 256 / LANES;
-    uint64_t best[kRows][kGroups];
-    uint64_t floor[kRows];
+    float best[kRows][kGroups];
     uint32_t found[kRows];
     uint64_t keys[kRows][kCandidates];
 };
 
 // A row of LANES lanes; R eights a lane in registers, or R = 0: read again from
 // memory for each pass.
+// Held to 64 registers where the row takes at most half of them, so that two
+// workgroups of 1024 share a compute unit: one waits while the other computes.
 template <class T, int LANES, int R, bool GRAD>
-__global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(const LogprobParams p)
+__global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16 ? 8 : 4) rar_logprob_rows(const LogprobParams p)
 {
     typedef RowJoin<LANES, 2> Join;
     constexpr int kRows = Join::kThreads / LANES;
@@ -79,20 +96,23 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
         const T *const z = (const T *)p.z + row * p.ldz;
         Eight<T> held[kHeld];
         if (R) {
+            const int mine = forgotten(lane);
 #pragma unroll
             for (int k = 0; k < kHeld; ++k) {
-                const int64_t c = ((int64_t)k * LANES + lane) * 8;
+                const int64_t c = ((int64_t)k * LANES + mine) * 8;
                 held[k].load(z + c, live ? clamp8(p.cols - c) : 0, -kInf);
             }
         }
         // f(column, how many of the eight exist, values; the others -infinity)
         auto each = [&](auto &&f) __attribute__((always_inline)) {
             if (R) {
+                const int mine = forgotten(lane);
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
-                    const int64_t c = ((int64_t)k * LANES + lane) * 8;
+                    const int64_t c = ((int64_t)k * LANES + mine) * 8;
                     held[k].forget();
                     f(c, live ? clamp8(p.cols - c) : 0, held[k]);
+                    one_after_another();
                 }
             } else {
                 for (int64_t c = (int64_t)lane * 8; c < p.cols; c += LANES * 8) {
@@ -113,51 +133,51 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
                 zt = to_f32(z[target]);
         }
 
-        float t[2] = {-kInf, 0.0f};
+        // the largest of each eight: the row's maximum, and where alternatives can be
+        float best[kHeld], m[1] = {-kInf};
+        int at = 0;
         each([&](int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
+            float b = v.get(0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                t[0] = __builtin_fmaxf(t[0], v.get(i));
+            for (int i = 1; i < 8; ++i)
+                b = __builtin_fmaxf(b, v.get(i));
+            if (R)
+                best[at++] = b;
+            m[0] = __builtin_fmaxf(m[0], b);
         });
-        float m[1] = {t[0]};
+        const float mine = m[0];
         join.max(m);
-        const float base = m[0] == -kInf ? 0.0f : m[0];
-        t[0] = 0.0f;
+        const float base = m[0] == -kInf ? 0.0f : m[0], unit = p.scale * kLog2e;
+        float t[2] = {0.0f, 0.0f};
         each([&](int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = (base - v.get(i)) * p.scale;
-                const float e = __builtin_amdgcn_exp2f(d * -kLog2e);
+                const float x = (v.get(i) - base) * unit;
+                const float e = __builtin_amdgcn_exp2f(x);
                 t[0] += e;
-                t[1] = __builtin_fmaf(e, __builtin_fminf(d, 1e30f), t[1]);  // a masked element adds 0 * 1e30
+                t[1] = __builtin_fmaf(e, __builtin_fmaxf(x, kNothing), t[1]);  // a masked element adds 0 * kNothing
             }
         });
         join.sum(t);
         const bool none = t[0] == 0.0f;  // (NaN: false)
         const float ls = none ? 0.0f : logf(t[0]);
-        const float inv = none ? 0.0f : 1.0f / t[0];
-        const float ent = none ? 0.0f : __builtin_fmaf(t[1], inv, ls);
+        const float ent = none ? 0.0f : __builtin_fmaf(t[1] / t[0], -kLn2, ls);
         if (lane == 0 && live) {
             if (p.entropy)
                 p.entropy[row] = ent;
             if (p.logp)
-                p.logp[row] = target < 0 ? 0.0f : (none ? -kInf : -((base - zt) * p.scale) - ls);
+                p.logp[row] = target < 0 ? 0.0f : (none ? -kInf : (zt - base) * p.scale - ls);
         }
 
         if (GRAD) {
             const float dl = p.dlogp && target >= 0 && !none ? p.dlogp[row] : 0.0f;
             const float de = p.dentropy && live ? p.dentropy[row] : 0.0f;
-            const float add = de == 0.0f ? 0.0f : ent - ls;
+            const float l2 = ls * kLog2e;
+            // dz = p (flat + slope t)
+            const float flat = -p.scale * (de == 0.0f ? dl : __builtin_fmaf(de, ent, dl));
+            const float slope = -p.scale * (de * kLn2);
             T *const dz = (T *)p.dz + row * p.lddz;
-            each([&](int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
-                float g[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = (base - v.get(i)) * p.scale;
-                    const float e = __builtin_amdgcn_exp2f(d * -kLog2e) * inv;
-                    const float w = __builtin_fmaf(de, add - __builtin_fminf(d, 1e30f), dl);
-                    g[i] = -(e * w) * p.scale;
-                }
+            auto write = [&](int64_t c, int cnt, float (&g)[8]) __attribute__((always_inline)) {
                 if (target >= c && target < c + 8)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -165,7 +185,25 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
                             g[i] = __builtin_fmaf(p.scale, dl, g[i]);
                 if (live)
                     store8<true>(dz + c, cnt, g);
-            });
+            };
+            if (p.dentropy)
+                each([&](int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
+                    float g[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = __builtin_fmaf(v.get(i) - base, unit, -l2);
+                        g[i] = __builtin_amdgcn_exp2f(x) * __builtin_fmaf(slope, __builtin_fmaxf(x, kNothing), flat);
+                    }
+                    write(c, cnt, g);
+                });
+            else
+                each([&](int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
+                    float g[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        g[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v.get(i) - base, unit, -l2)) * flat;
+                    write(c, cnt, g);
+                });
             continue;
         }
         if (!p.top)
@@ -173,60 +211,56 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
 
         // ---- alternatives ----
         const bool bad = t[0] != t[0];
-        uint64_t mine = 0;
-        each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
+        constexpr int kEach = LANES / kGroups;          // lanes of a group
+        constexpr int kSome = kGroups * kGroups / LANES;  // groups that a lane compares its own with
+        float group = mine;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t k = key_of(v.get(i));
-                const uint64_t key = (uint64_t)k << 32 | (uint32_t)~(uint32_t)(c + i);
-                if (k && key > mine)
-                    mine = key;
-            }
-        });
-        uint64_t group = mine;
-#pragma unroll
-        for (int d = 1; d < LANES / kGroups; d *= 2) {
-            const uint64_t o = shfl_xor64(group, d);
-            group = o > group ? o : group;
-        }
-        if (lane % (LANES / kGroups) == 0)
-            top.best[sub][lane / (LANES / kGroups)] = group;
+        for (int d = 1; d < kEach; d *= 2)
+            group = __builtin_fmaxf(group, __shfl_xor(group, d));
+        if (lane % kEach == 0)
+            top.best[sub][lane / kEach] = group;
         if (lane == 0)
             top.found[sub] = 0;
         __syncthreads();
-        if (lane < 64) {
-            const uint64_t own = top.best[sub][lane];
-            int above = 0;
-            for (int i = 0; i < kGroups; ++i)
-                above += top.best[sub][i] > own;
-            // the group's best at rank K - 1; equal ones are empty groups, of which each writes zero
-            if (lane == 0)
-                top.floor[sub] = 0;
-            if (above == p.top - 1 && own)
-                top.floor[sub] = own;
+        {
+            // the lanes of a group count the groups that are as large; those that K or more are not
+            // smaller than (and the K-th itself) have the K-th largest value or one above it
+            int reach = 0;
+#pragma unroll
+            for (int i = 0; i < kSome; ++i)
+                reach += top.best[sub][lane % kEach * kSome + i] >= group;
+#pragma unroll
+            for (int d = 1; d < kEach; d *= 2)
+                reach += __shfl_xor(reach, d);
+            __syncthreads();
+            if (lane % kEach == 0)
+                top.best[sub][lane / kEach] = reach >= p.top ? group : -kInf;
         }
         __syncthreads();
-        const uint64_t low = top.floor[sub] ? top.floor[sub] : 1;
-        if (mine >= low && !bad)
+        const float low = wave_max(top.best[sub][threadIdx.x & 63]);
+        if (!bad) {
+            at = 0;
             each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
+                if (R && !__any(best[at++] >= low))
+                    return;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t k = key_of(v.get(i));
-                    const uint64_t key = (uint64_t)k << 32 | (uint32_t)~(uint32_t)(c + i);
-                    if (k && key >= low) {
-                        const uint32_t at = atomicAdd(&top.found[sub], 1u);
-                        if (at < kCandidates)
-                            top.keys[sub][at] = key;
+                    const float x = v.get(i);
+                    if (x >= low && x > -kInf) {
+                        const uint32_t n = atomicAdd(&top.found[sub], 1u);
+                        if (n < kCandidates)
+                            top.keys[sub][n] = key_at(x, c + i);
                     }
                 }
             });
+        }
         __syncthreads();
         const uint32_t found = top.found[sub];
         int64_t *const ids = p.top_ids + row * p.top;
         float *const lps = p.top_logp + row * p.top;
         auto put = [&](int at, uint64_t key) __attribute__((always_inline)) {
             ids[at] = (int64_t)(uint32_t)~(uint32_t)key;
-            lps[at] = -((base - value_of((uint32_t)(key >> 32))) * p.scale) - ls;
+            lps[at] = (value_of((uint32_t)(key >> 32)) - base) * p.scale - ls;
         };
         if (found <= kCandidates) {
             if (live)
@@ -253,9 +287,9 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
                     each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint32_t w = key_of(v.get(i));
-                            const uint64_t key = (uint64_t)w << 32 | (uint32_t)~(uint32_t)(c + i);
-                            if (w && key < last && key > b)
+                            const float x = v.get(i);
+                            const uint64_t key = key_at(x, c + i);
+                            if (x > -kInf && key < last && key > b)
                                 b = key;
                         }
                     });
@@ -276,9 +310,9 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_logprob_rows(co
                 each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = key_of(v.get(i));
-                        const uint64_t key = (uint64_t)w << 32 | (uint32_t)~(uint32_t)(c + i);
-                        if (w && key < last && key > b)
+                        const float x = v.get(i);
+                        const uint64_t key = key_at(x, c + i);
+                        if (x > -kInf && key < last && key > b)
                             b = key;
                     }
                 });

@@ -29,13 +29,15 @@ template <> struct Eight<float> {
             hi = q[1];
             return;
         }
+        set(fill);
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {  // a row's end: few lanes, so short code
+            const float v = p[i];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = i < cnt ? p[i] : fill;
-            if (i < 4)
-                lo[i & 3] = v;
-            else
-                hi[i & 3] = v;
+            for (int k = 0; k < 4; ++k) {
+                lo[k] = i == k ? v : lo[k];
+                hi[k] = i == k + 4 ? v : hi[k];
+            }
         }
     }
 };
@@ -58,11 +60,15 @@ template <> struct Eight<bf16> {
             w = *reinterpret_cast<const u32x4_any *>(p);
             return;
         }
-        const uint32_t f = __float_as_uint(fill) >> 16;
+        set(fill);
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {
+            const uint32_t v = p[i].u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a = 2 * i < cnt ? p[2 * i].u : f, b = 2 * i + 1 < cnt ? p[2 * i + 1].u : f;
-            w[i] = a | b << 16;
+            for (int k = 0; k < 4; ++k) {
+                w[k] = i == 2 * k ? (w[k] & 0xffff0000u) | v : w[k];
+                w[k] = i == 2 * k + 1 ? (w[k] & 0xffffu) | v << 16 : w[k];
+            }
         }
     }
 };
