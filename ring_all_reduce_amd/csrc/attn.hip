@@ -1033,11 +1033,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
-    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles);
-    const int64_t tile = at.in, hk = at.hk, b = at.b;
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles * p.splits);
+    const int64_t tile = at.in % p.tiles, split = at.in / p.tiles, hk = at.hk, b = at.b;
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
     const int64_t rows = p.Tq * p.share;
-    const int64_t first = tile * 128, row = first + wave * 32 + (lane & 31);
+    const int64_t first = tile * kAttnRows, row = first + wave * 32 + (lane & 31);
     const int64_t t = row / p.share, h = hk * p.share + row % p.share;
     const bool live = row < rows && t < qlen;
     Frag<T> q[STEPS], g[STEPS];
@@ -1047,10 +1047,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
     const float lse = live ? p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
     const float scale = p.scale * kUnit<T>;
 
-    const int stages = first / p.share < qlen ? (int)((klen + F::kStage - 1) / F::kStage) : 0;
+    // this workgroup's stages of keys
+    const int64_t all = first / p.share < qlen ? (klen + F::kStage - 1) / F::kStage : 0;
+    const int64_t begin = all * split / p.splits, k0 = begin * F::kStage;
+    const int stages = (int)(all * (split + 1) / p.splits - begin);
     Loader<T, F::S::PITCH, F::kStage, 4> lk, lv;
-    lk.init(p.k, b * p.Tk, hk, klen);
-    lv.init(p.v, b * p.Tk, hk, klen);
+    lk.init(p.k, b * p.Tk + k0, hk, klen - k0);
+    lv.init(p.v, b * p.Tk + k0, hk, klen - k0);
     f32x16 acc[W];
 #pragma unroll
     for (int d = 0; d < W; ++d)
@@ -1069,7 +1072,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
             lk.load(next);
             lv.load(next + F::kHalf);
         }
-        const int rest = (int)(klen - (int64_t)n * F::kStage);
+        const int rest = (int)(klen - k0 - (int64_t)n * F::kStage);
         f32x16 s[F::kTiles], dp[F::kTiles];
         Frag<T> k[STEPS], v[STEPS], kt[2][W];
         auto scores = [&](int e) __attribute__((always_inline)) {
@@ -1124,15 +1127,20 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
     if (row >= rows)
         return;
     T *const out = (T *)p.dq + (b * p.Tq + t) * p.lddq + h * p.dh;
+    float *const part = p.part + (split * p.part_rows + (b * p.Hkv + hk) * rows + row) * (W * 32);
 #pragma unroll
     for (int d = 0; d < W; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            const int c = d * 32 + 8 * i + 4 * half;
             f32x4 v;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 v[x] = live ? acc[d][4 * i + x] * p.scale : 0.0f;
-            put4(out, d * 32 + 8 * i + 4 * half, p.dh, v);
+            if (p.splits > 1)
+                store4(part + c, v);
+            else
+                put4(out, c, p.dh, v);
         }
 #endif
 }
@@ -1160,10 +1168,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
     RAR_LDS char *const lds = (RAR_LDS char *)memory;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
 
-    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles);
-    const int64_t tile = at.in, hk = at.hk, b = at.b;
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles * p.splits);
+    const int64_t tile = at.in % p.tiles, split = at.in / p.tiles, hk = at.hk, b = at.b;
     const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
-    const int64_t key = tile * 128 + wave * 32 + (lane & 31);
+    const int64_t key = tile * kAttnRows + wave * 32 + (lane & 31);
     const bool live = key < klen;
     Frag<T> k[STEPS], v[STEPS];
     load_row<T>(k, p.k, b * p.Tk + key, hk, live);
@@ -1175,15 +1183,20 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
         dv[d] = zeros();
     }
     const float scale = p.scale * kUnit<T>;
-    const int per_head = (int)((qlen + F::kStage - 1) / F::kStage);
-    const int stages = tile * 128 < klen ? per_head * (int)p.share : 0;
+    // this workgroup's stages of queries: one head after the other
+    const int64_t per_head = (qlen + F::kStage - 1) / F::kStage;
+    const int64_t all = tile * kAttnRows < klen ? per_head * p.share : 0;
+    const int64_t begin = all * split / p.splits;
+    const int stages = (int)(all * (split + 1) / p.splits - begin);
     Loader<T, F::S::PITCH, F::kStage, 4> lq, lg;
-    int ahead = 0;  // stage within the head that is loaded next
-    int64_t head = hk * p.share;
+    int64_t head = hk * p.share + (all ? begin / per_head : 0);
+    int64_t ahead = all ? begin % per_head : 0;  // stage within the head that is loaded next
+    bool entered = false;
     auto load = [&](RAR_LDS char *to) __attribute__((always_inline)) {
-        if (ahead == 0) {
-            lq.init(p.q, b * p.Tq, head, qlen);
-            lg.init(p.g, b * p.Tq, head, qlen);
+        if (!entered) {
+            lq.init(p.q, b * p.Tq + ahead * F::kStage, head, qlen - ahead * F::kStage);
+            lg.init(p.g, b * p.Tq + ahead * F::kStage, head, qlen - ahead * F::kStage);
+            entered = true;
         }
         lq.load(to);
         lg.load(to + F::kHalf);
@@ -1200,6 +1213,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
         if (++ahead == per_head) {
             ahead = 0;
             ++head;
+            entered = false;
         }
     };
     if (stages)
@@ -1282,12 +1296,50 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
                 a[x] = live ? dk[d][4 * i + x] * p.scale : 0.0f;
                 e[x] = live ? dv[d][4 * i + x] : 0.0f;
             }
+            if (p.splits > 1) {
+                float *const part = p.part + (split * p.part_rows + (b * p.Hkv + hk) * p.Tk + key) * (2 * W * 32);
+                store4(part + c, a);
+                store4(part + W * 32 + c, e);
+                continue;
+            }
             if (p.dk)
                 put4((T *)p.dk + (b * p.Tk + key) * p.lddk + hk * p.dh, c, p.dh, a);
             if (p.dv)
                 put4((T *)p.dv + (b * p.Tk + key) * p.lddv + hk * p.dh, c, p.dh, e);
         }
 #endif
+}
+
+// Joins the parts of split gradients, in order: first dq's rows, then those of dk and
+// dv; four columns a lane.
+template <class T>
+__global__ void __launch_bounds__(256) rar_attn_sum(const AttnSum p)
+{
+    const int quads = p.pitch / 4;
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool keys = i >= p.q_rows * quads;
+    if (keys)
+        i -= p.q_rows * quads;
+    const int width = keys ? 2 * quads : quads;
+    const int64_t place = i / width, rows = keys ? p.k_rows : p.q_rows;
+    if (place >= rows)
+        return;
+    const int at = (int)(i - place * width), splits = keys ? p.k_splits : p.q_splits;
+    const float *from = (keys ? p.k_part : p.q_part) + place * (width * 4) + at * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s)
+        v += load4(from + s * rows * (width * 4));
+    const int64_t per = keys ? p.Tk : p.Tq * p.share, hk = place / per % p.Hkv, b = place / per / p.Hkv, r = place % per;
+    if (!keys) {
+        const int64_t t = r / p.share, h = hk * p.share + r % p.share;
+        put4((T *)p.dq + (b * p.Tq + t) * p.lddq + h * p.dh, at * 4, p.dh, v);
+    } else if (at < quads) {
+        if (p.dk)
+            put4((T *)p.dk + (b * p.Tk + r) * p.lddk + hk * p.dh, at * 4, p.dh, v);
+    } else if (p.dv) {
+        put4((T *)p.dv + (b * p.Tk + r) * p.lddv + hk * p.dh, (at - quads) * 4, p.dh, v);
+    }
 }
 
 // Copies of operands whose heads are not whole 16-byte groups at 16-byte aligned
@@ -1400,6 +1452,12 @@ hipError_t launch_attn_dkv(rar_dtype dt, const AttnParams &p, hipStream_t st)
 {
     const int w = (p.dh + 31) / 32;
     return launch(dt == RAR_BF16 ? dkv_kernel<bf16>(w) : dkv_kernel<float>(w), (unsigned)p.blocks, 256, st, p);
+}
+
+hipError_t launch_attn_sum(rar_dtype dt, const AttnSum &p, hipStream_t st)
+{
+    const int64_t lanes = (p.q_rows + 2 * p.k_rows) * (p.pitch / 4);
+    return launch(dt == RAR_BF16 ? rar_attn_sum<bf16> : rar_attn_sum<float>, (unsigned)((lanes + 255) / 256), 256, st, p);
 }
 
 hipError_t launch_attn_pack(rar_dtype dt, const AttnPack &p, hipStream_t st)

@@ -163,9 +163,11 @@ extern "C" rar_status rar_norm_backward(rar_norm_t plan, int64_t T, const void *
         dh = du = o = h = nullptr;
         dx = d_o = nullptr;
     }
-    if (!post)
+    if (!post || !o)
         post_w = post_b = nullptr;
-    if (!pre)
+    if (!o)
+        gate = nullptr;
+    if (!pre || !du)
         pre_w = nullptr;
     if (!all_aligned({dh, du, o, h, post_w, post_b, gate, pre_w, dx, d_o, dpost_w, dpost_b, dgate, dpre_w, dpre_b},
                      es) ||
@@ -282,7 +284,8 @@ struct AttnShape {
     bool few;          // the keys are shared out among a workgroup's waves
     int64_t tiles;     // of query rows, a key head
     int64_t splits, stages;
-    int64_t key_tiles; // of dk and dv
+    int64_t q_tiles, q_splits;    // of dq: rows, and parts of the keys
+    int64_t key_tiles, k_splits;  // of dk and dv: keys, and parts of the queries
     int64_t padded;
 
     AttnShape(const rar_attn_s &a, int64_t B_, int64_t Tq_, int64_t Tk_)
@@ -300,8 +303,18 @@ struct AttnShape {
         splits = std::min<int64_t>(std::min<int64_t>(div_up(few ? 256 : 512, work), std::max<int64_t>(1, all / 2)), 64);
         stages = div_up(all, splits);
         splits = div_up(all, stages);
-        key_tiles = div_up(Tk, kAttnRows);
         padded = up(Tq, kAttnPad);
+        // The backward kernels fill a compute unit with one workgroup.  With fewer of them than units the long axis
+        // of each is cut, into parts of at least two stages, and joined.
+        q_tiles = div_up(rows, kAttnRows);
+        key_tiles = div_up(Tk, kAttnRows);
+        q_splits = parts(B * Hkv * q_tiles, div_up(Tk, attn_backward_stage(dt)));
+        k_splits = parts(B * Hkv * key_tiles, div_up(Tq, attn_backward_stage(dt)) * share);
+    }
+
+    static int64_t parts(int64_t work, int64_t most)
+    {
+        return std::min<int64_t>(div_up(256, std::max<int64_t>(1, work)), std::max<int64_t>(1, most / 2));
     }
 
     int64_t blocks() const { return B * Hkv * splits * tiles; }
@@ -310,7 +323,8 @@ struct AttnShape {
     bool fits() const
     {
         const int64_t per = 16 / esize(dt);
-        return blocks() <= kMaxLanes / 256 && B * Hkv * key_tiles <= kMaxLanes / 256 &&
+        return blocks() <= kMaxLanes / 512 && B * Hkv * key_tiles * k_splits <= kMaxLanes / 256 &&
+               B * Hkv * q_tiles * q_splits <= kMaxLanes / 256 &&
                div_up(B * H * padded, 32) <= kMaxLanes / 256 &&
                div_up((2 * B * Tq * H + 2 * B * Tk * Hkv) * (cols / per), 256) <= kMaxLanes / 256;
     }
@@ -324,7 +338,7 @@ bool valid_attn(const rar_attn_s *a, int64_t B, int64_t Tq, int64_t Tk)
 
 struct AttnWs {
     void *q, *k, *v, *g;
-    float *part, *stats, *lse, *delta;
+    float *part, *stats, *lse, *delta, *q_part, *k_part;
     int64_t bytes;
 };
 
@@ -341,6 +355,10 @@ AttnWs attn_ws(const AttnShape &s, bool backward, void *ws)
         w.g = c.take(wide);
         w.lse = (float *)c.take(s.B * s.H * s.padded * 4);
         w.delta = (float *)c.take(s.B * s.H * s.padded * 4);
+        if (s.q_splits > 1)
+            w.q_part = (float *)c.take(s.q_splits * s.part_rows() * s.width * 4);
+        if (s.k_splits > 1)
+            w.k_part = (float *)c.take(s.k_splits * s.B * s.Hkv * s.Tk * 2 * s.width * 4);
     } else if (s.splits > 1) {
         w.part = (float *)c.take(s.splits * s.part_rows() * s.width * 4);
         w.stats = (float *)c.take(s.splits * s.part_rows() * 8);
@@ -545,15 +563,47 @@ extern "C" rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, 
     rar_status rc = pack.count ? launched(launch_attn_pack(s.dt, pack, st)) : RAR_OK;
     if (rc == RAR_OK && queries)
         rc = launched(launch_attn_delta(s.dt, p, st));
+    AttnSum sum{};
     if (rc == RAR_OK && dq) {
-        p.tiles = div_up(s.rows, kAttnRows);
-        p.blocks = B * s.Hkv * p.tiles;
+        p.tiles = s.q_tiles;
+        p.splits = (int)s.q_splits;
+        p.blocks = B * s.Hkv * p.tiles * p.splits;
+        p.part = w.q_part;
+        p.part_rows = s.part_rows();
         rc = launched(launch_attn_dq(s.dt, p, st));
+        if (p.splits > 1) {
+            sum.q_part = w.q_part;
+            sum.q_rows = s.part_rows();
+        }
     }
     if (rc == RAR_OK && (dk || dv)) {
         p.tiles = s.key_tiles;
-        p.blocks = B * s.Hkv * p.tiles;
+        p.splits = (int)s.k_splits;
+        p.blocks = B * s.Hkv * p.tiles * p.splits;
+        p.part = w.k_part;
+        p.part_rows = B * s.Hkv * Tk;
         rc = launched(launch_attn_dkv(s.dt, p, st));
+        if (p.splits > 1) {
+            sum.k_part = w.k_part;
+            sum.k_rows = B * s.Hkv * Tk;
+        }
+    }
+    if (rc == RAR_OK && (sum.q_rows || sum.k_rows)) {
+        sum.Tq = Tq;
+        sum.Tk = Tk;
+        sum.Hkv = s.Hkv;
+        sum.share = s.share;
+        sum.q_splits = (int)s.q_splits;
+        sum.k_splits = (int)s.k_splits;
+        sum.pitch = s.width;
+        sum.dh = (int)s.dh;
+        sum.dq = dq;
+        sum.lddq = lddq;
+        sum.dk = dk;
+        sum.lddk = lddk;
+        sum.dv = dv;
+        sum.lddv = lddv;
+        rc = launched(launch_attn_sum(s.dt, sum, st));
     }
     return rc;
 }

@@ -33,20 +33,16 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_rows(const
     Join join{lds};
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / (float)p.cols;
-    const int64_t c = (int64_t)lane * 8;
-    const int cols = clamp8(p.cols - c);
-    Eight<T> gate, w1, b1, w2, b2;
-    load_or(gate, p.o ? p.gate : nullptr, c, cols, 1.0f);
-    load_or(w1, p.post ? p.post_w : nullptr, c, cols, 1.0f);
-    load_or(b1, p.post ? p.post_b : nullptr, c, cols, 0.0f);
-    load_or(w2, p.pre ? p.pre_w : nullptr, c, cols, 1.0f);
-    load_or(b2, p.pre ? p.pre_b : nullptr, c, cols, 0.0f);
-    Eight<T> xr, orow;
-    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
-        const int cnt = row < p.rows ? cols : 0;
-        xr.load((const T *)p.x + row * p.ldx + c, cnt);
+    const Slot at((int64_t)lane * 8, p.cols);
+    const int64_t c = at.c;
+    const int cols = at.cnt;
+    // (the vectors that a call does not use are null)
+    Eight<T> gate, w1, b1, w2, b2, xr, orow;
+    auto ahead = [&](int64_t row) __attribute__((always_inline)) {
+        row = row < p.rows ? row : p.rows - 1;
+        fetch(xr, (const T *)p.x + row * p.ldx, at);
         if (p.o)
-            orow.load((const T *)p.o + row * p.ldo + c, cnt);
+            fetch(orow, (const T *)p.o + row * p.ldo, at);
     };
     // v becomes the normalised row; elements behind the row stay zero
     auto normalise = [&](float (&v)[8], int kind) __attribute__((always_inline)) {
@@ -74,15 +70,31 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_rows(const
 
     const int64_t stride = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    fetch(row);
+    ahead(row);
+    fetch_or(gate, p.gate, at, 1.0f);
+    fetch_or(w1, p.post_w, at, 1.0f);
+    fetch_or(b1, p.post_b, at, 0.0f);
+    fetch_or(w2, p.pre_w, at, 1.0f);
+    fetch_or(b2, p.pre_b, at, 0.0f);
+    settle_or(gate, p.gate, at);
+    settle_or(w1, p.post_w, at);
+    settle_or(b1, p.post_b, at);
+    settle_or(w2, p.pre_w, at);
+    settle_or(b2, p.pre_b, at);
     for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += stride, row += stride) {
+        settle(xr, at);
+        if (p.o)
+            settle(orow, at);
         float h[8], n[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             h[i] = p.a * xr.get(i);
             n[i] = p.o ? orow.get(i) : 0.0f;
         }
-        fetch(row + stride);
+        // h over x: the lane at a row's end has read what a lane of another wave may write from here on
+        if (LANES > 64 && p.h == p.x)
+            __syncthreads();
+        ahead(row + stride);
         if (p.o) {
             if (p.post)
                 normalise(n, p.post);
@@ -117,52 +129,65 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
     Join join{lds};
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / (float)p.cols;
-    const int64_t c = (int64_t)lane * 8;
-    const int cols = clamp8(p.cols - c);
+    const Slot at((int64_t)lane * 8, p.cols);
+    const int64_t c = at.c;
+    const int cols = at.cnt;
     Eight<T> gate, w1, w2;
-    load_or(gate, p.o ? p.gate : nullptr, c, cols, 1.0f);
-    load_or(w1, p.post ? p.post_w : nullptr, c, cols, 1.0f);
-    load_or(w2, p.pre ? p.pre_w : nullptr, c, cols, 1.0f);
     constexpr bool kAhead = LANES < 1024;  // 1024 lanes have 128 registers each
     float sums[kSums][8] = {};
     Eight<T> rdh, rdu, ro, rh;
-    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
-        const int cnt = row < p.rows ? cols : 0;
-        if (p.dh)
-            rdh.load((const T *)p.dh + row * p.lddh + c, cnt);
-        else
-            rdh.set(0.0f);
-        if (p.du)
-            rdu.load((const T *)p.du + row * p.lddu + c, cnt);
-        else
-            rdu.set(0.0f);
+    rdh.set(0.0f);
+    rdu.set(0.0f);
+    ro.set(0.0f);
+    rh.set(0.0f);
+    const bool use_h = p.pre && p.du;
+    // (a row in two parts: its gradients are needed later than what its statistics are made of)
+    auto ahead = [&](int64_t row) __attribute__((always_inline)) {
+        row = row < p.rows ? row : p.rows - 1;
         if (p.o)
-            ro.load((const T *)p.o + row * p.ldo + c, cnt);
-        else
-            ro.set(0.0f);
-        if (p.pre && p.du)
-            rh.load((const T *)p.h + row * p.ldh + c, cnt);
-        else
-            rh.set(0.0f);
+            fetch(ro, (const T *)p.o + row * p.ldo, at);
+        if (use_h)
+            fetch(rh, (const T *)p.h + row * p.ldh, at);
+    };
+    auto ahead_gradients = [&](int64_t row) __attribute__((always_inline)) {
+        row = row < p.rows ? row : p.rows - 1;
+        if (p.du)
+            fetch(rdu, (const T *)p.du + row * p.lddu, at);
+        if (p.dh)
+            fetch(rdh, (const T *)p.dh + row * p.lddh, at);
     };
     const int64_t stride = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    if (kAhead)
-        fetch(row);
+    if (kAhead) {
+        ahead(row);
+        ahead_gradients(row);
+    }
+    fetch_or(gate, p.gate, at, 1.0f);
+    fetch_or(w1, p.post_w, at, 1.0f);
+    fetch_or(w2, p.pre_w, at, 1.0f);
+    settle_or(gate, p.gate, at);
+    settle_or(w1, p.post_w, at);
+    settle_or(w2, p.pre_w, at);
     for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += stride, row += stride) {
         const bool live = row < p.rows;
-        if (!kAhead)
-            fetch(row);
+        if (!kAhead) {
+            ahead(row);
+            ahead_gradients(row);
+        }
+        settle(ro, at);
+        settle(rh, at);
+        if (!live) {
+            ro.set(0.0f);
+            rh.set(0.0f);
+        }
         float o[8], h[8], g[8], du[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             o[i] = ro.get(i);
             h[i] = rh.get(i);
-            g[i] = rdh.get(i);
-            du[i] = rdu.get(i);
         }
         if (kAhead)
-            fetch(row + stride);
+            ahead(row + stride);
         if (p.post == RAR_NORM_LAYER || p.pre == RAR_NORM_LAYER) {
             float t[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -179,6 +204,20 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
                 h[i] = i < cols ? h[i] - mh : 0.0f;
             }
         }
+        // (arrived before the meeting below, behind which dx may be written over dh)
+        settle(rdu, at);
+        settle(rdh, at);
+        if (!live) {
+            rdu.set(0.0f);
+            rdh.set(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            du[i] = rdu.get(i);
+            g[i] = rdh.get(i);
+        }
+        if (kAhead)
+            ahead_gradients(row + stride);
         float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -484,37 +523,40 @@ __global__ void __launch_bounds__(kWideLanes) rar_norm_grad_wide(const NormGradP
 // Column sums
 // ---------------------------------------------------------------------------
 //
-// A workgroup joins 16 columns of every chunk: four lanes of four columns, 256
+// A workgroup joins 16 columns of every chunk, of both sums of one norm: four lanes of four columns, 256
 // of them beside each other, joined by lane exchanges and through LDS in a
 // fixed order.
 template <class T>
 __global__ void __launch_bounds__(1024) rar_norm_sums(const NormGradParams p)
 {
-    __shared__ float joined[kSums][16][16];
+    __shared__ float joined[2][16][16];
     const int quad = threadIdx.x & 3, slice = threadIdx.x >> 2, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 16 + quad * 4;
+    const int pair = p.sum_post ? (int)blockIdx.y * 2 : 2;  // the sums of this workgroup
+    f32x4 t[2] = {};
+    if (c < p.pitch)
+#pragma unroll 4
+        for (int64_t k = slice; k < p.chunks; k += 256)
 #pragma unroll
-    for (int j = 0; j < kSums; ++j) {
-        f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
-        if ((j < 2 ? p.sum_post : p.sum_pre) && c < p.pitch)
-            for (int64_t k = slice; k < p.chunks; k += 256)
-                t += load4(p.part + (k * kSums + j) * p.pitch + c);
+            for (int j = 0; j < 2; ++j)
+                t[j] += load4(p.part + (k * kSums + pair + j) * p.pitch + c);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int d = 4; d < 64; d *= 2)
-                t[i] += __shfl_xor(t[i], d);
+                t[j][i] += __shfl_xor(t[j][i], d);
             if ((threadIdx.x & 63) < 4)
-                joined[j][wave][quad * 4 + i] = t[i];
+                joined[j][wave][quad * 4 + i] = t[j][i];
         }
-    }
     __syncthreads();
     const int64_t col = (int64_t)blockIdx.x * 16 + threadIdx.x;
     if (threadIdx.x >= 16 || col >= p.cols)
         return;
-    float v[kSums];
+    float v[2];
 #pragma unroll
-    for (int j = 0; j < kSums; ++j) {
+    for (int j = 0; j < 2; ++j) {
         v[j] = 0.0f;
 #pragma unroll
         for (int w = 0; w < 16; ++w)
@@ -525,12 +567,15 @@ __global__ void __launch_bounds__(1024) rar_norm_sums(const NormGradParams p)
         if (q)
             ((T *)q)[col] = from_f32<T>(p.accumulate ? to_f32(((const T *)q)[col]) + r : r);
     };
+    if (pair == 2) {
+        put(p.dpre_w, v[0]);
+        put(p.dpre_b, v[1]);
+        return;
+    }
     const float sg = p.s * vec(p.gate, 1.0f);
     put(p.dpost_w, sg * v[0]);
     put(p.dpost_b, sg * v[1]);
     put(p.dgate, p.s * (p.post ? __builtin_fmaf(vec(p.post_w, 1.0f), v[0], vec(p.post_b, 0.0f) * v[1]) : v[0]));
-    put(p.dpre_w, v[2]);
-    put(p.dpre_b, v[3]);
 }
 
 // Lanes of a row at eight columns a lane: a wave at least, a workgroup of 1024 at
@@ -555,8 +600,10 @@ struct RowKernels {
 
 int64_t norm_chunks(int64_t rows, int64_t cols)
 {
+    // Three workgroups a compute unit, as many as the registers let in at once.  65536 x 2048 bf16, kernel and
+    // sums: 768 chunks 350 us, 512 369, 1024 (a second turn for some) 398.
     const int lanes = row_lanes(cols), per = rows_of(lanes);
-    const int64_t most = lanes ? 1024 : (cols <= 65536 ? 256 : (int64_t(1) << 24) / cols);
+    const int64_t most = lanes ? 768 / per : (cols <= 65536 ? 256 : (int64_t(1) << 24) / cols);
     return std::min((rows + per - 1) / per, most) * per;
 }
 
@@ -592,7 +639,7 @@ hipError_t launch_norm_grad(rar_dtype dt, const NormGradParams &p, hipStream_t s
 
 hipError_t launch_norm_sums(rar_dtype dt, const NormGradParams &p, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((p.pitch + 15) / 16);
+    const dim3 grid((unsigned)((p.pitch + 15) / 16), p.sum_post && p.sum_pre ? 2 : 1);
     return launch(dt == RAR_BF16 ? rar_norm_sums<bf16> : rar_norm_sums<float>, grid, 1024, st, p);
 }
 

@@ -206,8 +206,21 @@ inline int attn_stage(rar_dtype dt, int64_t rows)
     return rows <= kAttnFewRows ? kAttnFewStage : (dt == RAR_BF16 ? 64 : 32);
 }
 
+// Rows of a stage of the backward kernels.
+inline int attn_backward_stage(rar_dtype dt) { return dt == RAR_BF16 ? 64 : 32; }
+
 // Waves of a workgroup that share out the keys, by the bytes of a row in LDS: what fills LDS.
 constexpr int attn_few_waves(int row_bytes) { return 512 / row_bytes; }
+
+// Parts of dq (q_rows rows, 0: none) and of dk and dv (k_rows): [splits][rows][pitch]
+// and [splits][rows][dk's pitch, dv's pitch].
+struct AttnSum {
+    const float *q_part, *k_part;
+    int64_t q_rows, k_rows, Tq, Tk, Hkv, share;
+    int q_splits, k_splits, pitch, dh;
+    void *dq, *dk, *dv;
+    int64_t lddq, lddk, lddv;
+};
 
 struct AttnPack {
     struct Item {
@@ -278,6 +291,7 @@ hipError_t launch_attn_join(rar_dtype dt, const AttnParams &p, hipStream_t st);
 hipError_t launch_attn_delta(rar_dtype dt, const AttnParams &p, hipStream_t st);
 hipError_t launch_attn_dq(rar_dtype dt, const AttnParams &p, hipStream_t st);
 hipError_t launch_attn_dkv(rar_dtype dt, const AttnParams &p, hipStream_t st);
+hipError_t launch_attn_sum(rar_dtype dt, const AttnSum &p, hipStream_t st);
 hipError_t launch_attn_pack(rar_dtype dt, const AttnPack &p, hipStream_t st);
 hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st);
 

@@ -7,14 +7,33 @@
 namespace rar {
 
 // Eight consecutive elements as stored, of which the first cnt exist; the others
-// read as `fill`.
+// read as `fill`.  A row's end is read one by one, in short code: few lanes have one.
 template <class T> struct Eight;
+
+__device__ __forceinline__ int clamp8(int64_t left) { return left >= 8 ? 8 : (left < 0 ? 0 : (int)left); }
 
 template <> struct Eight<float> {
     f32x4 lo, hi;
     // What is computed of these values before and after is not shared: kept
     // results would take more registers than the values.
     __device__ __forceinline__ void forget() { asm volatile("" : "+v"(lo), "+v"(hi)); }
+    // Moved down by s places, 1 .. 8; zeros follow.
+    __device__ __forceinline__ void shift(int s)
+    {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (s & 12) {
+            lo = s & 8 ? zero : hi;
+            hi = zero;
+        }
+        if (s & 2) {
+            lo = f32x4{lo.z, lo.w, hi.x, hi.y};
+            hi = f32x4{hi.z, hi.w, 0.0f, 0.0f};
+        }
+        if (s & 1) {
+            lo = f32x4{lo.y, lo.z, lo.w, hi.x};
+            hi = f32x4{hi.y, hi.z, hi.w, 0.0f};
+        }
+    }
     __device__ __forceinline__ float get(int i) const { return i < 4 ? lo[i & 3] : hi[i & 3]; }
     __device__ __forceinline__ void set(float v)
     {
@@ -31,7 +50,7 @@ template <> struct Eight<float> {
         }
         set(fill);
 #pragma unroll 1
-        for (int i = 0; i < cnt; ++i) {  // a row's end: few lanes, so short code
+        for (int i = 0; i < cnt; ++i) {
             const float v = p[i];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -42,9 +61,35 @@ template <> struct Eight<float> {
     }
 };
 
+// Where a lane's eight of a row of `cols` is read: whole eights at their place, the
+// end of a row by the row's last eight elements, shifted into place by settle() once
+// they have arrived, and nothing by any eight of the row.  So every lane reads in
+// one load, and none waits for a branch.  (A row of less than eight is read one by one.)
+struct Slot {
+    int64_t c, from;
+    int cnt;      // of the eight, how many exist
+    bool tiny;
+    __device__ __forceinline__ Slot(int64_t column, int64_t cols)
+        : c(column), cnt(clamp8(cols - column)), tiny(cols < 8)
+    {
+        from = tiny || cnt == 0 ? 0 : (cnt == 8 ? column : cols - 8);
+    }
+};
+
 template <> struct Eight<bf16> {
     u32x4 w;
     __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ void shift(int s)
+    {
+        if (s & 8)
+            w = u32x4{0, 0, 0, 0};
+        if (s & 4)
+            w = u32x4{w.z, w.w, 0, 0};
+        if (s & 2)
+            w = u32x4{w.y, w.z, w.w, 0};
+        if (s & 1)
+            w = u32x4{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
+    }
     __device__ __forceinline__ float get(int i) const
     {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
@@ -73,17 +118,40 @@ template <> struct Eight<bf16> {
     }
 };
 
+template <class T>
+__device__ __forceinline__ void fetch(Eight<T> &v, const void *row, const Slot &at)
+{
+    if (at.tiny)
+        v.load((const T *)row, at.cnt);
+    else
+        v.load((const T *)row + at.from, 8);
+}
+
+// To be called before the values are used; what does not exist is zero.
+template <class T>
+__device__ __forceinline__ void settle(Eight<T> &v, const Slot &at)
+{
+    v.forget();  // arrived, and not before: others may write the row from here on
+    if (at.cnt < 8 && !at.tiny)
+        v.shift(8 - at.cnt);
+}
+
 // A vector of a row's columns, or a constant in its place.
 template <class T>
-__device__ __forceinline__ void load_or(Eight<T> &v, const void *p, int64_t c, int cnt, float other)
+__device__ __forceinline__ void fetch_or(Eight<T> &v, const void *p, const Slot &at, float other)
 {
     if (p)
-        v.load((const T *)p + c, cnt);
+        fetch(v, p, at);
     else
         v.set(other);
 }
 
-__device__ __forceinline__ int clamp8(int64_t left) { return left >= 8 ? 8 : (left < 0 ? 0 : (int)left); }
+template <class T>
+__device__ __forceinline__ void settle_or(Eight<T> &v, const void *p, const Slot &at)
+{
+    if (p)
+        settle(v, at);
+}
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp(float v, float other)
