@@ -972,9 +972,10 @@ __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
 // Backward
 // ---------------------------------------------------------------------------
 
-// delta and lse (in the weights' unit) of every row of a head, query after query, in
-// whole stages: rows that do not count have lse = infinity, so that their weights are zero.  Eight
-// lanes a row.
+// -lse / scale and -delta of every row of a head, query after query, in whole
+// stages: what the accumulators of scores and of dP start from, so that the
+// products end with (scores - lse) / scale and dP - delta.  Rows that do not count
+// start from -infinity, so that their weights are zero.  Eight lanes a row.
 template <class T>
 __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
 {
@@ -1007,8 +1008,8 @@ __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
     for (int d = 1; d < 8; d *= 2)
         sum += __shfl_xor(sum, d);
     if (lane == 0) {
-        p.row_lse[at] = lse * kUnit<T>;
-        p.row_delta[at] = sum;
+        p.row_lse[at] = -lse / p.scale;
+        p.row_delta[at] = -sum;
     }
 }
 
@@ -1044,7 +1045,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
     load_row<T>(q, p.q, b * p.Tq + t, h, live);
     load_row<T>(g, p.g, b * p.Tq + t, h, live);
     const int64_t place = (b * p.H + h) * p.padded + t;
-    const float lse = live ? p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
+    const float lse = live ? -p.row_lse[place] * (p.scale * kUnit<T>) : kInf, delta = live ? p.row_delta[place] : 0.0f;
     const float scale = p.scale * kUnit<T>;
 
     // this workgroup's stages of keys
@@ -1102,7 +1103,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
                 scores(e + 1);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s[e][i] = weight<T>(s[e][i], scale, lse) * (dp[e][i] - delta);
+                s[e][i] = weight<T>(s[e][i], scale, lse) * (dp[e][i] + delta);
             if (rest < F::kStage)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -1145,6 +1146,19 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
 #endif
 }
 
+// Rows r0 .. r0 + 31 of a result start from the values at `from`.
+__device__ __forceinline__ void start(f32x16 &v, const RAR_LDS float *__restrict__ from, int r0)
+{
+    const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 a = *(const RAR_LDS f32x4 *)(from + r0 + 8 * i + 4 * half);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            v[4 * i + x] = a[x];
+    }
+}
+
 // dk and dv: a wave holds 32 keys, and the queries of every head that shares
 // them pass by in stages.
 template <class T, int W>
@@ -1182,7 +1196,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
         dk[d] = zeros();
         dv[d] = zeros();
     }
-    const float scale = p.scale * kUnit<T>;
+    const float scale2 = p.scale * kLog2e;
     // this workgroup's stages of queries: one head after the other
     const int64_t per_head = (qlen + F::kStage - 1) / F::kStage;
     const int64_t all = tile * kAttnRows < klen ? per_head * p.share : 0;
@@ -1223,12 +1237,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
         RAR_LDS char *const here = lds + BUF() * F::kBuffer;
         if (n + 1 < stages)
             load(lds + (1 - BUF()) * F::kBuffer);
-        const RAR_LDS float *const lse = (const RAR_LDS float *)(here + 2 * F::kHalf);
+        const RAR_LDS float *const starts = (const RAR_LDS float *)(here + 2 * F::kHalf);
         f32x16 s[F::kTiles], dp[F::kTiles];
         Frag<T> q[STEPS], g[STEPS], qt[2][W], gt[2][W];
         auto scores = [&](int e) __attribute__((always_inline)) {
-            s[e] = zeros();
-            dp[e] = zeros();
+            start(s[e], starts, e * 32);
+            start(dp[e], starts + 64, e * 32);
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 q[i] = Lds::rows(here, e * 32, i);
@@ -1254,15 +1268,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
             if (e + 1 < F::kTiles)
                 scores(e + 1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 a = *(const RAR_LDS f32x4 *)(lse + e * 32 + 8 * i + 4 * half);
-                const f32x4 c = *(const RAR_LDS f32x4 *)(lse + 64 + e * 32 + 8 * i + 4 * half);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float w = weight<T>(s[e][4 * i + x], scale, a[x]);
-                    s[e][4 * i + x] = w;
-                    dp[e][4 * i + x] = w * (dp[e][4 * i + x] - c[x]);
-                }
+            for (int i = 0; i < 16; ++i) {
+                s[e][i] = __builtin_amdgcn_exp2f(s[e][i] * scale2);
+                dp[e][i] *= s[e][i];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {

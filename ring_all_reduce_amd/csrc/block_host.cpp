@@ -314,7 +314,7 @@ struct AttnShape {
 
     static int64_t parts(int64_t work, int64_t most)
     {
-        return std::min<int64_t>(div_up(256, std::max<int64_t>(1, work)), std::max<int64_t>(1, most / 2));
+        return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, work), most / 2));
     }
 
     int64_t blocks() const { return B * Hkv * splits * tiles; }
