@@ -1318,6 +1318,247 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
 #endif
 }
 
+// The same for bf16, with the schedule in the text: products as statements that keep
+// their order, accumulators, keys and values in accumulation registers, scores in
+// ordinary ones.  (Left to itself the compiler moves scores between the register
+// files, three moves a product, and lets products, arithmetic and LDS reads wait
+// for each other.)  One wave a SIMD, and what would wait runs under the products:
+//   A(n)  scores of 32 queries n + 1, between them the weights of queries n, and the
+//         reads of their transposed fragments
+//   B(n)  products into dk and dv of queries n, under them the reads of the rows of n + 2
+// Stages of 64 queries pass through a ring of three in LDS, so that a stage's loads
+// have the time of one stage to arrive.
+__device__ __forceinline__ void product_v(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
+{
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "a"(b));
+}
+
+__device__ __forceinline__ void product_a(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
+{
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+template <int W>
+__global__ void __launch_bounds__(256, 1) rar_attn_dkv_bf16(const AttnParams p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef BackwardK<bf16, W> F;
+    typedef typename F::Lds Lds;
+    constexpr int STEPS = F::S::STEPS, kProducts = 2 * STEPS;
+    __shared__ __attribute__((aligned(1024))) char memory[3 * F::kBuffer];
+    RAR_LDS char *const lds = (RAR_LDS char *)memory;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+
+    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles * p.splits);
+    const int64_t tile = at.in % p.tiles, split = at.in / p.tiles, hk = at.hk, b = at.b;
+    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
+    const int64_t key = tile * kAttnRows + wave * 32 + (lane & 31);
+    const bool live = key < klen;
+    bf16x8 k[STEPS], v[STEPS];
+    {
+        Frag<bf16> f[STEPS];
+        load_row<bf16>(f, p.k, b * p.Tk + key, hk, live);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            k[i] = f[i].v;
+        load_row<bf16>(f, p.v, b * p.Tk + key, hk, live);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            v[i] = f[i].v;
+    }
+    f32x16 dk[W], dv[W];
+#pragma unroll
+    for (int d = 0; d < W; ++d) {
+        dk[d] = zeros();
+        dv[d] = zeros();
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        asm volatile("" : "+a"(k[i]), "+a"(v[i]));
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+        asm volatile("" : "+a"(dk[d]), "+a"(dv[d]));
+    const float scale2 = p.scale * kLog2e;
+
+    // this workgroup's stages of queries: one head after the other
+    const int64_t per_head = (qlen + F::kStage - 1) / F::kStage;
+    const int64_t all = tile * kAttnRows < klen ? per_head * p.share : 0;
+    const int64_t begin = all * split / p.splits;
+    const int stages = (int)(all * (split + 1) / p.splits - begin);
+    Loader<bf16, F::S::PITCH, F::kStage, 4> lq, lg;
+    int64_t head = hk * p.share + (all ? begin / per_head : 0);
+    int64_t ahead = all ? begin % per_head : 0;  // stage within the head that is loaded next
+    bool entered = false;
+    auto load = [&](RAR_LDS char *to) __attribute__((always_inline)) {
+        if (!entered) {
+            lq.init(p.q, b * p.Tq + ahead * F::kStage, head, qlen - ahead * F::kStage);
+            lg.init(p.g, b * p.Tq + ahead * F::kStage, head, qlen - ahead * F::kStage);
+            entered = true;
+        }
+        lq.load(to);
+        lg.load(to + F::kHalf);
+        if (wave < 2) {
+            const float *const from = (wave ? p.row_delta : p.row_lse) + (b * p.H + head) * p.padded + ahead * F::kStage;
+            const __amdgpu_buffer_rsrc_t r =
+                __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, F::kStage * 4, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(to + 2 * F::kHalf + wave * 256), 4, lane * 4, 0,
+                                                     0, 0);
+        }
+        lq.advance();
+        lg.advance();
+        if (++ahead == per_head) {
+            ahead = 0;
+            ++head;
+            entered = false;
+        }
+    };
+    bf16x8 q[STEPS], g[STEPS], qt[2][W], gt[2][W];
+    f32x16 s[2], dp[2];
+    bf16x8 w[2], ds[2];
+    // one of a tile's fragments: of a row, or transposed, in the order of their use
+    auto read_row = [&](const RAR_LDS char *from, int e, int m) __attribute__((always_inline)) {
+        if (m & 1)
+            g[m / 2] = Lds::rows(from + F::kHalf, e * 32, m / 2).v;
+        else
+            q[m / 2] = Lds::rows(from, e * 32, m / 2).v;
+    };
+    auto read_col = [&](const RAR_LDS char *from, int e, int m) __attribute__((always_inline)) {
+        const int j = m / (2 * W), d = m / 2 % W;
+        if (m & 1)
+            qt[j][d] = Lds::cols(from, e * 32, j, d).v;
+        else
+            gt[j][d] = Lds::cols(from + F::kHalf, e * 32, j, d).v;
+    };
+    auto begin_scores = [&](auto E, const RAR_LDS char *from) __attribute__((always_inline)) {
+        const RAR_LDS float *const starts = (const RAR_LDS float *)(from + 2 * F::kHalf);
+        start(s[E()], starts, E() * 32);
+        start(dp[E()], starts + 64, E() * 32);
+    };
+    auto score = [&](auto E, int m) __attribute__((always_inline)) {
+        if (m & 1)
+            product_v(dp[E()], g[m / 2], v[m / 2]);
+        else
+            product_v(s[E()], q[m / 2], k[m / 2]);
+    };
+    // A: scores of tile N with the weights of the other tile, and the reads of its fragments, between them
+    auto phase_a = [&](auto N, const RAR_LDS char *from) __attribute__((always_inline)) {
+        constexpr int O = 1 - N();
+        // the other tile's products were issued before phase B; its last ones write until here at the latest
+        asm volatile("s_nop 15" : "+v"(s[O]), "+v"(dp[O]));
+        float x[16], y[16];
+        uint32_t pw[8], pd[8];
+        auto finish = [&](int i) __attribute__((always_inline)) {
+            y[i] = dp[O][i] * x[i];
+            if (i & 1) {
+                pw[i / 2] = pack_bf16(x[i - 1], x[i]);
+                pd[i / 2] = pack_bf16(y[i - 1], y[i]);
+                asm volatile("" : "+v"(pw[i / 2]), "+v"(pd[i / 2]));
+            }
+        };
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m) {
+            score(N, m);
+            read_col(from, O, m);
+#pragma unroll
+            for (int i = m * 16 / kProducts; i < (m + 1) * 16 / kProducts; ++i) {
+                x[i] = __builtin_amdgcn_exp2f(s[O][i] * scale2);
+                asm volatile("" : "+v"(x[i]));
+            }
+            // (an exponential's result is used one product later)
+            if (m > 0)
+#pragma unroll
+                for (int i = (m - 1) * 16 / kProducts; i < m * 16 / kProducts; ++i)
+                    finish(i);
+        }
+#pragma unroll
+        for (int i = (kProducts - 1) * 16 / kProducts; i < 16; ++i)
+            finish(i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[j] = __builtin_bit_cast(bf16x8, u32x4{pw[4 * j], pw[4 * j + 1], pw[4 * j + 2], pw[4 * j + 3]});
+            ds[j] = __builtin_bit_cast(bf16x8, u32x4{pd[4 * j], pd[4 * j + 1], pd[4 * j + 2], pd[4 * j + 3]});
+        }
+        // packed by the vector units, read by the matrix ones
+        asm volatile("s_nop 3" : "+v"(w[0]), "+v"(w[1]), "+v"(ds[0]), "+v"(ds[1]));
+    };
+    auto phase_b = [&](const RAR_LDS char *from, int e) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m) {
+            const int j = m / (2 * W), d = m / 2 % W;
+            if (m & 1)
+                product_a(dk[d], qt[j][d], ds[j]);
+            else
+                product_a(dv[d], gt[j][d], w[j]);
+            read_row(from, e, m);
+        }
+    };
+
+    if (stages)
+        load(lds);
+    meet();
+    if (stages > 1)
+        load(lds + F::kBuffer);
+    if (stages) {
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m)
+            read_row(lds, 0, m);
+        begin_scores(Half<0>{}, lds);
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m)
+            score(Half<0>{}, m);
+        begin_scores(Half<1>{}, lds);
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m)
+            read_row(lds, 1, m);
+    }
+    int slot = 0;
+    for (int n = 0; n < stages; ++n) {
+        RAR_LDS char *const here = lds + slot * F::kBuffer;
+        slot = slot == 2 ? 0 : slot + 1;
+        RAR_LDS char *const next = lds + slot * F::kBuffer;
+        phase_a(Half<1>{}, here);
+        // the next stage has arrived, and the one before this is no longer read
+        meet();
+        if (n + 2 < stages)
+            load(lds + (slot == 2 ? 0 : slot + 1) * F::kBuffer);
+        begin_scores(Half<0>{}, next);  // (behind the last stage: of what lies there, for nothing)
+        phase_b(next, 0);
+        phase_a(Half<0>{}, here);
+        begin_scores(Half<1>{}, next);
+        phase_b(next, 1);
+    }
+    // wait for the last products, and tie every use of the accumulators to what follows the wait
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+        asm volatile("" : "+a"(dk[d]), "+a"(dv[d]));
+    if (key >= p.Tk)
+        return;
+#pragma unroll
+    for (int d = 0; d < W; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = d * 32 + 8 * i + 4 * half;
+            f32x4 a, e;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                a[x] = live ? dk[d][4 * i + x] * p.scale : 0.0f;
+                e[x] = live ? dv[d][4 * i + x] : 0.0f;
+            }
+            if (p.splits > 1) {
+                float *const part = p.part + (split * p.part_rows + (b * p.Hkv + hk) * p.Tk + key) * (2 * W * 32);
+                store4(part + c, a);
+                store4(part + W * 32 + c, e);
+                continue;
+            }
+            if (p.dk)
+                put4((bf16 *)p.dk + (b * p.Tk + key) * p.lddk + hk * p.dh, c, p.dh, a);
+            if (p.dv)
+                put4((bf16 *)p.dv + (b * p.Tk + key) * p.lddv + hk * p.dh, c, p.dh, e);
+        }
+#endif
+}
+
 // Joins the parts of split gradients, in order: first dq's rows, then those of dk and
 // dv; four columns a lane.
 template <class T>
@@ -1412,14 +1653,14 @@ void (*dq_kernel(int w))(AttnParams)
     }
 }
 
-template <class T>
-void (*dkv_kernel(int w))(AttnParams)
+void (*dkv_kernel(rar_dtype dt, int w))(AttnParams)
 {
+    const bool wide = dt == RAR_F32;
     switch (w) {
-    case 1: return rar_attn_dkv<T, 1>;
-    case 2: return rar_attn_dkv<T, 2>;
-    case 3: return rar_attn_dkv<T, 3>;
-    default: return rar_attn_dkv<T, 4>;
+    case 1: return wide ? rar_attn_dkv<float, 1> : rar_attn_dkv_bf16<1>;
+    case 2: return wide ? rar_attn_dkv<float, 2> : rar_attn_dkv_bf16<2>;
+    case 3: return wide ? rar_attn_dkv<float, 3> : rar_attn_dkv_bf16<3>;
+    default: return wide ? rar_attn_dkv<float, 4> : rar_attn_dkv_bf16<4>;
     }
 }
 
@@ -1459,7 +1700,7 @@ hipError_t launch_attn_dq(rar_dtype dt, const AttnParams &p, hipStream_t st)
 hipError_t launch_attn_dkv(rar_dtype dt, const AttnParams &p, hipStream_t st)
 {
     const int w = (p.dh + 31) / 32;
-    return launch(dt == RAR_BF16 ? dkv_kernel<bf16>(w) : dkv_kernel<float>(w), (unsigned)p.blocks, 256, st, p);
+    return launch(dkv_kernel(dt, w), (unsigned)p.blocks, 256, st, p);
 }
 
 hipError_t launch_attn_sum(rar_dtype dt, const AttnSum &p, hipStream_t st)
