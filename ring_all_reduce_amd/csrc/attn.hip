@@ -1050,10 +1050,13 @@ struct BackwardQ {
     static constexpr int kHalf = kStage * Lds::kBytes;
 };
 
-template <class T, int W>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn_dq(const AttnParams p)
+// (Binary32.  A product of a tile takes the matrix cores long enough that the reads of
+// the next are hidden one fragment ahead, which the compiler does.)
+template <int W>
+__global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
+    typedef float T;
     typedef BackwardQ<T, W> F;
     typedef typename F::Lds Lds;
     constexpr int STEPS = F::S::STEPS;
@@ -1101,49 +1104,27 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
             lv.load(next + F::kHalf);
         }
         const int rest = (int)(klen - k0 - (int64_t)n * F::kStage);
-        f32x16 s[F::kTiles], dp[F::kTiles];
-        Frag<T> k[STEPS], v[STEPS], kt[2][W];
-        auto scores = [&](int e) __attribute__((always_inline)) {
-            s[e] = zeros();
-            dp[e] = zeros();
+        f32x16 s = zeros(), dp = zeros();
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                k[i] = Lds::rows(here, e * 32, i);
-                v[i] = Lds::rows(here + F::kHalf, e * 32, i);
-            }
-            schedule_fence();
+        for (int i = 0; i < STEPS; ++i) {
+            mma(s, Lds::rows(here, 0, i), q[i]);
+            mma(dp, Lds::rows(here + F::kHalf, 0, i), g[i]);
+        }
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                mma(s[e], k[i], q[i]);
-                mma(dp[e], v[i], g[i]);
-            }
-        };
-        scores(0);
-#pragma unroll
-        for (int e = 0; e < F::kTiles; ++e) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int d = 0; d < W; ++d)
-                    kt[j][d] = Lds::cols(here, e * 32, j, d);
-            if (e + 1 < F::kTiles)
-                scores(e + 1);
+        for (int i = 0; i < 16; ++i)
+            s[i] = weight<T>(s[i], scale, lse) * (dp[i] + delta);
+        if (rest < F::kStage)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s[e][i] = weight<T>(s[e][i], scale, lse) * (dp[e][i] + delta);
-            if (rest < F::kStage)
+                if (row_of(i) + 4 * half >= rest)
+                    s[i] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (e * 32 + row_of(i) + 4 * half >= rest)
-                        s[e][i] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+            Frag<T> w;
+            w.set(s, 8 * j);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                Frag<T> w;
-                w.set(s[e], 8 * j);
-#pragma unroll
-                for (int d = 0; d < W; ++d)
-                    mma(acc[d], kt[j][d], w);
-            }
+            for (int d = 0; d < W; ++d)
+                mma(acc[d], Lds::cols(here, 0, j, d), w);
         }
         meet();
     };
@@ -1381,10 +1362,11 @@ struct BackwardK {
     static constexpr int kBuffer = 2 * kHalf + 1024;    // q, do, lse and delta
 };
 
-template <class T, int W>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn_dkv(const AttnParams p)
+template <int W>
+__global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
+    typedef float T;
     typedef BackwardK<T, W> F;
     typedef typename F::Lds Lds;
     constexpr int STEPS = F::S::STEPS;
@@ -1448,50 +1430,28 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && W < 4 ? 2 : 1) rar_attn
         if (n + 1 < stages)
             load(lds + (1 - BUF()) * F::kBuffer);
         const RAR_LDS float *const starts = (const RAR_LDS float *)(here + 2 * F::kHalf);
-        f32x16 s[F::kTiles], dp[F::kTiles];
-        Frag<T> q[STEPS], g[STEPS], qt[2][W], gt[2][W];
-        auto scores = [&](int e) __attribute__((always_inline)) {
-            start(s[e], starts, e * 32);
-            start(dp[e], starts + 64, e * 32);
+        f32x16 s, dp;
+        start(s, starts, 0);
+        start(dp, starts + 64, 0);
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                q[i] = Lds::rows(here, e * 32, i);
-                g[i] = Lds::rows(here + F::kHalf, e * 32, i);
-            }
-            schedule_fence();
+        for (int i = 0; i < STEPS; ++i) {
+            mma(s, Lds::rows(here, 0, i), k[i]);
+            mma(dp, Lds::rows(here + F::kHalf, 0, i), v[i]);
+        }
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                mma(s[e], q[i], k[i]);
-                mma(dp[e], g[i], v[i]);
-            }
-        };
-        scores(0);
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(s[i] * scale2);
+            dp[i] *= s[i];
+        }
 #pragma unroll
-        for (int e = 0; e < F::kTiles; ++e) {
+        for (int j = 0; j < 2; ++j) {
+            Frag<T> w, ds;
+            w.set(s, 8 * j);
+            ds.set(dp, 8 * j);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int d = 0; d < W; ++d) {
-                    gt[j][d] = Lds::cols(here + F::kHalf, e * 32, j, d);
-                    qt[j][d] = Lds::cols(here, e * 32, j, d);
-                }
-            if (e + 1 < F::kTiles)
-                scores(e + 1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[e][i] = __builtin_amdgcn_exp2f(s[e][i] * scale2);
-                dp[e][i] *= s[e][i];
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                Frag<T> w, ds;
-                w.set(s[e], 8 * j);
-                ds.set(dp[e], 8 * j);
-#pragma unroll
-                for (int d = 0; d < W; ++d) {
-                    mma(dv[d], gt[j][d], w);
-                    mma(dk[d], qt[j][d], ds);
-                }
+            for (int d = 0; d < W; ++d) {
+                mma(dv[d], Lds::cols(here + F::kHalf, 0, j, d), w);
+                mma(dk[d], Lds::cols(here, 0, j, d), ds);
             }
         }
         meet();
@@ -1837,10 +1797,10 @@ void (*dq_kernel(rar_dtype dt, int w))(AttnParams)
 {
     const bool wide = dt == RAR_F32;
     switch (w) {
-    case 1: return wide ? rar_attn_dq<float, 1> : rar_attn_dq_bf16<1>;
-    case 2: return wide ? rar_attn_dq<float, 2> : rar_attn_dq_bf16<2>;
-    case 3: return wide ? rar_attn_dq<float, 3> : rar_attn_dq_bf16<3>;
-    default: return wide ? rar_attn_dq<float, 4> : rar_attn_dq_bf16<4>;
+    case 1: return wide ? rar_attn_dq_f32<1> : rar_attn_dq_bf16<1>;
+    case 2: return wide ? rar_attn_dq_f32<2> : rar_attn_dq_bf16<2>;
+    case 3: return wide ? rar_attn_dq_f32<3> : rar_attn_dq_bf16<3>;
+    default: return wide ? rar_attn_dq_f32<4> : rar_attn_dq_bf16<4>;
     }
 }
 
@@ -1848,10 +1808,10 @@ void (*dkv_kernel(rar_dtype dt, int w))(AttnParams)
 {
     const bool wide = dt == RAR_F32;
     switch (w) {
-    case 1: return wide ? rar_attn_dkv<float, 1> : rar_attn_dkv_bf16<1>;
-    case 2: return wide ? rar_attn_dkv<float, 2> : rar_attn_dkv_bf16<2>;
-    case 3: return wide ? rar_attn_dkv<float, 3> : rar_attn_dkv_bf16<3>;
-    default: return wide ? rar_attn_dkv<float, 4> : rar_attn_dkv_bf16<4>;
+    case 1: return wide ? rar_attn_dkv_f32<1> : rar_attn_dkv_bf16<1>;
+    case 2: return wide ? rar_attn_dkv_f32<2> : rar_attn_dkv_bf16<2>;
+    case 3: return wide ? rar_attn_dkv_f32<3> : rar_attn_dkv_bf16<3>;
+    default: return wide ? rar_attn_dkv_f32<4> : rar_attn_dkv_bf16<4>;
     }
 }
 
