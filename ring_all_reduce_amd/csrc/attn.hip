@@ -972,10 +972,11 @@ __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
 // Backward
 // ---------------------------------------------------------------------------
 
-// -lse / scale and -delta of every row of a head, query after query, in whole
-// stages: what the accumulators of scores and of dP start from, so that the
-// products end with (scores - lse) / scale and dP - delta.  Rows that do not count
-// start from -infinity, so that their weights are zero.  Eight lanes a row.
+// -lse and -delta of every row of a head, query after query, in whole stages: what is
+// added to scores and to dP.  bf16 has -lse / scale, which the scores' accumulator
+// starts from, so that the products end with (scores - lse) / scale; in binary32 a
+// sum that starts so far from zero would lose a digit.  Rows that do not count have
+// -infinity, so that their weights are zero.  Eight lanes a row.
 template <class T>
 __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
 {
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
     for (int d = 1; d < 8; d *= 2)
         sum += __shfl_xor(sum, d);
     if (lane == 0) {
-        p.row_lse[at] = -lse / p.scale;
+        p.row_lse[at] = sizeof(T) == 2 ? -lse / p.scale : -lse;
         p.row_delta[at] = -sum;
     }
 }
@@ -1075,8 +1076,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
     load_row<T>(q, p.q, b * p.Tq + t, h, live);
     load_row<T>(g, p.g, b * p.Tq + t, h, live);
     const int64_t place = (b * p.H + h) * p.padded + t;
-    const float lse = live ? -p.row_lse[place] * (p.scale * kUnit<T>) : kInf, delta = live ? p.row_delta[place] : 0.0f;
-    const float scale = p.scale * kUnit<T>;
+    const float lse = live ? -p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
 
     // this workgroup's stages of keys
     const int64_t all = first / p.share < qlen ? (klen + F::kStage - 1) / F::kStage : 0;
@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            s[i] = weight<T>(s[i], scale, lse) * (dp[i] + delta);
+            s[i] = weight<T>(s[i], p.scale, lse) * (dp[i] + delta);
         if (rest < F::kStage)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -1337,7 +1337,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_bf16(const AttnParams p)
 #endif
 }
 
-// Rows r0 .. r0 + 31 of a result start from the values at `from`.
+// Rows r0 .. r0 + 31 of a result become the values at `from`.
 __device__ __forceinline__ void start(f32x16 &v, const RAR_LDS float *__restrict__ from, int r0)
 {
     const int half = (threadIdx.x & 63) >> 5;
@@ -1388,7 +1388,6 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
         dk[d] = zeros();
         dv[d] = zeros();
     }
-    const float scale2 = p.scale * kLog2e;
     // this workgroup's stages of queries: one head after the other
     const int64_t per_head = (qlen + F::kStage - 1) / F::kStage;
     const int64_t all = tile * kAttnRows < klen ? per_head * p.share : 0;
@@ -1430,17 +1429,17 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
         if (n + 1 < stages)
             load(lds + (1 - BUF()) * F::kBuffer);
         const RAR_LDS float *const starts = (const RAR_LDS float *)(here + 2 * F::kHalf);
-        f32x16 s, dp;
-        start(s, starts, 0);
+        f32x16 s = zeros(), dp, lse;
         start(dp, starts + 64, 0);
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             mma(s, Lds::rows(here, 0, i), k[i]);
             mma(dp, Lds::rows(here + F::kHalf, 0, i), v[i]);
         }
+        start(lse, starts, 0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(s[i] * scale2);
+            s[i] = weight<T>(s[i], p.scale, -lse[i]);
             dp[i] *= s[i];
         }
 #pragma unroll
