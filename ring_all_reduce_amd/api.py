@@ -10,9 +10,10 @@ integer hipStream_t, or None for torch's current stream on the current
 device (the default stream when torch has no GPU).
 
 The operators on matrices (rar_embed_*, rar_linear_*, rar_ckpt_*, rar_norm_*,
-rar_dropout, rar_attn_*, rar_logprob*) take 2-D tensors whose rows are contiguous; the distance between rows is the leading
-dimension.  An integer address stands for a contiguous matrix.  Their tensors
-must be on the current device.  ``ws`` is a uint8 tensor of at least the
+rar_dropout, rar_attn_*, rar_logprob*) take 2-D tensors whose rows are
+contiguous; the distance between rows is the leading dimension.  An integer
+address stands for a contiguous matrix.  Their tensors must be on the current
+device.  ``ws`` is a uint8 tensor of at least the
 queried bytes, or None: then one is allocated for the call, and returned to
 torch's allocator in the order of the call's stream.
 
@@ -657,6 +658,41 @@ def _ckpt(codes, scales, T: int, D: int):
 # cross attention, log probabilities
 # ---------------------------------------------------------------------------
 
+# The usual arguments in as few steps as they take (a short call is bound by the host): the current device is asked
+# once a call, and what _matrix, _dense and _on do for others is left to them.
+
+def _there() -> int:
+    """The current device's index, or one that no tensor has."""
+    dev = _here()
+    return dev if dev >= 0 else -2
+
+
+def _mat(x, what: str, tdtype, rows: int, cols: int, here: int):
+    if x is None:
+        return 0, cols
+    if (getattr(x, "dtype", None) is tdtype and x.get_device() == here and x.shape == (rows, cols) and x.is_contiguous()
+            and rows):
+        return x.data_ptr(), cols
+    return _matrix(x, what, tdtype, rows, cols)
+
+
+def _vec(x, what: str, tdtype, numel: int, here: int) -> int:
+    if x is None:
+        return 0
+    if getattr(x, "dtype", None) is tdtype and x.get_device() == here and x.numel() == numel and x.is_contiguous():
+        return x.data_ptr()
+    return _dense(x, what, tdtype, numel)
+
+
+def _queue(stream, here: int) -> int:
+    if stream is None and here >= 0:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(here)
+    return _on(stream)
+
+
 class Norm:
     """Owner of a rar_norm_t; destroyed with the object or by rar_norm_destroy."""
 
@@ -697,15 +733,16 @@ def rar_norm_forward(plan: Norm, T: int, x, o, post_w, post_b, gate, pre_w, pre_
     """n = post(o), h = a x + s gate n, u = pre(h).  o (then h = a x), the
     vectors (weights and gate one, biases zero) and one of h and u may be None;
     h may be x."""
+    here = _there()
     T, D, td = int(T), plan.D, _torch_dtype(plan.dtype)
-    xp, ldx = _matrix(x, "x", td, T, D)
-    op, ldo = _matrix(o, "o", td, T, D)
-    hp, ldh = _matrix(h, "h", td, T, D)
-    up, ldu = _matrix(u, "u", td, T, D)
-    vs = [_dense(v, n, td, D) for v, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"), (pre_w, "pre_w"),
-                                           (pre_b, "pre_b"))]
+    xp, ldx = _mat(x, "x", td, T, D, here)
+    op, ldo = _mat(o, "o", td, T, D, here)
+    hp, ldh = _mat(h, "h", td, T, D, here)
+    up, ldu = _mat(u, "u", td, T, D, here)
+    vs = [_vec(v, n, td, D, here) for v, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"),
+                                               (pre_w, "pre_w"), (pre_b, "pre_b"))]
     _check(lib().rar_norm_forward(plan.handle, T, xp, ldx, op, ldo, vs[0], vs[1], vs[2], float(a), float(s), vs[3],
-                                  vs[4], hp, ldh, up, ldu, _on(stream)), "rar_norm_forward")
+                                  vs[4], hp, ldh, up, ldu, _queue(stream, here)), "rar_norm_forward")
 
 
 def rar_norm_backward(plan: Norm, T: int, dh, du, o, h, post_w, post_b, gate, pre_w, dx, do, dpost_w=None,
@@ -714,17 +751,18 @@ def rar_norm_backward(plan: Norm, T: int, dh, du, o, h, post_w, post_b, gate, pr
     """The gradients of rar_norm_forward from its o and h: dh and du (either may
     be None) reach h and u; every output may be None.  accumulate adds to the
     five vectors."""
+    here = _there()
     T, D, td = int(T), plan.D, _torch_dtype(plan.dtype)
     m = []
     for x, name in ((dh, "dh"), (du, "du"), (o, "o"), (h, "h"), (dx, "dx"), (do, "do")):
-        m.append(_matrix(x, name, td, T, D))
-    v = [_dense(x, n, td, D) for x, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"), (pre_w, "pre_w"))]
-    d = [_dense(x, n, td, D) for x, n in ((dpost_w, "dpost_w"), (dpost_b, "dpost_b"), (dgate, "dgate"),
-                                          (dpre_w, "dpre_w"), (dpre_b, "dpre_b"))]
+        m.append(_mat(x, name, td, T, D, here))
+    v = [_vec(x, n, td, D, here) for x, n in ((post_w, "post_w"), (post_b, "post_b"), (gate, "gate"), (pre_w, "pre_w"))]
+    d = [_vec(x, n, td, D, here) for x, n in ((dpost_w, "dpost_w"), (dpost_b, "dpost_b"), (dgate, "dgate"),
+                                              (dpre_w, "dpre_w"), (dpre_b, "dpre_b"))]
     need = rar_norm_workspace(plan, T) if ws is None and any(d) else 0
     wp, wb, _own = _workspace(ws, need, stream)
     _check(lib().rar_norm_backward(plan.handle, T, *m[0], *m[1], *m[2], *m[3], v[0], v[1], v[2], float(a), float(s),
-                                   v[3], *m[4], *m[5], *d, int(bool(accumulate)), wp, wb, _on(stream)),
+                                   v[3], *m[4], *m[5], *d, int(bool(accumulate)), wp, wb, _queue(stream, here)),
            "rar_norm_backward")
 
 
@@ -735,14 +773,16 @@ def rar_dropout(T: int, D: int, dtype: int, x, y, p: float, seed: int, step=None
     int64 on the GPU, or None for zero); the same call on dy is the backward
     pass.  y may be x or residual."""
     import torch
+    here = _there()
     T, D, td = int(T), int(D), _torch_dtype(dtype)
-    xp, ldx = _matrix(x, "x", td, T, D)
-    rp, ldr = _matrix(residual, "residual", td, T, D)
-    yp, ldy = _matrix(y, "y", td, T, D)
+    xp, ldx = _mat(x, "x", td, T, D, here)
+    rp, ldr = _mat(residual, "residual", td, T, D, here)
+    yp, ldy = _mat(y, "y", td, T, D, here)
     if not 0 <= int(seed) < 1 << 64:
         raise ValueError("seed: 64 bits")
-    _check(lib().rar_dropout(T, D, dtype, float(p), int(seed), _dense(step, "step", torch.int64, 1), xp, ldx, rp, ldr,
-                             yp, ldy, _on(stream)), "rar_dropout")
+    sp = _vec(step, "step", torch.int64, 1, here)
+    _check(lib().rar_dropout(T, D, dtype, float(p), int(seed), sp, xp, ldx, rp, ldr, yp, ldy, _queue(stream, here)),
+           "rar_dropout")
 
 
 class Attn:
@@ -788,15 +828,16 @@ def rar_attn_forward(plan: Attn, B: int, Tq: int, Tk: int, q, k, v, o, lse=None,
     None) say how many queries and keys of a sequence count.  lse ((B Tq) x H
     float32, or None) is what the backward call reads."""
     import torch
+    here = _there()
     B, Tq, Tk, td = int(B), int(Tq), int(Tk), _torch_dtype(plan.dtype)
     wide, narrow = plan.H * plan.dh, plan.Hkv * plan.dh
-    qp, op = _matrix(q, "q", td, B * Tq, wide), _matrix(o, "o", td, B * Tq, wide)
-    kp, vp = _matrix(k, "k", td, B * Tk, narrow), _matrix(v, "v", td, B * Tk, narrow)
-    nq, nk = _dense(qlen, "qlen", torch.int64, B), _dense(klen, "klen", torch.int64, B)
-    lp = _dense(lse, "lse", torch.float32, B * Tq * plan.H)
+    qp, op = _mat(q, "q", td, B * Tq, wide, here), _mat(o, "o", td, B * Tq, wide, here)
+    kp, vp = _mat(k, "k", td, B * Tk, narrow, here), _mat(v, "v", td, B * Tk, narrow, here)
+    nq, nk = _vec(qlen, "qlen", torch.int64, B, here), _vec(klen, "klen", torch.int64, B, here)
+    lp = _vec(lse, "lse", torch.float32, B * Tq * plan.H, here)
     need = rar_attn_workspace(plan, B, Tq, Tk)[0] if ws is None else 0
     wp, wb, _own = _workspace(ws, need, stream)
-    _check(lib().rar_attn_forward(plan.handle, B, Tq, Tk, *qp, *kp, *vp, nq, nk, *op, lp, wp, wb, _on(stream)),
+    _check(lib().rar_attn_forward(plan.handle, B, Tq, Tk, *qp, *kp, *vp, nq, nk, *op, lp, wp, wb, _queue(stream, here)),
            "rar_attn_forward")
 
 
@@ -804,16 +845,17 @@ def rar_attn_backward(plan: Attn, B: int, Tq: int, Tk: int, do, q, k, v, o, lse,
                       ws=None, stream=None) -> None:
     """The gradients of q, k and v (each output may be None) from the forward call's inputs, o and lse."""
     import torch
+    here = _there()
     B, Tq, Tk, td = int(B), int(Tq), int(Tk), _torch_dtype(plan.dtype)
     wide, narrow = plan.H * plan.dh, plan.Hkv * plan.dh
-    m = [_matrix(x, n, td, B * Tq, wide) for x, n in ((do, "do"), (q, "q"), (o, "o"), (dq, "dq"))]
-    n = [_matrix(x, n, td, B * Tk, narrow) for x, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv"))]
-    nq, nk = _dense(qlen, "qlen", torch.int64, B), _dense(klen, "klen", torch.int64, B)
-    lp = _dense(lse, "lse", torch.float32, B * Tq * plan.H)
+    m = [_mat(x, n, td, B * Tq, wide, here) for x, n in ((do, "do"), (q, "q"), (o, "o"), (dq, "dq"))]
+    n = [_mat(x, n, td, B * Tk, narrow, here) for x, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv"))]
+    nq, nk = _vec(qlen, "qlen", torch.int64, B, here), _vec(klen, "klen", torch.int64, B, here)
+    lp = _vec(lse, "lse", torch.float32, B * Tq * plan.H, here)
     need = rar_attn_workspace(plan, B, Tq, Tk)[1] if ws is None else 0
     wp, wb, _own = _workspace(ws, need, stream)
     _check(lib().rar_attn_backward(plan.handle, B, Tq, Tk, *m[0], *m[1], *n[0], *n[1], nq, nk, *m[2], lp, *m[3], *n[2],
-                                   *n[3], wp, wb, _on(stream)), "rar_attn_backward")
+                                   *n[3], wp, wb, _queue(stream, here)), "rar_attn_backward")
 
 
 def rar_logprob(T: int, V: int, dtype: int, logits, targets, logp, entropy=None, top_ids=None, top_logp=None,
@@ -822,8 +864,9 @@ def rar_logprob(T: int, V: int, dtype: int, logits, targets, logp, entropy=None,
     the entropy (T float32), and the K best alternatives (T x K int64 and
     float32).  Each may be None."""
     import torch
+    here = _there()
     T, V, td = int(T), int(V), _torch_dtype(dtype)
-    zp, ldz = _matrix(logits, "logits", td, T, V)
+    zp, ldz = _mat(logits, "logits", td, T, V, here)
     K = 0
     if top_ids is not None or top_logp is not None:
         if not all(hasattr(x, "data_ptr") and x.dim() == 2 for x in (top_ids, top_logp)):
@@ -831,10 +874,11 @@ def rar_logprob(T: int, V: int, dtype: int, logits, targets, logp, entropy=None,
         K = top_ids.shape[1]
         if top_ids.shape != (T, K) or top_logp.shape != (T, K):
             raise ValueError(f"top_ids {tuple(top_ids.shape)} and top_logp {tuple(top_logp.shape)}: expected ({T}, K)")
-    _check(lib().rar_logprob(T, V, dtype, zp, ldz, float(scale), _dense(targets, "targets", torch.int64, T),
-                             _dense(logp, "logp", torch.float32, T), _dense(entropy, "entropy", torch.float32, T), K,
-                             _dense(top_ids, "top_ids", torch.int64, T * K),
-                             _dense(top_logp, "top_logp", torch.float32, T * K), _on(stream)), "rar_logprob")
+    tp, lp = _vec(targets, "targets", torch.int64, T, here), _vec(logp, "logp", torch.float32, T, here)
+    ep, ip = _vec(entropy, "entropy", torch.float32, T, here), _vec(top_ids, "top_ids", torch.int64, T * K, here)
+    vp = _vec(top_logp, "top_logp", torch.float32, T * K, here)
+    _check(lib().rar_logprob(T, V, dtype, zp, ldz, float(scale), tp, lp, ep, K, ip, vp, _queue(stream, here)),
+           "rar_logprob")
 
 
 def rar_logprob_grad(T: int, V: int, dtype: int, logits, targets, dlogp, dentropy, dz, logp=None, entropy=None,
@@ -843,10 +887,12 @@ def rar_logprob_grad(T: int, V: int, dtype: int, logits, targets, dlogp, dentrop
     entropy) in the logits; dlogp and dentropy are T float32 or None.  logp and
     entropy receive what rar_logprob gives."""
     import torch
+    here = _there()
     T, V, td = int(T), int(V), _torch_dtype(dtype)
-    zp, ldz = _matrix(logits, "logits", td, T, V)
-    dp, lddz = _matrix(dz, "dz", td, T, V)
-    f = [_dense(x, n, torch.float32, T) for x, n in ((dlogp, "dlogp"), (dentropy, "dentropy"), (logp, "logp"),
-                                                     (entropy, "entropy"))]
-    _check(lib().rar_logprob_grad(T, V, dtype, zp, ldz, float(scale), _dense(targets, "targets", torch.int64, T), *f,
-                                  dp, lddz, _on(stream)), "rar_logprob_grad")
+    zp, ldz = _mat(logits, "logits", td, T, V, here)
+    dp, lddz = _mat(dz, "dz", td, T, V, here)
+    f = [_vec(x, n, torch.float32, T, here) for x, n in ((dlogp, "dlogp"), (dentropy, "dentropy"), (logp, "logp"),
+                                                         (entropy, "entropy"))]
+    tp = _vec(targets, "targets", torch.int64, T, here)
+    _check(lib().rar_logprob_grad(T, V, dtype, zp, ldz, float(scale), tp, *f, dp, lddz, _queue(stream, here)),
+           "rar_logprob_grad")
