@@ -668,8 +668,9 @@ extern "C" rar_status rar_logprob_grad(int64_t T, int64_t V, rar_dtype dtype, co
     if (!all_aligned({logits, dz}, es) || !aligned(targets, 8) || !all_aligned({dlogp, dentropy, logp, entropy}, 4))
         return RAR_EALIGN;
     const Mat mz{logits, T, V, ldz, es}, md{dz, T, V, lddz, es};
-    if (!apart({md, vec(logp, T, 4), vec(entropy, T, 4)}, {vec(targets, T, 8), vec(dlogp, T, 4), vec(dentropy, T, 4)}) ||
-        !apart({vec(logp, T, 4), vec(entropy, T, 4)}, {mz}) || (!same(md, mz) && overlap(md, mz)))
+    const Mat ml = vec(logp, T, 4), me = vec(entropy, T, 4);
+    if (!apart({md, ml, me}, {vec(targets, T, 8), vec(dlogp, T, 4), vec(dentropy, T, 4)}) || !apart({ml, me}, {mz}) ||
+        (!same(md, mz) && overlap(md, mz)))
         return RAR_EINVAL;
     LogprobParams p{};
     p.z = logits;

@@ -72,7 +72,10 @@ inline bool apart(std::initializer_list<Mat> outs, std::initializer_list<Mat> in
 }
 
 // The same matrix given twice: an output that an input may be.
-inline bool same(const Mat &a, const Mat &b) { return a.p == b.p && a.ld == b.ld && a.rows == b.rows && a.cols == b.cols; }
+inline bool same(const Mat &a, const Mat &b)
+{
+    return a.p == b.p && a.ld == b.ld && a.rows == b.rows && a.cols == b.cols;
+}
 
 inline bool aligned(const void *p, int to) { return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0; }
 

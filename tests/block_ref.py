@@ -248,7 +248,8 @@ def attn_forward(q, k, v, B, H, Hkv, scale, qlen, klen, dtype):
     safe = torch.where(l == 0, 1.0, l)
     o = (P @ v) / safe
     mag = (P @ v.abs()) / safe
-    eo = ((P * (rel + low) + torch.where(live, TINY, 0.0)) @ v.abs()) / safe + mag * (el / safe + n * 2 * E) + 4 * E * mag
+    eo = ((P * (rel + low) + torch.where(live, TINY, 0.0)) @ v.abs()) / safe
+    eo = eo + mag * (el / safe + n * 2 * E) + 4 * E * mag
     on = (torch.arange(Tq) < ql.view(-1, 1)).view(B, 1, Tq, 1)
     o, eo = torch.where(on, o, 0.0), torch.where(on, eo, 0.0)
     lse = torch.where(on & (l > 0), base + torch.log(safe), -INF)

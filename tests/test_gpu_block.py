@@ -55,8 +55,8 @@ def same_bits(a, b):
 # ---------------------------------------------------------------------------
 
 # (T, D): one element, one row, widths at and around what a wave, a workgroup and registers take, and beyond them
-NORM = [(1, 1), (3, 7), (1, 64), (17, 511), (9, 512), (5, 513), (130, 1000), (33, 1024), (40, 1025), (70, 2048), (6, 2049),
-        (31, 4096), (3, 4100), (5, 8192), (4, 8193), (3, 20011), (2, 70001), (5001, 40), (2100, 96)]
+NORM = [(1, 1), (3, 7), (1, 64), (17, 511), (9, 512), (5, 513), (130, 1000), (33, 1024), (40, 1025), (70, 2048),
+        (6, 2049), (31, 4096), (3, 4100), (5, 8192), (4, 8193), (3, 20011), (2, 70001), (5001, 40), (2100, 96)]
 NORM_KINDS = [("none", "layer"), ("layer", "layer"), ("rms", "rms"), ("layer", "none"), ("rms", "layer"),
               ("none", "none")]
 
@@ -129,7 +129,8 @@ def test_norm_parts(D, dtype):
             R.check(t, *want[n], f"{n} of {dh or du}")
     dx, dw = nan(T, D, dtype=dtype), nan(D, dtype=dtype)
     api.rar_norm_backward(plan, T, w["dh"], w["du"], None, w["h"], None, None, None, d["pre_w"], dx, None, dpre_w=dw)
-    want = R.norm_backward(m["dh"], m["du"], None, m["h"], None, None, None, v["pre_w"], "rms", "layer", eps, 1, 1, dtype)
+    want = R.norm_backward(m["dh"], m["du"], None, m["h"], None, None, None, v["pre_w"], "rms", "layer", eps, 1, 1,
+                           dtype)
     R.check(dx, *want["dx"], "dx without o")
     R.check(dw, *want["dpre_w"], "dpre_w without o")
 
@@ -291,8 +292,8 @@ def test_dropout_step_is_read_in_every_replay():
 # widths in each class and between, split keys
 ATTN = [(1, 1, 1, 1, 1, 1), (1, 1, 5, 1, 1, 16), (2, 1, 300, 4, 2, 64), (3, 7, 129, 3, 1, 40), (2, 5, 1000, 8, 1, 128),
         (1, 32, 33, 1, 1, 96), (1, 33, 64, 2, 2, 32), (2, 130, 70, 2, 1, 60), (1, 257, 300, 4, 2, 128),
-        (2, 64, 128, 6, 3, 77), (1, 1, 4100, 2, 1, 128), (5, 3, 65, 1, 1, 100), (2, 200, 31, 2, 2, 127), (1, 700, 20, 2, 1, 8),
-        (3, 96, 257, 4, 4, 33)]
+        (2, 64, 128, 6, 3, 77), (1, 1, 4100, 2, 1, 128), (5, 3, 65, 1, 1, 100), (2, 200, 31, 2, 2, 127),
+        (1, 700, 20, 2, 1, 8), (3, 96, 257, 4, 4, 33)]
 
 
 def attn_inputs(g, B, Tq, Tk, H, Hkv, dh, dtype, scale=1.0):

@@ -93,8 +93,8 @@ class Step:
             self.grad[n] = self.arena[at:at + math.prod(s)].view(s)
             at += math.prod(s)
         new = lambda *s: torch.full(s, math.nan, device=DEV)  # noqa: E731
-        self.m = {n: new(T, D) for n in ("x0", "u0", "z", "zd", "h1", "u1", "f2", "h2", "u2", "du2", "dh2", "df2", "du1",
-                                         "dh1", "dzd", "dz", "dx0", "du0", "o", "do", "q", "dq")}
+        self.m = {n: new(T, D) for n in ("x0", "u0", "z", "zd", "h1", "u1", "f2", "h2", "u2", "du2", "dh2", "df2",
+                                         "du1", "dh1", "dzd", "dz", "dx0", "du0", "o", "do", "q", "dq")}
         self.kv, self.dkv = new(TE, 2 * NARROW), new(TE, 2 * NARROW)
         self.f, self.pre, self.df = new(T, F), new(T, F), new(T, F)
         self.logits, self.lse, self.logp = new(T, V), new(T, H), new(T)
@@ -122,7 +122,8 @@ class Step:
                              w["ln2_b"], m["h1"], m["u1"], s=0.5)
         self.linear("1", m["u1"], w, self.f, w["b1"], pre=self.pre)
         self.linear("2", self.f, w, m["f2"], w["b2"])
-        api.rar_norm_forward(self.first, T, m["h1"], m["f2"], None, None, None, w["ln3_w"], w["ln3_b"], m["h2"], m["u2"])
+        api.rar_norm_forward(self.first, T, m["h1"], m["f2"], None, None, None, w["ln3_w"], w["ln3_b"], m["h2"],
+                             m["u2"])
         self.linear("_out", m["u2"], w, self.logits)
         # the loss and its gradient, over the logits
         api.rar_logprob_grad(T, V, api.F32, self.logits, targets, self.dlogp, None, self.logits, logp=self.logp)
