@@ -173,9 +173,9 @@ def philox(counter, key):
     return np.stack(c, 1)
 
 
-def keep_mask(T, D, p, seed, step):
+def keep_mask(T, D, p, seed, step, first=0):
     G = -(-D // 8)
-    g = np.arange(T * G, dtype=np.uint64)
+    g = np.arange(first, first + T * G, dtype=np.uint64)
     step &= (1 << 64) - 1
     counter = np.stack([g & np.uint64(0xFFFFFFFF), g >> np.uint64(32), np.full(T * G, step & 0xFFFFFFFF, np.uint64),
                         np.full(T * G, step >> 32, np.uint64)], 1)

@@ -266,6 +266,20 @@ def test_dropout_edges(dtype):
     api.rar_dropout(0, D, CODE[dtype], e, e, 0.5, 1)
 
 
+def test_dropout_numbers_pass_32_bits():
+    # groups of eight are numbered past 2^32: the first and the last rows against the definition, in place
+    T, D, p, seed, last = 1 << 24, 2056, 0.25, 99, 3
+    x = torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+    x.fill_(1.0)
+    api.rar_dropout(T, D, api.BF16, x, x, p, seed)
+    first = (T - last) * (D // 8)
+    assert first > 1 << 32
+    assert torch.equal(x[T - last:].cpu() != 0, R.keep_mask(last, D, p, seed, 0, first)[0])
+    assert torch.equal(x[:last].cpu() != 0, R.keep_mask(last, D, p, seed, 0)[0])
+    del x
+    torch.cuda.empty_cache()
+
+
 def test_dropout_step_is_read_in_every_replay():
     T, D, p, seed = 33, 100, 0.3, 77
     x = torch.randn(T, D, device=DEV)
@@ -462,6 +476,34 @@ def test_attention_long_cache(dtype):
     api.rar_attn_backward(plan, B, 2, Tk, do3, q3, ks, vs, o, lse, dq, None, None, klen=dev(kl))
     want = R.attn_backward(do, q, k, v, o[4:].cpu(), lse[4:].cpu(), 1, H, H, dh ** -0.5, None, None, dtype)
     R.check(dq[4:], *want[0], "dq")
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("Tq", [2, 10, 130])
+def test_attention_rows_as_far_apart_as_allowed(Tq, dtype):
+    # leading dimension 2^22: a tile's last row lies almost 2^31 bytes behind its first; all matrices in one
+    Tk, H, Hkv, dh, ld = 140, 2, 1, 128, 1 << 22
+    g = torch.Generator().manual_seed(12)
+    q, k, v, do = attn_inputs(g, 1, Tq, Tk, H, Hkv, dh, dtype)
+    big = torch.full((Tk, ld), NAN, dtype=R.DT[dtype], device=DEV)
+    at = iter(range(ld - 8 * 256, ld, 256))
+
+    def inside(rows, cols, t=None):
+        c = next(at)
+        m = big[:rows, c:c + cols]
+        return m if t is None else m.copy_(dev(t))
+
+    sq, sdo, sk, sv = inside(Tq, H * dh, q), inside(Tq, H * dh, do), inside(Tk, dh, k), inside(Tk, dh, v)
+    o, dq, dk, dv = inside(Tq, H * dh), inside(Tq, H * dh), inside(Tk, dh), inside(Tk, dh)
+    lse = nan(Tq, H, dtype="f32")
+    plan = api.rar_attn_plan(H, Hkv, dh, CODE[dtype])
+    api.rar_attn_forward(plan, 1, Tq, Tk, sq, sk, sv, o, lse=lse)
+    (ro, eo), _ = R.attn_forward(q, k, v, 1, H, Hkv, dh ** -0.5, None, None, dtype)
+    R.check(o, ro, eo, "o")
+    api.rar_attn_backward(plan, 1, Tq, Tk, sdo, sq, sk, sv, o, lse, dq, dk, dv)
+    want = R.attn_backward(do, q, k, v, o.cpu(), lse.cpu(), 1, H, Hkv, dh ** -0.5, None, None, dtype)
+    for t, (r, e), n in zip((dq, dk, dv), want, ("dq", "dk", "dv")):
+        R.check(t, r, e, n)
 
 
 def test_attention_gradient_against_differences():
