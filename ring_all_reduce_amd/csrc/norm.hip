@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_rows(const
 }
 
 template <class T, int LANES>
-__global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(const NormGradParams p)
+__global__ void __launch_bounds__(LANES > 256 ? LANES : 256, LANES >= 512 ? 4 : 1)
+    rar_norm_grad_rows(const NormGradParams p)
 {
     typedef RowJoin<LANES, 4> Join;
     constexpr int kRows = Join::kThreads / LANES;
@@ -137,8 +138,29 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
     const int64_t c = at.c;
     const int cols = at.cnt;
     Eight<T> gate, w1, w2;
-    constexpr bool kAhead = LANES < 1024;  // 1024 lanes have 128 registers each
+    // Long rows keep their column sums in LDS (a lane's own, so nothing waits): without them 128 registers hold the
+    // rest and the next row, and a compute unit holds 1024 lanes.  16384 x 8192 in bf16 360 us (1.6 GB), 1200 with the
+    // sums in registers; 16384 x 4096 176 and 214.
+    constexpr bool kInLds = LANES >= 512;
+    __shared__ f32x4 kept[kInLds ? kSums * 2 : 1][kInLds ? LANES : 1];
     float sums[kSums][8] = {};
+    auto put_sums = [&](int q) __attribute__((always_inline)) {
+        if (kInLds)
+#pragma unroll
+            for (int j = 0; j < kSums; ++j)
+                kept[j * 2 + q][lane] =
+                    f32x4{sums[j][q * 4], sums[j][q * 4 + 1], sums[j][q * 4 + 2], sums[j][q * 4 + 3]};
+    };
+    auto get_sums = [&](int q) __attribute__((always_inline)) {
+        if (kInLds)
+#pragma unroll
+            for (int j = 0; j < kSums; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sums[j][q * 4 + i] = kept[j * 2 + q][lane][i];
+    };
+    put_sums(0);
+    put_sums(1);
     Eight<T> rdh, rdu, ro, rh;
     rdh.set(0.0f);
     rdu.set(0.0f);
@@ -162,10 +184,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
     };
     const int64_t stride = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    if (kAhead) {
-        ahead(row);
-        ahead_gradients(row);
-    }
+    ahead(row);
+    ahead_gradients(row);
     fetch_or(gate, p.gate, at, 1.0f);
     fetch_or(w1, p.post_w, at, 1.0f);
     fetch_or(w2, p.pre_w, at, 1.0f);
@@ -174,10 +194,6 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
     settle_or(w2, p.pre_w, at);
     for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += stride, row += stride) {
         const bool live = row < p.rows;
-        if (!kAhead) {
-            ahead(row);
-            ahead_gradients(row);
-        }
         settle(ro, at);
         settle(rh, at);
         if (!live) {
@@ -190,8 +206,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
             o[i] = ro.get(i);
             h[i] = rh.get(i);
         }
-        if (kAhead)
-            ahead(row + stride);
+        ahead(row + stride);
         if (p.post == RAR_NORM_LAYER || p.pre == RAR_NORM_LAYER) {
             float t[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -220,8 +235,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
             du[i] = rdu.get(i);
             g[i] = rdh.get(i);
         }
-        if (kAhead)
-            ahead_gradients(row + stride);
+        ahead_gradients(row + stride);
         float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -239,6 +253,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
         float e[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            if (i % 4 == 0)
+                get_sums(i / 4);
             const float hh = h[i] * rpre, oh = o[i] * rpost;
             sums[2][i] = __builtin_fmaf(du[i], hh, sums[2][i]);
             sums[3][i] += du[i];
@@ -252,6 +268,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
             e[1] = __builtin_fmaf(q, oh, e[1]);
             g[i] = gv;
             o[i] = oh;
+            if (i % 4 == 3)
+                put_sums(i / 4);
         }
         if (p.dx && live) {
             float v[8];
@@ -275,7 +293,27 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_grad_rows(
             store8((T *)p.d_o + row * p.lddo + c, cols, v);
         }
     }
-    float *const out = p.part + ((int64_t)blockIdx.x * kRows + sub) * kSums * p.pitch;
+    get_sums(0);
+    get_sums(1);
+    // the rows that stood beside each other are one chunk: the first of them adds up
+    if (kRows > 1) {
+        __shared__ f32x4 beside[kRows > 1 ? kRows - 1 : 1][kSums * 2][LANES];
+        if (sub > 0)
+#pragma unroll
+            for (int j = 0; j < kSums * 2; ++j)
+                beside[sub - 1][j][lane] = *reinterpret_cast<const f32x4 *>(&sums[j / 2][j % 2 * 4]);
+        __syncthreads();
+        if (sub > 0)
+            return;
+#pragma unroll
+        for (int n = 0; n < kRows - 1; ++n)
+#pragma unroll
+            for (int j = 0; j < kSums * 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sums[j / 2][j % 2 * 4 + i] += beside[n][j][lane][i];
+    }
+    float *const out = p.part + (int64_t)blockIdx.x * kSums * p.pitch;
 #pragma unroll
     for (int j = 0; j < kSums; ++j)
         if (cols > 0 && (j < 2 ? p.sum_post : p.sum_pre))
@@ -605,11 +643,19 @@ struct RowKernels {
 
 int64_t norm_chunks(int64_t rows, int64_t cols)
 {
-    // Three workgroups a compute unit, as many as the registers let in at once.  65536 x 2048 bf16, kernel and
-    // sums: 768 chunks 350 us, 512 369, 1024 (a second turn for some) 398.
+    // A chunk a workgroup, as many as the registers (or, of rows longer than 2048, the column sums in LDS) let in at
+    // once: 65536 x 2048 bf16, kernel and sums, 768 chunks 350 us, 512 369, 1024 (a second turn for some) 398.  The
+    // rows are spread evenly over the turns, and few rows take two of them: 1027 x 1001 binary32, 257 chunks of two
+    // turns 12.6 us and their sums 4.8, 514 of one 13.2 and 6.5.
     const int lanes = row_lanes(cols), per = rows_of(lanes);
-    const int64_t most = lanes ? 768 / per : (cols <= 65536 ? 256 : (int64_t(1) << 24) / cols);
-    return std::min((rows + per - 1) / per, most) * per;
+    int64_t most = 768;
+    if (lanes > 256)
+        most = 256 * 1024 / lanes;
+    else if (!lanes)
+        most = cols <= 65536 ? 256 : (int64_t(1) << 24) / cols;
+    const int64_t groups = (rows + per - 1) / per;
+    const int64_t turns = groups > 256 && groups < most ? 2 : (groups + most - 1) / most;
+    return (groups + turns - 1) / turns;
 }
 
 hipError_t launch_norm(rar_dtype dt, const NormParams &p, hipStream_t st)
@@ -639,7 +685,7 @@ hipError_t launch_norm_grad(rar_dtype dt, const NormGradParams &p, hipStream_t s
     case 512: k = {rar_norm_grad_rows<float, 512>, rar_norm_grad_rows<bf16, 512>}; break;
     case 1024: k = {rar_norm_grad_rows<float, 1024>, rar_norm_grad_rows<bf16, 1024>}; break;
     }
-    return launch(dt == RAR_BF16 ? k.bf : k.f32, (unsigned)(p.chunks / rows_of(lanes)), threads_of(lanes), st, p);
+    return launch(dt == RAR_BF16 ? k.bf : k.f32, (unsigned)p.chunks, threads_of(lanes), st, p);
 }
 
 hipError_t launch_norm_sums(rar_dtype dt, const NormGradParams &p, hipStream_t st)

@@ -214,11 +214,32 @@ struct RowJoin {
             for (int i = 0; i < M; ++i)
                 at[wave * N + i] = v[i];
         __syncthreads();
+        constexpr int kEach = LANES / 64;
+        if (kEach * M > 32) {
+            // a wave's value a lane, joined by shifts: read by every lane they would take more registers than the rows
+            const float none = MAX ? -__builtin_inff() : 0.0f;
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                float t = at[(threadIdx.x & (kEach - 1)) * N + i], o;
+                o = dpp<0x111, 0xf>(t, none);
+                t = MAX ? __builtin_fmaxf(t, o) : t + o;
+                o = dpp<0x112, 0xf>(t, none);
+                t = MAX ? __builtin_fmaxf(t, o) : t + o;
+                o = dpp<0x114, 0xf>(t, none);
+                t = MAX ? __builtin_fmaxf(t, o) : t + o;
+                if (kEach == 16) {
+                    o = dpp<0x118, 0xf>(t, none);
+                    t = MAX ? __builtin_fmaxf(t, o) : t + o;
+                }
+                v[i] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(t), kEach - 1));
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             float t = at[first * N + i];
 #pragma unroll
-            for (int w = 1; w < LANES / 64; ++w) {
+            for (int w = 1; w < kEach; ++w) {
                 const float o = at[(first + w) * N + i];
                 t = MAX ? __builtin_fmaxf(t, o) : t + o;
             }
