@@ -951,6 +951,18 @@ __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
     const int64_t hk = place / rows % p.Hkv, b = place / rows / p.Hkv;
     const RowPlace r = row_place(p, hk, place % rows, length_of(p.qlen, b, p.Tq));
     const int lane = threadIdx.x & 63, c = lane * 2;
+    // four parts' values at a time, the first of them on their way before the weights are known
+    constexpr int kParts = 4;
+    f32x2 a[kParts] = {};
+    auto load = [&](int first) __attribute__((always_inline)) {
+        if (c < p.pitch)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int s = first + i < p.splits ? first + i : p.splits - 1;  // (lanes behind the last weigh zero)
+                a[i] = *reinterpret_cast<const f32x2 *>(p.part + (s * p.part_rows + place) * p.pitch + c);
+            }
+    };
+    load(0);
     float m = -kInf, l = 0.0f;
     if (lane < p.splits) {
         m = p.stats[(lane * p.part_rows + place) * 2];
@@ -960,14 +972,15 @@ __global__ void __launch_bounds__(256) rar_attn_join(const AttnParams p)
     const float w = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((m - (top == -kInf ? 0.0f : top)) * kLog2e);
     const float sum = wave_sum(w * l);
     f32x2 v = {0.0f, 0.0f};
-#pragma unroll 8
-    for (int s = 0; s < p.splits; ++s) {
-        const float ws = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(w), s));
-        f32x2 a = {0.0f, 0.0f};
-        if (c < p.pitch)
-            a = *reinterpret_cast<const f32x2 *>(p.part + (s * p.part_rows + place) * p.pitch + c);
-        v.x = ws == 0.0f ? v.x : __builtin_fmaf(ws, a.x, v.x);  // (no key of such a part counts)
-        v.y = ws == 0.0f ? v.y : __builtin_fmaf(ws, a.y, v.y);
+    for (int first = 0; first < p.splits; first += kParts) {
+        if (first)
+            load(first);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const float ws = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(w), first + i));
+            v.x = ws == 0.0f ? v.x : __builtin_fmaf(ws, a[i].x, v.x);  // (no key of such a part counts)
+            v.y = ws == 0.0f ? v.y : __builtin_fmaf(ws, a[i].y, v.y);
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     T *const o = (T *)p.o + (b * p.Tq + r.t) * p.ldo + r.h * p.dh;

@@ -300,7 +300,14 @@ struct AttnShape {
         // 45 in two parts and 41 in four, and the join 4 more.
         const int64_t all = std::max<int64_t>(1, div_up(Tk, attn_stage(dt, rows)));
         const int64_t work = std::max<int64_t>(1, B * Hkv * tiles);
-        splits = std::min<int64_t>(std::min<int64_t>(div_up(few ? 256 : 512, work), std::max<int64_t>(1, all / 2)), 64);
+        // Binary32 is bound by the matrix cores, which a second workgroup on some units would keep the call waiting
+        // for: at most one a unit.  3 x 6 heads of 60 on 3, 333 queries on 517 keys: 22 us and a join of 6.6 to 19 and
+        // 5.2; 4 x 8 heads of 128, 512 on 512: 55 and 12 to 49 and 11.
+        if (!few && dt == RAR_F32)
+            splits = parts(work, all);
+        else
+            splits = std::min<int64_t>(div_up(few ? 256 : 512, work), std::max<int64_t>(1, all / 2));
+        splits = std::min<int64_t>(splits, 64);
         stages = div_up(all, splits);
         splits = div_up(all, stages);
         padded = up(Tq, kAttnPad);
