@@ -366,7 +366,7 @@ hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st)
     // registers hold the row: four workgroups a unit wait for each other less than two.  8192 x 32000 bf16 with 8
     // alternatives takes 172 us at 1024 lanes and 138 at 512, its gradient 223 and 211; eight rows take 8 at 1024.
     const bool grad = p.dz != nullptr, many = p.rows > 512;
-    Kernels k;
+    Kernels k{};
     int lanes = 1024;
     if (p.cols <= 64 * 8 * 4) {
         k = kernels_of<64, 4>(grad);
@@ -384,6 +384,8 @@ hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st)
         k = kernels_of<1024, 4>(grad);
     } else if (p.cols <= 1024 * 8 * 8) {
         k = kernels_of<1024, 8>(grad);
+    } else if (dt == RAR_BF16 && p.cols <= 1024 * 8 * 16) {
+        k.bf = grad ? rar_logprob_rows<bf16, 1024, 16, true> : rar_logprob_rows<bf16, 1024, 16, false>;
     } else {
         k = kernels_of<1024, 0>(grad);
     }

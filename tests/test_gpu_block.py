@@ -537,7 +537,7 @@ def test_attention_gradient_against_differences():
 
 # (T, V): one element, widths at and around what a wave, a workgroup and registers take, and beyond
 LOGPROB = [(1, 1), (3, 2), (5, 33), (7, 500), (9, 2048), (6, 2049), (4, 8192), (3, 8195), (5, 32000), (2, 32769),
-           (3, 65536), (2, 65537), (1, 200_003), (300, 40), (2100, 64), (515, 16001), (600, 32001)]
+           (3, 65536), (2, 65537), (2, 131_072), (1, 200_003), (300, 40), (2100, 64), (515, 16001), (600, 32001)]
 
 
 def logits(g, T, V, dtype):
@@ -599,7 +599,7 @@ def test_logprob_gradient(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
-@pytest.mark.parametrize("V", [300, 5000, 30001, 70000])
+@pytest.mark.parametrize("V", [300, 5000, 30001, 70000, 140_000])
 def test_logprob_ties_masks_and_bad_values(V, dtype):
     T, K = 10, 20
     g = torch.Generator().manual_seed(V)
