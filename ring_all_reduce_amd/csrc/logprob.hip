@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
     __shared__ TopLds<LANES> top;
     Join join{lds};
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const int first_lane = __builtin_amdgcn_readfirstlane(lane & ~63);
 
     for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += (int64_t)gridDim.x * kRows) {
         const int64_t row = first + sub;
@@ -110,22 +111,25 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
                 held[k].load(z + c, live ? clamp8(p.cols - c) : 0, -kInf);
             }
         }
-        // f(column, how many of the eight exist, values; the others -infinity)
+        // f(which eight, column, how many of it exist, values; the others -infinity); a wave passes over those of which
+        // it has nothing
         auto each = [&](auto &&f) __attribute__((always_inline)) {
             if (R) {
                 const int mine = forgotten(lane);
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
+                    if (k >= R / 2 && (k * LANES + first_lane) * 8 >= (int)p.cols)
+                        continue;
                     const int64_t c = ((int64_t)k * LANES + mine) * 8;
                     held[k].forget();
-                    f(c, live ? clamp8(p.cols - c) : 0, held[k]);
+                    f(k, c, live ? clamp8(p.cols - c) : 0, held[k]);
                     one_after_another();
                 }
             } else {
                 for (int64_t c = (int64_t)lane * 8; c < p.cols; c += LANES * 8) {
                     Eight<T> v;
                     v.load(z + c, clamp8(p.cols - c), -kInf);
-                    f(c, clamp8(p.cols - c), v);
+                    f(0, c, clamp8(p.cols - c), v);
                 }
             }
         };
@@ -142,21 +146,23 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
 
         // the largest of each eight: the row's maximum, and where alternatives can be
         float best[kHeld], m[1] = {-kInf};
-        int at = 0;
-        each([&](int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            best[k] = -kInf;
+        each([&](int k, int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
             float b = v.get(0);
 #pragma unroll
             for (int i = 1; i < 8; ++i)
                 b = __builtin_fmaxf(b, v.get(i));
             if (R)
-                best[at++] = b;
+                best[k] = b;
             m[0] = __builtin_fmaxf(m[0], b);
         });
         const float mine = m[0];
         join.max(m);
         const float base = m[0] == -kInf ? 0.0f : m[0], unit = p.scale * kLog2e;
         float t[2] = {0.0f, 0.0f};
-        each([&](int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
+        each([&](int, int64_t, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float x = (v.get(i) - base) * unit;
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
                     store8<true>(dz + c, cnt, g);
             };
             if (p.dentropy)
-                each([&](int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
+                each([&](int, int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
                     float g[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
                     write(c, cnt, g);
                 });
             else
-                each([&](int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
+                each([&](int, int64_t c, int cnt, const Eight<T> &v) __attribute__((always_inline)) {
                     float g[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -246,9 +252,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
         __syncthreads();
         const float low = wave_max(top.best[sub][threadIdx.x & 63]);
         if (!bad) {
-            at = 0;
-            each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
-                if (R && !__any(best[at++] >= low))
+            each([&](int k, int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
+                if (R && !__any(best[k] >= low))
                     return;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
                 uint64_t last = ~(uint64_t)0;
                 for (int k = 0; k < p.top; ++k) {
                     uint64_t b = 0;
-                    each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
+                    each([&](int, int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float x = v.get(i);
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
             uint64_t last = ~(uint64_t)0;
             for (int k = 0; k < p.top; ++k) {
                 uint64_t b = 0;
-                each([&](int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
+                each([&](int, int64_t c, int, const Eight<T> &v) __attribute__((always_inline)) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float x = v.get(i);
@@ -365,6 +370,7 @@ hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st)
     // Lanes of a row and eights a lane.  More rows than two to a compute unit go to half the lanes as long as 64
     // registers hold the row: four workgroups a unit wait for each other less than two.  8192 x 32000 bf16 with 8
     // alternatives takes 172 us at 1024 lanes and 138 at 512, its gradient 223 and 211; eight rows take 8 at 1024.
+    // bf16 rows up to 131072 fit 128 registers: 2048 x 128256 takes 166 and 257 us, read again from memory 220 and 306.
     const bool grad = p.dz != nullptr, many = p.rows > 512;
     Kernels k{};
     int lanes = 1024;
