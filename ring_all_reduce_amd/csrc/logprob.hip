@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
     typedef RowJoin<LANES, 2> Join;
     constexpr int kRows = Join::kThreads / LANES;
     constexpr int kHeld = R ? R : 1;
+    constexpr bool kSkip = R == 4 || R == 16;  // (of 8192 x 32000, 6 and 8 eights, it would cost 6%: more registers)
     __shared__ float lds[Join::kFloats];
     __shared__ TopLds<LANES> top;
     Join join{lds};
@@ -111,14 +112,14 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
                 held[k].load(z + c, live ? clamp8(p.cols - c) : 0, -kInf);
             }
         }
-        // f(which eight, column, how many of it exist, values; the others -infinity); a wave passes over those of which
-        // it has nothing
+        // f(which eight, column, how many of it exist, values; the others -infinity); where rows may fill half the
+        // lanes, a wave passes over what it has nothing of
         auto each = [&](auto &&f) __attribute__((always_inline)) {
             if (R) {
                 const int mine = forgotten(lane);
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
-                    if (k >= R / 2 && (k * LANES + first_lane) * 8 >= (int)p.cols)
+                    if (kSkip && k >= R / 2 && (k * LANES + first_lane) * 8 >= (int)p.cols)
                         continue;
                     const int64_t c = ((int64_t)k * LANES + mine) * 8;
                     held[k].forget();
@@ -355,12 +356,16 @@ struct Kernels {
     void (*f32)(LogprobParams), (*bf)(LogprobParams);
 };
 
+template <class T, int LANES, int R>
+auto kernel_of(bool grad)
+{
+    return grad ? rar_logprob_rows<T, LANES, R, true> : rar_logprob_rows<T, LANES, R, false>;
+}
+
 template <int LANES, int R>
 Kernels kernels_of(bool grad)
 {
-    if (grad)
-        return {rar_logprob_rows<float, LANES, R, true>, rar_logprob_rows<bf16, LANES, R, true>};
-    return {rar_logprob_rows<float, LANES, R, false>, rar_logprob_rows<bf16, LANES, R, false>};
+    return {kernel_of<float, LANES, R>(grad), kernel_of<bf16, LANES, R>(grad)};
 }
 
 }  // namespace
@@ -370,6 +375,7 @@ hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st)
     // Lanes of a row and eights a lane.  More rows than two to a compute unit go to half the lanes as long as 64
     // registers hold the row: four workgroups a unit wait for each other less than two.  8192 x 32000 bf16 with 8
     // alternatives takes 172 us at 1024 lanes and 138 at 512, its gradient 223 and 211; eight rows take 8 at 1024.
+    // Six eights besides four and eight: 4096 x 20000 bf16 takes 54 us and 80 with the gradient, 69 and 98 with eight.
     // bf16 rows up to 131072 fit 128 registers: 2048 x 128256 takes 166 and 257 us, read again from memory 220 and 306.
     const bool grad = p.dz != nullptr, many = p.rows > 512;
     Kernels k{};
@@ -383,15 +389,20 @@ hipError_t launch_logprob(rar_dtype dt, const LogprobParams &p, hipStream_t st)
     } else if (many && p.cols <= 512 * 8 * 4) {
         k = kernels_of<512, 4>(grad);
         lanes = 512;
+    } else if (many && dt == RAR_BF16 && p.cols <= 512 * 8 * 6) {
+        k.bf = kernel_of<bf16, 512, 6>(grad);
+        lanes = 512;
     } else if (many && dt == RAR_BF16 && p.cols <= 512 * 8 * 8) {
-        k = kernels_of<512, 8>(grad);
+        k.bf = kernel_of<bf16, 512, 8>(grad);
         lanes = 512;
     } else if (p.cols <= 1024 * 8 * 4) {
         k = kernels_of<1024, 4>(grad);
+    } else if (p.cols <= 1024 * 8 * 6) {
+        k = kernels_of<1024, 6>(grad);
     } else if (p.cols <= 1024 * 8 * 8) {
         k = kernels_of<1024, 8>(grad);
     } else if (dt == RAR_BF16 && p.cols <= 1024 * 8 * 16) {
-        k.bf = grad ? rar_logprob_rows<bf16, 1024, 16, true> : rar_logprob_rows<bf16, 1024, 16, false>;
+        k.bf = kernel_of<bf16, 1024, 16>(grad);
     } else {
         k = kernels_of<1024, 0>(grad);
     }

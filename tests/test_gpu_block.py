@@ -537,7 +537,8 @@ def test_attention_gradient_against_differences():
 
 # (T, V): one element, widths at and around what a wave, a workgroup and registers take, and beyond
 LOGPROB = [(1, 1), (3, 2), (5, 33), (7, 500), (9, 2048), (6, 2049), (4, 8192), (3, 8195), (5, 32000), (2, 32769),
-           (3, 65536), (2, 65537), (2, 131_072), (1, 200_003), (300, 40), (2100, 64), (515, 16001), (600, 32001)]
+           (3, 65536), (2, 65537), (2, 131_072), (1, 200_003), (300, 40), (2100, 64), (515, 16001), (600, 32001),
+           (520, 20_011), (3, 40_009)]
 
 
 def logits(g, T, V, dtype):
