@@ -17,10 +17,10 @@
 // share of head r % share.
 //
 // Measured at 8 x 16 heads of 128 in bf16, 1152 to 2048 queries on 576 to 1024 keys
-// (products of 42 GFLOP each): forward 115 to 124 us (two products, 680 TFLOP/s), delta
-// 24 (4.4 TB/s), dq 192 to 201 (three, 630), dk and dv 211 to 221 (four, 760).  A large
+// (products of 42 GFLOP each): forward 115 to 127 us (two products, 680 TFLOP/s), delta
+// 24 (4.4 TB/s), dq 192 to 206 (three, 630), dk and dv 211 to 229 (four, 760).  A large
 // product of torch's reaches 1380 on that card.  Binary32, 4 x 8 heads of 128, 512 on 512:
-// forward 55 us and a join of 12, dq 65, dk and dv 87 and a sum of 14.
+// forward 49 us and a join of 11, dq 65, dk and dv 87 and a sum of 14.
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -1178,8 +1178,8 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
 #endif
 }
 
-// The same for bf16: a wave's queries and their gradients are its own.  192 to
-// 201 us at the size above, where the compiler's schedule takes 206.
+// The same for bf16: a wave's queries and their gradients are its own.  200 us
+// at the size above, where the compiler's schedule takes 206.
 template <int W>
 __global__ void __launch_bounds__(256, 1) rar_attn_dq_bf16(const AttnParams p)
 {

@@ -9,7 +9,7 @@
 // twenty 32 x 32 products of a call are most of the kernel's arithmetic, and
 // halves of its words serve twice as many elements.  1 - p is off by at most
 // 2^-17, and the scale is that of the draws that are kept, so the mean is not.
-// Bound by HBM: 65536 x 2048 in bf16 with a residual 139 us (5.8 TB/s),
+// Bound by HBM: 65536 x 2048 in bf16 with a residual 140 us (5.8 TB/s),
 // vector units busy half of that.
 #include "ops_internal.h"
 #include "row.h"

@@ -16,8 +16,8 @@
 // ranked by counting.  Where they are too many (rows of equal or sorted values),
 // K rounds each take the largest key under the last.
 //
-// 8192 x 32000 in bf16: with entropy 120 us (524 MB, 4.4 TB/s), with eight alternatives
-// besides 149 (vector units busy for 72%), with the gradient 217 (1.05 GB, 4.8 TB/s); in
+// 8192 x 32000 in bf16: with entropy 121 us (524 MB, 4.3 TB/s), with eight alternatives
+// besides 147 (vector units busy for 73%), with the gradient 219 (1.05 GB, 4.8 TB/s); in
 // binary32 213 with alternatives and 443 with the gradient, at HBM's rate.  Eight rows in
 // binary32 with alternatives: 8 us, a launch and a row's own chain of joins.
 #include "ops_internal.h"

@@ -13,7 +13,7 @@
 // columns a lane; a workgroup keeps the vectors and takes rows in turn, the next
 // row's loads under this row's sums.  The variance is taken of the centred row, so
 // that a mean far from zero costs no digits.  65536 x 2048 in bf16, norms on both
-// sides: forward 220 us (1.07 GB, 4.9 TB/s), backward 326 and 12 for the column sums
+// sides: forward 220 us (1.07 GB, 4.9 TB/s), backward 330 and 12 for the column sums
 // (1.61 GB, 4.9 TB/s); torch's copy of 2 GB reaches 4.9 TB/s on that card.  8 x 2048
 // in binary32: 4 us, a launch.
 #include <algorithm>
