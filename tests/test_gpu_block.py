@@ -137,7 +137,7 @@ def test_norm_parts(D, dtype):
 
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("extra,offset", [(8, 0), (8, 8), (3, 1)])
-@pytest.mark.parametrize("D", [200, 8200])
+@pytest.mark.parametrize("D", [200, 1001, 5003, 8200])
 def test_norm_strides_and_in_place(D, extra, offset, dtype):
     T, eps = 37, 1e-5
     g = torch.Generator().manual_seed(4)
