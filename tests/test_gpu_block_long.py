@@ -56,3 +56,51 @@ def test_attention_in_bf16_rounds_weights_once():
         t = R.rows(t)
         once = (t.bfloat16().double() - t).norm()
         assert (got.double() - t).norm() <= 1.1 * math.sqrt(2) * once, n
+
+
+# (B, Tq, Tk, H, Hkv, dh): so many workgroups that nothing is cut and each passes 5 to 16 stages, or is cut into long
+# parts; runs of queries that go from one shared head to the next; every width class
+LONG = [(3, 500, 430, 16, 16, 128), (5, 200, 400, 24, 8, 60), (1, 1000, 1000, 12, 12, 96), (4, 1024, 350, 16, 16, 32),
+        (2, 470, 900, 16, 8, 77)]
+# one token, some rows on the vector units, up to a tile on rings of a wave's own: 256 key heads, so nothing is cut
+FEW = [(16, 1, 1000, 16, 16, 128), (16, 1, 700, 32, 16, 72), (32, 2, 900, 16, 8, 64), (16, 5, 1000, 32, 16, 128),
+       (16, 32, 700, 16, 16, 64), (16, 9, 1000, 16, 16, 30), (32, 3, 1000, 32, 8, 90)]
+
+
+def lengths(B, most):
+    """Whole, and then ever shorter: down to half, one and nothing."""
+    n = [most - i * most // (2 * B) for i in range(B)]
+    if B > 2:
+        n[-1], n[-2] = 0, 1
+    return torch.tensor(n)
+
+
+@pytest.mark.parametrize("shape", LONG + FEW, ids=str)
+@pytest.mark.parametrize("dtype", BOTH)
+def test_attention_of_many_stages(shape, dtype):
+    B, Tq, Tk, H, Hkv, dh = shape
+    g = torch.Generator().manual_seed(sum(shape))
+    q, do = (rand(g, B * Tq, H * dh, dtype=dtype) for _ in range(2))
+    k, v = (rand(g, B * Tk, Hkv * dh, dtype=dtype) for _ in range(2))
+    ql, kl = lengths(B, Tq).flip(0), lengths(B, Tk)
+    ql[B // 2] = Tq
+    plan = api.rar_attn_plan(H, Hkv, dh, CODE[dtype])
+    d = [dev(t) for t in (q, k, v)]
+    lens = dict(qlen=dev(ql), klen=dev(kl))
+    ws = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in api.rar_attn_workspace(plan, B, Tq, Tk)]
+    out = []
+    for _ in range(2):
+        o, lse = nan(B * Tq, H * dh, dtype=dtype), nan(B * Tq, H)
+        api.rar_attn_forward(plan, B, Tq, Tk, *d, o, lse=lse, ws=ws[0], **lens)
+        grads = [torch.full_like(t, NAN) for t in d]
+        api.rar_attn_backward(plan, B, Tq, Tk, dev(do), *d, o, lse, *grads, ws=ws[1], **lens)
+        out.append([o, lse, *grads])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    (ro, eo), (rl, el) = R.attn_forward(q, k, v, B, H, Hkv, dh ** -0.5, ql, kl, dtype)
+    R.check(o, ro, eo, "o")
+    gone = rl == -INF
+    assert (lse.cpu()[gone] == -INF).all()
+    R.check(torch.where(gone, 0.0, lse.cpu()), torch.where(gone, 0.0, rl), el, "lse")
+    want = R.attn_backward(do, q, k, v, o.cpu(), lse.cpu(), B, H, Hkv, dh ** -0.5, ql, kl, dtype)
+    for t, (r, e), n in zip(grads, want, ("dq", "dk", "dv")):
+        R.check(t, r, e, n)
