@@ -19,12 +19,12 @@ TURNS = [(16421, 100), (8253, 700), (4129, 1500), (2069, 3000), (1043, 5000), (1
 
 
 def column_sums(v, m, post, pre, eps, s, dtype, turns):
-    """{name: (value, bound)} of the vectors' gradients.  A term is added in its workgroup (`turns` rows, of up to four
-    beside each other), then over at most three chunks, four exchanges and 16 waves."""
+    """{name: (value, bound)} of the vectors' gradients.  A term is added in its workgroup (`turns` rows, of up to
+    four beside each other), then over at most three chunks, four exchanges and 16 waves."""
     E, u = R.E, R.U[dtype]
     n = turns + 3 + 3 + 4 + 16
-    g, eg = R.norm_backward(m["dh"], m["du"], m["o"], m["h"], v["post_w"], v["post_b"], v["gate"], v["pre_w"], post, pre,
-                            eps, 1.0, s, "f32")["dx"]
+    g, eg = R.norm_backward(m["dh"], m["du"], m["o"], m["h"], v["post_w"], v["post_b"], v["gate"], v["pre_w"], post,
+                            pre, eps, 1.0, s, "f32")["dx"]
     zero = torch.zeros_like(g)
     oh, eoh, _ = R._stats(m["o"].double(), zero, post, eps)
     hh, ehh, _ = R._stats(m["h"].double(), zero, pre, eps)
@@ -66,8 +66,8 @@ def test_norm_of_many_turns(shape, kinds, dtype):
     h, u = (torch.full_like(w["x"], math.nan) for _ in range(2))
     vectors = [d[n] for n in ("post_w", "post_b", "gate", "pre_w", "pre_b")]
     api.rar_norm_forward(plan, T, w["x"], w["o"], *vectors, h, u, s=s)
-    want = R.norm_forward(m["x"], m["o"], *(v[n] for n in ("post_w", "post_b", "gate", "pre_w", "pre_b")), post, pre, eps,
-                          1.0, s, dtype)
+    want = R.norm_forward(m["x"], m["o"], *(v[n] for n in ("post_w", "post_b", "gate", "pre_w", "pre_b")), post, pre,
+                          eps, 1.0, s, dtype)
     R.check(h, *want[0], "h")
     R.check(u, *want[1], "u")
     x, u2 = w["x"].clone(), torch.full_like(u, math.nan)
@@ -89,13 +89,14 @@ def test_norm_of_many_turns(shape, kinds, dtype):
     turns = -(-T // (most * max(1, 256 // lanes)))
     assert turns >= 3
     want = column_sums(v, m, post, pre, eps, s, dtype, turns)
-    # (the bounds tell a row too few: without the last one they would not hold.  In bf16 a long sum's rounding hides it.)
+    # (the bounds tell a row too few: without the last one they would not hold; in bf16 a long sum's rounding hides it)
     short = column_sums(v, {n: t[:-1] for n, t in m.items()}, post, pre, eps, s, dtype, turns)
     for n, (t, e) in want.items():
         R.check(out[n], t, e, n)
         assert dtype == "bf16" or ((t - short[n][0]).abs() > e + short[n][1]).any()
     again = {n: torch.full_like(t, math.nan) for n, t in out.items()}
     dh, o = w["dh"].clone(), w["o"].clone()
-    api.rar_norm_backward(plan, T, dh, w["du"], o, w["h"], *vectors, dh, o, **again, s=s, ws=ws)   # dx over dh, do over o
+    # dx over dh, do over o
+    api.rar_norm_backward(plan, T, dh, w["du"], o, w["h"], *vectors, dh, o, **again, s=s, ws=ws)
     assert torch.equal(dh, dx) and torch.equal(o, do)
     assert all(torch.equal(again[n], out[n]) for n in names)
