@@ -324,6 +324,8 @@ struct AttnShape {
         return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, work), most / 2));
     }
 
+    // forward: few enough rows for the vector units, which read at any address
+    bool token() const { return rows <= kAttnTokenRows; }
     int64_t blocks() const { return B * Hkv * splits * tiles; }
     int64_t part_rows() const { return B * H * Tq; }
     // every launch has at most 2^32 lanes
@@ -355,9 +357,11 @@ AttnWs attn_ws(const AttnShape &s, bool backward, void *ws)
     AttnWs w{};
     const int es = esize(s.dt);
     const int64_t wide = s.B * s.Tq * s.H * s.cols * es, narrow = s.B * s.Tk * s.Hkv * s.cols * es;
-    w.q = c.take(wide);
-    w.k = c.take(narrow);
-    w.v = c.take(narrow);
+    if (backward || !s.token()) {
+        w.q = c.take(wide);
+        w.k = c.take(narrow);
+        w.v = c.take(narrow);
+    }
     if (backward) {
         w.g = c.take(wide);
         w.lse = (float *)c.take(s.B * s.H * s.padded * 4);
@@ -458,7 +462,7 @@ extern "C" rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, i
     const int es = esize(s.dt);
     const int64_t wide = s.H * s.dh, narrow = s.Hkv * s.dh;
     const AttnWs w = attn_ws(s, false, ws);
-    if (!q || !o || (Tk > 0 && (!k || !v)) || !ws)
+    if (!q || !o || (Tk > 0 && (!k || !v)) || (!ws && w.bytes))
         return RAR_EINVAL;
     if (Tk == 0)
         k = v = nullptr;
@@ -477,7 +481,7 @@ extern "C" rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, i
     pack.dh = (int)s.dh;
     pack.cols = (int)s.cols;
     AttnParams p = attn_params(*plan, s, qlen, klen);
-    if (s.rows <= kAttnTokenRows) {  // read at any address
+    if (s.token()) {
         p.q = AttnOperand{q, ldq, s.dh, (int)s.dh};
         p.k = AttnOperand{k, ldk, s.dh, (int)s.dh};
         p.v = AttnOperand{v, ldv, s.dh, (int)s.dh};
