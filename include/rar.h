@@ -508,7 +508,7 @@ rar_status rar_norm_plan(int64_t D, rar_dtype dtype, rar_norm_kind post, rar_nor
 
 rar_status rar_norm_destroy(rar_norm_t plan);
 
-/* Workspace of a backward call on T rows. */
+/* Workspace of a backward call on T rows; it serves calls on fewer rows too. */
 rar_status rar_norm_workspace(rar_norm_t plan, int64_t T, int64_t *bytes);
 
 /* n = post(o),  h = a x + s (gate . n),  u = pre(h), all T x D.

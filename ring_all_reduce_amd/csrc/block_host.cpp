@@ -37,7 +37,8 @@ bool all_aligned(std::initializer_list<const void *> ps, int to)
     return true;
 }
 
-int64_t norm_ws_bytes(int64_t T, int64_t D) { return T ? norm_chunks(T, D) * 4 * up(D, 8) * 4 : 0; }
+// (enough for every call of fewer rows too)
+int64_t norm_ws_bytes(int64_t T, int64_t D) { return T ? norm_chunks_up_to(T, D) * 4 * up(D, 8) * 4 : 0; }
 
 }  // namespace
 

@@ -634,6 +634,21 @@ int row_lanes(int64_t cols)
 int rows_of(int lanes) { return lanes && lanes < 256 ? 256 / lanes : 1; }
 unsigned threads_of(int lanes) { return lanes ? std::max(lanes, 256) : kWideLanes; }
 
+int64_t row_groups(int64_t rows, int64_t cols)
+{
+    const int per = rows_of(row_lanes(cols));
+    return (rows + per - 1) / per;
+}
+
+// Workgroups of the backward kernel at once.
+int64_t most_chunks(int64_t cols)
+{
+    const int lanes = row_lanes(cols);
+    if (!lanes)
+        return cols <= 65536 ? 256 : (int64_t(1) << 24) / cols;
+    return lanes > 256 ? 256 * 1024 / lanes : 768;
+}
+
 template <class P>
 struct RowKernels {
     void (*f32)(P), (*bf)(P);
@@ -647,15 +662,16 @@ int64_t norm_chunks(int64_t rows, int64_t cols)
     // once: 65536 x 2048 bf16, kernel and sums, 768 chunks 350 us, 512 369, 1024 (a second turn for some) 398.  The
     // rows are spread evenly over the turns, and few rows take two of them: 1027 x 1001 binary32, 257 chunks of two
     // turns 12.6 us and their sums 4.8, 514 of one 13.2 and 6.5.
-    const int lanes = row_lanes(cols), per = rows_of(lanes);
-    int64_t most = 768;
-    if (lanes > 256)
-        most = 256 * 1024 / lanes;
-    else if (!lanes)
-        most = cols <= 65536 ? 256 : (int64_t(1) << 24) / cols;
-    const int64_t groups = (rows + per - 1) / per;
+    const int64_t most = most_chunks(cols), groups = row_groups(rows, cols);
     const int64_t turns = groups > 256 && groups < most ? 2 : (groups + most - 1) / most;
     return (groups + turns - 1) / turns;
+}
+
+int64_t norm_chunks_up_to(int64_t rows, int64_t cols)
+{
+    // (the number falls where two turns begin)
+    const int64_t most = most_chunks(cols), groups = row_groups(rows, cols);
+    return groups >= most ? most : std::min(groups, std::max<int64_t>(256, (groups + 1) / 2));
 }
 
 hipError_t launch_norm(rar_dtype dt, const NormParams &p, hipStream_t st)

@@ -279,8 +279,9 @@ hipError_t launch_embed_grad(rar_dtype dt, const EmbedGradParams &p, hipStream_t
 int64_t embed_grad_workspace(int64_t T, int64_t V, int64_t D);
 // Whether each of its launches has at most `lanes` lanes.
 bool embed_grad_fits(int64_t T, int64_t D, int64_t grad_bytes, int64_t lanes);
-// Rows of column sums that the norms' backward kernel writes.
+// Rows of column sums that the norms' backward kernel writes, and the most of any call of up to `rows` rows.
 int64_t norm_chunks(int64_t rows, int64_t cols);
+int64_t norm_chunks_up_to(int64_t rows, int64_t cols);
 hipError_t launch_norm(rar_dtype dt, const NormParams &p, hipStream_t st);
 hipError_t launch_norm_grad(rar_dtype dt, const NormGradParams &p, hipStream_t st);
 hipError_t launch_norm_sums(rar_dtype dt, const NormGradParams &p, hipStream_t st);

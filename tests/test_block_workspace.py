@@ -29,3 +29,13 @@ def test_a_token_needs_no_copy_of_its_cache(dtype):
     p = api.rar_attn_plan(16, 16, 128, dtype)
     es = 4 if dtype == api.F32 else 2
     assert forward_bytes(p, 16, 5, 2048) >= 2 * 16 * 2048 * 16 * 128 * es
+
+
+def test_norm_workspace_serves_fewer_rows():
+    for D in (40, 512, 520, 1024, 2048, 2056, 4096, 8192, 8200, 70_000, 1 << 20):
+        p = api.rar_norm_plan(D, api.BF16, api.NORM_LAYER, api.NORM_LAYER)
+        last = 0
+        for T in [*range(1, 4000), *range(4000, 40_000, 7), 1 << 16, 1 << 20, 1 << 24]:
+            n = api.rar_norm_workspace(p, T)
+            assert n >= last, (D, T)
+            last = n
