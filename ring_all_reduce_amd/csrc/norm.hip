@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256) rar_norm_rows(const
             if (p.post)
                 normalise(n, p.post);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = __builtin_fmaf(n[i], w1.get(i), b1.get(i));
-                    h[i] = i < cols ? __builtin_fmaf(p.s, gate.get(i) * y, h[i]) : 0.0f;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float y = __builtin_fmaf(n[i], w1.get(i), b1.get(i));
+                h[i] = i < cols ? __builtin_fmaf(p.s, gate.get(i) * y, h[i]) : 0.0f;
+            }
         }
         const bool live = row < p.rows;
         if (p.h && live)
