@@ -276,74 +276,15 @@ namespace {
 
 constexpr int64_t kMaxBatch = 65535;
 
-// A call's sizes and how its work is cut.
-struct AttnShape {
-    int64_t B, Tq, Tk, H, Hkv, share, dh, rows;
-    rar_dtype dt;
-    int64_t cols;      // a head's columns in whole 16-byte groups
-    int width;         // of a row of partial results: whole 32 columns
-    bool few;          // the keys are shared out among a workgroup's waves
-    int64_t tiles;     // of query rows, a key head
-    int64_t splits, stages;
-    int64_t q_tiles, q_splits;    // of dq: rows, and parts of the keys
-    int64_t key_tiles, k_splits;  // of dk and dv: keys, and parts of the queries
-    int64_t padded;
-
-    AttnShape(const rar_attn_s &a, int64_t B_, int64_t Tq_, int64_t Tk_)
-        : B(B_), Tq(Tq_), Tk(Tk_), H(a.H), Hkv(a.Hkv), share(a.H / a.Hkv), dh(a.dh), rows(Tq_ * share), dt(a.dtype)
-    {
-        cols = up(dh, 16 / esize(dt));
-        width = (int)up(dh, 32);
-        few = rows <= kAttnFewRows;
-        tiles = div_up(rows, few ? kAttnFewRows : kAttnRows);
-        // two workgroups a compute unit, or one where a workgroup fills it or the caches' ports (few rows); each
-        // with at least two stages of keys.  16 x 16 heads of 128, a token on 2048 keys in bf16: 44 us unsplit,
-        // 45 in two parts and 41 in four, and the join 4 more.
-        const int64_t all = std::max<int64_t>(1, div_up(Tk, attn_stage(dt, rows)));
-        const int64_t work = std::max<int64_t>(1, B * Hkv * tiles);
-        // Binary32 is bound by the matrix cores, which a second workgroup on some units would keep the call waiting
-        // for: at most one a unit.  3 x 6 heads of 60 on 3, 333 queries on 517 keys: 22 us and a join of 6.6 to 19 and
-        // 5.2; 4 x 8 heads of 128, 512 on 512: 55 and 12 to 49 and 11.
-        if (!few && dt == RAR_F32)
-            splits = parts(work, all);
-        else
-            splits = std::min<int64_t>(div_up(few ? 256 : 512, work), std::max<int64_t>(1, all / 2));
-        splits = std::min<int64_t>(splits, 64);
-        stages = div_up(all, splits);
-        splits = div_up(all, stages);
-        padded = up(Tq, kAttnPad);
-        // The backward kernels fill a compute unit with one workgroup.  With fewer of them than units the long axis
-        // of each is cut, into parts of at least two stages, and joined.
-        q_tiles = div_up(rows, kAttnRows);
-        key_tiles = div_up(Tk, kAttnRows);
-        q_splits = parts(B * Hkv * q_tiles, div_up(Tk, attn_backward_stage(dt)));
-        k_splits = parts(B * Hkv * key_tiles, div_up(Tq, attn_backward_stage(dt)) * share);
-    }
-
-    static int64_t parts(int64_t work, int64_t most)
-    {
-        return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, work), most / 2));
-    }
-
-    // forward: few enough rows for the vector units, which read at any address
-    bool token() const { return rows <= kAttnTokenRows; }
-    int64_t blocks() const { return B * Hkv * splits * tiles; }
-    int64_t part_rows() const { return B * H * Tq; }
-    // every launch has at most 2^32 lanes
-    bool fits() const
-    {
-        const int64_t per = 16 / esize(dt);
-        return blocks() <= kMaxLanes / 512 && B * Hkv * key_tiles * k_splits <= kMaxLanes / 256 &&
-               B * Hkv * q_tiles * q_splits <= kMaxLanes / 256 &&
-               div_up(B * H * padded, 32) <= kMaxLanes / 256 &&
-               div_up((2 * B * Tq * H + 2 * B * Tk * Hkv) * (cols / per), 256) <= kMaxLanes / 256;
-    }
-};
+AttnShape attn_shape(const rar_attn_s &a, int64_t B, int64_t Tq, int64_t Tk)
+{
+    return AttnShape(a.H, a.Hkv, a.dh, a.dtype, B, Tq, Tk);
+}
 
 bool valid_attn(const rar_attn_s *a, int64_t B, int64_t Tq, int64_t Tk)
 {
     return a && B >= 0 && B <= kMaxBatch && Tq >= 0 && Tk >= 0 && Tq <= kMaxRows && Tk <= kMaxRows &&
-           B * Tq <= kMaxRows && B * Tk <= kMaxRows && AttnShape(*a, B, Tq, Tk).fits();
+           B * Tq <= kMaxRows && B * Tk <= kMaxRows && attn_shape(*a, B, Tq, Tk).fits();
 }
 
 struct AttnWs {
@@ -442,7 +383,7 @@ extern "C" rar_status rar_attn_workspace(rar_attn_t plan, int64_t B, int64_t Tq,
 {
     if (!valid_attn(plan, B, Tq, Tk))
         return RAR_EINVAL;
-    const AttnShape s(*plan, B, Tq, Tk);
+    const AttnShape s = attn_shape(*plan, B, Tq, Tk);
     if (forward_bytes)
         *forward_bytes = attn_ws(s, false, nullptr).bytes;
     if (backward_bytes)
@@ -459,7 +400,7 @@ extern "C" rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, i
         return RAR_EINVAL;
     if (B * Tq == 0)
         return RAR_OK;
-    const AttnShape s(*plan, B, Tq, Tk);
+    const AttnShape s = attn_shape(*plan, B, Tq, Tk);
     const int es = esize(s.dt);
     const int64_t wide = s.H * s.dh, narrow = s.Hkv * s.dh;
     const AttnWs w = attn_ws(s, false, ws);
@@ -517,7 +458,7 @@ extern "C" rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, 
 {
     if (!valid_attn(plan, B, Tq, Tk))
         return RAR_EINVAL;
-    const AttnShape s(*plan, B, Tq, Tk);
+    const AttnShape s = attn_shape(*plan, B, Tq, Tk);
     const int es = esize(s.dt);
     const int64_t wide = s.H * s.dh, narrow = s.Hkv * s.dh;
     const AttnWs w = attn_ws(s, true, ws);

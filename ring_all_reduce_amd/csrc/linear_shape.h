@@ -6,16 +6,11 @@
 #include <cmath>
 #include <cstdint>
 
-#include "rar.h"
+#include "sizes.h"
 
 namespace rar {
 
-constexpr int64_t kMaxLanes = (int64_t(1) << 32) - 1;  // of a grid, along x
 constexpr int64_t kMaxOutputs = int64_t(1) << 37;      // elements of a layer's matrix
-
-inline int esize(rar_dtype d) { return d == RAR_BF16 ? 2 : 4; }
-inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-inline int64_t div_up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
 // Workgroups of a launch: those of a 256-tile have 512 lanes, all others 256.
 // kMaxOutputs in the larger tile take fewer, whatever the sides: at most

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attn_shape.h"
 #include "rar.h"
 
 namespace rar {
@@ -193,24 +194,6 @@ struct AttnParams {
     void *dq, *dk, *dv;
     int64_t lddq, lddk, lddv;
 };
-
-constexpr int kAttnRows = 128;       // query rows of a workgroup, or keys of one of dk and dv
-constexpr int kAttnFewRows = 32;     // rows of a key head that share one tile: the waves share out the keys
-constexpr int kAttnTokenRows = 4;    // rows of a key head that the vector units take
-constexpr int kAttnFewStage = 128;   // keys that such a call's split is a multiple of
-constexpr int kAttnPad = 64;         // whole stages of queries
-
-// Keys of a stage of the forward kernel for `rows` rows a key head.
-inline int attn_stage(rar_dtype dt, int64_t rows)
-{
-    return rows <= kAttnFewRows ? kAttnFewStage : (dt == RAR_BF16 ? 64 : 32);
-}
-
-// Rows of a stage of the backward kernels.
-inline int attn_backward_stage(rar_dtype dt) { return dt == RAR_BF16 ? 64 : 32; }
-
-// Waves of a workgroup that share out the keys, by the bytes of a row in LDS: what fills LDS.
-constexpr int attn_few_waves(int row_bytes) { return 512 / row_bytes; }
 
 // Parts of dq (q_rows rows, 0: none) and of dk and dv (k_rows): [splits][rows][pitch]
 // and [splits][rows][dk's pitch, dv's pitch].
