@@ -575,7 +575,8 @@ rar_status rar_attn_destroy(rar_attn_t plan);
  * address and of any leading dimension.  Either output may be NULL.  A forward
  * call of at most four rows a key head (Tq H / Hkv: a decoding step) reads its
  * matrices as they stand and needs no more than the parts that its keys are cut
- * into.  Where a query gives zero, ws may be NULL. */
+ * into.  Where a query gives zero, ws may be NULL.  A workspace serves every
+ * call of fewer sequences, queries or keys too. */
 rar_status rar_attn_workspace(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, int64_t *forward_bytes,
                               int64_t *backward_bytes);
 

@@ -77,6 +77,33 @@ struct AttnShape {
         return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, work), most / 2));
     }
 
+    // Rows of partial results that a call of at most these sizes may write, each at least what this one writes, and
+    // none smaller for larger sizes: a workspace serves every smaller call.  (Fewer sequences are cut into more parts,
+    // so a call's own rows fall where its parts become fewer.)  A call is cut where its whole stages allow two parts,
+    // and then into fewer than twice as many workgroups as are aimed at: at most `groups`, of at most `tile` rows.
+    static int64_t room(int64_t groups, int64_t tile, int64_t head_rows, int64_t heads, int64_t parts)
+    {
+        parts = std::min<int64_t>(parts, 256);
+        return parts < 2 ? 0 : std::min(groups * std::min(tile, head_rows), heads * head_rows * parts);
+    }
+    int64_t part_room() const
+    {
+        const int64_t few_rows = std::min<int64_t>(rows, kAttnFewRows);
+        const int64_t most = room(2 * 256, kAttnFewRows, few_rows, B * Hkv,
+                                  std::min<int64_t>(64, div_up(Tk, kAttnFewStage) / 2));
+        return few ? most
+                   : std::max(most, room(dt == RAR_F32 ? 256 : 2 * 512, kAttnRows, rows, B * Hkv,
+                                         std::min<int64_t>(64, div_up(Tk, attn_stage(dt, rows)) / 2)));
+    }
+    int64_t q_room() const
+    {
+        return room(256, kAttnRows, rows, B * Hkv, div_up(Tk, attn_backward_stage(dt)) / 2);
+    }
+    int64_t k_room() const
+    {
+        return room(256, kAttnRows, Tk, B * Hkv, div_up(Tq, attn_backward_stage(dt)) * share / 2);
+    }
+
     // forward: few enough rows for the vector units, which read at any address
     bool token() const { return rows <= kAttnTokenRows; }
     int64_t blocks() const { return B * Hkv * splits * tiles; }

@@ -308,13 +308,11 @@ AttnWs attn_ws(const AttnShape &s, bool backward, void *ws)
         w.g = c.take(wide);
         w.lse = (float *)c.take(s.B * s.H * s.padded * 4);
         w.delta = (float *)c.take(s.B * s.H * s.padded * 4);
-        if (s.q_splits > 1)
-            w.q_part = (float *)c.take(s.q_splits * s.part_rows() * s.width * 4);
-        if (s.k_splits > 1)
-            w.k_part = (float *)c.take(s.k_splits * s.B * s.Hkv * s.Tk * 2 * s.width * 4);
-    } else if (s.splits > 1) {
-        w.part = (float *)c.take(s.splits * s.part_rows() * s.width * 4);
-        w.stats = (float *)c.take(s.splits * s.part_rows() * 8);
+        w.q_part = (float *)c.take(s.q_room() * s.width * 4);
+        w.k_part = (float *)c.take(s.k_room() * 2 * s.width * 4);
+    } else {
+        w.part = (float *)c.take(s.part_room() * s.width * 4);
+        w.stats = (float *)c.take(s.part_room() * 8);
     }
     w.bytes = c.used;
     return w;

@@ -1,10 +1,17 @@
 """Workspaces of the norms and of cross attention, without a GPU: what a call asks
 for, and that a workspace for the largest call serves the smaller ones."""
+import ctypes
+import pathlib
+import random
+import shutil
+import subprocess
+
 import pytest
 
 from ring_all_reduce_amd import api
 from ring_all_reduce_amd._lib import lib
 
+ROOT = pathlib.Path(__file__).resolve().parents[1]
 A = [(i + 1) << 40 for i in range(24)]   # addresses far apart; never dereferenced
 
 
@@ -39,3 +46,73 @@ def test_norm_workspace_serves_fewer_rows():
             n = api.rar_norm_workspace(p, T)
             assert n >= last, (D, T)
             last = n
+
+
+def test_attention_workspace_serves_fewer_sequences_queries_and_keys():
+    rng = random.Random(7)
+    for H, Hkv, dh, dt in ((16, 4, 64, api.BF16), (8, 8, 128, api.F32), (6, 3, 60, api.F32), (16, 16, 128, api.BF16),
+                           (1, 1, 8, api.BF16), (64, 1, 128, api.F32)):
+        p = api.rar_attn_plan(H, Hkv, dh, dt)
+
+        def grows(sizes):
+            last = (0, 0)
+            for size in sizes:
+                n = api.rar_attn_workspace(p, *size)
+                assert n[0] >= last[0] and n[1] >= last[1], (H, Hkv, dh, dt, size)
+                last = n
+
+        for Tq, Tk in ((512, 512), (1, 2048), (40, 300), (9, 4096), (2000, 64)):
+            grows([(B, Tq, Tk) for B in range(1, 300)])
+            grows([(3, n, Tk) for n in range(0, 1500)])
+            grows([(3, Tq, n) for n in range(0, 3000, 3)])
+        for _ in range(300):
+            size = [1, 1, 1]
+            walk = []
+            while size[0] * max(size[1:]) < 1 << 16:
+                walk.append(tuple(size))
+                i = rng.randrange(3)
+                size[i] += 1 + int(size[i] * rng.random())
+            grows(walk)
+
+
+@pytest.fixture(scope="module")
+def cut(tmp_path_factory):
+    """cut(H, Hkv, dh, dtype, B, Tq, Tk) -> rows that the parts of o, dq and dk (and dv) take, and room for each."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("cut")
+    (d / "s.cpp").write_text(
+        '#include "attn_shape.h"\n'
+        'extern "C" void cut(int64_t H, int64_t Hkv, int64_t dh, int dt, int64_t B, int64_t Tq, int64_t Tk,\n'
+        '                    int64_t *o)\n'
+        '{ const rar::AttnShape s(H, Hkv, dh, (rar_dtype)dt, B, Tq, Tk);\n'
+        '  o[0] = s.splits > 1 ? s.splits * s.part_rows() : 0; o[1] = s.part_room();\n'
+        '  o[2] = s.q_splits > 1 ? s.q_splits * s.part_rows() : 0; o[3] = s.q_room();\n'
+        '  o[4] = s.k_splits > 1 ? s.k_splits * B * Hkv * Tk : 0; o[5] = s.k_room(); }\n')
+    subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{ROOT / 'include'}",
+                    f"-I{ROOT / 'ring_all_reduce_amd' / 'csrc'}", str(d / "s.cpp"), "-o", str(d / "s.so")], check=True)
+    fn = ctypes.CDLL(str(d / "s.so")).cut
+    fn.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] + [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_int64)]
+    fn.restype = None
+
+    def call(*a):
+        out = (ctypes.c_int64 * 6)()
+        fn(*a, out)
+        return tuple(out)
+
+    return call
+
+
+def test_parts_stay_in_their_room(cut):
+    rng = random.Random(8)
+    cuts = 0
+    for _ in range(200_000):
+        Hkv = int(2 ** rng.uniform(0, 7))
+        share = rng.choice([1, 1, 2, 3, 4, 8, 33])
+        B, Tq, Tk = (int(2 ** rng.uniform(0, b)) for b in (9, 13, 18))
+        size = (Hkv * share, Hkv, rng.randint(1, 128), rng.randint(0, 1), B, rng.choice([1, 2, Tq, Tq]), Tk)
+        n = cut(*size)
+        cuts += n[0] > 0
+        assert n[0] <= n[1] and n[2] <= n[3] and n[4] <= n[5], (size, n)
+    assert cuts > 10_000
