@@ -571,12 +571,14 @@ rar_status rar_attn_plan(int64_t H, int64_t Hkv, int64_t dh, rar_dtype dtype, fl
 rar_status rar_attn_destroy(rar_attn_t plan);
 
 /* Workspaces of a forward and of a backward call on B sequences of Tq queries
- * and Tk keys (B Tq and B Tk at most 2^24, B at most 65535), for matrices at any
- * address and of any leading dimension.  Either output may be NULL.  A forward
- * call of at most four rows a key head (Tq H / Hkv: a decoding step) reads its
- * matrices as they stand and needs no more than the parts that its keys are cut
- * into.  Where a query gives zero, ws may be NULL.  A workspace serves every
- * call of fewer sequences, queries or keys too. */
+ * and Tk keys, for matrices at any address and of any leading dimension.  B is at
+ * most 65535, B Tq and B Tk at most 2^24; a launch's 2^32 lanes allow less than
+ * 2^23 of B Hkv ceil(Tq H / (128 Hkv)) and of B H ceil(Tq / 64), and less than
+ * 2^24 of B Hkv ceil(Tk / 128).  Either output may be NULL.  A forward call of at
+ * most four rows a key head (Tq H / Hkv: a decoding step) reads its matrices as
+ * they stand and needs no more than the parts that its keys are cut into.  Where
+ * a query gives zero, ws may be NULL.  A workspace serves every call of fewer
+ * sequences, queries or keys too. */
 rar_status rar_attn_workspace(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, int64_t *forward_bytes,
                               int64_t *backward_bytes);
 

@@ -1781,30 +1781,33 @@ __global__ void __launch_bounds__(256) rar_attn_sum(const AttnSum p)
 }
 
 // Copies of operands whose heads are not whole 16-byte groups at 16-byte aligned
-// addresses: every head's columns to `cols`, zero behind dh.
+// addresses: every head's columns to `cols`, zero behind dh.  A lane takes group
+// after group, so that a launch takes operands of any size.
+constexpr int64_t kPackBlocks = 16384;
+
 template <class T>
-__global__ void __launch_bounds__(256) rar_attn_pack(const AttnPack p)
+__global__ void __launch_bounds__(256) rar_attn_pack(const AttnPack p, const int64_t chunks)
 {
     constexpr int kPer = 16 / sizeof(T);
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    int e = 0;
-    while (e < p.count && i >= p.item[e].chunks)
-        i -= p.item[e++].chunks;
-    if (e == p.count)
-        return;
-    const AttnPack::Item &m = p.item[e];
-    const int per_head = p.cols / kPer;
-    const int64_t row = i / (m.heads * per_head);
-    const int64_t in = i - row * (m.heads * per_head);
-    const int64_t head = in / per_head, c = (in - head * per_head) * kPer;
-    const T *const from = (const T *)m.src + row * m.ld + head * p.dh + c;
-    float v[8];
-    load8(from, clamp8(p.dh - c < kPer ? p.dh - c : kPer), v);
-    T *const to = (T *)m.dst + (row * m.heads + head) * p.cols + c;
-    if constexpr (sizeof(T) == 4)
-        store4(to, f32x4{v[0], v[1], v[2], v[3]});
-    else
-        store8(to, 8, v);
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < chunks; n += (int64_t)gridDim.x * 256) {
+        int64_t i = n;
+        int e = 0;
+        while (i >= p.item[e].chunks)
+            i -= p.item[e++].chunks;
+        const AttnPack::Item &m = p.item[e];
+        const int per_head = p.cols / kPer;
+        const int64_t row = i / (m.heads * per_head);
+        const int64_t in = i - row * (m.heads * per_head);
+        const int64_t head = in / per_head, c = (in - head * per_head) * kPer;
+        const T *const from = (const T *)m.src + row * m.ld + head * p.dh + c;
+        float v[8];
+        load8(from, clamp8(p.dh - c < kPer ? p.dh - c : kPer), v);
+        T *const to = (T *)m.dst + (row * m.heads + head) * p.cols + c;
+        if constexpr (sizeof(T) == 4)
+            store4(to, f32x4{v[0], v[1], v[2], v[3]});
+        else
+            store8(to, 8, v);
+    }
 }
 
 template <class P>
@@ -1904,8 +1907,8 @@ hipError_t launch_attn_pack(rar_dtype dt, const AttnPack &p, hipStream_t st)
     int64_t chunks = 0;
     for (int i = 0; i < p.count; ++i)
         chunks += p.item[i].chunks;
-    return launch(dt == RAR_BF16 ? rar_attn_pack<bf16> : rar_attn_pack<float>, (unsigned)((chunks + 255) / 256), 256,
-                  st, p);
+    return launch(dt == RAR_BF16 ? rar_attn_pack<bf16> : rar_attn_pack<float>,
+                  (unsigned)std::min((chunks + 255) / 256, kPackBlocks), 256, st, p, chunks);
 }
 
 }  // namespace rar

@@ -111,11 +111,9 @@ struct AttnShape {
     // every launch has at most 2^32 lanes
     bool fits() const
     {
-        const int64_t per = 16 / esize(dt);
         return blocks() <= kMaxLanes / 512 && B * Hkv * key_tiles * k_splits <= kMaxLanes / 256 &&
                B * Hkv * q_tiles * q_splits <= kMaxLanes / 256 &&
-               div_up(B * H * padded, 32) <= kMaxLanes / 256 &&
-               div_up((2 * B * Tq * H + 2 * B * Tk * Hkv) * (cols / per), 256) <= kMaxLanes / 256;
+               div_up(B * H * padded, 32) <= kMaxLanes / 256;
     }
 };
 

@@ -116,3 +116,23 @@ def test_parts_stay_in_their_room(cut):
         cuts += n[0] > 0
         assert n[0] <= n[1] and n[2] <= n[3] and n[4] <= n[5], (size, n)
     assert cuts > 10_000
+
+
+def test_attention_takes_every_size_that_its_launches_do():
+    def bytes_of(H, Hkv, dh, *size):
+        p = api.rar_attn_plan(H, Hkv, dh, api.BF16)
+        return api.rar_attn_workspace(p, *size)
+
+    # caches of 32 GiB and more: copies of them would take lanes beyond 2^32 if each had one group
+    assert bytes_of(16, 16, 128, 64, 1, 1 << 17)[0] <= 1 << 21
+    assert bytes_of(64, 64, 128, 16, 1, 1 << 20)[0] <= 1 << 23
+    assert bytes_of(16, 16, 128, 1, 5, 1 << 24)[0] >= 2 << 36
+    # both sides of the limits that rar.h names
+    for good, bad in (((128, 128, 8, 65535, 1, 1), (129, 129, 8, 65535, 1, 1)),
+                      ((2048, 2048, 8, 4, 1 << 15, 1), (4096, 4096, 8, 4, 1 << 15, 1)),
+                      ((127, 127, 8, 1, 1, 1 << 24), (128, 128, 8, 1, 1, 1 << 24)),
+                      ((31, 1, 8, 1, 1 << 24, 1), (32, 1, 8, 1, 1 << 24, 1))):
+        bytes_of(*good)
+        with pytest.raises(api.RarError) as e:
+            bytes_of(*bad)
+        assert e.value.status == api.EINVAL

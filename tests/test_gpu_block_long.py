@@ -104,3 +104,22 @@ def test_attention_of_many_stages(shape, dtype):
     want = R.attn_backward(do, q, k, v, o.cpu(), lse.cpu(), B, H, Hkv, dh ** -0.5, ql, kl, dtype)
     for t, (r, e), n in zip(grads, want, ("dq", "dk", "dv")):
         R.check(t, r, e, n)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_attention_copies_of_many_groups(dtype):
+    # more 16-byte groups to copy than lanes of a launch copy at once (2^22)
+    B, Tq, Tk, H, dh = 2, 5, 17000, 16, 63 if dtype == "bf16" else 31
+    g = torch.Generator().manual_seed(5)
+    q, do = (rand(g, B * Tq, H * dh, dtype=dtype) for _ in range(2))
+    k, v = (rand(g, B * Tk, H * dh, dtype=dtype) for _ in range(2))
+    plan = api.rar_attn_plan(H, H, dh, CODE[dtype])
+    o, lse = nan(B * Tq, H * dh, dtype=dtype), nan(B * Tq, H)
+    api.rar_attn_forward(plan, B, Tq, Tk, dev(q), dev(k), dev(v), o, lse=lse)
+    (ro, eo), _ = R.attn_forward(q, k, v, B, H, H, dh ** -0.5, None, None, dtype)
+    R.check(o, ro, eo, "o")
+    grads = [torch.full_like(dev(t), NAN) for t in (q, k, v)]
+    api.rar_attn_backward(plan, B, Tq, Tk, dev(do), dev(q), dev(k), dev(v), o, lse, *grads)
+    want = R.attn_backward(do, q, k, v, o.cpu(), lse.cpu(), B, H, H, dh ** -0.5, None, None, dtype)
+    for t, (r, e), n in zip(grads, want, ("dq", "dk", "dv")):
+        R.check(t, r, e, n)
