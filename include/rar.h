@@ -598,8 +598,11 @@ rar_status rar_attn_forward(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, 
                             void *stream);
 
 /* The gradients of q, k and v, given d_o and the forward call's inputs, o and
- * lse.  Rows of dq behind qlen and of dk and dv behind klen become zero; shared
- * heads' gradients are summed in a fixed order.  dq, dk and dv may each be NULL.
+ * lse.  Rows of dq behind qlen and of dk and dv behind klen become zero, and so do
+ * rows of dq of queries that no key is left for; shared heads' gradients are
+ * summed in a fixed order.  (An infinity within the lengths counts as in the
+ * formula: a weight of zero times an infinite key, query or d_o is NaN in the
+ * gradient that it belongs to.)  dq, dk and dv may each be NULL.
  * bf16: weights and score gradients are rounded to bf16 for their products. */
 rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk, const void *d_o, int64_t lddo,
                              const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,

@@ -202,7 +202,7 @@ struct Loader {
     typedef Tile<T, PITCH> Lds;
     static constexpr int kLoads = ROWS * Lds::kBytes / (WAVES * 1024);
     static_assert(kLoads * WAVES * 1024 == ROWS * Lds::kBytes, "whole loads");
-    uint32_t voff[kLoads];
+    uint32_t voff[kLoads], in_row;
     const char *base;
     int64_t pitch, width;  // bytes of a row in memory, and of a head
     int64_t left;          // rows from base that count
@@ -219,21 +219,27 @@ struct Loader {
             const int at = (j * WAVES + wave) * 1024 + lane * 16;
             const int r = at / Lds::kBytes, c = ((at % Lds::kBytes) / 16) ^ Lds::spread(r);
             voff[j] = c * 16 < width ? (uint32_t)(r * pitch) + c * 16 : kOutOfRange;
+            if (j == 0)
+                in_row = c * 16 < width ? c * 16 : kOutOfRange;
         }
     }
 
+    // LAST: the last row that counts stands in place of those behind it (left > 0).
+    template <bool LAST = false>
     __device__ __forceinline__ void load(RAR_LDS char *__restrict__ lds)
     {
+        static_assert(!LAST || WAVES * 1024 / Lds::kBytes % 16 == 0, "a lane's chunk is the same in all of its rows");
 #if defined(__HIP_DEVICE_COMPILE__)
         const int wave = WAVES > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
         int64_t n = left > 0 ? (left - 1) * pitch + width : 0;
         if (n > 0x7fffffff)
             n = 0x7fffffff;
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
+        const uint32_t last = (uint32_t)(n - width) + in_row;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * WAVES + wave) * 1024), 16, voff[j],
-                                                     0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (RAR_LDS void *)(lds + (j * WAVES + wave) * 1024), 16,
+                                                     LAST ? std::min(voff[j], last) : voff[j], 0, 0, 0);
 #endif
     }
 
@@ -1109,6 +1115,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
     load_row<T>(g, p.g, b * p.Tq + t, h, live);
     const int64_t place = (b * p.H + h) * p.padded + t;
     const float lse = live ? -p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
+    const bool some = lse != kInf;  // a key is left (weights are zero without, but a product with an infinity is not)
 
     // this workgroup's stages of keys
     const int64_t all = first / p.share < qlen ? (klen + F::kStage - 1) / F::kStage : 0;
@@ -1177,7 +1184,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
             f32x4 v;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                v[x] = live ? acc[d][4 * i + x] * p.scale : 0.0f;
+                v[x] = some ? acc[d][4 * i + x] * p.scale : 0.0f;
             if (p.splits > 1)
                 store4(part + c, v);
             else
@@ -1219,6 +1226,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_bf16(const AttnParams p)
     const int64_t place = (b * p.H + r.h) * p.padded + r.t;
     const float scale2 = p.scale * kLog2e;
     const float lse = r.live ? p.row_lse[place] * scale2 : -kInf, delta = r.live ? p.row_delta[place] : 0.0f;
+    const bool some = lse != -kInf;
     f32x16 dq[W];
 #pragma unroll
     for (int d = 0; d < W; ++d)
@@ -1361,7 +1369,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_bf16(const AttnParams p)
             f32x4 a;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                a[x] = r.live ? dq[d][4 * i + x] * p.scale : 0.0f;
+                a[x] = some ? dq[d][4 * i + x] * p.scale : 0.0f;
             if (p.splits > 1)
                 store4(part + c, a);
             else
@@ -1472,7 +1480,9 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
         start(lse, starts, 0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = weight<T>(s[i], p.scale, -lse[i]);
+            // The minimum with a NaN is the other: zeros in place of rows behind qlen make one with a key that holds an
+            // infinity, and lse takes it out.  (Where a row that counts has a NaN, its lse is one.)
+            s[i] = weight<T>(__builtin_fminf(s[i], 0x1.fffffep127f), p.scale, -lse[i]);
             dp[i] *= s[i];
         }
 #pragma unroll
@@ -1583,8 +1593,10 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_bf16(const AttnParams p)
             lg.init(p.g, b * p.Tq + ahead * F::kStage, head, qlen - ahead * F::kStage);
             entered = true;
         }
-        lq.load(to);
-        lg.load(to + F::kHalf);
+        // (zeros in place of rows behind qlen, whose weights are zero, would make a NaN with a key that holds an
+        // infinity: the last row makes one only where it does so itself)
+        lq.template load<true>(to);
+        lg.template load<true>(to + F::kHalf);
         if (wave < 2) {
             const int64_t row = (b * p.H + head) * p.padded + ahead * F::kStage;
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(

@@ -123,3 +123,44 @@ def test_attention_copies_of_many_groups(dtype):
     want = R.attn_backward(do, q, k, v, o.cpu(), lse.cpu(), B, H, H, dh ** -0.5, None, None, dtype)
     for t, (r, e), n in zip(grads, want, ("dq", "dk", "dv")):
         R.check(t, r, e, n)
+
+
+@pytest.mark.parametrize("Tq,Tk", [(2, 70), (40, 200), (300, 700)])
+@pytest.mark.parametrize("dtype", BOTH)
+def test_attention_gradient_of_queries_without_keys(Tq, Tk, dtype):
+    B, H, dh = 2, 2, 40
+    g = torch.Generator().manual_seed(Tq)
+    q, do = (rand(g, B * Tq, H * dh, dtype=dtype) for _ in range(2))
+    k, v = (rand(g, B * Tk, H * dh, dtype=dtype) for _ in range(2))
+    plan = api.rar_attn_plan(H, H, dh, CODE[dtype])
+
+    def run(q, k):
+        o, lse = nan(B * Tq, H * dh, dtype=dtype), nan(B * Tq, H)
+        api.rar_attn_forward(plan, B, Tq, Tk, dev(q), dev(k), dev(v), o, lse=lse)
+        grads = [torch.full_like(dev(t), NAN) for t in (q, k, v)]
+        api.rar_attn_backward(plan, B, Tq, Tk, dev(do), dev(q), dev(k), dev(v), o, lse, *grads)
+        return o.cpu(), lse.cpu(), *(t.cpu() for t in grads)
+
+    # every score of the first sequence is -infinity, none of the second's
+    q1, k1 = q.clone(), k.clone()
+    q1[:Tq], k1[:Tk] = q[:Tq].abs() + 1, -INF
+    o, lse, dq, dk, dv = run(q1, k1)
+    assert (o[:Tq] == 0).all() and (lse[:Tq] == -INF).all()
+    assert (dq[:Tq] == 0).all() and (dk[:Tk] == 0).all() and (dv[:Tk] == 0).all()
+    q1[:Tq] = k1[:Tk] = 0
+    want = R.attn_backward(do, q1, k1, v, o, lse, B, H, H, dh ** -0.5, None, None, dtype)
+    for t, (r, e), n in zip((dq, dk, dv), want, ("dq", "dk", "dv")):
+        R.check(t, r, e, n)
+    # one query's scores are: its dq is zero, the others' stay, and dk has what it multiplies in one column
+    k2 = k.clone()
+    k2[:, 0] = k[:, 0].abs() + 1
+    q2 = q.clone()
+    q2[1, 0] = -INF
+    o, lse, dq, dk, dv = run(q2, k2)
+    assert (o[1, :dh] == 0).all() and (lse[1, 0] == -INF).all() and (dq[1, :dh] == 0).all()
+    assert torch.isnan(dk[:Tk, 0]).all()
+    q2[1, 0] = dk[:Tk, 0] = 0
+    want = R.attn_backward(do, q2, k2, v, o, lse, B, H, H, dh ** -0.5, None, None, dtype)
+    want[1][0][:Tk, 0] = 0
+    for t, (r, e), n in zip((dq, dk, dv), want, ("dq", "dk", "dv")):
+        R.check(t, r, e, n)
