@@ -564,8 +564,9 @@ typedef struct rar_attn_s *rar_attn_t;
 
 /* Attention of H query heads of dh columns (1..RAR_ATTN_MAX_WIDTH) to an
  * encoder's states projected to Hkv key and value heads; Hkv divides H, and H /
- * Hkv neighbouring query heads share one.  H dh at most 2^20.  scale multiplies
- * the scores.  Host memory only, immutable, any number of threads and streams. */
+ * Hkv neighbouring query heads share one.  H dh at most 2^20.  scale, 2^-100 to
+ * 2^100, multiplies the scores.  Host memory only, immutable, any number of threads
+ * and streams. */
 rar_status rar_attn_plan(int64_t H, int64_t Hkv, int64_t dh, rar_dtype dtype, float scale, rar_attn_t *out);
 
 rar_status rar_attn_destroy(rar_attn_t plan);
@@ -614,7 +615,7 @@ rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, int64_t Tk,
 
 #define RAR_LOGPROB_MAX_TOP 32
 
-/* With z = scale * logits (T x V, scale > 0) and p = softmax(z) of a row:
+/* With z = scale * logits (T x V, 0 < scale <= 2^126) and p = softmax(z) of a row:
  *   logp[t]    = log p at targets[t]; zero for a target outside 0..V-1 (padding)
  *   entropy[t] = -sum p log p
  *   top_ids[t][k], top_logp[t][k], k < K: the K largest logits in falling order,

@@ -275,6 +275,8 @@ extern "C" rar_status rar_dropout(int64_t T, int64_t D, rar_dtype dtype, float p
 namespace {
 
 constexpr int64_t kMaxBatch = 65535;
+// The bf16 gradients start from -lse / scale, every call takes scale log2 e: neither may overflow where scores do not.
+constexpr float kAttnScale = 0x1p-100f;
 
 AttnShape attn_shape(const rar_attn_s &a, int64_t B, int64_t Tq, int64_t Tk)
 {
@@ -356,7 +358,7 @@ extern "C" rar_status rar_attn_plan(int64_t H, int64_t Hkv, int64_t dh, rar_dtyp
         return RAR_EINVAL;
     *out = nullptr;
     if (H < 1 || H > kMaxWidth || Hkv < 1 || Hkv > H || H % Hkv || dh < 1 || dh > RAR_ATTN_MAX_WIDTH ||
-        H * dh > kMaxWidth || !valid_dtype(dtype) || !(scale > 0) || !std::isfinite(scale))
+        H * dh > kMaxWidth || !valid_dtype(dtype) || !(scale >= kAttnScale) || !(scale <= 1 / kAttnScale))
         return RAR_EINVAL;
     rar_attn_s *p = new (std::nothrow) rar_attn_s;
     if (!p)
@@ -565,9 +567,11 @@ extern "C" rar_status rar_attn_backward(rar_attn_t plan, int64_t B, int64_t Tq, 
 
 namespace {
 
+constexpr float kLogprobScale = 0x1p126f;  // scale log2 e is finite: times the maximum's distance, zero, it is zero
+
 bool valid_logprob(int64_t T, int64_t V, rar_dtype dtype, float scale)
 {
-    return valid_rows(T) && valid_width(V) && valid_dtype(dtype) && scale > 0 && std::isfinite(scale);
+    return valid_rows(T) && valid_width(V) && valid_dtype(dtype) && scale > 0 && scale <= kLogprobScale;
 }
 
 }  // namespace
