@@ -26,7 +26,7 @@
 //
 // Measured at 8 x 16 heads of 128 in bf16, 1152 to 2048 queries on 576 to 1024 keys
 // (products of 42 GFLOP each): forward 115 to 127 us (two products, 680 TFLOP/s), delta
-// 24 (4.4 TB/s), dq 192 to 206 (three, 630), dk and dv 211 to 229 (four, 760).  A large
+// 24 (4.4 TB/s), dq 156 to 173 (three, 770), dk and dv 211 to 238 (four, 750).  A large
 // product of torch's reaches 1380 on that card.  Binary32, 4 x 8 heads of 128, 512 on 512:
 // forward 49 us and a join of 11, dq 65, dk and dv 87 and a sum of 14.
 #include <algorithm>
@@ -1052,33 +1052,6 @@ __global__ void __launch_bounds__(256) rar_attn_delta(const AttnParams p)
     }
 }
 
-// The kernels for bf16 have their schedule in the text: products as statements that
-// keep their order, accumulators and what a wave holds of its own in accumulation
-// registers, scores in ordinary ones.  (Left to itself the compiler moves scores
-// between the register files, three moves a product, and lets products, arithmetic
-// and LDS reads wait for each other.)  One wave a SIMD, and what would wait runs
-// under the products:
-//   A(n)  scores of tile n + 1, between them the weights of tile n and the reads of
-//         its transposed fragments
-//   B(n)  products into the gradients of tile n, under them the reads of the rows of
-//         tile n + 2
-// Stages of two tiles of 32 rows pass through a ring of three in LDS, so that a
-// stage's loads have the time of one stage to arrive.
-__device__ __forceinline__ void product_v(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
-{
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "a"(b));
-}
-
-__device__ __forceinline__ void product_0(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
-{
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "a"(b));
-}
-
-__device__ __forceinline__ void product_a(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
-{
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-
 // dq: a wave holds 32 query rows as in the forward kernel.
 template <class T, int W>
 struct BackwardQ {
@@ -1089,13 +1062,15 @@ struct BackwardQ {
     static constexpr int kHalf = kStage * Lds::kBytes;
 };
 
-// (Binary32.  A product of a tile takes the matrix cores long enough that the reads of
-// the next are hidden one fragment ahead, which the compiler does.)
-template <int W>
-__global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
+// bf16: two waves a SIMD, one under the other's chain of reads, products and exponentials; to fit, heads of over 96
+// columns spill seven registers.  8 x 16 heads of 128, 2048 queries on 1024 keys: 207 us (three products, 1000
+// TFLOP/s); one wave a SIMD takes 36% longer, and 19% with its schedule written out as that of dk and dv is.
+// Binary32: a product of a tile takes the matrix cores long enough that the reads of the next are hidden one
+// fragment ahead, which the compiler does.
+template <class T, int W>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) rar_attn_dq(const AttnParams p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    typedef float T;
     typedef BackwardQ<T, W> F;
     typedef typename F::Lds Lds;
     constexpr int STEPS = F::S::STEPS;
@@ -1114,7 +1089,9 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
     load_row<T>(q, p.q, b * p.Tq + t, h, live);
     load_row<T>(g, p.g, b * p.Tq + t, h, live);
     const int64_t place = (b * p.H + h) * p.padded + t;
-    const float lse = live ? -p.row_lse[place] : kInf, delta = live ? p.row_delta[place] : 0.0f;
+    const float scale = p.scale * kUnit<T>;
+    const float lse = live ? -p.row_lse[place] * (sizeof(T) == 2 ? scale : 1.0f) : kInf;
+    const float delta = live ? p.row_delta[place] : 0.0f;
     const bool some = lse != kInf;  // a key is left (weights are zero without, but a product with an infinity is not)
 
     // this workgroup's stages of keys
@@ -1143,27 +1120,30 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
             lv.load(next + F::kHalf);
         }
         const int rest = (int)(klen - k0 - (int64_t)n * F::kStage);
-        f32x16 s = zeros(), dp = zeros();
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            mma(s, Lds::rows(here, 0, i), q[i]);
-            mma(dp, Lds::rows(here + F::kHalf, 0, i), g[i]);
-        }
+        for (int e = 0; e < F::kTiles; ++e) {
+            f32x16 s = zeros(), dp = zeros();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s[i] = weight<T>(s[i], p.scale, lse) * (dp[i] + delta);
-        if (rest < F::kStage)
+            for (int i = 0; i < STEPS; ++i) {
+                mma(s, Lds::rows(here, e * 32, i), q[i]);
+                mma(dp, Lds::rows(here + F::kHalf, e * 32, i), g[i]);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (row_of(i) + 4 * half >= rest)
-                    s[i] = 0.0f;
+                s[i] = weight<T>(s[i], scale, lse) * (dp[i] + delta);
+            if (rest < F::kStage)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            Frag<T> w;
-            w.set(s, 8 * j);
+                for (int i = 0; i < 16; ++i)
+                    if (e * 32 + row_of(i) + 4 * half >= rest)
+                        s[i] = 0.0f;
 #pragma unroll
-            for (int d = 0; d < W; ++d)
-                mma(acc[d], Lds::cols(here, 0, j, d), w);
+            for (int j = 0; j < 2; ++j) {
+                Frag<T> w;
+                w.set(s, 8 * j);
+#pragma unroll
+                for (int d = 0; d < W; ++d)
+                    mma(acc[d], Lds::cols(here, e * 32, j, d), w);
+            }
         }
         meet();
     };
@@ -1189,191 +1169,6 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dq_f32(const AttnParams p)
                 store4(part + c, v);
             else
                 put4(out, c, p.dh, v);
-        }
-#endif
-}
-
-// The same for bf16: a wave's queries and their gradients are its own.  200 us
-// at the size above, where the compiler's schedule takes 206.
-template <int W>
-__global__ void __launch_bounds__(256, 1) rar_attn_dq_bf16(const AttnParams p)
-{
-#if defined(__HIP_DEVICE_COMPILE__)
-    typedef BackwardQ<bf16, W> F;
-    typedef typename F::Lds Lds;
-    constexpr int STEPS = F::S::STEPS, kProducts = 2 * STEPS, kBuffer = 2 * F::kHalf;
-    __shared__ __attribute__((aligned(1024))) char memory[3 * kBuffer];
-    RAR_LDS char *const lds = (RAR_LDS char *)memory;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
-
-    const Place at = place_of(p.B * p.Hkv, p.Hkv, p.tiles * p.splits);
-    const int64_t tile = at.in % p.tiles, split = at.in / p.tiles, hk = at.hk, b = at.b;
-    const int64_t klen = length_of(p.klen, b, p.Tk), qlen = length_of(p.qlen, b, p.Tq);
-    const int64_t rows = p.Tq * p.share, first = tile * kAttnRows;
-    const RowPlace r = row_place(p, hk, first + wave * 32 + (lane & 31), qlen);
-    bf16x8 q[STEPS], g[STEPS];
-    {
-        Frag<bf16> f[STEPS];
-        load_row<bf16>(f, p.q, b * p.Tq + r.t, r.h, r.live);
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            q[i] = f[i].v;
-        load_row<bf16>(f, p.g, b * p.Tq + r.t, r.h, r.live);
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            g[i] = f[i].v;
-    }
-    const int64_t place = (b * p.H + r.h) * p.padded + r.t;
-    const float scale2 = p.scale * kLog2e;
-    const float lse = r.live ? p.row_lse[place] * scale2 : -kInf, delta = r.live ? p.row_delta[place] : 0.0f;
-    const bool some = lse != -kInf;
-    f32x16 dq[W];
-#pragma unroll
-    for (int d = 0; d < W; ++d)
-        dq[d] = zeros();
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-        asm volatile("" : "+a"(q[i]), "+a"(g[i]));
-#pragma unroll
-    for (int d = 0; d < W; ++d)
-        asm volatile("" : "+a"(dq[d]));
-
-    // this workgroup's stages of keys
-    const int64_t all = first / p.share < qlen ? (klen + F::kStage - 1) / F::kStage : 0;
-    const int64_t begin = all * split / p.splits, k0 = begin * F::kStage;
-    const int stages = (int)(all * (split + 1) / p.splits - begin);
-    Loader<bf16, F::S::PITCH, F::kStage, 4> lk, lv;
-    lk.init(p.k, b * p.Tk + k0, hk, klen - k0);
-    lv.init(p.v, b * p.Tk + k0, hk, klen - k0);
-    auto load = [&](RAR_LDS char *to) __attribute__((always_inline)) {
-        lk.load(to);
-        lv.load(to + F::kHalf);
-        lk.advance();
-        lv.advance();
-    };
-    bf16x8 k[STEPS], v[STEPS], kt[2][W], w[2];
-    f32x16 s[2], dp[2];
-    // one of a tile's fragments: of a row, or transposed, in the order of their use
-    auto read_row = [&](const RAR_LDS char *from, int e, int m) __attribute__((always_inline)) {
-        if (m & 1)
-            v[m / 2] = Lds::rows(from + F::kHalf, e * 32, m / 2).v;
-        else
-            k[m / 2] = Lds::rows(from, e * 32, m / 2).v;
-    };
-    auto score = [&](auto E, int m) __attribute__((always_inline)) {
-        f32x16 &c = m & 1 ? dp[E()] : s[E()];
-        const bf16x8 &a = m & 1 ? v[m / 2] : k[m / 2], &o = m & 1 ? g[m / 2] : q[m / 2];
-        if (m < 2)
-            product_0(c, a, o);
-        else
-            product_v(c, a, o);
-    };
-    // A: scores of tile N with the weights of the other tile, of whose keys `rest` count, between them
-    auto phase_a = [&](auto N, const RAR_LDS char *from, int rest) __attribute__((always_inline)) {
-        constexpr int O = 1 - N();
-        // the other tile's products were issued before phase B; its last ones write until here at the latest
-        asm volatile("s_nop 15" : "+v"(s[O]), "+v"(dp[O]));
-        if (rest < 32)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (row_of(i) + 4 * half >= rest)
-                    s[O][i] = -kInf;
-        float x[16], y[16];
-        uint32_t pd[8];
-        auto finish = [&](int i) __attribute__((always_inline)) {
-            y[i] = (dp[O][i] + delta) * x[i];
-            if (i & 1) {
-                pd[i / 2] = pack_bf16(y[i - 1], y[i]);
-                asm volatile("" : "+v"(pd[i / 2]));
-            }
-        };
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m) {
-            score(N, m);
-            if (m & 1)
-                kt[m / (2 * W)][m / 2 % W] = Lds::cols(from, O * 32, m / (2 * W), m / 2 % W).v;
-#pragma unroll
-            for (int i = m * 16 / kProducts; i < (m + 1) * 16 / kProducts; ++i) {
-                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[O][i], scale2, lse));
-                asm volatile("" : "+v"(x[i]));
-            }
-            // (an exponential's result is used one product later)
-            if (m > 0)
-#pragma unroll
-                for (int i = (m - 1) * 16 / kProducts; i < m * 16 / kProducts; ++i)
-                    finish(i);
-        }
-#pragma unroll
-        for (int i = (kProducts - 1) * 16 / kProducts; i < 16; ++i)
-            finish(i);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            w[j] = __builtin_bit_cast(bf16x8, u32x4{pd[4 * j], pd[4 * j + 1], pd[4 * j + 2], pd[4 * j + 3]});
-        // packed by the vector units, read by the matrix ones
-        asm volatile("s_nop 3" : "+v"(w[0]), "+v"(w[1]));
-    };
-    auto phase_b = [&](const RAR_LDS char *from, int e) __attribute__((always_inline)) {
-#pragma unroll
-        for (int m = 0; m < STEPS; ++m) {
-            product_a(dq[m % W], kt[m / W][m % W], w[m / W]);
-            read_row(from, e, 2 * m);
-            read_row(from, e, 2 * m + 1);
-        }
-    };
-
-    if (stages)
-        load(lds);
-    meet();
-    if (stages > 1)
-        load(lds + kBuffer);
-    if (stages) {
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m)
-            read_row(lds, 0, m);
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m)
-            score(Half<0>{}, m);
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m)
-            read_row(lds, 1, m);
-    }
-    int slot = 0;
-    for (int n = 0; n < stages; ++n) {
-        RAR_LDS char *const here = lds + slot * kBuffer;
-        slot = slot == 2 ? 0 : slot + 1;
-        RAR_LDS char *const next = lds + slot * kBuffer;
-        const int rest = (int)(klen - k0 - (int64_t)n * F::kStage);
-        phase_a(Half<1>{}, here, rest);
-        // the next stage has arrived, and the one before this is no longer read
-        meet();
-        if (n + 2 < stages)
-            load(lds + (slot == 2 ? 0 : slot + 1) * kBuffer);
-        phase_b(next, 0);  // (behind the last stage: rows of what lies there, for nothing)
-        phase_a(Half<0>{}, here, rest - 32);
-        phase_b(next, 1);
-    }
-    // wait for the last products, and tie every use of the accumulators to what follows the wait
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-    for (int d = 0; d < W; ++d)
-        asm volatile("" : "+a"(dq[d]));
-    if (r.row >= rows)
-        return;
-    bf16 *const out = (bf16 *)p.dq + (b * p.Tq + r.t) * p.lddq + r.h * p.dh;
-    float *const part = p.part + (split * p.part_rows + (b * p.Hkv + hk) * rows + r.row) * (W * 32);
-#pragma unroll
-    for (int d = 0; d < W; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = d * 32 + 8 * i + 4 * half;
-            f32x4 a;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                a[x] = some ? dq[d][4 * i + x] * p.scale : 0.0f;
-            if (p.splits > 1)
-                store4(part + c, a);
-            else
-                put4(out, c, p.dh, a);
         }
 #endif
 }
@@ -1530,7 +1325,29 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
 #endif
 }
 
-// The same for bf16: a wave's keys and values are its own, scores start from LDS.
+// The kernel for bf16 has its schedule in the text: products as statements that
+// keep their order, accumulators and what a wave holds of its own in accumulation
+// registers, scores in ordinary ones.  (Left to itself the compiler moves scores
+// between the register files, three moves a product, and lets products, arithmetic
+// and LDS reads wait for each other.)  One wave a SIMD, and what would wait runs
+// under the products:
+//   A(n)  scores of tile n + 1, between them the weights of tile n and the reads of
+//         its transposed fragments
+//   B(n)  products into the gradients of tile n, under them the reads of the rows of
+//         tile n + 2
+// Stages of two tiles of 32 rows pass through a ring of three in LDS, so that a
+// stage's loads have the time of one stage to arrive.
+__device__ __forceinline__ void product_v(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
+{
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "a"(b));
+}
+
+__device__ __forceinline__ void product_a(f32x16 &c, const bf16x8 &a, const bf16x8 &b)
+{
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// A wave's keys and values are its own, scores start from LDS.
 // 218 us at the size above, where the compiler's schedule takes 254; of the units'
 // busy cycles the matrix cores take 44%, the vector units 28%.  Without the
 // exponentials, or without the transposed reads, it takes 6 to 8% less, without the
@@ -1850,10 +1667,10 @@ void (*dq_kernel(rar_dtype dt, int w))(AttnParams)
 {
     const bool wide = dt == RAR_F32;
     switch (w) {
-    case 1: return wide ? rar_attn_dq_f32<1> : rar_attn_dq_bf16<1>;
-    case 2: return wide ? rar_attn_dq_f32<2> : rar_attn_dq_bf16<2>;
-    case 3: return wide ? rar_attn_dq_f32<3> : rar_attn_dq_bf16<3>;
-    default: return wide ? rar_attn_dq_f32<4> : rar_attn_dq_bf16<4>;
+    case 1: return wide ? rar_attn_dq<float, 1> : rar_attn_dq<bf16, 1>;
+    case 2: return wide ? rar_attn_dq<float, 2> : rar_attn_dq<bf16, 2>;
+    case 3: return wide ? rar_attn_dq<float, 3> : rar_attn_dq<bf16, 3>;
+    default: return wide ? rar_attn_dq<float, 4> : rar_attn_dq<bf16, 4>;
     }
 }
 
