@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 && W > 2 ? 1 : 2) rar_attn
 // waits for another.  Bound by reading the keys: what counts is how much is in
 // flight, all of LDS but the tiles in use.  The waves are joined through LDS at
 // the end.  16 x 16 heads of 128, eight queries on 1024 to 2048 keys in bf16: 48 us
-// (201 MB, 4.1 TB/s).
+// (201 MB, 4.1 TB/s); in binary32, where LDS holds the ring of one wave only, 310
+// (403 MB, 1.3 TB/s).
 template <class T, int W>
 struct Few {
     typedef Shape<T, W> S;
@@ -766,7 +767,8 @@ __global__ void __launch_bounds__(64 * attn_few_waves((W <= 2 ? 64 : 128) * size
 // The eight waves of a workgroup take keys in turn and are joined through LDS.
 // Loads go straight to registers at any address, so no cache is copied.  Scores
 // and their maximum are in units of log 2.  Bound by HBM: 16 x 16 heads of 128 on
-// 1024 to 2048 keys in bf16, 201 MB, 44 us (4.6 TB/s; 5.4 at four times the batch).
+// 1024 to 2048 keys in bf16, 201 MB, 44 us (4.6 TB/s; 5.4 at four times the batch);
+// in binary32, 403 MB, 74 us (5.4 TB/s).
 template <class T>
 struct Piece {
     static constexpr int N = 16 / sizeof(T);
@@ -1198,6 +1200,7 @@ struct BackwardK {
     static constexpr int kBuffer = 2 * kHalf + 1024;    // q, do, lse and delta
 };
 
+// (Binary32.  Heads of over 96 columns take all 512 registers and spill 18.)
 template <int W>
 __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
 {
@@ -1335,6 +1338,7 @@ __global__ void __launch_bounds__(256, 1) rar_attn_dkv_f32(const AttnParams p)
 //         its transposed fragments
 //   B(n)  products into the gradients of tile n, under them the reads of the rows of
 //         tile n + 2
+// (Heads of up to 64 columns leave room for a second wave.)
 // Stages of two tiles of 32 rows pass through a ring of three in LDS, so that a
 // stage's loads have the time of one stage to arrive.
 __device__ __forceinline__ void product_v(f32x16 &c, const bf16x8 &a, const bf16x8 &b)

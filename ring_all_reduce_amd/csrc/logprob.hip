@@ -18,8 +18,10 @@
 //
 // 8192 x 32000 in bf16: with entropy 121 us (524 MB, 4.3 TB/s), with eight alternatives
 // besides 147 (vector units busy for 73%), with the gradient 219 (1.05 GB, 4.8 TB/s); in
-// binary32 213 with alternatives and 443 with the gradient, at HBM's rate.  Eight rows in
-// binary32 with alternatives: 8 us, a launch and a row's own chain of joins.
+// binary32 213 with alternatives and 443 with the gradient, at HBM's rate.  With
+// alternatives in bf16 a narrower row waits more for the chain of its joins, under
+// which nothing is loaded: 4096 x 20000 54 us (3.0 TB/s), 4096 x 10000 36 (2.3).  Eight
+// rows in binary32 with alternatives: 8 us, a launch and a row's own chain of joins.
 #include "ops_internal.h"
 #include "row.h"
 
@@ -85,6 +87,9 @@ struct TopLds {
 // memory for each pass.
 // Held to 64 registers where the row takes at most half of them, so that two
 // workgroups of 1024 share a compute unit: one waits while the other computes.
+// (Two to eight registers a lane are spilled for it, in binary32 with alternatives
+// and in bf16 of eight eights: 8192 x 32000 in bf16 with eight alternatives writes
+// 16 MB for results of 0.9 and reads 586 for 524.)
 template <class T, int LANES, int R, bool GRAD>
 __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16 ? 8 : 4)
     rar_logprob_rows(const LogprobParams p)
@@ -92,7 +97,8 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, R * sizeof(T) <= 16
     typedef RowJoin<LANES, 2> Join;
     constexpr int kRows = Join::kThreads / LANES;
     constexpr int kHeld = R ? R : 1;
-    constexpr bool kSkip = R == 4 || R == 16;  // (of 8192 x 32000, 6 and 8 eights, it would cost 6%: more registers)
+    // (with six or eight eights it takes registers that are short there: 6% of 8192 x 32000)
+    constexpr bool kSkip = R == 4 || R == 16;
     __shared__ float lds[Join::kFloats];
     __shared__ TopLds<LANES> top;
     Join join{lds};

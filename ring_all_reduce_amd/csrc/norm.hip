@@ -9,13 +9,15 @@
 // mean(q) for rms.  The backward kernel makes mean and r again from the rows o
 // and h that it reads in any case, so nothing but them is kept.
 //
-// Bound by HBM: a row passes once through the registers of its lanes, eight
-// columns a lane; a workgroup keeps the vectors and takes rows in turn, the next
-// row's loads under this row's sums.  The variance is taken of the centred row, so
-// that a mean far from zero costs no digits.  65536 x 2048 in bf16, norms on both
-// sides: forward 220 us (1.07 GB, 4.9 TB/s), backward 330 and 12 for the column sums
-// (1.61 GB, 4.9 TB/s); torch's copy of 2 GB reaches 4.9 TB/s on that card.  8 x 2048
-// in binary32: 4 us, a launch.
+// A row passes once through the registers of its lanes, eight columns a lane; a
+// workgroup keeps the vectors and takes rows in turn, the next row's loads under
+// this row's sums.  The variance is taken of the centred row, so that a mean far from
+// zero costs no more than the mean's own rounding.  65536 x 2048, norms on both
+// sides: forward 220 us in bf16 and 415 in binary32 (1.07 and 2.15 GB, 4.9 and 5.2
+// TB/s), bound by HBM at the rate of torch's copy of 2 GB, 4.9; backward 330 and 650
+// (1.61 and 3.22 GB, 4.9 TB/s) and 12 for the column sums.  Two reads a write can go
+// at 5.9 TB/s (dropout does): the backward kernel's vector units are 76% busy, and
+// what they do not hide of the rest is some 20%.  8 x 2048 in binary32: 4 us, a launch.
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(LANES > 256 ? LANES : 256, LANES >= 512 ? 4 : 
     Eight<T> gate, w1, w2;
     // Long rows keep their column sums in LDS (a lane's own, so nothing waits): without them 128 registers hold the
     // rest and the next row, and a compute unit holds 1024 lanes.  16384 x 8192 in bf16 360 us (1.6 GB), 1200 with the
-    // sums in registers; 16384 x 4096 176 and 214.
+    // sums in registers; 16384 x 4096 176 and 214.  (In binary32 14 registers are spilled at 512 lanes, 2 at 1024.)
     constexpr bool kInLds = LANES >= 512;
     __shared__ f32x4 kept[kInLds ? kSums * 2 : 1][kInLds ? LANES : 1];
     float sums[kSums][8] = {};
